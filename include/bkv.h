@@ -2,8 +2,10 @@
  * bkv.h -- C ABI of libbkv.so, the GB300 (sm_103a) paged (block) KV cache
  * hot path: slot mapping, manager-to-kernel block expansion, the KV cache
  * scatter (bf16 / fp32, or quantised to FP8), GQA paged decode attention
- * with a split-KV merge, mixed-step attention, and the context-parallel
- * slot filter and merge.
+ * with a split-KV merge, mixed-step attention, the context-parallel
+ * slot filter and merge, and the speculative step around them: query / key
+ * norm and rotation fused with the cache write, attention of drafted trees,
+ * verification of drafts.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -522,6 +524,192 @@ int bkv_paged_decode_noalloc(const void *q, const void *k_cache, const void *v_c
                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                              int64_t total_blocks, float softmax_scale, int mask_mode, int dtype,
                              void *out, int32_t *err_count, bkv_stream_t stream);
+
+/*
+ * bkv_qk_norm_rope_cache_write, bkv_qk_norm_rope_cache_write_fp8
+ *   A step's tokens from their projections to the cache in one pass: the norm
+ *   of every query and key head, the position rotation, slot mapping, and the
+ *   K/V write of bkv_slot_mapping_cache_write (or, into E4M3 caches, of
+ *   bkv_slot_mapping_cache_write_fp8).  Slots, -1 padding and the caches are
+ *   those calls' ("Padding and Batching with Block KV", The Core Formula;
+ *   Slot ID -1: Padding Tokens; Block Structure); the norm and the rotation
+ *   have no counterpart on the pages.
+ *
+ *   For a head row x of q (weight q_weight) or k (weight k_weight), in fp32:
+ *     y = x * rsqrt(mean(x^2) + norm_eps) * weight     (weight null: y = x)
+ *     (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i),  i < rot_dim / 2,
+ *   with (c_i, s_i) = (cos_sin[p][i], cos_sin[p][rot_dim / 2 + i]), p the
+ *   token's rotation position, and (a, b) = (i, i + rot_dim / 2), or
+ *   (2 i, 2 i + 1) when `interleaved`; elements from rot_dim on stay.  The
+ *   query goes to q_out, the key to its cache row, each rounded once from
+ *   fp32 (E4M3: the code of the binary32 quotient by k_scale); v is copied
+ *   bit for bit (E4M3: quantised by v_scale).
+ *
+ *   q [num_tokens, q_token_stride], k, v likewise, of `dtype`: the first
+ *             num_q_heads (num_kv_heads) * head_dim of each row, so that the
+ *             three may be slices of one fused projection.
+ *   q_weight, k_weight  [head_dim] of `dtype`, each nullable (no norm).
+ *   cos_sin   fp32 [max_position, rot_dim]; null only with rot_dim 0 (no
+ *             rotation).
+ *   positions int64 [num_tokens]: cache positions (the slots').
+ *   rope_positions  int64 [num_tokens] or null (= positions): rotation
+ *             positions, which differ from the cache's for the tokens of a
+ *             drafted tree (base + depth in the tree).
+ *   q_out     [num_tokens, num_q_heads, head_dim] of `dtype`.  It may be q
+ *             itself where q is dense; no other output may overlap an input.
+ *   Rows of padding tokens (request < 0) and of tokens whose rotation
+ *   position is outside [0, max_position) are left as they were in q_out and
+ *   get slot -1; the latter count once in *err_count.  A token with a null
+ *   table entry, or whose slot is bad (counted as in
+ *   bkv_slot_mapping_cache_write), still gets its query.
+ *   Other arguments as bkv_slot_mapping_cache_write(_fp8).
+ *   INVALID_ARG: the union of those calls' checks, rot_dim odd or outside
+ *   [0, head_dim], norm_eps negative or not finite.
+ *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd.
+ */
+int bkv_qk_norm_rope_cache_write(const void *q, const void *k, const void *v, int64_t q_token_stride,
+                                 int64_t k_token_stride, int64_t v_token_stride, const void *q_weight,
+                                 const void *k_weight, float norm_eps, const float *cos_sin,
+                                 int64_t max_position, int32_t rot_dim, int interleaved,
+                                 const int32_t *block_table, int32_t num_reqs, int64_t bt_stride,
+                                 int32_t bt_cols, const int32_t *req_indices, const int64_t *positions,
+                                 const int64_t *rope_positions, int64_t num_tokens,
+                                 int64_t max_num_tokens, int64_t *slot_mapping, void *q_out,
+                                 void *k_cache, void *v_cache, int64_t total_blocks, int32_t block_size,
+                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int dtype,
+                                 int32_t *err_count, bkv_stream_t stream);
+int bkv_qk_norm_rope_cache_write_fp8(const void *q, const void *k, const void *v, int64_t q_token_stride,
+                                     int64_t k_token_stride, int64_t v_token_stride,
+                                     const void *q_weight, const void *k_weight, float norm_eps,
+                                     const float *cos_sin, int64_t max_position, int32_t rot_dim,
+                                     int interleaved, const int32_t *block_table, int32_t num_reqs,
+                                     int64_t bt_stride, int32_t bt_cols, const int32_t *req_indices,
+                                     const int64_t *positions, const int64_t *rope_positions,
+                                     int64_t num_tokens, int64_t max_num_tokens, int64_t *slot_mapping,
+                                     void *q_out, uint8_t *k_cache, uint8_t *v_cache,
+                                     int64_t total_blocks, int32_t block_size, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int dtype, float k_scale,
+                                     float v_scale, int32_t *err_count, bkv_stream_t stream);
+
+/*
+ * bkv_paged_decode_tree_workspace_size
+ *   Bytes of device workspace bkv_paged_decode_tree needs for these sizes on
+ *   the CURRENT device; 0 for invalid sizes.
+ */
+size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                            int32_t max_context_len);
+
+/*
+ * bkv_paged_decode_tree
+ *   bkv_paged_decode for a tree of drafted tokens: the q_len tokens of a
+ *   request are its last q_len cached positions, and which of them a token
+ *   sees is any mask the caller gives ("Padding and Batching with Block KV",
+ *   Cache Masking: mask_cache, and mask_active between this step's tokens).
+ *   For request r with L = context_lens[r] (INCLUDING the q_len tokens), token
+ *   t sees key j < L iff its block entry is a real block and
+ *     j < L - q_len, or bit i of its mask row is set, i = j - (L - q_len):
+ *     bit i % 32 of tree_mask[r * mask_req_stride + t * words + i / 32],
+ *     words = ceil(q_len / 32)
+ *   (a tree's mask: the token's ancestors and itself).  out = softmax-weighted
+ *   V, 0 where no key is seen.  Causal bits give bkv_paged_decode's causal
+ *   mask, all bits its BKV_MASK_ALL.  Bits from q_len on are ignored.
+ *   Cache memory at positions a token does not see does not reach its output
+ *   (it may hold NaN or infinities).  An element of K or V that is not finite
+ *   at a position of the tree that a token sees makes the token's output row
+ *   NaN (for V: the whole row of head_dim values).
+ *
+ *   tree_mask  words of 32 bits as above; mask_req_stride words between the
+ *              requests' masks, or 0: one tree for all requests.
+ *   workspace  device scratch of workspace_bytes >=
+ *              bkv_paged_decode_tree_workspace_size(...), 16-byte aligned,
+ *              used only while the call's kernels run; its contents on entry
+ *              do not matter.
+ *   Other arguments, bounds and error counts as bkv_paged_decode.  bf16 with
+ *   head_dim 128 and at most 128 query heads per KV head runs a tcgen05
+ *   kernel (block sizes from 8 that divide 128 or are multiples of it, at
+ *   most 2048 requests); anything else a CUDA-core kernel.
+ *   INVALID_ARG: as bkv_paged_decode, or mask_req_stride neither 0 nor at
+ *   least q_len * words, or tree_mask null.
+ *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd, q_len
+ *   > 256.
+ */
+int bkv_paged_decode_tree(const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
+                          const int32_t *context_lens, int32_t max_context_len, int32_t num_reqs,
+                          int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t block_size, int64_t total_blocks, float softmax_scale,
+                          const uint32_t *tree_mask, int64_t mask_req_stride, int dtype, void *out,
+                          void *workspace, size_t workspace_bytes, int32_t *err_count,
+                          bkv_stream_t stream);
+
+/*
+ * bkv_verify_draft_chain
+ *   Which of a request's drafted tokens stand against the target model's
+ *   probabilities, and the token after them, from given random numbers, so
+ *   that the tokens are distributed as the target's own.  The pages name
+ *   speculative tokens ("Padding and Batching with Block KV", Cache Masking)
+ *   and print nothing about their verification.
+ *   With K = num_drafts, len = draft_lens[r] (null: K), x_i =
+ *   draft_tokens[r][i], p_i and q_i rows i of the request's probabilities:
+ *     drafts are accepted in order while accept_u[r][i] * q_i(x_i) < p_i(x_i)
+ *     (the product exact); n = num_accepted[r] = the accepted drafts;
+ *     the next token is sampled by sample_u[r] from max(p_n - q_n, 0) if
+ *     n < len, from p_len otherwise;
+ *     out_tokens[r] = x_0 .. x_{n-1}, the next token, then -1.
+ *   A sample by u from weights w is the lowest v with w_0 + .. + w_v > u S, S
+ *   their sum; the sums are exact in units of 2^-56, to which each
+ *   probability (clamped to [0, 1], NaN: 0) is rounded.  Weights that are all
+ *   0 fall back to the row p itself; a row without any weight gives token -1
+ *   and counts in *err_count.  A row may sum to 256 at most.
+ *   A draft outside [0, vocab_size) among the first len is rejected and
+ *   counted; a length outside [0, K] is clamped and counted.
+ *
+ *   target_probs fp32, row i of request r at r * target_req_stride + i *
+ *             target_row_stride, K + 1 rows of vocab_size; draft_probs fp32
+ *             likewise, K rows.  draft_tokens int64 [num_reqs, K],
+ *             draft_lens int32 [num_reqs] or null, accept_u fp32 [num_reqs, K],
+ *             sample_u fp32 [num_reqs], uniform in [0, 1).
+ *   out_tokens int64 [num_reqs, K + 1]; num_accepted int32 [num_reqs].
+ *   INVALID_ARG: negative sizes, vocab_size <= 0, a row stride below
+ *   vocab_size, null pointers.  UNSUPPORTED: num_drafts > 1024.
+ */
+int bkv_verify_draft_chain(const float *target_probs, int64_t target_req_stride, int64_t target_row_stride,
+                           const float *draft_probs, int64_t draft_req_stride, int64_t draft_row_stride,
+                           const int64_t *draft_tokens, const int32_t *draft_lens, const float *accept_u,
+                           const float *sample_u, int32_t num_reqs, int32_t num_drafts, int32_t vocab_size,
+                           int64_t *out_tokens, int32_t *num_accepted, int32_t *err_count,
+                           bkv_stream_t stream);
+
+/*
+ * bkv_verify_draft_tree
+ *   The same for a tree of drafts taken as they are (no draft probabilities):
+ *   node 0 is the root, whose token is settled; node i > 0 hangs under
+ *   parents[r][i] < i, or is padding (-1); p_i is the target's row after node
+ *   i.  From the root on, at node a with rem = 1, in index order over its
+ *   children c whose token x_c was not met before under a:
+ *     accept c if accept_u[r][c] * rem < p_a(x_c), and go on from c;
+ *     otherwise rem -= p_a(x_c)   (in 64 bits, not below 0)
+ *   (a child whose token was met before is rejected).  With no child accepted
+ *   the next token is sampled by sample_u[r], as in bkv_verify_draft_chain,
+ *   from p_a with the rejected children's tokens left out.
+ *     path[r] = 0, the accepted nodes, then -1; num_accepted[r] = their
+ *     number n without the root; out_tokens[r] = the accepted nodes' tokens,
+ *     the next token, then -1.
+ *   A node whose parent is neither -1 nor before it is padding, and one whose
+ *   token is outside [0, vocab_size) is rejected; each counts in *err_count.
+ *   accept_u[r][0], draft_tokens[r][0] and parents[r][0] are not used.
+ *
+ *   target_probs  num_nodes rows a request; draft_tokens int64, parents int32,
+ *             accept_u fp32, path int32 and out_tokens int64 [num_reqs,
+ *             num_nodes]; others as bkv_verify_draft_chain.
+ *   INVALID_ARG: as there, or num_nodes <= 0.  UNSUPPORTED: num_nodes > 1024.
+ */
+int bkv_verify_draft_tree(const float *target_probs, int64_t target_req_stride, int64_t target_row_stride,
+                          const int64_t *draft_tokens, const int32_t *parents, const float *accept_u,
+                          const float *sample_u, int32_t num_reqs, int32_t num_nodes, int32_t vocab_size,
+                          int64_t *out_tokens, int32_t *path, int32_t *num_accepted, int32_t *err_count,
+                          bkv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,6 +29,10 @@ Functions and the passages they follow (page titles and sections):
   with Block KV", Block ID 0 vs. Sentinel -1 names a non-FP8 pathway, nothing
   more; the format and per-tensor scale convention are reading R16 of the C
   source.
+* :func:`norm_rope`, :func:`paged_decode_tree_request`, :func:`verify_chain`,
+  :func:`verify_tree` -- the speculative step: norm and rotation of heads, the
+  decode with a tree's mask ("Padding and Batching with Block KV", Cache
+  Masking), verification of drafts; readings R18 .. R20 of the C source.
 
 Every function is pinned by the ``-m "not gpu"`` tests in
 ``tests/test_oracle_*.py`` against worked values printed on the pages, brute
@@ -108,6 +112,15 @@ def _load():
             lib.orc_paged_decode_fp8_request.argtypes = [i32, vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, i32,
                                                          i32, i64, dbl, dbl, dbl, ctypes.c_int, i32, ctypes.c_int,
                                                          vp]
+            lib.orc_norm_rope.restype = i64
+            lib.orc_norm_rope.argtypes = [vp, i64, i32, i32, ctypes.c_int, vp, dbl, vp, i64, i32, ctypes.c_int, vp, vp]
+            lib.orc_paged_decode_tree_request.restype = i64
+            lib.orc_paged_decode_tree_request.argtypes = [i32, vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, i32,
+                                                          i32, i64, dbl, vp, i64, ctypes.c_int, vp]
+            lib.orc_verify_chain.restype = i64
+            lib.orc_verify_chain.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
+            lib.orc_verify_tree.restype = i64
+            lib.orc_verify_tree.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
             lib.orc_decode_bucket.restype = i64
             lib.orc_decode_bucket.argtypes = [vp, i64, i64, vp, i64, i64]
             _lib = lib
@@ -400,6 +413,75 @@ def paged_decode_fp8(q, k_cache, v_cache, block_table, context_lens, k_scale, v_
             raise ValueError("invalid paged_decode_fp8 arguments")
         err += e
     return out, int(err)
+
+
+def norm_rope(x, weight, eps, cos_sin, positions, interleaved=False):
+    """fp64 norm and rotation of head rows x (n, heads, D; bf16 bits or float32), weight (D,) of x's type or None,
+    cos_sin float32 (max_position, rot_dim) (reading R18).  Returns (out, rows with a position out of range)."""
+    xa = np.ascontiguousarray(x)
+    n, heads, d = xa.shape
+    w = None if weight is None else np.ascontiguousarray(weight)
+    cs = np.ascontiguousarray(cos_sin, np.float32)
+    pos = _c(positions, np.int64)
+    if len(pos) != n or (w is not None and (w.dtype != xa.dtype or w.size != d)):
+        raise ValueError("positions / weight mismatch")
+    out = np.zeros(xa.shape, np.float64)
+    bad = _load().orc_norm_rope(_ptr(xa), n, heads, d, _dtype_code(xa), None if w is None else _ptr(w), float(eps),
+                                _ptr(cs), cs.shape[0], cs.shape[1], int(bool(interleaved)), _ptr(pos), _ptr(out))
+    if bad < 0:
+        raise ValueError("invalid norm_rope arguments")
+    return out, int(bad)
+
+
+def paged_decode_tree_request(r, q, k_cache, v_cache, block_table, context_lens, tree_mask, scale=None):
+    """fp64 output (q_len, H_q, D) of request ``r`` with a tree's mask: tree_mask uint32 (num_reqs, q_len, words), or
+    (q_len, words) for one tree of all requests (reading R19).  Returns (out, bad table entries)."""
+    qa, kc, vc = np.ascontiguousarray(q), np.ascontiguousarray(k_cache), np.ascontiguousarray(v_cache)
+    bt, cl = _c(block_table, np.int32), _c(context_lens, np.int32)
+    mask = np.ascontiguousarray(tree_mask, np.uint32)
+    nr, ql, hq, d = qa.shape
+    tb, bs, hkv, _ = kc.shape
+    words = (ql + 31) // 32
+    if mask.shape not in ((nr, ql, words), (ql, words)):
+        raise ValueError("tree_mask shape")
+    out = np.zeros((ql, hq, d), np.float64)
+    err = _load().orc_paged_decode_tree_request(
+        int(r), _ptr(qa), _ptr(kc), _ptr(vc), _ptr(bt), bt.shape[1], bt.shape[1], _ptr(cl), nr, ql, hq, hkv, d, bs, tb,
+        (1.0 / np.sqrt(d)) if scale is None else float(scale), _ptr(mask), ql * words if mask.ndim == 3 else 0,
+        _dtype_code(qa), _ptr(out))
+    if err < 0:
+        raise ValueError("invalid paged_decode_tree arguments")
+    return out, int(err)
+
+
+def verify_chain(target, draft, tokens, accept_u, sample_u, lens=None):
+    """Verification of drafted chains (reading R20): target (R, K + 1, V), draft (R, K, V) float32.  Returns
+    (out_tokens (R, K + 1), num_accepted (R,), errors)."""
+    p, q = np.ascontiguousarray(target, np.float32), np.ascontiguousarray(draft, np.float32)
+    r, k1, v = p.shape
+    tok, u, us = _c(tokens, np.int64), _c(accept_u, np.float32), _c(sample_u, np.float32)
+    ln = None if lens is None else _c(lens, np.int32)
+    out, count = np.zeros((r, k1), np.int64), np.zeros(r, np.int32)
+    err = _load().orc_verify_chain(_ptr(p), _ptr(q), _ptr(tok), None if ln is None else _ptr(ln), _ptr(u), _ptr(us), r,
+                                   k1 - 1, v, _ptr(out), _ptr(count))
+    if err < 0:
+        raise ValueError("invalid verify_chain arguments")
+    return out, count, int(err)
+
+
+def verify_tree(target, tokens, parents, accept_u, sample_u):
+    """Verification of drafted trees (reading R20): target (R, T, V) float32.  Returns (out_tokens (R, T), path (R, T),
+    num_accepted (R,), errors)."""
+    p = np.ascontiguousarray(target, np.float32)
+    r, t, v = p.shape
+    tok, par = _c(tokens, np.int64), _c(parents, np.int32)
+    u, us = _c(accept_u, np.float32), _c(sample_u, np.float32)
+    out, path, count = np.zeros((r, t), np.int64), np.zeros((r, t), np.int32), np.zeros(r, np.int32)
+    err = _load().orc_verify_tree(_ptr(p), _ptr(tok), _ptr(par), _ptr(u), _ptr(us), r, t, v, _ptr(out), _ptr(path),
+                                  _ptr(count))
+    if err < 0:
+        raise ValueError("invalid verify_tree arguments")
+    return out, path, count, int(err)
 
 
 def decode_bucket(num_computed, num_speculative_tokens, buckets, max_model_len):

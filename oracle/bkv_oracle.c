@@ -84,6 +84,19 @@
  *       infinities) saturated to 448, NaN to NaN; a stored code c stands for
  *       the value e4m3(c) * scale.  Attention over an FP8 cache is O4 on
  *       those values.
+ *   R18 norm and rotation of query and key heads (not on the pages): rms norm
+ *       over the head with a weight, then a rotation of element pairs by a
+ *       given table of cosines and sines; the key is then written as O3 / R16
+ *       writes it.
+ *   R19 a tree of drafted tokens ([P1 Cache Masking]: mask_active between this
+ *       step's tokens is an input): request r's T tokens are its last T
+ *       positions, and which of them each sees is a bit mask; all see the
+ *       positions before them.
+ *   R20 verification of drafts (not on the pages): accept draft x of a chain
+ *       while u q(x) < p(x), then sample from max(p - q, 0) (from p after the
+ *       last); in a tree accept children in order while u rem < p(x), rem = 1
+ *       less the rejected siblings' p, then sample from p without those.  A
+ *       sample by u is the lowest v whose running sum passes u times the sum.
  *   R17 an expanded kernel block id m*bpk + t above INT32_MAX cannot be
  *       held by the int32 kernel table: it is written as -1 (no block),
  *       the same outcome as an entry <= 0 under R2.
@@ -869,4 +882,275 @@ int64_t orc_decode_bucket(const int64_t *num_computed, int64_t n,
         if (buckets[k] >= needed)
             return buckets[k];
     return max_model_len >= needed ? max_model_len : -1;
+}
+
+/* ------------------------------------------------------------------ */
+/* The speculative step (R18 .. R20)                                   */
+/* ------------------------------------------------------------------ */
+
+/*
+ * Norm and rotation of head rows (R18): x [n][heads][D], positions pos[n].
+ * y = x / sqrt(mean(x^2) + eps) * w (no w: y = x), then the pairs (a, b) =
+ * (i, i + rot/2), or (2i, 2i + 1) when interleaved, turned by the table's
+ * (cos, sin) of the position: (a c - b s, b c + a s).  Rows whose position
+ * is outside [0, max_position) are left alone.  Returns their number.
+ */
+int64_t orc_norm_rope(const void *x, int64_t n, int32_t heads, int32_t head_dim, int dtype,
+                      const void *w, double eps, const float *cos_sin, int64_t max_position,
+                      int32_t rot_dim, int interleaved, const int64_t *pos, double *out)
+{
+    if (n < 0 || heads <= 0 || head_dim <= 0 || rot_dim < 0 || rot_dim > head_dim ||
+        rot_dim % 2 != 0 || orc_elem_bytes(dtype) == 0)
+        return -1;
+    int64_t bad = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (pos[i] < 0 || pos[i] >= max_position) {
+            bad += 1;
+            continue;
+        }
+        const float *cs = cos_sin + pos[i] * rot_dim;
+        for (int64_t h = 0; h < heads; ++h) {
+            const int64_t row = (i * heads + h) * head_dim;
+            double sq = 0.0;
+            for (int32_t d = 0; d < head_dim; ++d) {
+                const double v = orc_load(x, row + d, dtype);
+                sq += v * v;
+            }
+            const double norm = w ? sqrt(sq / head_dim + eps) : 1.0;
+            for (int32_t d = 0; d < head_dim; ++d)
+                out[row + d] = orc_load(x, row + d, dtype) / norm * (w ? orc_load(w, d, dtype) : 1.0);
+            for (int32_t j = 0; j < rot_dim / 2; ++j) {
+                const int32_t a = interleaved ? 2 * j : j;
+                const int32_t b = interleaved ? 2 * j + 1 : j + rot_dim / 2;
+                const double c = cs[j], s = cs[rot_dim / 2 + j];
+                const double ya = out[row + a], yb = out[row + b];
+                out[row + a] = ya * c - yb * s;
+                out[row + b] = yb * c + ya * s;
+            }
+        }
+    }
+    return bad;
+}
+
+/*
+ * O4 with a tree's mask (R19): request r's T tokens are its last T of L
+ * positions; token t sees key j < L with a real block iff j < L - T or bit
+ * i = j - (L - T) of its mask row is set.  out [T][H_q][D].  Returns the
+ * number of bad table entries among the blocks of [0, L), or -1.
+ */
+int64_t orc_paged_decode_tree_request(int32_t r, const void *q, const void *k_cache, const void *v_cache,
+                                      const int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
+                                      const int32_t *context_lens, int32_t num_reqs, int32_t q_len,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int64_t total_blocks, double scale,
+                                      const uint32_t *tree_mask, int64_t mask_req_stride, int dtype,
+                                      double *out)
+{
+    if (r < 0 || r >= num_reqs || q_len <= 0 || num_q_heads % num_kv_heads != 0 || orc_elem_bytes(dtype) == 0)
+        return -1;
+    const int64_t G = num_q_heads / num_kv_heads, D = head_dim, T = q_len;
+    const int64_t words = (T + 31) / 32;
+    const int64_t L = context_lens[r] > 0 ? context_lens[r] : 0;
+    int64_t errors = 0;
+    int64_t *row = (int64_t *)malloc(sizeof(int64_t) * (size_t)(L + 1));
+    double *s = (double *)malloc(sizeof(double) * (size_t)(L + 1));
+    if (!row || !s) {
+        free(row);
+        free(s);
+        return -1;
+    }
+    for (int64_t j = 0; j < L; ++j) {
+        const int64_t lb = j / block_size;
+        row[j] = -1;
+        if (lb >= bt_cols) {
+            errors += j % block_size == 0;
+            continue;
+        }
+        const int64_t b = block_table[(int64_t)r * bt_stride + lb];
+        if (b >= total_blocks) {
+            errors += j % block_size == 0;
+            continue;
+        }
+        if (b > 0)
+            row[j] = b * block_size + j % block_size;
+    }
+    for (int64_t t = 0; t < T; ++t) {
+        const uint32_t *bits = tree_mask + (int64_t)r * mask_req_stride + t * words;
+        for (int64_t h = 0; h < num_q_heads; ++h) {
+            const int64_t qo = (((int64_t)r * T + t) * num_q_heads + h) * D;
+            double *o = out + (t * num_q_heads + h) * D;
+            double top = -INFINITY, sum = 0.0;
+            for (int64_t j = 0; j < L; ++j) {
+                const int64_t i = j - (L - T);
+                s[j] = -INFINITY;
+                if (row[j] < 0 || (i >= 0 && !((bits[i / 32] >> (i % 32)) & 1u)))
+                    continue;
+                double dot = 0.0;
+                const int64_t ko = (row[j] * num_kv_heads + h / G) * D;
+                for (int64_t d = 0; d < D; ++d)
+                    dot += orc_load(q, qo + d, dtype) * orc_load(k_cache, ko + d, dtype);
+                s[j] = dot * scale;
+                if (s[j] > top)
+                    top = s[j];
+            }
+            for (int64_t d = 0; d < D; ++d)
+                o[d] = 0.0;
+            if (top == -INFINITY)
+                continue;
+            for (int64_t j = 0; j < L; ++j) {
+                if (s[j] == -INFINITY)
+                    continue;
+                const double w = exp(s[j] - top);
+                const int64_t vo = (row[j] * num_kv_heads + h / G) * D;
+                sum += w;
+                for (int64_t d = 0; d < D; ++d)
+                    o[d] += w * orc_load(v_cache, vo + d, dtype);
+            }
+            for (int64_t d = 0; d < D; ++d)
+                o[d] /= sum;
+        }
+    }
+    free(row);
+    free(s);
+    return errors;
+}
+
+/* A probability as R20 takes it: NaN and negative values are 0, above 1 is 1. */
+static double orc_prob(float x)
+{
+    return x > 0.f ? (x < 1.f ? (double)x : 1.0) : 0.0;
+}
+
+/* The lowest v with w_0 + .. + w_v > u sum(w); -1 without any weight. */
+static int64_t orc_sample(const double *w, int32_t V, double u)
+{
+    double sum = 0.0, run = 0.0;
+    int64_t last = -1;
+    for (int32_t v = 0; v < V; ++v) {
+        sum += w[v];
+        if (w[v] > 0.0)
+            last = v;
+    }
+    for (int32_t v = 0; v < V; ++v) {
+        run += w[v];
+        if (run > u * sum)
+            return v;
+    }
+    return last;   /* u >= 1, or the last weights lost in rounding */
+}
+
+/*
+ * Verification of a chain of drafts (R20).  target [R][K+1][V], draft
+ * [R][K][V].  Returns the count of bad inputs, or -1.
+ */
+int64_t orc_verify_chain(const float *target, const float *draft, const int64_t *tokens, const int32_t *lens,
+                         const float *u, const float *us, int32_t R, int32_t K, int32_t V, int64_t *out,
+                         int32_t *count)
+{
+    int64_t errors = 0;
+    double *w = (double *)malloc(sizeof(double) * (size_t)V);
+    if (!w || K < 0 || V <= 0) {
+        free(w);
+        return -1;
+    }
+    for (int64_t r = 0; r < R; ++r) {
+        int32_t len = lens ? lens[r] : K;
+        if (len < 0 || len > K) {
+            errors += 1;
+            len = len < 0 ? 0 : K;
+        }
+        const float *p = target + r * (K + 1) * (int64_t)V, *q = draft + r * K * (int64_t)V;
+        int32_t n = 0;
+        while (n < len) {
+            const int64_t x = tokens[r * K + n];
+            if (x < 0 || x >= V ||
+                !((double)u[r * K + n] * (double)q[n * (int64_t)V + x] < (double)p[n * (int64_t)V + x]))
+                break;
+            n += 1;
+        }
+        for (int32_t i = 0; i < len; ++i)
+            errors += tokens[r * K + i] < 0 || tokens[r * K + i] >= V;
+        double any = 0.0;
+        for (int32_t v = 0; v < V; ++v) {
+            w[v] = orc_prob(p[n * (int64_t)V + v]);
+            if (n < len) {
+                w[v] -= orc_prob(q[n * (int64_t)V + v]);
+                if (w[v] < 0.0)
+                    w[v] = 0.0;
+            }
+            any += w[v];
+        }
+        if (any == 0.0)
+            for (int32_t v = 0; v < V; ++v)
+                w[v] = orc_prob(p[n * (int64_t)V + v]);
+        for (int32_t i = 0; i <= K; ++i)
+            out[r * (K + 1) + i] = i < n ? tokens[r * K + i] : -1;
+        out[r * (K + 1) + n] = orc_sample(w, V, us[r]);
+        errors += out[r * (K + 1) + n] < 0;
+        count[r] = n;
+    }
+    free(w);
+    return errors;
+}
+
+/* Verification of a tree of drafts (R20).  target [R][T][V]. */
+int64_t orc_verify_tree(const float *target, const int64_t *tokens, const int32_t *parents, const float *u,
+                        const float *us, int32_t R, int32_t T, int32_t V, int64_t *out, int32_t *path,
+                        int32_t *count)
+{
+    int64_t errors = 0;
+    double *w = (double *)malloc(sizeof(double) * (size_t)V);
+    if (!w || T <= 0 || V <= 0) {
+        free(w);
+        return -1;
+    }
+    for (int64_t r = 0; r < R; ++r) {
+        const int64_t *tok = tokens + r * T;
+        const int32_t *par = parents + r * T;
+        for (int32_t c = 1; c < T; ++c) {
+            const int in = par[c] >= 0 && par[c] < c;
+            errors += in ? (tok[c] < 0 || tok[c] >= V) : par[c] != -1;
+        }
+        for (int32_t i = 0; i < T; ++i) {
+            out[r * T + i] = -1;
+            path[r * T + i] = -1;
+        }
+        path[r * T] = 0;
+        int32_t cur = 0, n = 0;
+        for (;;) {
+            const float *p = target + (r * T + cur) * (int64_t)V;
+            for (int32_t v = 0; v < V; ++v)
+                w[v] = orc_prob(p[v]);
+            double rem = 1.0;
+            int32_t taken = -1;
+            for (int32_t c = cur + 1; c < T && taken < 0; ++c) {
+                if (par[c] != cur || tok[c] < 0 || tok[c] >= V)
+                    continue;
+                if ((double)u[r * T + c] * (rem > 0.0 ? rem : 0.0) < w[tok[c]]) {
+                    taken = c;
+                } else {
+                    rem -= w[tok[c]];
+                    w[tok[c]] = 0.0;
+                }
+            }
+            if (taken < 0) {
+                double any = 0.0;
+                for (int32_t v = 0; v < V; ++v)
+                    any += w[v];
+                if (any == 0.0)
+                    for (int32_t v = 0; v < V; ++v)
+                        w[v] = orc_prob(p[v]);
+                break;
+            }
+            cur = taken;
+            out[r * T + n] = tok[cur];
+            n += 1;
+            path[r * T + n] = cur;
+        }
+        out[r * T + n] = orc_sample(w, V, us[r]);
+        errors += out[r * T + n] < 0;
+        count[r] = n;
+    }
+    free(w);
+    return errors;
 }

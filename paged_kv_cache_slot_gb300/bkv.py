@@ -98,6 +98,21 @@ def load() -> ctypes.CDLL:
         for fn in ("bkv_paged_decode_fp8", "bkv_paged_decode_fp8_partition", "bkv_paged_decode_fp8_merge"):
             getattr(lib, fn).restype = cint
             getattr(lib, fn).argtypes = dec8
+        rope = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, i64, i32, cint, vp, i32, i64, i32, vp, vp, vp, i64, i64, vp,
+                vp, vp, vp, i64, i32, i32, i32, i32, cint]
+        lib.bkv_qk_norm_rope_cache_write.restype = cint
+        lib.bkv_qk_norm_rope_cache_write.argtypes = rope + [vp, vp]
+        lib.bkv_qk_norm_rope_cache_write_fp8.restype = cint
+        lib.bkv_qk_norm_rope_cache_write_fp8.argtypes = rope + [f32, f32, vp, vp]
+        lib.bkv_paged_decode_tree_workspace_size.restype = sz
+        lib.bkv_paged_decode_tree_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        lib.bkv_paged_decode_tree.restype = cint
+        lib.bkv_paged_decode_tree.argtypes = [vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, i32, i64, f32,
+                                              vp, i64, cint, vp, vp, sz, vp, vp]
+        lib.bkv_verify_draft_chain.restype = cint
+        lib.bkv_verify_draft_chain.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+        lib.bkv_verify_draft_tree.restype = cint
+        lib.bkv_verify_draft_tree.argtypes = [vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
         _lib = lib
         return lib
 
@@ -446,6 +461,186 @@ def bkv_merge_attn_states(outs, lses, out, lse_out=None, stream=None):
         _dev(outs, "outs"), _dev(lses, "lses", torch.float32), parts, rows, d, _kv_dtype(outs), _dev(out, "out"),
         _opt(lse_out, "lse_out", torch.float32), _stream(stream)))
     return out
+
+
+def _same_device(*tensors):
+    """Every tensor on the current device, whose stream the call is enqueued on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def bkv_qk_norm_rope_cache_write(q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table, req_indices, positions,
+                                 slot_mapping, q_out, k_cache, v_cache, rope_positions=None, interleaved=False,
+                                 num_tokens=None, err_count=None, stream=None):
+    """Norm of every head of q and k (weights (D,) or None), position rotation by ``cos_sin`` (max_position,
+    rot_dim; None: no rotation), slot mapping and K/V write in one kernel: q (num_tokens, H_q, D) -> ``q_out``,
+    k / v (num_tokens, H_kv, D) -> the caches (see include/bkv.h).  Returns (q_out, slot_mapping)."""
+    return _norm_rope("bkv_qk_norm_rope_cache_write", (), q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table,
+                      req_indices, positions, slot_mapping, q_out, k_cache, v_cache, rope_positions, interleaved,
+                      num_tokens, err_count, stream)
+
+
+def bkv_qk_norm_rope_cache_write_fp8(q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table, req_indices,
+                                     positions, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                                     rope_positions=None, interleaved=False, num_tokens=None, err_count=None,
+                                     stream=None):
+    """bkv_qk_norm_rope_cache_write into uint8 E4M3 caches with per-tensor scales (see include/bkv.h)."""
+    return _norm_rope("bkv_qk_norm_rope_cache_write_fp8", (float(k_scale), float(v_scale)), q, k, v, q_weight, k_weight,
+                      norm_eps, cos_sin, block_table, req_indices, positions, slot_mapping, q_out, k_cache, v_cache,
+                      rope_positions, interleaved, num_tokens, err_count, stream)
+
+
+def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table, req_indices, positions,
+               slot_mapping, q_out, k_cache, v_cache, rope_positions, interleaved, num_tokens, err_count, stream):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("caches must be (total_blocks, block_size, H_kv, D) and equal in shape")
+    tb, bs, hkv, d = k_cache.shape
+    if q.dim() != 3 or q.shape[2] != d or k.dim() != 3 or tuple(k.shape[1:]) != (hkv, d) or k.shape != v.shape:
+        raise ValueError("q must be (num_tokens, H_q, D), k / v (num_tokens, H_kv, D) matching the cache")
+    nt, hq, _ = q.shape
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.stride(2) != 1 or t.stride(1) != d:
+            raise ValueError(f"{name} rows must be dense (a row stride is allowed)")
+        if t.dtype != q.dtype:
+            raise TypeError("mixed dtypes")
+    dt = _kv_dtype(q)
+    cache_dtype = torch.uint8 if scales else q.dtype
+    if k_cache.dtype != cache_dtype or v_cache.dtype != cache_dtype or q_out.dtype != q.dtype:
+        raise TypeError(f"caches must be {cache_dtype} and q_out {q.dtype}")
+    if q_out.dim() != 3 or q_out.shape[0] < nt or tuple(q_out.shape[1:]) != (hq, d):
+        raise ValueError("q_out must be (>= num_tokens, H_q, D)")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must have head_dim elements")
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be (max_position, rot_dim)")
+    if block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be 2-D with unit column stride")
+    n = positions.numel() if num_tokens is None else int(num_tokens)
+    if (n > nt or n > k.shape[0] or n > positions.numel() or n > req_indices.numel() or n > slot_mapping.numel() or
+            (rope_positions is not None and n > rope_positions.numel())):
+        raise ValueError("num_tokens exceeds q / k / positions / req_indices / slot_mapping / rope_positions")
+    ptrs = (_dev(q, "q", contiguous=False), _dev(k, "k", contiguous=False), _dev(v, "v", contiguous=False))
+    # a dimension of size 1 (one token) may carry any stride
+    stride = [t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d) for t in (q, k, v)]
+    args = (*ptrs, *stride, _opt(q_weight, "q_weight", q.dtype), _opt(k_weight, "k_weight", q.dtype), float(norm_eps),
+            _opt(cos_sin, "cos_sin", torch.float32), 1 << 62 if cos_sin is None else cos_sin.shape[0],
+            0 if cos_sin is None else cos_sin.shape[1], int(bool(interleaved)),
+            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.shape[0], block_table.stride(0),
+            block_table.shape[1], _dev(req_indices, "req_indices", torch.int32),
+            _dev(positions, "positions", torch.int64), _opt(rope_positions, "rope_positions", torch.int64), n,
+            slot_mapping.numel(), _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), tb, bs, hq, hkv, d, dt, *scales,
+            _opt(err_count, "err_count", torch.int32))
+    _same_device(q, k_cache)
+    _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+    return q_out, slot_mapping
+
+
+def bkv_paged_decode_tree_workspace_size(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                         max_context_len) -> int:
+    return int(load().bkv_paged_decode_tree_workspace_size(int(num_reqs), int(q_len), int(num_q_heads),
+                                                           int(num_kv_heads), int(head_dim), int(block_size),
+                                                           int(max_context_len)))
+
+
+def bkv_paged_decode_tree(q, k_cache, v_cache, block_table, context_lens, max_context_len, tree_mask, out, workspace,
+                          softmax_scale=0.0, err_count=None, stream=None):
+    """Paged attention of drafted trees into ``out`` (num_reqs, q_len, H_q, D): a request's q_len tokens are its
+    last cached positions, and bit i of token t's words in ``tree_mask`` (int32, (num_reqs, q_len, ceil(q_len /
+    32)), or (q_len, ..) for one tree of all requests) lets it see token i (see include/bkv.h)."""
+    if q.dim() != 4 or out.shape != q.shape or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("q/out must be (num_reqs, q_len, H_q, D); caches (total_blocks, bs, H_kv, D)")
+    nr, ql, hq, d = q.shape
+    tb, bs, hkv, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("head_dim mismatch")
+    if block_table.dim() != 2 or block_table.shape[0] < nr or block_table.stride(1) != 1:
+        raise ValueError("block_table must be (>= num_reqs, cols) with unit column stride")
+    if context_lens.numel() < nr:
+        raise ValueError("context_lens must have num_reqs elements")
+    words = (ql + 31) // 32
+    shape = tuple(tree_mask.shape)
+    if shape != (ql, words) and (len(shape) != 3 or shape[0] < nr or shape[1:] != (ql, words)):
+        raise ValueError("tree_mask must be (num_reqs, q_len, ceil(q_len / 32)) or (q_len, ceil(q_len / 32))")
+    dt = _kv_dtype(q)
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
+        raise TypeError(f"caches and out must be {q.dtype}")
+    if workspace.dtype != torch.uint8:
+        raise TypeError("workspace must be a uint8 tensor")
+    args = (_dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.stride(0),
+            block_table.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv,
+            d, bs, tb, float(softmax_scale), _dev(tree_mask, "tree_mask", torch.int32),
+            ql * words if len(shape) == 3 else 0, dt, _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(),
+            _opt(err_count, "err_count", torch.int32))
+    _same_device(q, k_cache)
+    _check("bkv_paged_decode_tree", load().bkv_paged_decode_tree(*args, _stream(stream)))
+    return out
+
+
+def bkv_verify_draft_chain(target_probs, draft_probs, draft_tokens, accept_u, sample_u, out_tokens, num_accepted,
+                           draft_lens=None, err_count=None, stream=None):
+    """Accepts drafted tokens (num_reqs, K) against the target's probabilities (num_reqs, K + 1, V) and the draft
+    model's (num_reqs, K, V), both fp32, by the uniform numbers accept_u (num_reqs, K) and sample_u (num_reqs)
+    -> out_tokens int64 (num_reqs, K + 1), num_accepted int32 (num_reqs) (see include/bkv.h)."""
+    nr, k1, vocab = target_probs.shape
+    k = k1 - 1
+    if (tuple(draft_probs.shape) != (nr, k, vocab) or tuple(draft_tokens.shape) != (nr, k) or
+            tuple(accept_u.shape) != (nr, k) or tuple(out_tokens.shape) != (nr, k1)):
+        raise ValueError("target_probs (R, K + 1, V), draft_probs (R, K, V), draft_tokens / accept_u (R, K) and "
+                         "out_tokens (R, K + 1) disagree")
+    if sample_u.numel() != nr or num_accepted.numel() != nr or (draft_lens is not None and draft_lens.numel() != nr):
+        raise ValueError("sample_u, num_accepted and draft_lens must have num_reqs elements")
+    if target_probs.stride(2) != 1 or (k > 0 and draft_probs.stride(2) != 1):
+        raise ValueError("probability rows must be dense")
+    args = (_dev(target_probs, "target_probs", torch.float32, contiguous=False), *_row_strides(target_probs),
+            _dev(draft_probs, "draft_probs", torch.float32, contiguous=False), *_row_strides(draft_probs),
+            _dev(draft_tokens, "draft_tokens", torch.int64), _opt(draft_lens, "draft_lens", torch.int32),
+            _dev(accept_u, "accept_u", torch.float32), _dev(sample_u, "sample_u", torch.float32), nr, k, vocab,
+            _dev(out_tokens, "out_tokens", torch.int64), _dev(num_accepted, "num_accepted", torch.int32),
+            _opt(err_count, "err_count", torch.int32))
+    _same_device(target_probs, out_tokens)
+    _check("bkv_verify_draft_chain", load().bkv_verify_draft_chain(*args, _stream(stream)))
+    return out_tokens, num_accepted
+
+
+def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_u, out_tokens, path, num_accepted,
+                          err_count=None, stream=None):
+    """Accepts a path of a tree of drafted tokens (num_reqs, T; node 0 the root, parents int32) against the
+    target's probabilities fp32 (num_reqs, T, V) by the uniform numbers accept_u (num_reqs, T) and sample_u
+    (num_reqs) -> out_tokens int64, path int32 (num_reqs, T), num_accepted int32 (num_reqs) (see include/bkv.h)."""
+    nr, t, vocab = target_probs.shape
+    for x, name in ((draft_tokens, "draft_tokens"), (parents, "parents"), (accept_u, "accept_u"),
+                    (out_tokens, "out_tokens"), (path, "path")):
+        if tuple(x.shape) != (nr, t):
+            raise ValueError(f"{name} must be (num_reqs, num_nodes)")
+    if sample_u.numel() != nr or num_accepted.numel() != nr:
+        raise ValueError("sample_u and num_accepted must have num_reqs elements")
+    if target_probs.stride(2) != 1:
+        raise ValueError("probability rows must be dense")
+    args = (_dev(target_probs, "target_probs", torch.float32, contiguous=False), *_row_strides(target_probs),
+            _dev(draft_tokens, "draft_tokens", torch.int64), _dev(parents, "parents", torch.int32),
+            _dev(accept_u, "accept_u", torch.float32), _dev(sample_u, "sample_u", torch.float32), nr, t, vocab,
+            _dev(out_tokens, "out_tokens", torch.int64), _dev(path, "path", torch.int32),
+            _dev(num_accepted, "num_accepted", torch.int32), _opt(err_count, "err_count", torch.int32))
+    _same_device(target_probs, out_tokens)
+    _check("bkv_verify_draft_tree", load().bkv_verify_draft_tree(*args, _stream(stream)))
+    return out_tokens, path, num_accepted
+
+
+def _row_strides(t):
+    """Request and row stride of probabilities (R, rows, V); a dimension of size 1 or 0 may carry any stride."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else t.shape[2]
+
+
+def alloc_tree_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, device=None):
+    """Convenience: a uint8 device tensor of the size bkv_paged_decode_tree needs."""
+    n = bkv_paged_decode_tree_workspace_size(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                             max_context_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
 def alloc_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, device=None):

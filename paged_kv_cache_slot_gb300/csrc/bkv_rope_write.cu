@@ -1,0 +1,237 @@
+// bkv_rope_write.cu -- norm of every query and key head, position rotation,
+// slot mapping and cache write of a step's tokens, in one pass.
+//
+// For a head row x of D elements (queries and keys; fp32 arithmetic on the
+// input's values, one rounding at the end):
+//   y = x * rsqrt(mean(x^2) + eps) * w            (no weight given: y = x)
+//   (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i),  i < rot / 2,
+// with c_i = cos_sin[p][i], s_i = cos_sin[p][rot / 2 + i] of the token's
+// rotation position p, (a, b) = (i, i + rot / 2), or (2i, 2i + 1) when
+// interleaved.  Queries go to q_out, keys to their cache rows (rounded to the
+// cache's type, or the E4M3 code of the binary32 quotient by k_scale), values
+// are copied (or quantised) as bkv_cache_write(_fp8) does.  Slots are
+// bkv_compute_slot_mapping's ("Padding and Batching with Block KV", The Core
+// Formula; Slot ID -1: Padding Tokens; Block Structure); the norm and the
+// rotation have no counterpart on the pages.
+//
+// Memory-bound: (Hq + 2 Hkv) D e bytes read and Hq D e + 2 Hkv D e_cache
+// written a token, once each; for a few tokens the chain request / position
+// -> table entry -> store and the launch are what counts, so the rows are
+// loaded before the table's answer is needed.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "bkv_internal.cuh"
+#include "bkv_slot.cuh"
+
+namespace bkv {
+namespace rope {
+
+struct Args {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;   // elements between tokens
+    const void *qw, *kw;                    // norm weights [D] or null
+    float eps;
+    const float *cos_sin;
+    int64_t max_position;
+    int32_t rot;
+    const int32_t *bt;
+    int32_t num_reqs;
+    int64_t bt_stride;
+    int32_t bt_cols;
+    const int32_t *req;
+    const int64_t *pos, *rpos;
+    int64_t n, max_n;
+    int64_t *slots;
+    void *q_out, *kc, *vc;
+    int64_t capacity;
+    int32_t bs, hq, hkv, d;
+    float k_scale, v_scale;
+    int32_t *err;
+};
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x, float) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(float *p, float x, float) { *p = x; }
+__device__ __forceinline__ void put(uint8_t *p, float x, float scale) {
+    *p = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3);
+}
+// a value copied into a cache of its own type keeps its bits
+__device__ __forceinline__ void copy(__nv_bfloat16 *p, __nv_bfloat16 x, float) { *p = x; }
+__device__ __forceinline__ void copy(float *p, float x, float) { *p = x; }
+template <typename T>
+__device__ __forceinline__ void copy(uint8_t *p, T x, float scale) { put(p, to_f(x), scale); }
+
+// What a token's row needs to know: whether it is a real token, its slot (-1:
+// nothing is cached) and its rotation row.
+struct Token {
+    bool real;
+    int64_t slot;
+    const float *cs;
+};
+
+// Token i < max_n.  `lead`: this thread writes the slot and counts errors.
+__device__ __forceinline__ Token token_at(const Args &a, int64_t i, bool lead) {
+    Token t{false, -1, nullptr};
+    if (i < a.n) {
+        const int32_t r = __ldg(a.req + i);
+        if (r >= 0) {
+            const int64_t p = __ldg(a.pos + i);
+            const int64_t rp = a.rpos ? __ldg(a.rpos + i) : p;
+            bool bad = rp < 0 || rp >= a.max_position;
+            if (!bad) {
+                t.real = true;
+                t.cs = a.cos_sin + rp * a.rot;
+                t.slot = slot_of(a.bt, a.num_reqs, a.bt_stride, a.bt_cols, r, p, a.bs, 1, 0, 1, &bad);
+            }
+            if (lead && a.err && (bad || t.slot >= a.capacity)) atomicAdd(a.err, 1);
+        }
+    }
+    if (lead) a.slots[i] = t.slot;
+    if (t.slot >= a.capacity) t.slot = -1;
+    return t;
+}
+
+// Any head_dim up to 256, any strides and alignments: one warp per (token,
+// head), lane l elements l, l + 32, ...; a rotated element reads its partner
+// again rather than exchanging it.
+template <typename T, typename C>
+__global__ void __launch_bounds__(128) rope_write_any_kernel(const Args a, bool inter) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int heads = a.hq + 2 * a.hkv;
+    const int64_t items = a.max_n * heads;
+    const int64_t step = (int64_t)gridDim.x * 4;
+    for (int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); it < items; it += step) {
+        const int64_t i = it / heads;
+        const int h = (int)(it - i * heads);
+        const Token t = token_at(a, i, h == 0 && lane == 0);
+        if (!t.real) continue;
+        const int kind = h < a.hq ? 0 : (h < a.hq + a.hkv ? 1 : 2);
+        if (kind > 0 && t.slot < 0) continue;
+        if (kind == 2) {
+            const int g = h - a.hq - a.hkv;
+            const T *src = static_cast<const T *>(a.v) + i * a.v_stride + (int64_t)g * a.d;
+            C *dst = static_cast<C *>(a.vc) + (t.slot * a.hkv + g) * a.d;
+            for (int e = lane; e < a.d; e += 32) copy(dst + e, src[e], a.v_scale);
+            continue;
+        }
+        const int g = kind == 0 ? h : h - a.hq;
+        const T *src = kind == 0 ? static_cast<const T *>(a.q) + i * a.q_stride + (int64_t)g * a.d
+                                 : static_cast<const T *>(a.k) + i * a.k_stride + (int64_t)g * a.d;
+        const T *w = static_cast<const T *>(kind == 0 ? a.qw : a.kw);
+        const int half = a.rot / 2;
+        float x[8], y[8];   // own element and the one it rotates with
+        float ss = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int e = lane + 32 * u;
+            x[u] = y[u] = 0.f;
+            if (e < a.d) {
+                x[u] = to_f(src[e]);
+                if (e < a.rot) y[u] = to_f(src[inter ? (e ^ 1) : (e < half ? e + half : e - half)]);
+                ss = fmaf(x[u], x[u], ss);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = w ? rsqrtf(ss / (float)a.d + a.eps) : 1.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int e = lane + 32 * u;
+            if (e >= a.d) break;
+            float r = x[u] * inv * (w ? to_f(w[e]) : 1.f);
+            if (e < a.rot) {
+                const int pe = inter ? (e ^ 1) : (e < half ? e + half : e - half);
+                const int ci = inter ? e >> 1 : (e < half ? e : e - half);
+                const float m = y[u] * inv * (w ? to_f(w[pe]) : 1.f);
+                const float c = __ldg(t.cs + ci), s = __ldg(t.cs + half + ci);
+                const bool first = inter ? !(e & 1) : e < half;
+                r = first ? r * c - m * s : r * c + m * s;
+            }
+            if (kind == 0)
+                put(static_cast<T *>(a.q_out) + (i * a.hq + g) * a.d + e, r, 1.f);
+            else
+                put(static_cast<C *>(a.kc) + (t.slot * a.hkv + g) * a.d + e, r, a.k_scale);
+        }
+    }
+}
+
+template <typename T, typename C>
+static cudaError_t launch_any(const Args &a, bool inter, cudaStream_t st) {
+    const int64_t items = a.max_n * (a.hq + 2 * a.hkv);
+    return launch_pdl(rope_write_any_kernel<T, C>, dim3(grid_for(items, 4, 64)), dim3(128), 0, st, a, inter);
+}
+
+static int run(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+               const void *q_weight, const void *k_weight, float norm_eps, const float *cos_sin, int64_t max_position,
+               int32_t rot_dim, int interleaved, const int32_t *block_table, int32_t num_reqs, int64_t bt_stride,
+               int32_t bt_cols, const int32_t *req_indices, const int64_t *positions, const int64_t *rope_positions,
+               int64_t num_tokens, int64_t max_num_tokens, int64_t *slot_mapping, void *q_out, void *k_cache,
+               void *v_cache, int64_t total_blocks, int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+               int32_t head_dim, int dtype, bool fp8, float k_scale, float v_scale, int32_t *err_count,
+               bkv_stream_t stream) {
+    if (dtype != BKV_BF16 && dtype != BKV_F32) return BKV_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || max_num_tokens < num_tokens || total_blocks < 0 || block_size <= 0 || num_q_heads <= 0 ||
+        num_kv_heads <= 0 || head_dim <= 0 || num_reqs < 0 || bt_cols < 0 || bt_stride < bt_cols || max_position < 0)
+        return BKV_ERR_INVALID_ARG;
+    if (head_dim > 256 || head_dim % 2 != 0) return BKV_ERR_UNSUPPORTED;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0 || !(norm_eps >= 0.f) || !isfinite(norm_eps))
+        return BKV_ERR_INVALID_ARG;
+    if (fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale)))
+        return BKV_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)num_q_heads * head_dim || k_stride < (int64_t)num_kv_heads * head_dim ||
+        v_stride < (int64_t)num_kv_heads * head_dim)
+        return BKV_ERR_INVALID_ARG;
+    if (max_num_tokens == 0) return BKV_OK;
+    if (!slot_mapping) return BKV_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!q || !k || !v || !q_out || !req_indices || !positions || (bt_cols > 0 && !block_table) ||
+                           (rot_dim > 0 && !cos_sin) || (total_blocks > 0 && (!k_cache || !v_cache))))
+        return BKV_ERR_INVALID_ARG;
+    Args a{q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, norm_eps, cos_sin, max_position, rot_dim,
+           block_table, num_reqs, bt_stride, bt_cols, req_indices, positions, rope_positions, num_tokens,
+           max_num_tokens, slot_mapping, q_out, k_cache, v_cache, total_blocks * (int64_t)block_size, block_size,
+           num_q_heads, num_kv_heads, head_dim, k_scale, v_scale, err_count};
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool inter = interleaved != 0;
+    cudaError_t e;
+    if (dtype == BKV_BF16)
+        e = fp8 ? launch_any<__nv_bfloat16, uint8_t>(a, inter, st) : launch_any<__nv_bfloat16, __nv_bfloat16>(a, inter, st);
+    else
+        e = fp8 ? launch_any<float, uint8_t>(a, inter, st) : launch_any<float, float>(a, inter, st);
+    if (e != cudaSuccess) set_cuda_error(e);
+    return launch_status();
+}
+
+}  // namespace rope
+}  // namespace bkv
+
+#define BKV_ROPE_PARAMS                                                                                            \
+    const void *q, const void *k, const void *v, int64_t q_token_stride, int64_t k_token_stride,                   \
+        int64_t v_token_stride, const void *q_weight, const void *k_weight, float norm_eps, const float *cos_sin,  \
+        int64_t max_position, int32_t rot_dim, int interleaved, const int32_t *block_table, int32_t num_reqs,      \
+        int64_t bt_stride, int32_t bt_cols, const int32_t *req_indices, const int64_t *positions,                  \
+        const int64_t *rope_positions, int64_t num_tokens, int64_t max_num_tokens, int64_t *slot_mapping,          \
+        void *q_out
+#define BKV_ROPE_ARGS                                                                                              \
+    q, k, v, q_token_stride, k_token_stride, v_token_stride, q_weight, k_weight, norm_eps, cos_sin, max_position,  \
+        rot_dim, interleaved, block_table, num_reqs, bt_stride, bt_cols, req_indices, positions, rope_positions,   \
+        num_tokens, max_num_tokens, slot_mapping, q_out
+
+extern "C" int bkv_qk_norm_rope_cache_write(BKV_ROPE_PARAMS, void *k_cache, void *v_cache, int64_t total_blocks,
+                                            int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int dtype, int32_t *err_count, bkv_stream_t stream) {
+    return bkv::rope::run(BKV_ROPE_ARGS, k_cache, v_cache, total_blocks, block_size, num_q_heads, num_kv_heads,
+                          head_dim, dtype, false, 1.f, 1.f, err_count, stream);
+}
+
+extern "C" int bkv_qk_norm_rope_cache_write_fp8(BKV_ROPE_PARAMS, uint8_t *k_cache, uint8_t *v_cache,
+                                                int64_t total_blocks, int32_t block_size, int32_t num_q_heads,
+                                                int32_t num_kv_heads, int32_t head_dim, int dtype, float k_scale,
+                                                float v_scale, int32_t *err_count, bkv_stream_t stream) {
+    return bkv::rope::run(BKV_ROPE_ARGS, k_cache, v_cache, total_blocks, block_size, num_q_heads, num_kv_heads,
+                          head_dim, dtype, true, k_scale, v_scale, err_count, stream);
+}

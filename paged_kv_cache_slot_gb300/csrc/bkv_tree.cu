@@ -1,0 +1,493 @@
+// bkv_tree.cu -- attention of drafted trees over the paged cache: planner,
+// the CUDA-core kernel, the merge of split streams and the ABI entry points.
+//
+// Request r has T tree tokens, the last T of its L cached positions.  Token t
+// sees the committed positions [0, L - T) and those of the tree's own that its
+// mask row names (its ancestors and itself, as the caller builds it):
+//   out_t = sum_j softmax_j(scale q_t . k_j) v_j, 0 where no key is seen.
+// "Padding and Batching with Block KV", Cache Masking: mask_cache over the
+// committed positions, mask_active between this step's tokens, here any mask;
+// Special Block and Slot Values: null and sentinel entries contribute nothing.
+//
+// Every query row of a KV head (T * G) shares each K and V row, so the cache
+// is read once: memory-bound up to about 280 rows a KV head in bf16 (4 D
+// operations a row against 4 D bytes a position and head, at the measured
+// rates), bound by the multiply-adds in fp32 from a few rows on.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "bkv_tree.cuh"
+
+namespace bkv {
+namespace tree {
+
+static constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxT = 256;       // tree tokens a request
+constexpr int kBK = 32;          // keys a tile of the CUDA-core kernel
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void store_out(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store_out(float *p, float x) { *p = x; }
+
+// ---------------------------------------------------------------------------
+// CUDA-core kernel: any dtype, head_dim <= DP, any block size.  CTA = (stream
+// (request, KV head), split of positions; BR query rows).  Keys come in tiles
+// of 32 through shared memory as fp32; eight consecutive lanes own a query row:
+// lane x of them the keys x, x + 8, .. of S and the elements 4 x + 32 j of O,
+// so the row's max and sum are three shuffles and P only crosses its own warp.
+// A V row of the tree that is not finite is taken as 0 for the rows that do
+// not see it, and makes the rows that do NaN.
+// ---------------------------------------------------------------------------
+template <typename T, int DP, int BR>
+__global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
+    constexpr int LD = DP + 4, RPT = BR / 16, DJ = DP / 32;
+    extern __shared__ float sm[];
+    float *Qs = sm;                    // [BR][LD], scaled to base 2
+    float *Ks = Qs + BR * LD;          // [kBK][LD]
+    float *Vs = Ks + kBK * LD;         // [kBK][LD]
+    float *Ps = Vs + kBK * LD;         // [BR][kBK + 4]
+    __shared__ int64_t rowoff[kBK];    // element offset of each key's row, -1: not there
+    __shared__ uint32_t live, poison;
+    pdl_wait();
+    pdl_trigger();
+    const int rg = blockIdx.x / a.n_chunks, c = blockIdx.x - rg * a.n_chunks;
+    const int r = rg / a.H_kv, g = rg - r * a.H_kv;
+    const int nq = a.T * a.G, i0 = blockIdx.y * BR;
+    const int ty = threadIdx.x >> 3, tx = threadIdx.x & 7;
+    const int32_t ctx = __ldg(a.ctx + r);
+    const int32_t L = tree_len(a, ctx), first = L - a.T;
+    if (ctx > a.max_ctx && c == 0 && g == 0 && blockIdx.y == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+    const int32_t start = c * a.chunk;
+    if (start >= L) return;
+    const int32_t end = min(start + a.chunk, L);
+    if (a.err && blockIdx.y == 0) {   // splits hold whole blocks: each needed block counts once a KV head
+        for (int32_t lb = start / a.bs + threadIdx.x; lb <= (end - 1) / a.bs; lb += kThreads) {
+            const bool bad = lb >= a.bt_cols || __ldg(a.bt + (int64_t)r * a.bt_stride + lb) >= a.total_blocks;
+            if (bad) atomicAdd(a.err, 1);
+        }
+    }
+    const T *Q = static_cast<const T *>(a.q);
+    for (int e = threadIdx.x; e < BR * DP; e += kThreads) {
+        const int i = e / DP, d = e - i * DP, row = i0 + i;
+        float x = 0.f;
+        if (row < nq && d < a.D) {
+            const int t = row / a.G, h = g * a.G + (row - t * a.G);
+            x = to_f(Q[(((int64_t)r * a.T + t) * a.H_q + h) * a.D + d]) * a.scale_log2;
+        }
+        Qs[i * LD + d] = x;
+    }
+    float o[RPT][DJ][4], m[RPT], l[RPT];
+    const uint32_t *mrow[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        const int row = min(i0 + ty + 16 * i, nq - 1);
+        mrow[i] = a.mask + (int64_t)r * a.mask_stride + (int64_t)(row / a.G) * a.mask_words;
+#pragma unroll
+        for (int j = 0; j < DJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    }
+    for (int32_t k0 = start; k0 < end; k0 += kBK) {
+        __syncthreads();   // the last tile is read out
+        if (threadIdx.x < kBK) {
+            const int32_t j = k0 + threadIdx.x;
+            int64_t off = -1;
+            if (j < end) {
+                const int32_t lb = j / a.bs;
+                const int64_t b = lb < a.bt_cols ? __ldg(a.bt + (int64_t)r * a.bt_stride + lb) : -1;
+                if (b > 0 && b < a.total_blocks) off = ((b * a.bs + (j - lb * a.bs)) * a.H_kv + g) * a.D;
+            }
+            rowoff[threadIdx.x] = off;
+            const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
+            if (threadIdx.x == 0) {
+                live = ok;
+                poison = 0u;
+            }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < kBK * DP; e += kThreads) {
+            const int i = e / DP, d = e - i * DP;
+            const int64_t off = rowoff[i];
+            const bool in = off >= 0 && d < a.D;
+            const float kx = in ? to_f(static_cast<const T *>(a.k)[off + d]) : 0.f;
+            const float vx = in ? to_f(static_cast<const T *>(a.v)[off + d]) : 0.f;
+            Ks[i * LD + d] = kx;
+            Vs[i * LD + d] = vx;
+            if (k0 + i >= first && !isfinite(vx)) atomicOr(&poison, 1u << i);
+        }
+        __syncthreads();
+        const uint32_t bad = poison;
+        if (bad) {
+            for (int e = threadIdx.x; e < kBK * DP; e += kThreads) {
+                const int i = e / DP;
+                if ((bad >> i) & 1u) Vs[i * LD + (e - i * DP)] = 0.f;
+            }
+            __syncthreads();
+        }
+        float s[RPT][4];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < DP; d += 4) {
+            float4 kk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4 *>(Ks + (tx + 8 * j) * LD + d);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const float4 qq = *reinterpret_cast<const float4 *>(Qs + (ty + 16 * i) * LD + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qq.x, kk[j].x, s[i][j]);
+                    s[i][j] = fmaf(qq.y, kk[j].y, s[i][j]);
+                    s[i][j] = fmaf(qq.z, kk[j].z, s[i][j]);
+                    s[i][j] = fmaf(qq.w, kk[j].w, s[i][j]);
+                }
+            }
+        }
+        __syncwarp();   // this warp's P rows of the last tile are read
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const uint32_t vis = live & (k0 + kBK <= first ? 0xffffffffu
+                                                           : tree_vis32(mrow[i], a.mask_words, first, L, k0));
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = (vis >> (tx + 8 * j)) & 1u ? s[i][j] : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            const float mn = fmaxf(m[i], top);
+            const float corr = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a seen NaN score stays NaN (fmaxf dropped it from the maximum)
+                const float p = (vis >> (tx + 8 * j)) & 1u ? exp2f(s[i][j] - mn) : 0.f;
+                Ps[(ty + 16 * i) * (kBK + 4) + tx + 8 * j] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            if (vis & bad) sum = NAN;
+            l[i] = fmaf(l[i], corr, sum);
+            m[i] = mn;
+#pragma unroll
+            for (int j = 0; j < DJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][j][e] *= corr;
+        }
+        __syncwarp();
+#pragma unroll 2
+        for (int k = 0; k < kBK; k += 4) {
+            float4 p[RPT];
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+                p[i] = *reinterpret_cast<const float4 *>(Ps + (ty + 16 * i) * (kBK + 4) + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int j = 0; j < DJ; ++j) {
+                    const float4 vv = *reinterpret_cast<const float4 *>(Vs + (k + e) * LD + 4 * tx + 32 * j);
+#pragma unroll
+                    for (int i = 0; i < RPT; ++i) {
+                        const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+                        o[i][j][0] = fmaf(w, vv.x, o[i][j][0]);
+                        o[i][j][1] = fmaf(w, vv.y, o[i][j][1]);
+                        o[i][j][2] = fmaf(w, vv.z, o[i][j][2]);
+                        o[i][j][3] = fmaf(w, vv.w, o[i][j][3]);
+                    }
+                }
+            }
+        }
+    }
+    const int64_t slot = (int64_t)rg * a.n_chunks + c;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        const int row = i0 + ty + 16 * i;
+        if (row >= nq) continue;
+        const int64_t pr = slot * a.NR + row;
+#pragma unroll
+        for (int j = 0; j < DJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = 4 * tx + 32 * j + e;
+                if (d < a.D) a.ws_o[pr * a.D + d] = o[i][j][e];
+            }
+        if (tx == 0) {
+            a.ws_ml[pr * 2] = m[i];
+            a.ws_ml[pr * 2 + 1] = l[i];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of a stream's partials: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M)
+// l_c, 0 where nothing was seen.  CTA = (stream, 32 of its rows), a warp a row
+// at a time.  The tensor-core kernel writes streams that one CTA finished
+// itself; the merge leaves those alone.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeArgs a) {
+    __shared__ int64_t red[2][4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_req = a.H_kv * a.groups;
+    const int64_t st = blockIdx.x;
+    const int r = (int)(st / per_req), hp = (int)(st - (int64_t)r * per_req);
+    const int g = hp / a.groups, p = hp - g * a.groups;
+    const int32_t L = tree_len(a, __ldg(a.ctx + r));
+    int nch = 0;
+    int64_t slot0 = 0;
+    if (a.tc) {
+        int64_t all = 0, before = 0;
+        for (int rr = threadIdx.x; rr < a.num_reqs; rr += kThreads) {
+            const int64_t t = (tree_len(a, __ldg(a.ctx + rr)) + kTreeTile - 1) / kTreeTile;
+            all += t;
+            if (rr < r) before += t;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            all += __shfl_xor_sync(0xffffffffu, all, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        if (lane == 0) {
+            red[0][warp] = all;
+            red[1][warp] = before;
+        }
+        __syncthreads();
+        all = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+        before = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+        const int64_t Ts = (L + kTreeTile - 1) / kTreeTile;
+        if (Ts > 0) {
+            // column q of peff covers tiles [q all / peff, (q + 1) all / peff); its part of this stream is
+            // slot hp (P + R) + q + r
+            const int64_t peff = all < a.P ? all : a.P;
+            const int64_t q0 = ((before + 1) * peff - 1) / all;
+            const int64_t q1 = ((before + Ts) * peff - 1) / all;
+            nch = (int)(q1 - q0 + 1);
+            slot0 = (int64_t)hp * (a.P + a.num_reqs) + q0 + r;
+        }
+    } else if (L > 0) {
+        nch = (L + a.chunk - 1) / a.chunk;
+        slot0 = st * a.n_chunks;
+    }
+    pdl_wait();   // by every CTA: this grid's end stands for the partials' and the rows written there
+    pdl_trigger();
+    if (a.tc && nch == 1) return;   // one CTA had the whole stream and wrote its rows
+    const int rows = min(a.NR, (a.T - p * a.TS) * a.G);
+    const int row_end = min(rows, ((int)blockIdx.y + 1) * 32);
+    for (int row = blockIdx.y * 32 + warp; row < row_end; row += 4) {
+        const int t = p * a.TS + row / a.G, h = g * a.G + row % a.G;
+        T *out = static_cast<T *>(a.out) + (((int64_t)r * a.T + t) * a.H_q + h) * a.D;
+        float M = -INFINITY;
+        for (int c = lane; c < nch; c += 32) M = fmaxf(M, a.ws_ml[((slot0 + c) * a.NR + row) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float sum = 0.f;
+        for (int c = lane; c < nch; c += 32) {
+            const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + ((slot0 + c) * a.NR + row) * 2);
+            // a part that saw nothing but NaN scores has no maximum, and a NaN sum
+            const float w = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : 1.f) : exp2f(ml.x - M);
+            sum = fmaf(w, ml.y, sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int d = 2 * lane; d < a.D; d += 64) {
+            float x = 0.f, y = 0.f;
+            for (int c = 0; c < nch; ++c) {
+                const int64_t pr = (slot0 + c) * a.NR + row;
+                const float mc = a.ws_ml[pr * 2];
+                const float w = mc == -INFINITY ? 0.f : exp2f(mc - M);
+                const float2 v = *reinterpret_cast<const float2 *>(a.ws_o + pr * a.D + d);
+                x = fmaf(w, v.x, x);
+                y = fmaf(w, v.y, y);
+            }
+            store_out(out + d, x * inv);
+            store_out(out + d + 1, y * inv);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Planner
+// ---------------------------------------------------------------------------
+struct Plan {
+    int32_t chunk, n_chunks;
+    int64_t slots_cc, slots_tc, rows_tc;   // tensor-core slots are bounded over its two forms
+    int64_t part_bytes;
+    size_t ws_bytes;
+};
+
+static int64_t gcd64(int64_t x, int64_t y) {
+    while (y) {
+        const int64_t t = x % y;
+        x = y;
+        y = t;
+    }
+    return x;
+}
+
+// Tokens of a slot and CTA columns of the tensor-core kernel: a stream's T G
+// rows are one query tile of 128 / G tokens, or pairs of them.
+static void tc_split(int32_t T, int32_t G, int32_t H_kv, int32_t *TS, int32_t *groups, int32_t *P) {
+    const int32_t tt = G <= 128 ? 128 / G : 1;
+    *TS = T <= tt ? T : 2 * tt;
+    *groups = (T + *TS - 1) / *TS;
+    const int64_t cols = (int64_t)H_kv * *groups;
+    const int64_t sms = current_sm_count();
+    *P = (int32_t)(cols < sms ? sms / cols : 1);
+}
+
+static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, int32_t D, int32_t bs, int32_t max_ctx,
+                      Plan *p) {
+    if (num_reqs <= 0 || T <= 0 || T > kMaxT || H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || D <= 0 || D > 256 ||
+        D % 2 != 0 || bs <= 0 || bs > 65536 || max_ctx < 0)
+        return false;
+    const int32_t G = H_q / H_kv;
+    const int64_t nq = (int64_t)T * G;
+    const int64_t units = (int64_t)num_reqs * H_kv;
+    const int64_t sms = current_sm_count();
+    // splits hold whole blocks, of 128 positions at least; about four CTAs an SM where the batch alone has fewer
+    const int64_t align = (int64_t)bs / gcd64(bs, 128) * 128;
+    const int64_t row_tiles = ceil_div<int64_t>(nq, 64);
+    int64_t chunk = ceil_div<int64_t>((int64_t)max_ctx * units * row_tiles, 4 * sms);
+    chunk = ceil_div<int64_t>(chunk < 1 ? 1 : chunk, align) * align;
+    if (chunk > (int64_t)1 << 30) return false;
+    p->chunk = (int32_t)chunk;
+    p->n_chunks = max_ctx > 0 ? (int32_t)ceil_div<int64_t>(max_ctx, chunk) : 1;
+    p->slots_cc = units * p->n_chunks;
+    if (p->slots_cc >= ((int64_t)1 << 31) || ceil_div<int64_t>(nq, 16) > 65535) return false;
+    int64_t rows = p->slots_cc * nq;
+    p->slots_tc = 0;
+    if (D == 128 && G <= 128) {
+        int32_t TS, groups, P;
+        tc_split(T, G, H_kv, &TS, &groups, &P);
+        p->slots_tc = (int64_t)H_kv * groups * (P + (int64_t)num_reqs);
+        const int64_t rt = p->slots_tc * TS * G;
+        if (rt > rows) rows = rt;
+    }
+    p->ws_bytes = (size_t)(ceil_div<int64_t>(rows * D * 4, 256) * 256 + ceil_div<int64_t>(rows * 8, 256) * 256);
+    return true;
+}
+
+template <typename T, int DP, int BR>
+static cudaError_t launch_cc(const TreeArgs &a, cudaStream_t st) {
+    constexpr int smem = ((BR + 2 * kBK) * (DP + 4) + BR * (kBK + 4)) * 4;
+    auto kern = tree_cc_kernel<T, DP, BR>;
+    if (smem > 48 * 1024) {
+        static bool set[64] = {};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if (dev < 0 || dev >= 64 || !set[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            if (dev >= 0 && dev < 64) set[dev] = true;
+        }
+    }
+    const dim3 grid((unsigned)(a.num_reqs * a.H_kv * a.n_chunks), (unsigned)ceil_div(a.T * a.G, BR));
+    return launch_pdl(kern, grid, dim3(kThreads), smem, st, a);
+}
+
+// Few rows take the small query tile (16 rows), more the large one (64; 32 with
+// head_dim above 128, for its registers).
+template <typename T>
+static cudaError_t launch_cc_dims(const TreeArgs &a, cudaStream_t st) {
+    const bool few = a.T * a.G <= 16;
+    if (a.D <= 32) return few ? launch_cc<T, 32, 16>(a, st) : launch_cc<T, 32, 64>(a, st);
+    if (a.D <= 64) return few ? launch_cc<T, 64, 16>(a, st) : launch_cc<T, 64, 64>(a, st);
+    if (a.D <= 128) return few ? launch_cc<T, 128, 16>(a, st) : launch_cc<T, 128, 64>(a, st);
+    return few ? launch_cc<T, 256, 16>(a, st) : launch_cc<T, 256, 32>(a, st);
+}
+
+static int launch_merge(const TreeArgs &a, cudaStream_t st) {
+    const int64_t streams = (int64_t)a.num_reqs * a.H_kv * a.groups;
+    const dim3 grid((unsigned)streams, (unsigned)ceil_div(a.NR, 32));
+    const cudaError_t e = a.dtype == BKV_BF16 ? launch_pdl(tree_merge_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a)
+                                              : launch_pdl(tree_merge_kernel<float>, grid, dim3(kThreads), 0, st, a);
+    if (e != cudaSuccess) set_cuda_error(e);
+    return launch_status();
+}
+
+}  // namespace tree
+}  // namespace bkv
+
+extern "C" size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int32_t num_q_heads,
+                                                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                                       int32_t max_context_len) {
+    bkv::tree::Plan p;
+    if (!bkv::tree::make_plan(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, &p))
+        return 0;
+    return p.ws_bytes;
+}
+
+extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const void *v_cache,
+                                     const int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
+                                     const int32_t *context_lens, int32_t max_context_len, int32_t num_reqs,
+                                     int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t block_size, int64_t total_blocks, float softmax_scale,
+                                     const uint32_t *tree_mask, int64_t mask_req_stride, int dtype, void *out,
+                                     void *workspace, size_t workspace_bytes, int32_t *err_count,
+                                     bkv_stream_t stream) {
+    using namespace bkv;
+    using namespace bkv::tree;
+    if (dtype != BKV_BF16 && dtype != BKV_F32) return BKV_ERR_UNSUPPORTED;
+    if (head_dim > 256 || head_dim % 2 != 0 || q_len > kMaxT) return BKV_ERR_UNSUPPORTED;
+    if (bt_cols < 0 || bt_stride < bt_cols || total_blocks < 0) return BKV_ERR_INVALID_ARG;
+    Plan plan;
+    if (!make_plan(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, &plan))
+        return BKV_ERR_INVALID_ARG;
+    const int32_t words = (q_len + 31) / 32;
+    if (mask_req_stride != 0 && mask_req_stride < (int64_t)q_len * words) return BKV_ERR_INVALID_ARG;
+    if (!q || !out || !context_lens || !tree_mask || (bt_cols > 0 && !block_table)) return BKV_ERR_INVALID_ARG;
+    if (max_context_len > 0 && (!k_cache || !v_cache)) return BKV_ERR_INVALID_ARG;
+    if (workspace_bytes < plan.ws_bytes || !workspace || !aligned(workspace, 16)) return BKV_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf((float)head_dim);
+    TreeArgs a{};
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.bt = block_table;
+    a.bt_stride = bt_stride;
+    a.bt_cols = bt_cols;
+    a.ctx = context_lens;
+    a.max_ctx = max_context_len;
+    a.num_reqs = num_reqs;
+    a.T = q_len;
+    a.H_q = num_q_heads;
+    a.H_kv = num_kv_heads;
+    a.D = head_dim;
+    a.bs = block_size;
+    a.G = num_q_heads / num_kv_heads;
+    a.total_blocks = total_blocks;
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.mask = tree_mask;
+    a.mask_stride = mask_req_stride;
+    a.mask_words = words;
+    a.dtype = dtype;
+    a.out = out;
+    a.err = err_count;
+    a.chunk = plan.chunk;
+    a.n_chunks = plan.n_chunks;
+    auto set_slots = [&](int64_t slots) {
+        a.ws_o = static_cast<float *>(workspace);
+        a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                            ceil_div<int64_t>(slots * a.NR * head_dim * 4, 256) * 256);
+    };
+    cudaStream_t st = (cudaStream_t)stream;
+    // one query-row group for all tokens: the CUDA-core kernel's slots
+    a.TS = q_len;
+    a.NR = q_len * a.G;
+    a.groups = 1;
+    set_slots(plan.slots_cc);
+    const cudaError_t e = dtype == BKV_BF16 ? launch_cc_dims<__nv_bfloat16>(a, st) : launch_cc_dims<float>(a, st);
+    if (e != cudaSuccess) set_cuda_error(e);
+    const int rc = launch_status();
+    return rc != BKV_OK ? rc : launch_merge(a, st);
+}
