@@ -481,6 +481,18 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
                                             ceil_div<int64_t>(slots * a.NR * head_dim * 4, 256) * 256);
     };
     cudaStream_t st = (cudaStream_t)stream;
+    TreeTc t;
+    if (plan.slots_tc > 0) {
+        tc_split(a.T, a.G, a.H_kv, &a.TS, &a.groups, &a.P);
+        a.NR = a.TS * a.G;
+        a.tc = 1;
+        if (prepare_tree_tc(a, &t)) {
+            set_slots(plan.slots_tc);
+            const int rc = launch_tree_tc(a, t, st);
+            return rc != BKV_OK ? rc : launch_merge(a, st);
+        }
+    }
+    a.tc = 0;
     // one query-row group for all tokens: the CUDA-core kernel's slots
     a.TS = q_len;
     a.NR = q_len * a.G;

@@ -74,7 +74,6 @@ struct TreeTc {
     int seg_rows;
     int tok_per_tile;   // tree tokens a 128-row query tile holds: 128 / G
     int box_tok;        // tokens a load of q brings
-    int dual;           // two query tiles share every key tile (otherwise two key tiles share one query tile)
 };
 bool prepare_tree_tc(const TreeArgs &a, TreeTc *t);
 int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t stream);

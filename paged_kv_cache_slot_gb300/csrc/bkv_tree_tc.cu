@@ -1,0 +1,793 @@
+// bkv_tree_tc.cu -- tensor-core (tcgen05 + TMA) kernel of the attention of
+// drafted trees: bf16, head_dim 128, any tree and any group size up to 128.
+//
+// For a stream (request, KV head, token group) and a run of its 128-position
+// tiles: S = Q K^T, an online softmax under the tree's mask, O += P V ("Padding
+// and Batching with Block KV", Cache Masking).  The cache is read once for all
+// the rows of a group; a stream that one CTA finishes is written to `out`
+// there, one that several CTAs share leaves partials for the merge.
+//
+// Design (sm_103a):
+// * Schedule: the grid is P columns of one CTA per (KV head, token group).  The
+//   requests' position tiles are laid end to end and column q takes [q TP / P,
+//   (q + 1) TP / P) of them, so every SM gets the same number of tiles to one,
+//   whatever the lengths.  A column's CTAs read the same positions of all heads
+//   together.
+// * A query tile is 128 / G tokens times the G heads, rows (token, head): one
+//   3-D TMA box of q.  A group of at most one query tile runs its key tiles
+//   alternately on two softmax streams with their own S, P and O (columns of
+//   tensor memory), so that one stream's softmax runs beside the other's MMAs;
+//   their O are joined when the unit ends.  A group of two query tiles gives
+//   each its own stream, and every K and V tile serves both.
+// * Warp roles (608 threads): warp 0 loads Q and gathers K tiles, the last warp
+//   gathers V tiles (2-slot rings of 32 KB), warp 1 issues every MMA from one
+//   thread; eight softmax warps a stream, four lane quarters times two halves
+//   of a tile's keys, one query row a thread; quarters without rows are idle.
+// * P (bf16, two per column) goes over its own S columns and enters P V from
+//   tensor memory.  The running max is a lazy reference (it moves when a tile's
+//   max passes it by 8 in log2 units), so O is seldom rescaled.
+// * Masks: tiles wholly before the tree and without null entries take no
+//   per-key tests.  V rows that were not loaded, or lie at or past the cache
+//   end, are zeroed in shared memory before P V; a V row of the tree that is not
+//   finite is zeroed too and remembered, and rows that see it become NaN.
+// * Every wait is bounded (~2 s), after which the CTA records 1 << 24 in
+//   err_count, frees its tensor memory and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "bkv_tc_ptx.cuh"
+#include "bkv_tree.cuh"
+
+namespace bkv {
+namespace ttc {
+
+using namespace tc;
+
+constexpr int kTile = kTreeTile;
+constexpr int kD = 128;
+constexpr int kStages = 2;
+constexpr int kHalfBytes = kTile * 128;
+constexpr int kTileBytes = 2 * kHalfBytes;
+constexpr int kThreads = 608;
+constexpr int kWarpV = kThreads / 32 - 1;
+constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (128 columns each)
+constexpr int kTimeoutErr = 1 << 24;
+constexpr int kMaxReqs = 2048;
+constexpr float kSlack = 8.f;
+
+constexpr int kOffQ = 0;                                  // two query tiles (or two units' one tile)
+constexpr int kOffK = kOffQ + 2 * kTileBytes;
+constexpr int kOffV = kOffK + kStages * kTileBytes;
+constexpr int kOffMask = kOffV + kStages * kTileBytes;    // 8 words: loaded segments per tile (ring)
+constexpr int kOffPoison = kOffMask + 8 * 4;              // 8 x 4 words: V rows of the tile that are not finite
+constexpr int kOffBar = kOffPoison + 8 * 4 * 4;
+constexpr int kNumBars = 4 * kStages + 4 + 2 + 2 + 2 + 8 + 8 + 4;
+constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
+constexpr int kOffAbort = kOffTmemSlot + 4;
+constexpr int kOffPre = (kOffAbort + 4 + 15) / 16 * 16;   // [kMaxReqs + 1] tiles before request r
+constexpr int kOffLen = kOffPre + (kMaxReqs + 4) * 4;     // [kMaxReqs] clamped lengths
+constexpr int kOffXmax = kOffLen + kMaxReqs * 4;          // [stream][half][tile parity][row]
+constexpr int kOffXm = kOffXmax + 2 * 2 * 2 * kTile * 4;  // [stream][row]
+constexpr int kOffXsum = kOffXm + 2 * kTile * 4;          // [stream][half][row]
+constexpr int kSmemUsed = kOffXsum + 2 * 2 * kTile * 4;
+constexpr int kSmemBytes = kSmemUsed + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
+
+__host__ __device__ constexpr uint32_t col_s(int x) { return 128u * (uint32_t)x; }
+__host__ __device__ constexpr uint32_t col_o(int x) { return 256u + 128u * (uint32_t)x; }
+
+__device__ __forceinline__ float tree_max32(const float (&v)[32]) {
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = fmaxf(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) t[i] = fmaxf(t[2 * i], t[2 * i + 1]);
+    return t[0];
+}
+
+// One unit: tiles [f, f + nt) of request r.  whole: they are all of its tiles.
+struct Unit {
+    int r, L, f, nt, slot;
+    bool whole;
+};
+
+// Walks this CTA's units: column q's share of the tiles laid end to end.
+struct Units {
+    const int32_t *pre, *len;
+    int n, r, q;
+    int64_t t, t1;
+    __device__ Units(const TreeArgs &a, const int32_t *pre_, const int32_t *len_, int q_) {
+        pre = pre_;
+        len = len_;
+        n = a.num_reqs;
+        q = q_;
+        const int64_t TP = pre[n];
+        const int64_t peff = TP < a.P ? TP : a.P;
+        t = q < peff ? TP * q / peff : TP;
+        t1 = q < peff ? TP * (q + 1) / peff : TP;
+        int lo = 0, hi = n;   // first request whose tiles end after t
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid + 1] > t) hi = mid;
+            else lo = mid + 1;
+        }
+        r = lo;
+    }
+    __device__ bool next(Unit &x) {
+        if (t >= t1) return false;
+        while (pre[r + 1] <= t) ++r;
+        const int s = pre[r], e = pre[r + 1];
+        x.r = r;
+        x.L = len[r];
+        x.f = (int)(t - s);
+        const int end = t1 < e ? (int)(t1 - s) : e - s;
+        x.nt = end - x.f;
+        x.whole = x.nt == e - s;
+        x.slot = q + r;
+        t = s + end;
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ CUtensorMap tmQ, const TreeArgs a, int seg_rows, int tok_per_tile,
+                   int box_tok) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    volatile uint32_t *mask_words = reinterpret_cast<uint32_t *>(smem + kOffMask);
+    volatile uint32_t *poison = reinterpret_cast<uint32_t *>(smem + kOffPoison);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmemSlot);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + kOffPre);
+    int32_t *len = reinterpret_cast<int32_t *>(smem + kOffLen);
+    const uint32_t bar0 = sbase + kOffBar;
+    auto bar_kfull = [&](int s) { return bar0 + 8u * s; };
+    auto bar_kempty = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto bar_vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
+    auto bar_vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
+    constexpr int kB = 4 * kStages;
+    auto bar_qfull = [&](int b) { return bar0 + 8u * (kB + b); };
+    auto bar_qempty = [&](int b) { return bar0 + 8u * (kB + 2 + b); };
+    auto bar_sfull = [&](int x) { return bar0 + 8u * (kB + 4 + x); };
+    auto bar_pfull = [&](int x) { return bar0 + 8u * (kB + 6 + x); };
+    const uint32_t bar_ofull = bar0 + 8u * (kB + 8);
+    const uint32_t bar_oempty = bar0 + 8u * (kB + 9);
+    auto bar_mask = [&](int m) { return bar0 + 8u * (kB + 10 + m); };
+    // the two warps (one per key half) of a lane quarter of a stream; the four of a quarter of both
+    auto bar_pair = [&](int x, int qw) { return bar0 + 8u * (kB + 18 + 4 * x + qw); };
+    auto bar_quad = [&](int qw) { return bar0 + 8u * (kB + 26 + qw); };
+    const uint32_t sm_q = sbase + kOffQ;
+    const uint32_t sm_k = sbase + kOffK;
+    const uint32_t sm_v = sbase + kOffV;
+
+    // what this CTA is: column q, KV head g, token group p, and its rows
+    const int G = a.G;
+    const int HP = a.H_kv * a.groups;
+    const int q = (int)blockIdx.x / HP, hp = (int)blockIdx.x - q * HP;
+    const int g = hp / a.groups, p = hp - g * a.groups;
+    const int tok0 = p * a.TS;
+    const int ntok = min(a.TS, a.T - tok0);
+    const bool dual = ntok > tok_per_tile;   // two query tiles, every key tile for both
+    const int rows0 = (dual ? tok_per_tile : ntok) * G;
+    const int rows1 = dual ? (ntok - tok_per_tile) * G : rows0;
+    const int aq0 = (rows0 + 31) >> 5, aq1 = (rows1 + 31) >> 5;   // lane quarters with rows
+    const int nbuf = dual ? 1 : 2;                                // units whose queries fit
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_kfull(s), 1);
+            mbar_init(bar_kempty(s), 1);
+            mbar_init(bar_vfull(s), 1);
+            mbar_init(bar_vempty(s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar_qfull(x), 1);
+            mbar_init(bar_qempty(x), 1);
+            mbar_init(bar_sfull(x), 1);
+            mbar_init(bar_pfull(x), 2 * (x ? aq1 : aq0));
+            for (int qw = 0; qw < 4; ++qw) mbar_init(bar_pair(x, qw), 2);
+        }
+        mbar_init(bar_ofull, 2);
+        mbar_init(bar_oempty, 2 * (aq0 + aq1));
+        for (int m = 0; m < 8; ++m) mbar_init(bar_mask(m), 1);
+        for (int qw = 0; qw < 4; ++qw) mbar_init(bar_quad(qw), 4);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        prefetch_tmap(&tmQ);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();   // global memory is read from here on
+    pdl_trigger();
+    for (int r = threadIdx.x; r < a.num_reqs; r += kThreads) {
+        const int32_t c = __ldg(a.ctx + r);
+        const int32_t L = tree_len(a, c);
+        if (c > a.max_ctx && blockIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+        len[r] = L;
+        pre[r] = (L + kTile - 1) / kTile;
+    }
+    __syncthreads();
+    if (warp == 0) {   // exclusive prefix sum of the tiles
+        const int n = a.num_reqs;
+        const int per = (n + 31) / 32;
+        const int lo = min(n, lane * per), hi = min(n, lo + per);
+        int32_t sum = 0;
+        for (int r = lo; r < hi; ++r) sum += pre[r];
+        int32_t inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        int32_t run = inc - sum;
+        for (int r = lo; r < hi; ++r) {
+            const int32_t t = pre[r];
+            pre[r] = run;
+            run += t;
+        }
+        if (lane == 31) pre[n] = inc;
+    }
+    __syncthreads();
+    const uint32_t tmem = *tmem_slot;
+    const int nseg = kTile / seg_rows;
+    const int seg_shift = 31 - __clz(seg_rows);
+    const uint32_t all_seg = (1u << nseg) - 1u;   // at most 16 segments
+
+    if (warp == 0 || warp == kWarpV) {
+        // ================= TMA producers (warp 0: Q and K, last warp: V) =================
+        const bool is_v = warp == kWarpV;
+        const bool count = !is_v && p == 0 && a.err;   // bad entries count once a KV head
+        int64_t j = 0;
+        int uq = 0;
+        Units units(a, pre, len, q);
+        Unit x;
+        for (; !*abort_flag && units.next(x); ++uq) {
+            if (!is_v) {
+                const int b = uq % nbuf;
+                if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((uq / nbuf) & 1) ^ 1u, abort_flag)) break;
+                if (lane == 0) {
+                    const uint32_t bytes = (uint32_t)(box_tok * G) * 256u;
+                    mbar_arrive_expect_tx(bar_qfull(b), dual ? 2 * bytes : bytes);
+                    for (int xb = 0; xb < (dual ? 2 : 1); ++xb) {
+                        const int tq = x.r * a.T + tok0 + xb * tok_per_tile;
+                        const uint32_t dq = sm_q + (b + xb) * kTileBytes;
+                        tma_load_3d(dq, &tmQ, bar_qfull(b), 0, g * G, tq);
+                        tma_load_3d(dq + kHalfBytes, &tmQ, bar_qfull(b), 64, g * G, tq);
+                    }
+                }
+            }
+            // block entry of this lane's segment of key tile kt: the cache row to load, or -1
+            auto entry = [&](int kt) -> int64_t {
+                if (lane >= nseg) return -1;
+                const int32_t p0 = kt * kTile + lane * seg_rows;
+                if (p0 >= x.L) return -1;
+                const int32_t lb = p0 / a.bs;
+                const int32_t off = p0 - lb * a.bs;
+                const int64_t e = lb < a.bt_cols ? __ldg(a.bt + (int64_t)x.r * a.bt_stride + lb) : a.total_blocks;
+                if (e >= a.total_blocks) {
+                    if (count && off == 0) atomicAdd(a.err, 1);
+                    return -1;
+                }
+                return e > 0 ? e * a.bs + off : -1;
+            };
+            int64_t row_cur = entry(x.f);
+            for (int kt = 0; kt < x.nt; ++kt, ++j) {
+                const int64_t row_nxt = kt + 1 < x.nt ? entry(x.f + kt + 1) : -1;   // in flight meanwhile
+                const int s = (int)(j % kStages);
+                const uint32_t bar_e = is_v ? bar_vempty(s) : bar_kempty(s);
+                const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
+                if (!mbar_wait_warp(bar_e, (uint32_t)((j / kStages) & 1) ^ 1u, abort_flag)) break;
+                const bool load = row_cur >= 0;
+                const uint32_t ballot = __ballot_sync(0xffffffffu, load);
+                if (lane == 0) {
+                    // a word is rewritten 8 tiles on; its readers are at most 4 tiles behind
+                    if (!is_v) {
+                        mask_words[j & 7] = ballot;
+                        mbar_arrive(bar_mask((int)(j & 7)));
+                    }
+                    mbar_arrive_expect_tx(bar_f, (uint32_t)__popc(ballot) * (uint32_t)seg_rows * 256u);
+                }
+                __syncwarp();
+                if (load) {
+                    const uint32_t dst = (is_v ? sm_v : sm_k) + s * kTileBytes + lane * seg_rows * 128;
+                    const CUtensorMap *map = is_v ? &tmV : &tmK;
+                    tma_load_3d(dst, map, bar_f, 0, g, (int)row_cur);
+                    tma_load_3d(dst + kHalfBytes, map, bar_f, 64, g, (int)row_cur);
+                }
+                __syncwarp();
+                row_cur = row_nxt;
+            }
+        }
+        if (*abort_flag) {   // let copies in flight land
+            const unsigned long long t0 = global_ns();
+            while (global_ns() - t0 < 200000ull) {
+            }
+        }
+    } else if (warp == 1) {
+        // ================= MMA issuer (one thread) =================
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);   // Q (K-major) x K (K-major)
+            constexpr uint32_t kIdescO = idesc_bf16(128, 128, 0, 1);   // P (TMEM) x V (MN-major)
+            int np[2] = {0, 0};   // P tiles consumed
+            // O_x += P_x V(tile j): `first` overwrites O_x, once the unit before has been read out
+            auto issue_pv = [&](int xb, int64_t j, bool first, int unit) -> bool {
+                const int s = (int)(j % kStages);
+                if (!mbar_wait(bar_vfull(s), (uint32_t)((j / kStages) & 1), abort_flag) ||
+                    !mbar_wait(bar_pfull(xb), (uint32_t)(np[xb] & 1), abort_flag))
+                    return false;
+                ++np[xb];
+                if (first && unit > 0 && !mbar_wait(bar_oempty, (uint32_t)((unit - 1) & 1), abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t v_base = sm_v + s * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk) {
+                    // P of keys 0..63 lies over S columns 0..31, of keys 64..127 over columns 64..95
+                    const uint32_t pcol = (kk < 4 ? 0u : 64u) + 8u * (uint32_t)(kk & 3);
+                    mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + pcol, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
+                                kIdescO, (first && kk == 0) ? 0u : 1u);
+                }
+                return true;
+            };
+            auto issue_s = [&](int xb, int s, int qb) {
+                const uint32_t k_base = sm_k + s * kTileBytes;
+                const uint32_t q_base = sm_q + qb * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk) {
+                    const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (kk & 3) * 32;
+                    mma_bf16(tmem + col_s(xb), sdesc(q_base + off, 16, 1024), sdesc(k_base + off, 16, 1024), kIdescS,
+                             kk > 0 ? 1u : 0u);
+                }
+                mma_commit(bar_sfull(xb));
+            };
+            // The unit's last P V: O is settled.  The plain arrival carries the softmax warps' own
+            // shared-memory writes (acquired with P) on to the other warps.
+            auto finish = [&]() {
+                mma_commit(bar_ofull);
+                mbar_arrive(bar_ofull);
+            };
+            Units units(a, pre, len, q);
+            Unit x;
+            int64_t j = 0;
+            bool ok = true;
+            if (!dual) {
+                // stream j & 1 has tile j; its P V is issued before the S of tile j + 2, over the same columns
+                struct {
+                    int64_t j;
+                    int unit;
+                    bool on, first, last;
+                } pend[2] = {{0, 0, false, false, false}, {0, 0, false, false, false}};
+                auto settle = [&](int xb) -> bool {
+                    auto &w = pend[xb];
+                    if (!w.on) return true;
+                    w.on = false;
+                    if (!issue_pv(xb, w.j, w.first, w.unit)) return false;
+                    mma_commit(bar_vempty((int)(w.j % kStages)));
+                    if (w.last) finish();
+                    return true;
+                };
+                for (int uq = 0; ok && units.next(x); ++uq) {
+                    const int b = uq & 1;
+                    for (int kt = 0; kt < x.nt; ++kt, ++j) {
+                        const int xb = (int)(j & 1), s = (int)(j % kStages);
+                        ok = settle(xb) && (kt > 0 || mbar_wait(bar_qfull(b), (uint32_t)((uq >> 1) & 1), abort_flag)) &&
+                             mbar_wait(bar_kfull(s), (uint32_t)((j / kStages) & 1), abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(xb, s, b);
+                        mma_commit(bar_kempty(s));
+                        if (kt == x.nt - 1) mma_commit(bar_qempty(b));
+                        pend[xb].j = j;
+                        pend[xb].unit = uq;
+                        pend[xb].on = true;
+                        pend[xb].first = kt < 2;
+                        pend[xb].last = kt == x.nt - 1;
+                    }
+                }
+                if (ok) ok = settle((int)(j & 1)) && settle((int)((j + 1) & 1));
+            } else {
+                // per key tile: O_A += P_A V(-1), S_A; O_B += P_B V(-1), S_B
+                for (int uq = 0; ok && units.next(x); ++uq) {
+                    ok = mbar_wait(bar_qfull(0), (uint32_t)(uq & 1), abort_flag);
+                    for (int kt = 0; ok && kt <= x.nt; ++kt) {
+                        const int s = (int)(j % kStages);
+                        if (kt < x.nt && !mbar_wait(bar_kfull(s), (uint32_t)((j / kStages) & 1), abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        for (int xb = 0; xb < 2; ++xb) {
+                            if (kt > 0 && !issue_pv(xb, j - 1, kt == 1, uq)) {
+                                ok = false;
+                                break;
+                            }
+                            if (kt < x.nt) issue_s(xb, s, xb);
+                        }
+                        if (!ok) break;
+                        if (kt > 0) mma_commit(bar_vempty((int)((j - 1) % kStages)));
+                        if (kt < x.nt) {
+                            mma_commit(bar_kempty(s));
+                            if (kt == x.nt - 1) mma_commit(bar_qempty(0));
+                            ++j;
+                        } else {
+                            finish();
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ====== softmax: stream xb, key half kh, lane quarter qw, one query row a thread ======
+        const int xb = (warp - 2) >> 3;
+        const int kh = ((warp - 2) >> 2) & 1;
+        const int qw = warp & 3;
+        const int aq = xb ? aq1 : aq0;
+        if (qw < aq) {
+            const int row = 32 * qw + lane;
+            const bool valid = row < (xb ? rows1 : rows0);
+            const int tok = tok0 + (dual ? xb * tok_per_tile : 0) + min(row, (xb ? rows1 : rows0) - 1) / G;
+            const int hh = valid ? row % G : 0;
+            const int srow = row + (dual ? xb * tok_per_tile * G : 0);   // row of the slot
+            const uint32_t lane_base = (uint32_t)(32 * qw) << 16;
+            const uint32_t s_col = tmem + lane_base + col_s(xb);
+            float *xmax = reinterpret_cast<float *>(smem + kOffXmax) + xb * (2 * 2 * kTile);   // [half][parity][row]
+            float *xm = reinterpret_cast<float *>(smem + kOffXm);                              // [stream][row]
+            float *xsum = reinterpret_cast<float *>(smem + kOffXsum);                          // [stream][half][row]
+            uint32_t pphase = 0;
+            int64_t j = 0;
+            int ns = 0;          // S tiles of this stream seen so far
+            int no = 0;          // units finished so far
+            bool ok = true;
+            auto pair_sync = [&]() -> bool {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pair(xb, qw));
+                const bool r = mbar_wait_warp(bar_pair(xb, qw), pphase, abort_flag);
+                pphase ^= 1u;
+                return r;
+            };
+            Units units(a, pre, len, q);
+            Unit x;
+            while (ok && units.next(x)) {
+                const int first = x.L - a.T;   // position of the tree's first token
+                const uint32_t *mrow = a.mask + (int64_t)x.r * a.mask_stride + (int64_t)tok * a.mask_words;
+                const int64_t jb = j;
+                j += x.nt;
+                float m = -INFINITY, l = 0.f;
+                bool any = false;   // this stream had a tile of the unit
+                for (int kt = 0; kt < x.nt; ++kt) {
+                    const int64_t jj = jb + kt;
+                    if (!dual && (int)(jj & 1) != xb) continue;
+                    const int s = (int)(jj % kStages);
+                    if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
+                        !mbar_wait_warp(bar_mask((int)(jj & 7)), (uint32_t)((jj >> 3) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t mword = mask_words[jj & 7];
+                    const int k0 = (x.f + kt) * kTile;
+                    const bool near = k0 + kTile > first;    // positions of the tree, or past the cache end
+                    const bool full = !near && mword == all_seg;
+                    // keys [32 c, 32 c + 32) of the tile that this row sees, as bits
+                    auto vis32 = [&](int c) -> uint32_t {
+                        const int lo = 32 * c;
+                        uint32_t v = near ? tree_vis32(mrow, a.mask_words, first, x.L, k0 + lo) : 0xffffffffu;
+                        if (mword != all_seg) {
+                            uint32_t sb = 0u;
+                            if (seg_rows >= 32) {
+                                sb = ((mword >> (lo >> seg_shift)) & 1u) ? 0xffffffffu : 0u;
+                            } else {
+                                const uint32_t ones = (1u << seg_rows) - 1u;
+                                const uint32_t bits = mword >> (lo >> seg_shift);
+                                for (int i = 0; i < (32 >> seg_shift); ++i)
+                                    if ((bits >> i) & 1u) sb |= ones << (i * seg_rows);
+                            }
+                            v &= sb;
+                        }
+                        return v;
+                    };
+                    // pass 1: this half's max of the raw scores, then the row's from the two halves
+                    float mraw = -INFINITY;
+#pragma unroll 1
+                    for (int c = 2 * kh; c < 2 * kh + 2; ++c) {
+                        float sv[32];
+                        tmem_ld32(s_col + 32u * c, sv);
+                        if (!full) {
+                            const uint32_t vm = vis32(c);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) sv[k] = (vm & (1u << k)) ? sv[k] : -INFINITY;
+                        }
+                        mraw = fmaxf(mraw, tree_max32(sv));
+                    }
+                    float *xt = xmax + (ns & 1) * kTile;
+                    xt[kh * 2 * kTile + row] = mraw;
+                    if (!pair_sync()) {
+                        ok = false;
+                        break;
+                    }
+                    mraw = fmaxf(mraw, xt[(1 - kh) * 2 * kTile + row]);
+                    ++ns;
+                    const float mt = mraw * a.scale_log2;
+                    const bool bump = mt > m + kSlack;
+                    const float mn = bump ? mt : m;
+                    const float corr = bump ? fast_exp2(m - mn) : 1.f;
+                    // the stream's last P V completed before this S did: rescale this half's O columns
+                    if (any && __any_sync(0xffffffffu, corr != 1.f)) {
+                        const uint32_t o_col = tmem + lane_base + col_o(xb);
+#pragma unroll 1
+                        for (int c = 2 * kh; c < 2 * kh + 2; ++c) {
+                            float ov[32];
+                            tmem_ld32(o_col + 32u * c, ov);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) ov[k] *= corr;
+                            tmem_st32(o_col + 32u * c, ov);
+                        }
+                    }
+                    any = true;
+                    // pass 2: weights, their sum, and P over the first 32 of this half's S columns
+                    float psum = 0.f;
+                    {
+                        const float nb = -mn;
+                        uint32_t vm = 0;
+#pragma unroll 1
+                        for (int c = 4 * kh; c < 4 * kh + 4; ++c) {
+                            float sv[16];
+                            tmem_ld16(s_col + 16u * c, sv);
+                            if (full) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) sv[k] = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
+                            } else {
+                                if ((c & 1) == 0) vm = vis32(c >> 1);
+                                const uint32_t vh = (c & 1) ? (vm >> 16) : vm;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const float e = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
+                                    sv[k] = (vh & (1u << k)) ? e : 0.f;
+                                }
+                            }
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const __nv_bfloat162 pb = __floats2bfloat162_rn(sv[k], sv[k + 1]);
+                                pk[k >> 1] = *reinterpret_cast<const uint32_t *>(&pb);
+                                psum += sv[k] + sv[k + 1];
+                            }
+                            tmem_st8(s_col + 64u * kh + 8u * (c & 3), pk);
+                        }
+                        tmem_st_wait();
+                    }
+                    l = fmaf(l, corr, psum);
+                    m = mn;
+                    // V rows that must not reach P V: not loaded, at or past the cache end, or of the tree and
+                    // not finite.  The warps of the stream share the tile's 128 rows.
+                    if (!full && (!dual || xb == 0)) {
+                        if (!mbar_wait_warp(bar_vfull(s), (uint32_t)((jj / kStages) & 1), abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        for (int c = kh * aq + qw; c < 4; c += 2 * aq) {
+                            const int vr = 32 * c + lane;
+                            uint4 *v0 = reinterpret_cast<uint4 *>(smem + kOffV + s * kTileBytes + vr * 128);
+                            uint4 *v1 = reinterpret_cast<uint4 *>(smem + kOffV + s * kTileBytes + kHalfBytes + vr * 128);
+                            const bool there = ((mword >> (vr >> seg_shift)) & 1u) && k0 + vr < x.L;
+                            bool bad = false;
+                            if (there && k0 + vr >= first) {
+#pragma unroll 1
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint4 w = e < 8 ? v0[e] : v1[e - 8];
+                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int h = 0; h < 4; ++h)   // an exponent of all ones in either half
+                                        bad |= (ws[h] & 0x7f80u) == 0x7f80u || (ws[h] & 0x7f800000u) == 0x7f800000u;
+                                }
+                            }
+                            if (!there || bad) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    v0[e] = make_uint4(0, 0, 0, 0);
+                                    v1[e] = make_uint4(0, 0, 0, 0);
+                                }
+                            }
+                            const uint32_t word = __ballot_sync(0xffffffffu, bad);
+                            if (lane == 0 && near) poison[(jj & 7) * 4 + c] = word;
+                        }
+                        fence_proxy_async();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_pfull(xb));
+                }
+                if (!ok) break;
+                // ---- the unit's end: O of both streams is settled ----
+                if (!mbar_wait_warp(bar_ofull, (uint32_t)(no & 1), abort_flag)) break;
+                tc_fence_after();
+                if (kh == 0) xm[xb * kTile + row] = any ? m : -INFINITY;
+                xsum[(2 * xb + kh) * kTile + row] = l;
+                if (dual) {
+                    if (!pair_sync()) break;
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_quad(qw));
+                    if (!mbar_wait_warp(bar_quad(qw), (uint32_t)(no & 1), abort_flag)) break;
+                }
+                ++no;
+                float M, fa, fb = 0.f, lsum;
+                bool use_a = true, use_b = false;
+                if (dual) {
+                    M = m;
+                    fa = 1.f;
+                    lsum = xsum[2 * xb * kTile + row] + xsum[(2 * xb + 1) * kTile + row];
+                } else {
+                    const float ma = xm[row], mb = xm[kTile + row];
+                    M = fmaxf(ma, mb);
+                    fa = ma == -INFINITY ? 0.f : fast_exp2(ma - M);
+                    fb = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
+                    lsum = fa * (xsum[row] + xsum[kTile + row]) + fb * (xsum[2 * kTile + row] + xsum[3 * kTile + row]);
+                    use_a = x.nt > 1 || (jb & 1) == 0;   // a stream without a tile leaves its O unwritten
+                    use_b = x.nt > 1 || (jb & 1) == 1;
+                }
+                // a V row of the tree that was not finite makes the rows that see it NaN
+                for (int kt = max(0, (first >> 7) - x.f); kt < x.nt; ++kt) {
+                    const int k0 = (x.f + kt) * kTile;
+                    if (k0 + kTile <= first) continue;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t w = poison[((jb + kt) & 7) * 4 + c];
+                        if (w && (w & tree_vis32(mrow, a.mask_words, first, x.L, k0 + 32 * c))) lsum = NAN;
+                    }
+                }
+                const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+                const int64_t slot = (int64_t)hp * (a.P + a.num_reqs) + x.slot;
+                float *po = a.ws_o + (slot * a.NR + srow) * kD;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                                     (((int64_t)x.r * a.T + tok) * a.H_q + (int64_t)g * G + hh) * kD;
+                // one query tile: the quarter's four warps take 32 columns each; two: a half each of its own
+                const int c0 = dual ? 2 * kh : 2 * xb + kh, c1 = dual ? c0 + 2 : c0 + 1;
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    float ov[32];
+                    tmem_ld32(tmem + lane_base + col_o(dual ? xb : 0) + 32u * c, ov);
+                    if (!dual) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] = use_a ? ov[k] * fa : 0.f;
+                        if (use_b) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float ob[16];
+                                tmem_ld16(tmem + lane_base + col_o(1) + 32u * c + 16u * h, ob);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) ov[16 * h + k] = fmaf(fb, ob[k], ov[16 * h + k]);
+                            }
+                        }
+                    }
+                    if (!valid) continue;
+                    if (x.whole) {
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 h2 =
+                                    __floats2bfloat162_rn(ov[8 * q4 + 2 * e] * inv, ov[8 * q4 + 2 * e + 1] * inv);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                            }
+                            *reinterpret_cast<uint4 *>(out + 32 * c + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(po + 32 * c + k) =
+                                make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+                    }
+                }
+                if (!x.whole && valid && kh == 0 && (dual || xb == 0))
+                    *reinterpret_cast<float2 *>(a.ws_ml + (slot * a.NR + srow) * 2) = make_float2(M, lsum);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_oempty);
+            }
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0 && a.err) atomicAdd(a.err, kTimeoutErr);
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+static bool encode_3d(CUtensorMap *m, const void *base, uint64_t d1, uint64_t d2, uint32_t b1, uint32_t b2) {
+    const cuuint64_t dims[3] = {kD, d1, d2};
+    const cuuint64_t strides[2] = {kD * 2, d1 * kD * 2};
+    const cuuint32_t box[3] = {64, b1, b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace ttc
+
+bool prepare_tree_tc(const TreeArgs &a, TreeTc *t) {
+    using namespace ttc;
+    if (a.dtype != BKV_BF16 || a.D != kD || a.G < 1 || a.G > 128) return false;
+    if (a.bs < 8 || !((kTile % a.bs == 0) || (a.bs % kTile == 0))) return false;
+    if (a.num_reqs > kMaxReqs || (int64_t)a.num_reqs * a.T >= ((int64_t)1 << 31)) return false;
+    if (a.total_blocks <= 0 || (int64_t)a.total_blocks * a.bs >= ((int64_t)1 << 31)) return false;
+    // the tiles' prefix stays within int32
+    if ((int64_t)a.num_reqs * ((a.max_ctx + (int64_t)kTile - 1) / kTile) >= ((int64_t)1 << 31)) return false;
+    if ((int64_t)a.P * a.H_kv * a.groups >= ((int64_t)1 << 31)) return false;
+    if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q, 16) || !aligned(a.out, 16)) return false;
+    if (!encode_fn()) return false;
+    t->seg_rows = a.bs < kTile ? a.bs : kTile;
+    t->tok_per_tile = kTile / a.G;
+    t->box_tok = a.T < t->tok_per_tile ? a.T : t->tok_per_tile;
+    const uint64_t rows = (uint64_t)a.total_blocks * (uint64_t)a.bs;
+    return encode_3d(&t->mk, a.k, a.H_kv, rows, 1, t->seg_rows) &&
+           encode_3d(&t->mv, a.v, a.H_kv, rows, 1, t->seg_rows) &&
+           encode_3d(&t->mq, a.q, a.H_q, (uint64_t)a.num_reqs * a.T, a.G, t->box_tok);
+}
+
+int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t st) {
+    using namespace ttc;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) {
+            set_cuda_error(e);
+            (void)launch_status();   // clears the sticky status
+            return BKV_ERR_CUDA;
+        }
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const cudaError_t e = launch_pdl(tree_tc_kernel, dim3((unsigned)(a.P * a.H_kv * a.groups)), dim3(kThreads), kSmemBytes,
+                                     st, t.mk, t.mv, t.mq, a, t.seg_rows, t.tok_per_tile, t.box_tok);
+    if (e != cudaSuccess) set_cuda_error(e);
+    return launch_status();
+}
+
+}  // namespace bkv
