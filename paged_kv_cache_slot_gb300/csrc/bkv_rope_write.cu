@@ -160,8 +160,226 @@ __global__ void __launch_bounds__(128) rope_write_any_kernel(const Args a, bool 
     }
 }
 
+// ---------------------------------------------------------------------------
+// The common shapes: head_dim 32, 64, 128 or 256, a rotated part of whole
+// 16-element pieces, 16-byte alignment everywhere.  LPH = head_dim / 16 lanes a
+// head; a lane holds two pieces of 8 elements that rotate with one another:
+// [8 l, ..) and [rot / 2 + 8 l, ..), or, interleaved and past the rotated part,
+// 16 consecutive ones, so a pair never leaves its lane and both layouts use
+// table entries 8 l .. 8 l + 7.  A CTA takes a token at a time, 128 / LPH heads
+// a round, U rounds' loads in flight before the token's own answers (table
+// entry, rotation row) are needed.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Piece {   // 8 elements as they are in memory
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = *(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = __uint_as_float(w[i].x);
+                f[4 * i + 1] = __uint_as_float(w[i].y);
+                f[4 * i + 2] = __uint_as_float(w[i].z);
+                f[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void put8(__nv_bfloat16 *p, const float (&f)[8], float) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void put8(float *p, const float (&f)[8], float) {
+    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void put8(uint8_t *p, const float (&f)[8], float scale) {
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            h[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[4 * i + 2 * j], scale),
+                                                        __fdiv_rn(f[4 * i + 2 * j + 1], scale)),
+                                            __NV_SATFINITE, __NV_E4M3);
+        u[i] = h[0] | (h[1] << 16);
+    }
+    *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
+}
+
+template <typename T, typename C, int LPH, int U>
+__global__ void __launch_bounds__(128) rope_write_kernel(const Args a, bool inter) {
+    constexpr int D = 16 * LPH, NG = 128 / LPH;
+    const int l = threadIdx.x % LPH, grp = threadIdx.x / LPH;
+    const int heads = a.hq + 2 * a.hkv, half = a.rot / 2;
+    const bool turns = 16 * l < a.rot;
+    const int ea = inter || !turns ? 16 * l : 8 * l;        // this lane's two pieces
+    const int eb = inter || !turns ? ea + 8 : half + 8 * l;
+    pdl_wait();
+    pdl_trigger();
+    for (int64_t i = blockIdx.x; i < a.max_n; i += gridDim.x) {
+        const bool lead = blockIdx.y == 0 && threadIdx.x == 0;
+        if (i >= a.n) {
+            if (lead) a.slots[i] = -1;
+            continue;
+        }
+        bool known = false;
+        Token t{};
+        float cs[8], sn[8];
+        for (int h0 = blockIdx.y * NG * U; h0 < heads; h0 += gridDim.y * NG * U) {
+            Piece<T> pa[U], pb[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * NG + grp;
+                if (h < heads) {
+                    const T *src = h < a.hq ? static_cast<const T *>(a.q) + i * a.q_stride + (int64_t)h * D
+                                   : h < a.hq + a.hkv
+                                       ? static_cast<const T *>(a.k) + i * a.k_stride + (int64_t)(h - a.hq) * D
+                                       : static_cast<const T *>(a.v) + i * a.v_stride + (int64_t)(h - a.hq - a.hkv) * D;
+                    pa[u].load(src + ea);
+                    pb[u].load(src + eb);
+                }
+            }
+            if (!known) {
+                known = true;
+                t = token_at(a, i, lead);
+                if (t.real && turns) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 c4 = __ldg(reinterpret_cast<const float4 *>(t.cs + 8 * l + e));
+                        const float4 s4 = __ldg(reinterpret_cast<const float4 *>(t.cs + half + 8 * l + e));
+                        cs[e] = c4.x, cs[e + 1] = c4.y, cs[e + 2] = c4.z, cs[e + 3] = c4.w;
+                        sn[e] = s4.x, sn[e + 1] = s4.y, sn[e + 2] = s4.z, sn[e + 3] = s4.w;
+                    }
+                }
+            }
+            if (!t.real) break;   // the same for the whole CTA
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * NG + grp;
+                float x[8], y[8];
+                float ss = 0.f;
+                if (h < heads) {
+                    pa[u].get(x);
+                    pb[u].get(y);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+                }
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (h >= heads) continue;
+                const int kind = h < a.hq ? 0 : (h < a.hq + a.hkv ? 1 : 2);
+                if (kind > 0 && t.slot < 0) continue;
+                if (kind == 2) {
+                    C *dst = static_cast<C *>(a.vc) + (t.slot * a.hkv + (h - a.hq - a.hkv)) * D;
+                    if constexpr (sizeof(C) == 1) {
+                        put8(dst + ea, x, a.v_scale);
+                        put8(dst + eb, y, a.v_scale);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < (int)sizeof(T) / 2; ++w) {
+                            reinterpret_cast<uint4 *>(dst + ea)[w] = pa[u].w[w];
+                            reinterpret_cast<uint4 *>(dst + eb)[w] = pb[u].w[w];
+                        }
+                    }
+                    continue;
+                }
+                const T *w = static_cast<const T *>(kind == 0 ? a.qw : a.kw);
+                if (w) {
+                    const float inv = rsqrtf(ss / (float)D + a.eps);
+                    Piece<T> wa, wb;
+                    wa.load(w + ea);
+                    wb.load(w + eb);
+                    float fa[8], fb[8];
+                    wa.get(fa);
+                    wb.get(fb);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] *= inv * fa[e];
+                        y[e] *= inv * fb[e];
+                    }
+                }
+                if (turns) {
+                    if (inter) {   // pairs (2 i, 2 i + 1): four in each piece
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float xa = x[2 * e], xb = x[2 * e + 1], ya = y[2 * e], yb = y[2 * e + 1];
+                            x[2 * e] = xa * cs[e] - xb * sn[e];
+                            x[2 * e + 1] = xb * cs[e] + xa * sn[e];
+                            y[2 * e] = ya * cs[4 + e] - yb * sn[4 + e];
+                            y[2 * e + 1] = yb * cs[4 + e] + ya * sn[4 + e];
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float xa = x[e], xb = y[e];
+                            x[e] = xa * cs[e] - xb * sn[e];
+                            y[e] = xb * cs[e] + xa * sn[e];
+                        }
+                    }
+                }
+                if (kind == 0) {
+                    T *dst = static_cast<T *>(a.q_out) + (i * a.hq + h) * D;
+                    put8(dst + ea, x, 1.f);
+                    put8(dst + eb, y, 1.f);
+                } else {
+                    C *dst = static_cast<C *>(a.kc) + (t.slot * a.hkv + (h - a.hq)) * D;
+                    put8(dst + ea, x, a.k_scale);
+                    put8(dst + eb, y, a.k_scale);
+                }
+            }
+        }
+    }
+}
+
+template <typename T, typename C, int LPH>
+static cudaError_t launch_pieces(const Args &a, bool inter, cudaStream_t st) {
+    // three rounds of 16-bit rows in flight (48 heads of 128 elements), two of 32-bit ones: registers
+    constexpr int U = sizeof(T) == 2 ? 3 : 2;
+    const int rounds = ceil_div(a.hq + 2 * a.hkv, 128 / LPH);
+    // few tokens: a token's heads over several CTAs
+    const int64_t room = 2 * current_sm_count() / (a.max_n < 1 ? 1 : a.max_n);
+    const int64_t tokens = a.max_n < (int64_t)current_sm_count() * 16 ? a.max_n : (int64_t)current_sm_count() * 16;
+    if (room >= 2 && rounds > 1) {
+        const unsigned y = (unsigned)(room < rounds ? room : rounds);
+        return launch_pdl(rope_write_kernel<T, C, LPH, 1>, dim3((unsigned)tokens, y), dim3(128), 0, st, a, inter);
+    }
+    return launch_pdl(rope_write_kernel<T, C, LPH, U>, dim3((unsigned)tokens), dim3(128), 0, st, a, inter);
+}
+
+static bool in_pieces(const Args &a, int e, int ec) {
+    return (a.d == 32 || a.d == 64 || a.d == 128 || a.d == 256) && a.rot % 16 == 0 && aligned(a.q, 16) &&
+           aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.q_out, 16) && aligned(a.kc, ec == 1 ? 8 : 16) &&
+           aligned(a.vc, ec == 1 ? 8 : 16) && aligned(a.qw, 16) && aligned(a.kw, 16) && aligned(a.cos_sin, 16) &&
+           a.q_stride * e % 16 == 0 && a.k_stride * e % 16 == 0 && a.v_stride * e % 16 == 0;
+}
+
 template <typename T, typename C>
-static cudaError_t launch_any(const Args &a, bool inter, cudaStream_t st) {
+static cudaError_t launch_rope(const Args &a, bool inter, cudaStream_t st) {
+    if (in_pieces(a, sizeof(T), sizeof(C))) {
+        if (a.d == 32) return launch_pieces<T, C, 2>(a, inter, st);
+        if (a.d == 64) return launch_pieces<T, C, 4>(a, inter, st);
+        if (a.d == 128) return launch_pieces<T, C, 8>(a, inter, st);
+        return launch_pieces<T, C, 16>(a, inter, st);
+    }
     const int64_t items = a.max_n * (a.hq + 2 * a.hkv);
     return launch_pdl(rope_write_any_kernel<T, C>, dim3(grid_for(items, 4, 64)), dim3(128), 0, st, a, inter);
 }
@@ -199,9 +417,9 @@ static int run(const void *q, const void *k, const void *v, int64_t q_stride, in
     const bool inter = interleaved != 0;
     cudaError_t e;
     if (dtype == BKV_BF16)
-        e = fp8 ? launch_any<__nv_bfloat16, uint8_t>(a, inter, st) : launch_any<__nv_bfloat16, __nv_bfloat16>(a, inter, st);
+        e = fp8 ? launch_rope<__nv_bfloat16, uint8_t>(a, inter, st) : launch_rope<__nv_bfloat16, __nv_bfloat16>(a, inter, st);
     else
-        e = fp8 ? launch_any<float, uint8_t>(a, inter, st) : launch_any<float, float>(a, inter, st);
+        e = fp8 ? launch_rope<float, uint8_t>(a, inter, st) : launch_rope<float, float>(a, inter, st);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }

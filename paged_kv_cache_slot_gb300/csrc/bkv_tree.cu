@@ -229,88 +229,87 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
 
 // ---------------------------------------------------------------------------
 // Merge of a stream's partials: out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M)
-// l_c, 0 where nothing was seen.  CTA = (stream, 32 of its rows), a warp a row
-// at a time.  The tensor-core kernel writes streams that one CTA finished
-// itself; the merge leaves those alone.
+// l_c, 0 where nothing was seen.  A warp has one row: lane k keeps the weight of
+// slot k, and the first eight slots' partials are loaded beside the (m, l)
+// pairs, so a stream of few slots costs one round of loads.  The CUDA-core
+// kernel's streams are all split by the host's plan; of the tensor-core
+// kernel's, its table names the split one of each column, and those that one
+// CTA finished are written already.
 // ---------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeArgs a) {
-    __shared__ int64_t red[2][4];
+constexpr int kMergeWarps = 8;
+
+template <typename T, bool kTc>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
+    constexpr int kUnroll = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per_req = a.H_kv * a.groups;
-    const int64_t st = blockIdx.x;
-    const int r = (int)(st / per_req), hp = (int)(st - (int64_t)r * per_req);
-    const int g = hp / a.groups, p = hp - g * a.groups;
-    const int32_t L = tree_len(a, __ldg(a.ctx + r));
-    int nch = 0;
-    int64_t slot0 = 0;
-    if (a.tc) {
-        int64_t all = 0, before = 0;
-        for (int rr = threadIdx.x; rr < a.num_reqs; rr += kThreads) {
-            const int64_t t = (tree_len(a, __ldg(a.ctx + rr)) + kTreeTile - 1) / kTreeTile;
-            all += t;
-            if (rr < r) before += t;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            all += __shfl_xor_sync(0xffffffffu, all, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
-        if (lane == 0) {
-            red[0][warp] = all;
-            red[1][warp] = before;
-        }
-        __syncthreads();
-        all = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-        before = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-        const int64_t Ts = (L + kTreeTile - 1) / kTreeTile;
-        if (Ts > 0) {
-            // column q of peff covers tiles [q all / peff, (q + 1) all / peff); its part of this stream is
-            // slot hp (P + R) + q + r
-            const int64_t peff = all < a.P ? all : a.P;
-            const int64_t q0 = ((before + 1) * peff - 1) / all;
-            const int64_t q1 = ((before + Ts) * peff - 1) / all;
-            nch = (int)(q1 - q0 + 1);
-            slot0 = (int64_t)hp * (a.P + a.num_reqs) + q0 + r;
-        }
-    } else if (L > 0) {
-        nch = (L + a.chunk - 1) / a.chunk;
-        slot0 = st * a.n_chunks;
-    }
-    pdl_wait();   // by every CTA: this grid's end stands for the partials' and the rows written there
+    pdl_wait();
     pdl_trigger();
-    if (a.tc && nch == 1) return;   // one CTA had the whole stream and wrote its rows
-    const int rows = min(a.NR, (a.T - p * a.TS) * a.G);
-    const int row_end = min(rows, ((int)blockIdx.y + 1) * 32);
-    for (int row = blockIdx.y * 32 + warp; row < row_end; row += 4) {
-        const int t = p * a.TS + row / a.G, h = g * a.G + row % a.G;
-        T *out = static_cast<T *>(a.out) + (((int64_t)r * a.T + t) * a.H_q + h) * a.D;
-        float M = -INFINITY;
-        for (int c = lane; c < nch; c += 32) M = fmaxf(M, a.ws_ml[((slot0 + c) * a.NR + row) * 2]);
+    const int HP = a.H_kv * a.groups;
+    int r, hp, nch;
+    int64_t slot0;
+    if (kTc) {
+        hp = (int)blockIdx.x % HP;
+        const int4 e = a.ws_split[blockIdx.x / HP];   // request, its slots, the first
+        r = e.x;
+        nch = e.y;
+        slot0 = (int64_t)hp * (a.P + a.num_reqs) + e.z;
+        if (nch == 0) return;
+    } else {
+        r = (int)(blockIdx.x / HP);
+        hp = (int)blockIdx.x - r * HP;
+        const int32_t L = tree_len(a, __ldg(a.ctx + r));
+        nch = L > 0 ? (L + a.chunk - 1) / a.chunk : 0;
+        slot0 = (int64_t)blockIdx.x * a.n_chunks;
+    }
+    const int g = hp / a.groups, tok0 = (hp - g * a.groups) * a.TS;
+    const int row = blockIdx.y * kMergeWarps + warp;
+    if (row >= min(a.NR, (a.T - tok0) * a.G)) return;
+    const int t = tok0 + row / a.G, h = g * a.G + row % a.G;
+    T *out = static_cast<T *>(a.out) + (((int64_t)r * a.T + t) * a.H_q + h) * a.D;
+    auto ml_of = [&](int c) {
+        return c < nch ? *reinterpret_cast<const float2 *>(a.ws_ml + ((slot0 + c) * a.NR + row) * 2)
+                       : make_float2(-INFINITY, 0.f);
+    };
+    const float2 ml0 = ml_of(lane);
+    for (int d0 = 0; d0 < a.D; d0 += 64) {   // two elements a lane
+        const int d = d0 + 2 * lane;
+        const bool act = d < a.D;
+        auto part = [&](int c) {
+            return act && c < nch ? *reinterpret_cast<const float2 *>(a.ws_o + ((slot0 + c) * a.NR + row) * a.D + d)
+                                  : make_float2(0.f, 0.f);
+        };
+        float2 v[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) v[k] = part(k);
+        float M = ml0.x;
+        for (int c = lane + 32; c < nch; c += 32) M = fmaxf(M, ml_of(c).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float sum = 0.f;
-        for (int c = lane; c < nch; c += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + ((slot0 + c) * a.NR + row) * 2);
+        float2 acc = make_float2(0.f, 0.f);
+        for (int base = 0; base < nch; base += 32) {
+            const float2 ml = base == 0 ? ml0 : ml_of(base + lane);
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
             // a part that saw nothing but NaN scores has no maximum, and a NaN sum
-            const float w = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : 1.f) : exp2f(ml.x - M);
-            sum = fmaf(w, ml.y, sum);
+            sum = fmaf(ml.x == -INFINITY && ml.y != ml.y ? 1.f : w, ml.y, sum);
+            for (int c = base; c < min(nch, base + 32); c += kUnroll) {
+                if (c > 0)
+#pragma unroll
+                    for (int k = 0; k < kUnroll; ++k) v[k] = part(c + k);
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, (c + k) & 31);
+                    acc.x = fmaf(wk, v[k].x, acc.x);
+                    acc.y = fmaf(wk, v[k].y, acc.y);
+                }
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        for (int d = 2 * lane; d < a.D; d += 64) {
-            float x = 0.f, y = 0.f;
-            for (int c = 0; c < nch; ++c) {
-                const int64_t pr = (slot0 + c) * a.NR + row;
-                const float mc = a.ws_ml[pr * 2];
-                const float w = mc == -INFINITY ? 0.f : exp2f(mc - M);
-                const float2 v = *reinterpret_cast<const float2 *>(a.ws_o + pr * a.D + d);
-                x = fmaf(w, v.x, x);
-                y = fmaf(w, v.y, y);
-            }
-            store_out(out + d, x * inv);
-            store_out(out + d + 1, y * inv);
+        if (act) {
+            store_out(out + d, acc.x * inv);
+            store_out(out + d + 1, acc.y * inv);
         }
     }
 }
@@ -320,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeArgs a) 
 // ---------------------------------------------------------------------------
 struct Plan {
     int32_t chunk, n_chunks;
-    int64_t slots_cc, slots_tc, rows_tc;   // tensor-core slots are bounded over its two forms
-    int64_t part_bytes;
+    int64_t slots_cc, slots_tc;   // the kernels' partial slots (tensor-core: 0 where it cannot run)
+    int64_t split_bytes;          // the tensor-core kernel's table of split streams
     size_t ws_bytes;
 };
 
@@ -373,7 +372,9 @@ static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, in
         const int64_t rt = p->slots_tc * TS * G;
         if (rt > rows) rows = rt;
     }
-    p->ws_bytes = (size_t)(ceil_div<int64_t>(rows * D * 4, 256) * 256 + ceil_div<int64_t>(rows * 8, 256) * 256);
+    p->split_bytes = p->slots_tc > 0 ? ceil_div<int64_t>(sms * 16, 256) * 256 : 0;   // at most a column an SM
+    p->ws_bytes = (size_t)(p->split_bytes + ceil_div<int64_t>(rows * D * 4, 256) * 256 +
+                           ceil_div<int64_t>(rows * 8, 256) * 256);
     return true;
 }
 
@@ -406,11 +407,12 @@ static cudaError_t launch_cc_dims(const TreeArgs &a, cudaStream_t st) {
     return few ? launch_cc<T, 256, 16>(a, st) : launch_cc<T, 256, 32>(a, st);
 }
 
+template <bool kTc>
 static int launch_merge(const TreeArgs &a, cudaStream_t st) {
-    const int64_t streams = (int64_t)a.num_reqs * a.H_kv * a.groups;
-    const dim3 grid((unsigned)streams, (unsigned)ceil_div(a.NR, 32));
-    const cudaError_t e = a.dtype == BKV_BF16 ? launch_pdl(tree_merge_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a)
-                                              : launch_pdl(tree_merge_kernel<float>, grid, dim3(kThreads), 0, st, a);
+    const int64_t x = (int64_t)(kTc ? a.P : a.num_reqs) * a.H_kv * a.groups;
+    const dim3 grid((unsigned)x, (unsigned)ceil_div(a.NR, kMergeWarps)), block(kMergeWarps * 32);
+    const cudaError_t e = a.dtype == BKV_BF16 ? launch_pdl(tree_merge_kernel<__nv_bfloat16, kTc>, grid, block, 0, st, a)
+                                              : launch_pdl(tree_merge_kernel<float, kTc>, grid, block, 0, st, a);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }
@@ -476,23 +478,22 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
     a.chunk = plan.chunk;
     a.n_chunks = plan.n_chunks;
     auto set_slots = [&](int64_t slots) {
-        a.ws_o = static_cast<float *>(workspace);
-        a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                            ceil_div<int64_t>(slots * a.NR * head_dim * 4, 256) * 256);
+        char *base = static_cast<char *>(workspace) + plan.split_bytes;
+        a.ws_split = static_cast<int4 *>(workspace);
+        a.ws_o = reinterpret_cast<float *>(base);
+        a.ws_ml = reinterpret_cast<float *>(base + ceil_div<int64_t>(slots * a.NR * head_dim * 4, 256) * 256);
     };
     cudaStream_t st = (cudaStream_t)stream;
     TreeTc t;
     if (plan.slots_tc > 0) {
         tc_split(a.T, a.G, a.H_kv, &a.TS, &a.groups, &a.P);
         a.NR = a.TS * a.G;
-        a.tc = 1;
         if (prepare_tree_tc(a, &t)) {
             set_slots(plan.slots_tc);
             const int rc = launch_tree_tc(a, t, st);
-            return rc != BKV_OK ? rc : launch_merge(a, st);
+            return rc != BKV_OK ? rc : launch_merge<true>(a, st);
         }
     }
-    a.tc = 0;
     // one query-row group for all tokens: the CUDA-core kernel's slots
     a.TS = q_len;
     a.NR = q_len * a.G;
@@ -501,5 +502,5 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
     const cudaError_t e = dtype == BKV_BF16 ? launch_cc_dims<__nv_bfloat16>(a, st) : launch_cc_dims<float>(a, st);
     if (e != cudaSuccess) set_cuda_error(e);
     const int rc = launch_status();
-    return rc != BKV_OK ? rc : launch_merge(a, st);
+    return rc != BKV_OK ? rc : launch_merge<false>(a, st);
 }

@@ -99,13 +99,14 @@ struct Unit {
 // Walks this CTA's units: column q's share of the tiles laid end to end.
 struct Units {
     const int32_t *pre, *len;
-    int n, r, q;
+    int n, r, q, P;
     int64_t t, t1;
     __device__ Units(const TreeArgs &a, const int32_t *pre_, const int32_t *len_, int q_) {
         pre = pre_;
         len = len_;
         n = a.num_reqs;
         q = q_;
+        P = a.P;
         const int64_t TP = pre[n];
         const int64_t peff = TP < a.P ? TP : a.P;
         t = q < peff ? TP * q / peff : TP;
@@ -117,6 +118,17 @@ struct Units {
             else lo = mid + 1;
         }
         r = lo;
+    }
+    // The stream that this column begins and does not end (before next() is called): its request, how
+    // many columns share it, and its first slot past the head's; all 0 without one.
+    __device__ int4 split() const {
+        if (t >= t1) return make_int4(0, 0, 0, 0);
+        int r1 = r;
+        while (pre[r1 + 1] < t1) ++r1;   // the request of tile t1 - 1
+        const int64_t TP = pre[n], peff = TP < P ? TP : P;
+        if (pre[r1 + 1] == t1 || pre[r1] < t) return make_int4(0, 0, 0, 0);
+        const int q1 = (int)(((int64_t)pre[r1 + 1] * peff - 1) / TP);   // the column of its last tile
+        return make_int4(r1, q1 - q + 1, q + r1, 0);
     }
     __device__ bool next(Unit &x) {
         if (t >= t1) return false;
@@ -249,6 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) pre[n] = inc;
     }
     __syncthreads();
+    // the merge's table, and the rows of requests without a position
+    if (hp == 0 && threadIdx.x == 32) a.ws_split[q] = Units(a, pre, len, q).split();
+    for (int r = q; r < a.num_reqs; r += a.P) {
+        if (len[r] > 0) continue;
+        for (int e = threadIdx.x; e < ntok * G * (kD / 8); e += kThreads) {
+            const int row = e / (kD / 8), t = tok0 + row / G, h = g * G + row % G;
+            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                      (((int64_t)r * a.T + t) * a.H_q + h) * kD)[e % (kD / 8)] = make_uint4(0, 0, 0, 0);
+        }
+    }
     const uint32_t tmem = *tmem_slot;
     const int nseg = kTile / seg_rows;
     const int seg_shift = 31 - __clz(seg_rows);

@@ -23,7 +23,8 @@
 // Memory-bound: one row of p (chain: of q too) of V fp32 a request.  A
 // cluster of CTAs shares a request's row; every CTA walks the drafts itself
 // (a few gathers), sums its part by warps, the CTA totals go round the
-// cluster, and the warp whose part holds the border scans it again (from L2).
+// cluster, and the CTA whose part holds the border scans the part of the warp
+// that does once more (from L2), a few elements a thread.
 #include <cooperative_groups.h>
 
 #include "bkv_internal.cuh"
@@ -37,6 +38,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxNodes = 1024;   // drafts (chain) or nodes (tree) a request
 constexpr int kMaxCluster = 8;
+constexpr int kUnroll = 8;        // elements of each row in flight a lane
 
 struct Args {
     const float *p;
@@ -58,12 +60,19 @@ struct Args {
 // A probability in units of 2^-56 (below 0 and NaN: 0; above 1: 1).
 __device__ __forceinline__ long long fixed(float x) { return __float2ll_rn(__saturatef(x) * 72057594037927936.f); }
 
+// What token v weighs: its probability p, less the draft's q in a chain.
+__device__ __forceinline__ unsigned long long weight(float p, float q) {
+    const long long w = fixed(p) - fixed(q);
+    return w > 0 ? w : 0;
+}
+
 struct Shared {
     float p[kMaxNodes], u[kMaxNodes];
     int32_t tok[kMaxNodes], par[kMaxNodes];
     int32_t ex[kMaxNodes];               // tree: rejected children's tokens at the stop node
     int32_t n, cur, nex;                 // accepted drafts, stop row, rejected tokens
     unsigned long long seg[kWarps];      // sums of the warps' parts
+    unsigned long long run[kWarps];      // and of the warps' shares of the part with the border
     unsigned long long tot[2][kMaxCluster];
 };
 
@@ -200,13 +209,19 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
     for (int pass = 0; pass < 2; ++pass) {
         const bool plain = pass == 1;
         const float *qq = plain ? nullptr : qr;
-        auto weight = [&](int64_t v) -> long long {
-            const long long w = fixed(pr[v]);
-            return qq ? max(w - fixed(qq[v]), 0ll) : w;
-        };
         unsigned long long sum = 0;
-#pragma unroll 4
-        for (int64_t v = v0 + lane; v < v1; v += 32) sum += weight(v);
+        for (int64_t base = v0 + lane; base < v1; base += 32 * kUnroll) {
+            // every load of the round before the first conversion
+            float x[kUnroll], y[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int64_t v = base + 32 * k;
+                x[k] = v < v1 ? pr[v] : 0.f;
+                y[k] = v < v1 && qq ? qq[v] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) sum += weight(x[k], y[k]);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int nex = plain ? 0 : s.nex;
@@ -232,29 +247,41 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
             continue;
         }
         const unsigned long long border = __umul64hi(U, whole);   // floor(u * whole) < whole
-        for (int w = 0; w < warp; ++w) before += s.seg[w];
-        if (border >= before && border - before < s.seg[warp]) {
-            unsigned long long run = before;
-            for (int64_t base = v0; base < v1; base += 32) {
-                const int64_t v = base + lane;
-                unsigned long long w = v < v1 ? (unsigned long long)weight(v) : 0;
-                if (!kChain)
-                    for (int e = 0; e < nex; ++e)
-                        if (s.ex[e] == v) w = 0;
-                unsigned long long inc = w;
+        // the CTA whose part holds the border: its threads scan the warp's part that does, together
+        if (border < before || border - before >= s.tot[pass][rank]) break;
+        int w = 0;
+        while (border - before >= s.seg[w]) before += s.seg[w++];
+        const int64_t s0 = ((int64_t)rank * kWarps + w) * part;
+        const int64_t s1 = min((int64_t)a.V, s0 + part);
+        const int each = (part + kThreads - 1) / kThreads;
+        const int64_t e0 = s0 + (int64_t)threadIdx.x * each;
+        const int64_t e1 = min(s1, e0 + each);
+        auto at = [&](int64_t v) -> unsigned long long {
+            if (!kChain)
+                for (int e = 0; e < nex; ++e)
+                    if (s.ex[e] == v) return 0;
+            return weight(pr[v], qq ? qq[v] : 0.f);
+        };
+        unsigned long long mine = 0;
+        for (int64_t v = e0; v < e1; ++v) mine += at(v);
+        unsigned long long inc = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, run + inc > border);
-                if (hit) {
-                    if (lane == 0) out[n] = base + __ffs(hit) - 1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s.run[warp] = inc;
+        __syncthreads();
+        unsigned long long run = before + inc - mine;
+        for (int i = 0; i < warp; ++i) run += s.run[i];
+        if (border >= run && border - run < mine)
+            for (int64_t v = e0; v < e1; ++v) {
+                run += at(v);
+                if (run > border) {
+                    out[n] = v;
                     break;
                 }
-                run += __shfl_sync(0xffffffffu, inc, 31);
             }
-        }
         break;
     }
 }
