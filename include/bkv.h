@@ -689,8 +689,9 @@ int bkv_verify_draft_chain(const float *target_probs, int64_t target_req_stride,
  *   i.  From the root on, at node a with rem = 1, in index order over its
  *   children c whose token x_c was not met before under a:
  *     accept c if accept_u[r][c] * rem < p_a(x_c), and go on from c;
- *     otherwise rem -= p_a(x_c)   (in 64 bits, not below 0)
- *   (a child whose token was met before is rejected).  With no child accepted
+ *     otherwise rem -= p_a(x_c)   (not below 0)
+ *   in the units of 2^-56 of bkv_verify_draft_chain's samples, the product
+ *   exact (a child whose token was met before is rejected).  With no child accepted
  *   the next token is sampled by sample_u[r], as in bkv_verify_draft_chain,
  *   from p_a with the rejected children's tokens left out.
  *     path[r] = 0, the accepted nodes, then -1; num_accepted[r] = their

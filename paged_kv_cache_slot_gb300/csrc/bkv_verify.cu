@@ -17,8 +17,7 @@
 // rounding errors of one another, so weights are summed as integers in units
 // of 2^-56: exact for probabilities from 2^-32 up (24 significant bits) and
 // within 2^-57 below, associative, so the answer depends on no order, and
-// sums up to 256 fit 64 bits.  (Conversions to 64-bit integers run at 16 a
-// clock and SM; fp64 additions at 2.)
+// sums up to 256 fit 64 bits.
 //
 // Memory-bound: one row of p (chain: of q too) of V fp32 a request.  A
 // cluster of CTAs shares a request's row; every CTA walks the drafts itself
@@ -34,11 +33,24 @@ namespace verify {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxNodes = 1024;   // drafts (chain) or nodes (tree) a request
+constexpr int kMaxWarps = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;        // elements of each row in flight a lane
+constexpr int kUnroll = 16;       // elements of each row in flight a lane
+
+// CTA size, the CTAs an SM is built to hold, and how many of them an SM a launch
+// may ask for before its clusters get narrower.  Chains stream two rows and are
+// bound by bandwidth: small CTAs, several waves (100003 tokens: 256 requests 44.6
+// us, 61.7 with 512 threads and one wave; 100 requests of 90001 22.3 and 20.4).
+// Trees walk before they stream: large CTAs, one wave (64 requests of 131072
+// 14.6 us, 22.2 with 256 threads).
+template <bool kChain>
+struct Shape {
+    static constexpr int kThreads = kChain ? 256 : 512;
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kBuilt = kChain ? 3 : 2;
+    static constexpr int kAsked = kChain ? 7 : 2;
+};
 
 struct Args {
     const float *p;
@@ -57,8 +69,38 @@ struct Args {
     int32_t *err;
 };
 
-// A probability in units of 2^-56 (below 0 and NaN: 0; above 1: 1).
-__device__ __forceinline__ long long fixed(float x) { return __float2ll_rn(__saturatef(x) * 72057594037927936.f); }
+// A probability x in [0, 1] in units of 2^-56, as three integers h 2^34 + l 2^12
+// + m: adding a constant whose last place is 2^-22 (then 2^-44, 2^-56) leaves
+// the rounded multiple in the sum's low bits, and what it leaves over is exact,
+// so three sums and their differences do what a conversion to a 64-bit integer
+// would, at the full rate of fp32 additions (64-bit conversions run at 2 a
+// clock and SM here: they bound this kernel at 140 us where the rows' bytes
+// take 30, 256 requests of 100003 tokens).
+struct Limbs {
+    int32_t h, l, m;
+};
+__device__ __forceinline__ Limbs limbs(float x) {
+    constexpr float c1 = 2.f, c2 = 0x1.8p-21f, c3 = 0x1.8p-33f;
+    const float a = __fadd_rn(x, c1);
+    const float x1 = __fsub_rn(x, __fsub_rn(a, c1));
+    const float b = __fadd_rn(x1, c2);
+    const float x2 = __fsub_rn(x1, __fsub_rn(b, c2));
+    const float c = __fadd_rn(x2, c3);
+    return {__float_as_int(a) - __float_as_int(c1), __float_as_int(b) - __float_as_int(c2),
+            __float_as_int(c) - __float_as_int(c3)};
+}
+__device__ __forceinline__ long long whole_of(const Limbs &v) {
+    return ((long long)v.h << 34) + ((long long)v.l << 12) + v.m;
+}
+// Below 0 and NaN: 0; above 1: 1.
+__device__ __forceinline__ long long fixed(float p) { return whole_of(limbs(__saturatef(p))); }
+
+// A random number u in [0, 1) in units of 2^-64, exactly: floor(u n) is then the
+// high word of a product, and u n < m for integers is floor(u n) < m.  From 1 on
+// (and NaN) the largest, below 0 none.
+__device__ __forceinline__ unsigned long long unit64(float u) {
+    return u < 1.f ? __float2ull_rz(fmaxf(u, 0.f) * 18446744073709551616.f) : ~0ull;
+}
 
 // What token v weighs: its probability p, less the draft's q in a chain.
 __device__ __forceinline__ unsigned long long weight(float p, float q) {
@@ -66,18 +108,69 @@ __device__ __forceinline__ unsigned long long weight(float p, float q) {
     return w > 0 ? w : 0;
 }
 
+// The weights of tokens [v0, v1), a warp's part, of this lane: four at a time
+// where both rows start on 16 bytes (and v0 and v1 are whole fours), one
+// otherwise; the elements of a round are loaded before the first is used, and
+// their limbs fit 32 bits.
+template <bool kResidual, int kVec>
+__device__ __forceinline__ unsigned long long part_sum(const float *pr, const float *qr, int64_t v0, int64_t v1,
+                                                       int lane) {
+    long long sum = 0;
+    for (int64_t v = v0 + lane * kVec; v < v1; v += 32 * kUnroll) {
+        float x[kUnroll], y[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; k += kVec) {
+            const int64_t at = v + 32 * k;
+            if constexpr (kVec == 4) {
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(x + k) = at < v1 ? __ldg(reinterpret_cast<const float4 *>(pr + at)) : z;
+                if (kResidual)
+                    *reinterpret_cast<float4 *>(y + k) = at < v1 ? __ldg(reinterpret_cast<const float4 *>(qr + at)) : z;
+            } else {
+                x[k] = at < v1 ? __ldg(pr + at) : 0.f;
+                if (kResidual) y[k] = at < v1 ? __ldg(qr + at) : 0.f;
+            }
+        }
+        Limbs t{0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const float xs = __saturatef(x[k]);
+            const Limbs p = limbs(xs);
+            if (kResidual) {
+                const float ys = __saturatef(y[k]);
+                const Limbs q = limbs(ys);
+                if (xs > ys) {   // rounding keeps the order
+                    t.h += p.h - q.h;
+                    t.l += p.l - q.l;
+                    t.m += p.m - q.m;
+                }
+            } else {
+                t.h += p.h;
+                t.l += p.l;
+                t.m += p.m;
+            }
+        }
+        sum += whole_of(t);
+    }
+    return (unsigned long long)sum;
+}
+
 struct Shared {
-    float p[kMaxNodes], u[kMaxNodes];
+    long long fx[kMaxNodes];             // tree: the nodes' probabilities in units of 2^-56
+    float u[kMaxNodes];
     int32_t tok[kMaxNodes], par[kMaxNodes];
-    int32_t ex[kMaxNodes];               // tree: rejected children's tokens at the stop node
-    int32_t n, cur, nex;                 // accepted drafts, stop row, rejected tokens
-    unsigned long long seg[kWarps];      // sums of the warps' parts
-    unsigned long long run[kWarps];      // and of the warps' shares of the part with the border
+    int32_t next[kMaxNodes];             // tree: the child taken, kMaxNodes: none
+    int32_t path[kMaxNodes];             // tree: the accepted path
+    int32_t ex[kMaxNodes];               // tree: the rejected children of the stop node
+    int32_t n, cur, nex;                 // accepted drafts, stop row, rejected children
+    unsigned long long seg[kMaxWarps];      // sums of the warps' parts
+    unsigned long long run[kMaxWarps];      // and of the warps' shares of the part with the border
     unsigned long long tot[2][kMaxCluster];
 };
 
 template <bool kChain>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
+__global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt) verify_kernel(const Args a) {
+    constexpr int kThreads = Shape<kChain>::kThreads, kWarps = Shape<kChain>::kWarps;
     __shared__ Shared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -122,112 +215,93 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
             const bool node = par >= 0 && par < i;
             if (i > 0 && rank == 0 && a.err && ((!node && par != -1) || (node && !in))) atomicAdd(a.err, 1);
             s.par[i] = node ? par : -1;
+            s.next[i] = kMaxNodes;
             s.tok[i] = in ? (int32_t)x : -1;
             s.u[i] = u;
-            s.p[i] = node && in ? P[par * a.p_row + x] : 0.f;
+            s.fx[i] = node && in ? fixed(P[par * a.p_row + x]) : 0;
         }
     }
     __syncthreads();
-    if (!kChain && warp == 0) {
-        // One pass over the nodes in index order: the children of the current node follow it, and a
-        // child taken becomes the current node.  Lane 0's verdict goes round the warp.
-        int cur = 0, n = 0, nex = 0;
-        double rem = 1.0;
-        int32_t *path = a.path + r * a.nodes;
-        if (rank == 0 && lane == 0) path[0] = 0;
-        for (int base = 0; base < len; base += 32) {
-            const int c = base + lane;
+    if (!kChain) {
+        // A child is put to the test only when all its older siblings failed theirs, so each node's test
+        // stands by itself: its rem is 1 less its older siblings' probabilities, in their order, a token
+        // counted once.  next[a] = the first child of a that passes.
+        // Eight lanes a node.
+        const int sub = lane & 7;
+        for (int c0 = 0; c0 < len; c0 += kThreads / 8) {
+            const int c = c0 + (int)threadIdx.x / 8;
+            const int par = c < len ? s.par[c] : -1, x = c < len ? s.tok[c] : -1;
+            bool dup = false;
+            if (par >= 0)
+                for (int j = 1 + sub; j < c; j += 8) dup |= (s.par[j] == par) & (s.tok[j] == x);
+            const unsigned any = __ballot_sync(0xffffffffu, dup);
+            if (sub == 0 && ((any >> lane) & 0xffu)) s.fx[c] = 0;   // it is never taken and weighs nothing
+        }
+        __syncthreads();
+        for (int c0 = 0; c0 < len; c0 += kThreads / 8) {
+            const int c = c0 + (int)threadIdx.x / 8;
             const int par = c < len ? s.par[c] : -1;
-            unsigned todo = __ballot_sync(0xffffffffu, c > 0 && par == cur);
-            while (todo) {
-                const int l = __ffs(todo) - 1;
-                const int cc = base + l;
-                const int x = s.tok[cc];
-                bool dup = false;   // a token counts once under a node
-                for (int e = lane; e < nex; e += 32) dup |= s.ex[e] == x;
-                dup = __any_sync(0xffffffffu, dup);
-                const float pf = fminf(fmaxf(s.p[cc], 0.f), 1.f);
-                const double p = dup ? 0.0 : (double)pf;
-                if ((double)s.u[cc] * fmax(rem, 0.0) < p) {
-                    cur = cc;
-                    ++n;
-                    nex = 0;
-                    rem = 1.0;
-                    if (rank == 0 && lane == 0) {
-                        path[n] = cc;
-                        a.out[r * a.nodes + n - 1] = x;
-                    }
-                    todo = __ballot_sync(0xffffffffu, c > cc && par == cur);
-                } else {
-                    rem -= p;
-                    if (x >= 0 && !dup) {
-                        if (lane == 0) s.ex[nex] = x;
-                        ++nex;
-                        __syncwarp();
-                    }
-                    todo &= todo - 1;
-                }
+            long long out_of_it = 0;
+            if (par >= 0)
+                for (int j = 1 + sub; j < c; j += 8) out_of_it += s.par[j] == par ? s.fx[j] : 0;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) out_of_it += __shfl_xor_sync(0xffffffffu, out_of_it, o);
+            if (sub == 0 && par >= 0) {
+                const long long rem = max((1ll << 56) - out_of_it, 0ll);
+                const float u = s.u[c];
+                // (fp64 runs at 2 a clock and SM here; a u outside [0, 1) and NaN take it)
+                const bool ok = u >= 0.f && u < 1.f ? (long long)__umul64hi(unit64(u), rem) < s.fx[c]
+                                                    : (double)u * (double)rem < (double)s.fx[c];
+                if (ok) atomicMin(&s.next[par], c);
             }
         }
-        if (lane == 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int cur = 0, n = 0;
+            s.path[0] = 0;
+            while (s.next[cur] < len) {
+                cur = s.next[cur];
+                s.path[++n] = cur;
+            }
             s.n = n;
             s.cur = cur;
-            s.nex = nex;
         }
-        if (rank == 0) {
-            for (int i = n + 1 + lane; i < len; i += 32) {
-                path[i] = -1;
-                a.out[r * a.nodes + i] = -1;
-            }
-        }
+        __syncthreads();
+        // the stop node's children all failed: their tokens are left out of the sample
+        for (int c = threadIdx.x; c < len; c += kThreads)
+            if (s.par[c] == s.cur && s.fx[c] > 0) s.ex[atomicAdd(&s.nex, 1)] = c;
     }
     __syncthreads();
     const int n = s.n;
     const int cur = kChain ? n : s.cur;
     const bool residual = kChain && n < len;
     int64_t *out = a.out + r * (kChain ? a.nodes + 1 : a.nodes);
-    if (rank == 0) {
-        if (threadIdx.x == 0) {
-            a.count[r] = n;
-            out[n] = -1;   // until a warp finds the sample (it writes behind the cluster barrier)
-        }
-        if (kChain)
-            for (int i = threadIdx.x; i <= a.nodes; i += kThreads)
-                if (i != n) out[i] = i < n ? s.tok[i] : -1;
-    }
+    if (rank == 0 && threadIdx.x == 0) out[n] = -1;   // until the sample is found, behind the cluster barrier
 
     // ---- sample the next token ----
     const float *pr = P + cur * a.p_row;
     const float *qr = residual ? Q + cur * a.q_row : nullptr;
-    const int part = (int)((((int64_t)a.V + cs * kWarps - 1) / (cs * kWarps) + 31) / 32 * 32);   // a warp's elements
+    const int part = (int)((((int64_t)a.V + cs * kWarps - 1) / (cs * kWarps) + 127) / 128 * 128);   // a warp's elements
     const int64_t v0 = ((int64_t)rank * kWarps + warp) * part;
     const int64_t v1 = min((int64_t)a.V, v0 + part);
     const float us = __ldg(a.us + r);
-    // u in units of 2^-64; u >= 1 (and NaN) take the border to the whole sum's end, u < 0 to its start
-    const unsigned long long U = us < 1.f ? __float2ull_rz(fmaxf(us, 0.f) * 18446744073709551616.f) : ~0ull;
+    const unsigned long long U = unit64(us);
     // pass 0: the residual weights; where they are all 0, pass 1: the row itself
     for (int pass = 0; pass < 2; ++pass) {
         const bool plain = pass == 1;
         const float *qq = plain ? nullptr : qr;
-        unsigned long long sum = 0;
-        for (int64_t base = v0 + lane; base < v1; base += 32 * kUnroll) {
-            // every load of the round before the first conversion
-            float x[kUnroll], y[kUnroll];
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int64_t v = base + 32 * k;
-                x[k] = v < v1 ? pr[v] : 0.f;
-                y[k] = v < v1 && qq ? qq[v] : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) sum += weight(x[k], y[k]);
-        }
+        const bool fours = ((reinterpret_cast<uintptr_t>(pr) | reinterpret_cast<uintptr_t>(qq)) & 15) == 0 && a.V % 4 == 0;
+        unsigned long long sum;
+        if (kChain && qq) sum = fours ? part_sum<true, 4>(pr, qq, v0, v1, lane) : part_sum<true, 1>(pr, qq, v0, v1, lane);
+        else sum = fours ? part_sum<false, 4>(pr, qq, v0, v1, lane) : part_sum<false, 1>(pr, qq, v0, v1, lane);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int nex = plain ? 0 : s.nex;
         if (!kChain)
-            for (int e = 0; e < nex; ++e)
-                if (s.ex[e] >= v0 && s.ex[e] < v1) sum -= fixed(pr[s.ex[e]]);
+            for (int e = 0; e < nex; ++e) {
+                const int v = s.tok[s.ex[e]];
+                if (v >= v0 && v < v1) sum -= s.fx[s.ex[e]];
+            }
         if (lane == 0) s.seg[warp] = sum;
         __syncthreads();
         if (warp == 0) {
@@ -256,14 +330,14 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
         const int each = (part + kThreads - 1) / kThreads;
         const int64_t e0 = s0 + (int64_t)threadIdx.x * each;
         const int64_t e1 = min(s1, e0 + each);
-        auto at = [&](int64_t v) -> unsigned long long {
-            if (!kChain)
-                for (int e = 0; e < nex; ++e)
-                    if (s.ex[e] == v) return 0;
-            return weight(pr[v], qq ? qq[v] : 0.f);
-        };
+        auto at = [&](int64_t v) { return weight(pr[v], qq ? qq[v] : 0.f); };
         unsigned long long mine = 0;
         for (int64_t v = e0; v < e1; ++v) mine += at(v);
+        if (!kChain)
+            for (int e = 0; e < nex; ++e) {
+                const int v = s.tok[s.ex[e]];
+                if (v >= e0 && v < e1) mine -= s.fx[s.ex[e]];
+            }
         unsigned long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -276,7 +350,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
         for (int i = 0; i < warp; ++i) run += s.run[i];
         if (border >= run && border - run < mine)
             for (int64_t v = e0; v < e1; ++v) {
-                run += at(v);
+                bool out_of_it = false;
+                if (!kChain)
+                    for (int e = 0; e < nex; ++e) out_of_it |= s.tok[s.ex[e]] == v;
+                if (!out_of_it) run += at(v);
                 if (run > border) {
                     out[n] = v;
                     break;
@@ -284,16 +361,29 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
             }
         break;
     }
+    if (rank == 0) {
+        if (threadIdx.x == 0) a.count[r] = n;
+        if (kChain) {
+            for (int i = threadIdx.x; i <= a.nodes; i += kThreads)
+                if (i != n) out[i] = i < n ? s.tok[i] : -1;
+        } else {
+            for (int i = threadIdx.x; i < len; i += kThreads) {
+                a.path[r * a.nodes + i] = i <= n ? s.path[i] : -1;
+                if (i != n) out[i] = i < n ? s.tok[s.path[i + 1]] : -1;
+            }
+        }
+    }
 }
 
 template <bool kChain>
 static int launch(const Args &a, int32_t num_reqs, cudaStream_t st) {
-    // few requests: a wide cluster each, so that a row is read by many SMs
-    const int cs = kMaxCluster;
+    // few requests: a wide cluster each, so that a row is read by many SMs; many: narrower ones
+    int cs = kMaxCluster;
+    while (cs > 1 && (int64_t)num_reqs * cs > Shape<kChain>::kAsked * current_sm_count()) cs /= 2;
     if ((int64_t)num_reqs * cs > 0x7fffffff) return BKV_ERR_INVALID_ARG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(num_reqs * cs));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Shape<kChain>::kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
