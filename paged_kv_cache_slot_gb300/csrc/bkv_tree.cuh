@@ -69,11 +69,21 @@ __device__ __forceinline__ uint32_t tree_vis32(const uint32_t *row, int32_t word
     return lim >= 32 ? v : v & ((1u << lim) - 1u);
 }
 
-struct TreeTc {
-    CUtensorMap mk, mv, mq;
-    int seg_rows;
+// A launch of the tensor-core kernel: its boxes and its shared memory.
+struct TreeShape {
+    int seg_rows;       // cache rows of a load: min(block size, 128)
     int tok_per_tile;   // tree tokens a 128-row query tile holds: 128 / G
     int box_tok;        // tokens a load of q brings
+    int q_half;         // bytes of a query tile's head_dim half
+    int q_buffers;      // query tiles kept: two units' one, a unit's two, or one
+    int q_bytes;
+    int k_stages, v_stages;
+    int smem;
+};
+
+struct TreeTc {
+    CUtensorMap mk, mv, mq;
+    TreeShape sh;
 };
 bool prepare_tree_tc(const TreeArgs &a, TreeTc *t);
 int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t stream);

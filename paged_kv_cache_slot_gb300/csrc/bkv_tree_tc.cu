@@ -48,7 +48,6 @@ using namespace tc;
 
 constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
-constexpr int kStages = 2;
 constexpr int kHalfBytes = kTile * 128;
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kThreads = 608;
@@ -57,24 +56,37 @@ constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (
 constexpr int kTimeoutErr = 1 << 24;
 constexpr int kMaxReqs = 2048;
 constexpr float kSlack = 8.f;
+#ifndef QB
+#define QB 1
+#endif
 
-constexpr int kOffQ = 0;                                  // two query tiles (or two units' one tile)
-constexpr int kOffK = kOffQ + 2 * kTileBytes;
-constexpr int kOffV = kOffK + kStages * kTileBytes;
-constexpr int kOffMask = kOffV + kStages * kTileBytes;    // 8 words: loaded segments per tile (ring)
-constexpr int kOffPoison = kOffMask + 8 * 4;              // 8 x 4 words: V rows of the tile that are not finite
-constexpr int kOffBar = kOffPoison + 8 * 4 * 4;
-constexpr int kNumBars = 4 * kStages + 4 + 2 + 2 + 2 + 8 + 8 + 4;
+constexpr int kMaxStages = 3;                             // slots of a ring, at most
+constexpr int kOffMask = 0;                               // 8 words: loaded segments per tile (ring)
+constexpr int kOffPoison = kOffMask + 8 * 4;              // 8 x 32 bytes: V rows of the tile that are not finite
+constexpr int kOffBar = kOffPoison + 8 * 32;
+constexpr int kNumBars = 4 * kMaxStages + 4 + 2 + 2 + 2 + 8 + 8 + 4;
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 4;
 constexpr int kOffPre = (kOffAbort + 4 + 15) / 16 * 16;   // [kMaxReqs + 1] tiles before request r
-constexpr int kOffLen = kOffPre + (kMaxReqs + 4) * 4;     // [kMaxReqs] clamped lengths
-constexpr int kOffXmax = kOffLen + kMaxReqs * 4;          // [stream][half][tile parity][row]
+constexpr int kOffFill = kOffPre + (kMaxReqs + 4) * 4;    // [kMaxReqs] positions of its last tile, less one
+constexpr int kOffXmax = kOffFill + kMaxReqs;             // [stream][half][tile parity][row]
 constexpr int kOffXm = kOffXmax + 2 * 2 * 2 * kTile * 4;  // [stream][row]
 constexpr int kOffXsum = kOffXm + 2 * kTile * 4;          // [stream][half][row]
-constexpr int kSmemUsed = kOffXsum + 2 * 2 * kTile * 4;
-constexpr int kSmemBytes = kSmemUsed + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
+// queries, then the K and V rings: what a launch needs of the rest (see ring_shape)
+constexpr int kOffQ = (kOffXsum + 2 * 2 * kTile * 4 + 1023) / 1024 * 1024;
+constexpr int kSmemMax = 227 * 1024 - 1024;               // less the slack for 1024 alignment
+
+// A ring slot and its phase parity.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void advance(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 __host__ __device__ constexpr uint32_t col_s(int x) { return 128u * (uint32_t)x; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u + 128u * (uint32_t)x; }
@@ -98,12 +110,13 @@ struct Unit {
 
 // Walks this CTA's units: column q's share of the tiles laid end to end.
 struct Units {
-    const int32_t *pre, *len;
+    const int32_t *pre;
+    const uint8_t *fill;
     int n, r, q, P;
     int64_t t, t1;
-    __device__ Units(const TreeArgs &a, const int32_t *pre_, const int32_t *len_, int q_) {
+    __device__ Units(const TreeArgs &a, const int32_t *pre_, const uint8_t *fill_, int q_) {
         pre = pre_;
-        len = len_;
+        fill = fill_;
         n = a.num_reqs;
         q = q_;
         P = a.P;
@@ -135,7 +148,7 @@ struct Units {
         while (pre[r + 1] <= t) ++r;
         const int s = pre[r], e = pre[r + 1];
         x.r = r;
-        x.L = len[r];
+        x.L = (e - s - 1) * kTile + fill[r] + 1;
         x.f = (int)(t - s);
         const int end = t1 < e ? (int)(t1 - s) : e - s;
         x.nt = end - x.f;
@@ -148,25 +161,24 @@ struct Units {
 
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                   const __grid_constant__ CUtensorMap tmQ, const TreeArgs a, int seg_rows, int tok_per_tile,
-                   int box_tok) {
+                   const __grid_constant__ CUtensorMap tmQ, const TreeArgs a, const TreeShape sh) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     volatile uint32_t *mask_words = reinterpret_cast<uint32_t *>(smem + kOffMask);
-    volatile uint32_t *poison = reinterpret_cast<uint32_t *>(smem + kOffPoison);
+    uint8_t *poison = smem + kOffPoison;   // [tile & 7][32], four rows a byte
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
     int32_t *pre = reinterpret_cast<int32_t *>(smem + kOffPre);
-    int32_t *len = reinterpret_cast<int32_t *>(smem + kOffLen);
+    uint8_t *fill = smem + kOffFill;
     const uint32_t bar0 = sbase + kOffBar;
     auto bar_kfull = [&](int s) { return bar0 + 8u * s; };
-    auto bar_kempty = [&](int s) { return bar0 + 8u * (kStages + s); };
-    auto bar_vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
-    auto bar_vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
-    constexpr int kB = 4 * kStages;
+    auto bar_kempty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    auto bar_vfull = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
+    auto bar_vempty = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };
+    constexpr int kB = 4 * kMaxStages;
     auto bar_qfull = [&](int b) { return bar0 + 8u * (kB + b); };
     auto bar_qempty = [&](int b) { return bar0 + 8u * (kB + 2 + b); };
     auto bar_sfull = [&](int x) { return bar0 + 8u * (kB + 4 + x); };
@@ -177,9 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the two warps (one per key half) of a lane quarter of a stream; the four of a quarter of both
     auto bar_pair = [&](int x, int qw) { return bar0 + 8u * (kB + 18 + 4 * x + qw); };
     auto bar_quad = [&](int qw) { return bar0 + 8u * (kB + 26 + qw); };
+    const int seg_rows = sh.seg_rows, tok_per_tile = sh.tok_per_tile, box_tok = sh.box_tok;
+    const int nK = sh.k_stages, nV = sh.v_stages;
+    const int off_v = kOffQ + sh.q_bytes + nK * kTileBytes;
     const uint32_t sm_q = sbase + kOffQ;
-    const uint32_t sm_k = sbase + kOffK;
-    const uint32_t sm_v = sbase + kOffV;
+    const uint32_t sm_k = sm_q + sh.q_bytes;
+    const uint32_t sm_v = sbase + off_v;
 
     // what this CTA is: column q, KV head g, token group p, and its rows
     const int G = a.G;
@@ -192,10 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows0 = (dual ? tok_per_tile : ntok) * G;
     const int rows1 = dual ? (ntok - tok_per_tile) * G : rows0;
     const int aq0 = (rows0 + 31) >> 5, aq1 = (rows1 + 31) >> 5;   // lane quarters with rows
-    const int nbuf = dual ? 1 : 2;                                // units whose queries fit
+    // units whose queries fit (a group of two tiles takes both buffers)
+    const int nbuf = dual ? 1 : sh.q_buffers;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(bar_kfull(s), 1);
             mbar_init(bar_kempty(s), 1);
             mbar_init(bar_vfull(s), 1);
@@ -205,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar_qfull(x), 1);
             mbar_init(bar_qempty(x), 1);
             mbar_init(bar_sfull(x), 1);
-            mbar_init(bar_pfull(x), 2 * (x ? aq1 : aq0));
+            mbar_init(bar_pfull(x), (!dual || x == 0) ? 8 : 2 * aq1);
             for (int qw = 0; qw < 4; ++qw) mbar_init(bar_pair(x, qw), 2);
         }
         mbar_init(bar_ofull, 2);
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t c = __ldg(a.ctx + r);
         const int32_t L = tree_len(a, c);
         if (c > a.max_ctx && blockIdx.x == 0 && a.err) atomicAdd(a.err, 1);
-        len[r] = L;
+        fill[r] = (uint8_t)((L - 1) & (kTile - 1));
         pre[r] = (L + kTile - 1) / kTile;
     }
     __syncthreads();
@@ -262,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     // the merge's table, and the rows of requests without a position
-    if (hp == 0 && threadIdx.x == 32) a.ws_split[q] = Units(a, pre, len, q).split();
+    if (hp == 0 && threadIdx.x == 32) a.ws_split[q] = Units(a, pre, fill, q).split();
     for (int r = q; r < a.num_reqs; r += a.P) {
-        if (len[r] > 0) continue;
+        if (pre[r + 1] > pre[r]) continue;
         for (int e = threadIdx.x; e < ntok * G * (kD / 8); e += kThreads) {
             const int row = e / (kD / 8), t = tok0 + row / G, h = g * G + row % G;
             reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
@@ -276,26 +292,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int seg_shift = 31 - __clz(seg_rows);
     const uint32_t all_seg = (1u << nseg) - 1u;   // at most 16 segments
 
+    // V rows of a tile that must not reach P V are zeroed: not loaded, at or past the cache end (row lim), or
+    // of the tree (from row fst) and not finite, which is remembered.  Warp wi of the nw that share a tile.
+    auto fix_v = [&](int slot, int jj, uint32_t mword, int fst, int lim, int wi, int nw) {
+        fst = max(fst, 0);
+        uint4 *v0 = reinterpret_cast<uint4 *>(smem + off_v + slot * kTileBytes);   // 8 a row
+        uint4 *v1 = v0 + kHalfBytes / 16;
+        auto zero_rows = [&](int r0, int r1) {
+#pragma unroll 4
+            for (int e = 8 * r0 + 32 * wi + lane; e < 8 * r1; e += 32 * nw)
+                v0[e] = v1[e] = make_uint4(0, 0, 0, 0);
+        };
+        for (uint32_t miss = ~mword & all_seg; miss; miss &= miss - 1) {
+            const int r0 = (__ffs(miss) - 1) * seg_rows;
+            if (r0 < lim) zero_rows(r0, r0 + seg_rows);
+        }
+        if (fst < kTile) {
+            zero_rows(lim, kTile);
+            // the tree's rows: four at a time, eight lanes a row (16 bytes of each half)
+            const int g0 = fst >> 2, g1 = (min(lim, kTile) + 3) >> 2;
+            uint8_t *bad_rows = poison + (jj & 7) * 32;
+            if (wi == 0 && (lane < g0 || lane >= g1)) bad_rows[lane] = 0;
+            for (int i = g0 + wi; i < g1; i += nw) {
+                const int e = 32 * i + lane, vrow = 4 * i + (lane >> 3);
+                const uint4 p0 = v0[e], p1 = v1[e];
+                const uint32_t ws[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+                bool bad = false;
+#pragma unroll
+                for (int h = 0; h < 8; ++h)   // an exponent of all ones in either half
+                    bad |= (ws[h] & 0x7f80u) == 0x7f80u || (ws[h] & 0x7f800000u) == 0x7f800000u;
+                bad &= vrow >= fst && vrow < lim && ((mword >> (vrow >> seg_shift)) & 1u);
+                const uint32_t m8 = __ballot_sync(0xffffffffu, bad);
+                uint32_t rows = 0u;
+                if (m8) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) rows |= ((m8 >> (8 * h)) & 0xffu) ? 1u << h : 0u;
+                    if ((rows >> (lane >> 3)) & 1u) v0[e] = v1[e] = make_uint4(0, 0, 0, 0);
+                }
+                if (lane == 0) bad_rows[i] = (uint8_t)rows;
+            }
+        }
+        fence_proxy_async();
+    };
+
     if (warp == 0 || warp == kWarpV) {
         // ================= TMA producers (warp 0: Q and K, last warp: V) =================
         const bool is_v = warp == kWarpV;
         const bool count = !is_v && p == 0 && a.err;   // bad entries count once a KV head
-        int64_t j = 0;
-        int uq = 0;
-        Units units(a, pre, len, q);
+        const int stages = is_v ? nV : nK;
+        Ring ring;
+        int j = 0, uq = 0;
+        Units units(a, pre, fill, q);
         Unit x;
         for (; !*abort_flag && units.next(x); ++uq) {
             if (!is_v) {
-                const int b = uq % nbuf;
-                if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((uq / nbuf) & 1) ^ 1u, abort_flag)) break;
+                const int b = nbuf == 2 ? uq & 1 : 0;
+                if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1) ^ 1u, abort_flag)) break;
                 if (lane == 0) {
                     const uint32_t bytes = (uint32_t)(box_tok * G) * 256u;
                     mbar_arrive_expect_tx(bar_qfull(b), dual ? 2 * bytes : bytes);
                     for (int xb = 0; xb < (dual ? 2 : 1); ++xb) {
                         const int tq = x.r * a.T + tok0 + xb * tok_per_tile;
-                        const uint32_t dq = sm_q + (b + xb) * kTileBytes;
+                        const uint32_t dq = sm_q + (b + xb) * 2 * sh.q_half;
                         tma_load_3d(dq, &tmQ, bar_qfull(b), 0, g * G, tq);
-                        tma_load_3d(dq + kHalfBytes, &tmQ, bar_qfull(b), 64, g * G, tq);
+                        tma_load_3d(dq + sh.q_half, &tmQ, bar_qfull(b), 64, g * G, tq);
                     }
                 }
             }
@@ -316,17 +376,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t row_cur = entry(x.f);
             for (int kt = 0; kt < x.nt; ++kt, ++j) {
                 const int64_t row_nxt = kt + 1 < x.nt ? entry(x.f + kt + 1) : -1;   // in flight meanwhile
-                const int s = (int)(j % kStages);
+                const int s = ring.slot;
                 const uint32_t bar_e = is_v ? bar_vempty(s) : bar_kempty(s);
                 const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
-                if (!mbar_wait_warp(bar_e, (uint32_t)((j / kStages) & 1) ^ 1u, abort_flag)) break;
+                if (!mbar_wait_warp(bar_e, ring.phase ^ 1u, abort_flag)) break;
+                ring.advance(stages);
                 const bool load = row_cur >= 0;
                 const uint32_t ballot = __ballot_sync(0xffffffffu, load);
                 if (lane == 0) {
-                    // a word is rewritten 8 tiles on; its readers are at most 4 tiles behind
+                    // a word is rewritten 8 tiles on; its readers are at most 5 tiles behind
                     if (!is_v) {
                         mask_words[j & 7] = ballot;
-                        mbar_arrive(bar_mask((int)(j & 7)));
+                        mbar_arrive(bar_mask(j & 7));
                     }
                     mbar_arrive_expect_tx(bar_f, (uint32_t)__popc(ballot) * (uint32_t)seg_rows * 256u);
                 }
@@ -352,10 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);   // Q (K-major) x K (K-major)
             constexpr uint32_t kIdescO = idesc_bf16(128, 128, 0, 1);   // P (TMEM) x V (MN-major)
             int np[2] = {0, 0};   // P tiles consumed
-            // O_x += P_x V(tile j): `first` overwrites O_x, once the unit before has been read out
-            auto issue_pv = [&](int xb, int64_t j, bool first, int unit) -> bool {
-                const int s = (int)(j % kStages);
-                if (!mbar_wait(bar_vfull(s), (uint32_t)((j / kStages) & 1), abort_flag) ||
+            // O_x += P_x V(next tile): `first` overwrites O_x, once the unit before has been read out
+            Ring kr, vr;          // tiles are multiplied in their order
+            auto issue_pv = [&](int xb, bool first, int unit) -> bool {
+                const int s = vr.slot;
+                if (!mbar_wait(bar_vfull(s), vr.phase, abort_flag) ||
                     !mbar_wait(bar_pfull(xb), (uint32_t)(np[xb] & 1), abort_flag))
                     return false;
                 ++np[xb];
@@ -373,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto issue_s = [&](int xb, int s, int qb) {
                 const uint32_t k_base = sm_k + s * kTileBytes;
-                const uint32_t q_base = sm_q + qb * kTileBytes;
+                const uint32_t q_base = sm_q + qb * 2 * sh.q_half;
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (kk & 3) * 32;
-                    mma_bf16(tmem + col_s(xb), sdesc(q_base + off, 16, 1024), sdesc(k_base + off, 16, 1024), kIdescS,
-                             kk > 0 ? 1u : 0u);
+                    // (rows of the query tile past the group's: whatever lies there, their scores are not used)
+                    mma_bf16(tmem + col_s(xb), sdesc(q_base + (kk >> 2) * sh.q_half + (kk & 3) * 32, 16, 1024),
+                             sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(bar_sfull(xb));
             };
@@ -388,69 +450,71 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(bar_ofull);
                 mbar_arrive(bar_ofull);
             };
-            Units units(a, pre, len, q);
+            Units units(a, pre, fill, q);
             Unit x;
-            int64_t j = 0;
             bool ok = true;
             if (!dual) {
                 // stream j & 1 has tile j; its P V is issued before the S of tile j + 2, over the same columns
                 struct {
-                    int64_t j;
                     int unit;
                     bool on, first, last;
-                } pend[2] = {{0, 0, false, false, false}, {0, 0, false, false, false}};
+                } pend[2] = {{0, false, false, false}, {0, false, false, false}};
                 auto settle = [&](int xb) -> bool {
                     auto &w = pend[xb];
                     if (!w.on) return true;
                     w.on = false;
-                    if (!issue_pv(xb, w.j, w.first, w.unit)) return false;
-                    mma_commit(bar_vempty((int)(w.j % kStages)));
+                    if (!issue_pv(xb, w.first, w.unit)) return false;
+                    mma_commit(bar_vempty(vr.slot));
+                    vr.advance(nV);
                     if (w.last) finish();
                     return true;
                 };
+                int xb = 0;
                 for (int uq = 0; ok && units.next(x); ++uq) {
-                    const int b = uq & 1;
-                    for (int kt = 0; kt < x.nt; ++kt, ++j) {
-                        const int xb = (int)(j & 1), s = (int)(j % kStages);
-                        ok = settle(xb) && (kt > 0 || mbar_wait(bar_qfull(b), (uint32_t)((uq >> 1) & 1), abort_flag)) &&
-                             mbar_wait(bar_kfull(s), (uint32_t)((j / kStages) & 1), abort_flag);
+                    const int b = nbuf == 2 ? uq & 1 : 0;
+                    const uint32_t qphase = (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1);
+                    for (int kt = 0; kt < x.nt; ++kt, xb ^= 1) {
+                        ok = settle(xb) && (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
+                             mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
-                        issue_s(xb, s, b);
-                        mma_commit(bar_kempty(s));
+                        issue_s(xb, kr.slot, b);
+                        mma_commit(bar_kempty(kr.slot));
+                        kr.advance(nK);
                         if (kt == x.nt - 1) mma_commit(bar_qempty(b));
-                        pend[xb].j = j;
                         pend[xb].unit = uq;
                         pend[xb].on = true;
                         pend[xb].first = kt < 2;
                         pend[xb].last = kt == x.nt - 1;
                     }
                 }
-                if (ok) ok = settle((int)(j & 1)) && settle((int)((j + 1) & 1));
+                if (ok) ok = settle(xb) && settle(xb ^ 1);
             } else {
                 // per key tile: O_A += P_A V(-1), S_A; O_B += P_B V(-1), S_B
                 for (int uq = 0; ok && units.next(x); ++uq) {
                     ok = mbar_wait(bar_qfull(0), (uint32_t)(uq & 1), abort_flag);
                     for (int kt = 0; ok && kt <= x.nt; ++kt) {
-                        const int s = (int)(j % kStages);
-                        if (kt < x.nt && !mbar_wait(bar_kfull(s), (uint32_t)((j / kStages) & 1), abort_flag)) {
+                        if (kt < x.nt && !mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         for (int xb = 0; xb < 2; ++xb) {
-                            if (kt > 0 && !issue_pv(xb, j - 1, kt == 1, uq)) {
+                            if (kt > 0 && !issue_pv(xb, kt == 1, uq)) {
                                 ok = false;
                                 break;
                             }
-                            if (kt < x.nt) issue_s(xb, s, xb);
+                            if (kt < x.nt) issue_s(xb, kr.slot, xb);
                         }
                         if (!ok) break;
-                        if (kt > 0) mma_commit(bar_vempty((int)((j - 1) % kStages)));
+                        if (kt > 0) {
+                            mma_commit(bar_vempty(vr.slot));
+                            vr.advance(nV);
+                        }
                         if (kt < x.nt) {
-                            mma_commit(bar_kempty(s));
+                            mma_commit(bar_kempty(kr.slot));
+                            kr.advance(nK);
                             if (kt == x.nt - 1) mma_commit(bar_qempty(0));
-                            ++j;
                         } else {
                             finish();
                         }
@@ -465,7 +529,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kh = ((warp - 2) >> 2) & 1;
         const int qw = warp & 3;
         const int aq = xb ? aq1 : aq0;
-        if (qw < aq) {
+        const bool fixes = !dual || xb == 0;   // V serves both query tiles: the first one's stream mends it
+        if (qw >= aq) {
+            // a quarter without rows: it mends the stream's V tiles beside the softmax
+            if (fixes) {
+                Ring vr;
+                int j = 0, ns = 0;
+                bool ok = true;
+                Units units(a, pre, fill, q);
+                Unit x;
+                while (ok && units.next(x)) {
+                    for (int kt = 0; kt < x.nt; ++kt, ++j, vr.advance(nV)) {
+                        if (!dual && (j & 1) != xb) continue;
+                        if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
+                            !mbar_wait_warp(bar_mask(j & 7), (uint32_t)((j >> 3) & 1), abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        ++ns;
+                        const uint32_t mword = mask_words[j & 7];
+                        const int k0 = (x.f + kt) * kTile;
+                        if (mword != all_seg || k0 + kTile > x.L - a.T) {
+                            if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            fix_v(vr.slot, j, mword, x.L - a.T - k0, x.L - k0, kh * (4 - aq) + qw - aq, 2 * (4 - aq));
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_pfull(xb));
+                    }
+                }
+            }
+        } else {
             const int row = 32 * qw + lane;
             const bool valid = row < (xb ? rows1 : rows0);
             const int tok = tok0 + (dual ? xb * tok_per_tile : 0) + min(row, (xb ? rows1 : rows0) - 1) / G;
@@ -477,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *xm = reinterpret_cast<float *>(smem + kOffXm);                              // [stream][row]
             float *xsum = reinterpret_cast<float *>(smem + kOffXsum);                          // [stream][half][row]
             uint32_t pphase = 0;
-            int64_t j = 0;
+            Ring vr;             // the V slot of the tile at hand
+            int j = 0;
             int ns = 0;          // S tiles of this stream seen so far
             int no = 0;          // units finished so far
             bool ok = true;
@@ -488,55 +585,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pphase ^= 1u;
                 return r;
             };
-            Units units(a, pre, len, q);
+            Units units(a, pre, fill, q);
             Unit x;
             while (ok && units.next(x)) {
                 const int first = x.L - a.T;   // position of the tree's first token
                 const uint32_t *mrow = a.mask + (int64_t)x.r * a.mask_stride + (int64_t)tok * a.mask_words;
-                const int64_t jb = j;
+                const int jb = j;
                 j += x.nt;
                 float m = -INFINITY, l = 0.f;
                 bool any = false;   // this stream had a tile of the unit
-                for (int kt = 0; kt < x.nt; ++kt) {
-                    const int64_t jj = jb + kt;
-                    if (!dual && (int)(jj & 1) != xb) continue;
-                    const int s = (int)(jj % kStages);
+                for (int kt = 0; kt < x.nt; ++kt, vr.advance(nV)) {
+                    const int jj = jb + kt;
+                    if (!dual && (jj & 1) != xb) continue;
+                    const int k0 = (x.f + kt) * kTile;
+                    const bool near = k0 + kTile > first;    // positions of the tree, or past the cache end
+                    // what this row sees of its half's 64 keys, as bits (the mask's words are on their way
+                    // while the scores are waited for)
+                    uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+                    if (near) {
+                        vis[0] = tree_vis32(mrow, a.mask_words, first, x.L, k0 + 64 * kh);
+                        vis[1] = tree_vis32(mrow, a.mask_words, first, x.L, k0 + 64 * kh + 32);
+                    }
                     if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
-                        !mbar_wait_warp(bar_mask((int)(jj & 7)), (uint32_t)((jj >> 3) & 1), abort_flag)) {
+                        !mbar_wait_warp(bar_mask(jj & 7), (uint32_t)((jj >> 3) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t mword = mask_words[jj & 7];
-                    const int k0 = (x.f + kt) * kTile;
-                    const bool near = k0 + kTile > first;    // positions of the tree, or past the cache end
                     const bool full = !near && mword == all_seg;
-                    // keys [32 c, 32 c + 32) of the tile that this row sees, as bits
-                    auto vis32 = [&](int c) -> uint32_t {
-                        const int lo = 32 * c;
-                        uint32_t v = near ? tree_vis32(mrow, a.mask_words, first, x.L, k0 + lo) : 0xffffffffu;
-                        if (mword != all_seg) {
+                    if (mword != all_seg) {   // keys of entries that are not there
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t bits = mword >> ((64 * kh + 32 * h) >> seg_shift);
                             uint32_t sb = 0u;
                             if (seg_rows >= 32) {
-                                sb = ((mword >> (lo >> seg_shift)) & 1u) ? 0xffffffffu : 0u;
+                                sb = (bits & 1u) ? 0xffffffffu : 0u;
                             } else {
                                 const uint32_t ones = (1u << seg_rows) - 1u;
-                                const uint32_t bits = mword >> (lo >> seg_shift);
                                 for (int i = 0; i < (32 >> seg_shift); ++i)
                                     if ((bits >> i) & 1u) sb |= ones << (i * seg_rows);
                             }
-                            v &= sb;
+                            vis[h] &= sb;
                         }
-                        return v;
-                    };
+                    }
                     // pass 1: this half's max of the raw scores, then the row's from the two halves
                     float mraw = -INFINITY;
 #pragma unroll 1
-                    for (int c = 2 * kh; c < 2 * kh + 2; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         float sv[32];
-                        tmem_ld32(s_col + 32u * c, sv);
+                        tmem_ld32(s_col + 64u * kh + 32u * c, sv);
                         if (!full) {
-                            const uint32_t vm = vis32(c);
+                            const uint32_t vm = vis[c];
 #pragma unroll
                             for (int k = 0; k < 32; ++k) sv[k] = (vm & (1u << k)) ? sv[k] : -INFINITY;
                         }
@@ -571,17 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float psum = 0.f;
                     {
                         const float nb = -mn;
-                        uint32_t vm = 0;
 #pragma unroll 1
-                        for (int c = 4 * kh; c < 4 * kh + 4; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             float sv[16];
-                            tmem_ld16(s_col + 16u * c, sv);
+                            tmem_ld16(s_col + 64u * kh + 16u * c, sv);
                             if (full) {
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) sv[k] = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
                             } else {
-                                if ((c & 1) == 0) vm = vis32(c >> 1);
-                                const uint32_t vh = (c & 1) ? (vm >> 16) : vm;
+                                const uint32_t vh = (c < 2 ? vis[0] : vis[1]) >> (16 * (c & 1));
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
                                     const float e = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
@@ -595,46 +693,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pk[k >> 1] = *reinterpret_cast<const uint32_t *>(&pb);
                                 psum += sv[k] + sv[k + 1];
                             }
-                            tmem_st8(s_col + 64u * kh + 8u * (c & 3), pk);
+                            tmem_st8(s_col + 64u * kh + 8u * c, pk);
                         }
                         tmem_st_wait();
                     }
                     l = fmaf(l, corr, psum);
                     m = mn;
-                    // V rows that must not reach P V: not loaded, at or past the cache end, or of the tree and
-                    // not finite.  The warps of the stream share the tile's 128 rows.
-                    if (!full && (!dual || xb == 0)) {
-                        if (!mbar_wait_warp(bar_vfull(s), (uint32_t)((jj / kStages) & 1), abort_flag)) {
+                    if (!full && fixes && aq == 4) {
+                        if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        for (int c = kh * aq + qw; c < 4; c += 2 * aq) {
-                            const int vr = 32 * c + lane;
-                            uint4 *v0 = reinterpret_cast<uint4 *>(smem + kOffV + s * kTileBytes + vr * 128);
-                            uint4 *v1 = reinterpret_cast<uint4 *>(smem + kOffV + s * kTileBytes + kHalfBytes + vr * 128);
-                            const bool there = ((mword >> (vr >> seg_shift)) & 1u) && k0 + vr < x.L;
-                            bool bad = false;
-                            if (there && k0 + vr >= first) {
-#pragma unroll 1
-                                for (int e = 0; e < 16; ++e) {
-                                    const uint4 w = e < 8 ? v0[e] : v1[e - 8];
-                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int h = 0; h < 4; ++h)   // an exponent of all ones in either half
-                                        bad |= (ws[h] & 0x7f80u) == 0x7f80u || (ws[h] & 0x7f800000u) == 0x7f800000u;
-                                }
-                            }
-                            if (!there || bad) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    v0[e] = make_uint4(0, 0, 0, 0);
-                                    v1[e] = make_uint4(0, 0, 0, 0);
-                                }
-                            }
-                            const uint32_t word = __ballot_sync(0xffffffffu, bad);
-                            if (lane == 0 && near) poison[(jj & 7) * 4 + c] = word;
-                        }
-                        fence_proxy_async();
+                        fix_v(vr.slot, jj, mword, first - k0, x.L - k0, kh * 4 + qw, 8);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -671,12 +741,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // a V row of the tree that was not finite makes the rows that see it NaN
                 for (int kt = max(0, (first >> 7) - x.f); kt < x.nt; ++kt) {
-                    const int k0 = (x.f + kt) * kTile;
-                    if (k0 + kTile <= first) continue;
+                    const uint8_t *bad_rows = poison + ((jb + kt) & 7) * 32;
+                    const uint4 b0 = *reinterpret_cast<const uint4 *>(bad_rows);
+                    const uint4 b1 = *reinterpret_cast<const uint4 *>(bad_rows + 16);
+                    if ((b0.x | b0.y | b0.z | b0.w | b1.x | b1.y | b1.z | b1.w) == 0u) continue;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        const uint32_t w = poison[((jb + kt) & 7) * 4 + c];
-                        if (w && (w & tree_vis32(mrow, a.mask_words, first, x.L, k0 + 32 * c))) lsum = NAN;
+                        uint32_t w = 0u;
+                        for (int i = 0; i < 8; ++i) w |= (uint32_t)bad_rows[8 * c + i] << (4 * i);
+                        if (w & tree_vis32(mrow, a.mask_words, first, x.L, (x.f + kt) * kTile + 32 * c)) lsum = NAN;
                     }
                 }
                 const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
@@ -689,18 +762,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = c0; c < c1; ++c) {
                     float ov[32];
-                    tmem_ld32(tmem + lane_base + col_o(dual ? xb : 0) + 32u * c, ov);
-                    if (!dual) {
+                    if (dual) {
+                        tmem_ld32(tmem + lane_base + col_o(xb) + 32u * c, ov);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) ov[k] = use_a ? ov[k] * fa : 0.f;
-                        if (use_b) {
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t oa[16], ob[16];
+                            tmem_ld16_nw(tmem + lane_base + col_o(0) + 32u * c + 16u * h, oa);
+                            tmem_ld16_nw(tmem + lane_base + col_o(1) + 32u * c + 16u * h, ob);
+                            tmem_ld_wait();
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float ob[16];
-                                tmem_ld16(tmem + lane_base + col_o(1) + 32u * c + 16u * h, ob);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) ov[16 * h + k] = fmaf(fb, ob[k], ov[16 * h + k]);
-                            }
+                            for (int k = 0; k < 16; ++k)   // (columns of a stream without a tile may hold anything)
+                                ov[16 * h + k] = (use_a ? __uint_as_float(oa[k]) * fa : 0.f) +
+                                                 (use_b ? __uint_as_float(ob[k]) * fb : 0.f);
                         }
                     }
                     if (!valid) continue;
@@ -769,6 +843,25 @@ static bool encode_3d(CUtensorMap *m, const void *base, uint64_t d1, uint64_t d2
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Shared memory of a launch.  A query tile keeps only its own rows (whole
+// swizzle atoms of 8); the rest goes to the rings, up to three slots each.  Two
+// query tiles, or one of more than 64 rows twice, leave four slots.
+static void ring_shape(const TreeArgs &a, TreeShape *s) {
+    s->seg_rows = a.bs < kTile ? a.bs : kTile;
+    s->tok_per_tile = kTile / a.G;
+    s->box_tok = a.T < s->tok_per_tile ? a.T : s->tok_per_tile;
+    s->q_half = (s->box_tok * a.G + 7) / 8 * 1024;
+    s->q_buffers = 2;
+    auto slots = [&](int buffers) { return (kSmemMax - kOffQ - buffers * 2 * s->q_half) / kTileBytes; };
+    if (a.T <= s->tok_per_tile && slots(1) > slots(2) && slots(2) < 2 * kMaxStages) s->q_buffers = QB;
+    s->q_bytes = s->q_buffers * 2 * s->q_half;
+    int n = slots(s->q_buffers);
+    n = n < 2 * kMaxStages ? n : 2 * kMaxStages;
+    s->k_stages = n / 2;
+    s->v_stages = n - n / 2;
+    s->smem = kOffQ + s->q_bytes + n * kTileBytes + 1024;
+}
+
 }  // namespace ttc
 
 bool prepare_tree_tc(const TreeArgs &a, TreeTc *t) {
@@ -782,13 +875,11 @@ bool prepare_tree_tc(const TreeArgs &a, TreeTc *t) {
     if ((int64_t)a.P * a.H_kv * a.groups >= ((int64_t)1 << 31)) return false;
     if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q, 16) || !aligned(a.out, 16)) return false;
     if (!encode_fn()) return false;
-    t->seg_rows = a.bs < kTile ? a.bs : kTile;
-    t->tok_per_tile = kTile / a.G;
-    t->box_tok = a.T < t->tok_per_tile ? a.T : t->tok_per_tile;
+    ring_shape(a, &t->sh);
     const uint64_t rows = (uint64_t)a.total_blocks * (uint64_t)a.bs;
-    return encode_3d(&t->mk, a.k, a.H_kv, rows, 1, t->seg_rows) &&
-           encode_3d(&t->mv, a.v, a.H_kv, rows, 1, t->seg_rows) &&
-           encode_3d(&t->mq, a.q, a.H_q, (uint64_t)a.num_reqs * a.T, a.G, t->box_tok);
+    return encode_3d(&t->mk, a.k, a.H_kv, rows, 1, t->sh.seg_rows) &&
+           encode_3d(&t->mv, a.v, a.H_kv, rows, 1, t->sh.seg_rows) &&
+           encode_3d(&t->mq, a.q, a.H_q, (uint64_t)a.num_reqs * a.T, a.G, t->sh.box_tok);
 }
 
 int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t st) {
@@ -798,7 +889,7 @@ int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t st) {
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax + 1024);
         if (e != cudaSuccess) {
             set_cuda_error(e);
             (void)launch_status();   // clears the sticky status
@@ -806,8 +897,8 @@ int launch_tree_tc(const TreeArgs &a, const TreeTc &t, cudaStream_t st) {
         }
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    const cudaError_t e = launch_pdl(tree_tc_kernel, dim3((unsigned)(a.P * a.H_kv * a.groups)), dim3(kThreads), kSmemBytes,
-                                     st, t.mk, t.mv, t.mq, a, t.seg_rows, t.tok_per_tile, t.box_tok);
+    const cudaError_t e = launch_pdl(tree_tc_kernel, dim3((unsigned)(a.P * a.H_kv * a.groups)), dim3(kThreads),
+                                     (size_t)t.sh.smem, st, t.mk, t.mv, t.mq, a, t.sh);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }
