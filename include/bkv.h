@@ -622,7 +622,7 @@ size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int
  *   tree_mask  words of 32 bits as above; mask_req_stride words between the
  *              requests' masks, or 0: one tree for all requests.
  *   workspace  device scratch of workspace_bytes >=
- *              bkv_paged_decode_tree_workspace_size(...), 16-byte aligned,
+ *              bkv_paged_decode_tree_workspace_size(...), 32-byte aligned,
  *              used only while the call's kernels run; its contents on entry
  *              do not matter.
  *   Other arguments, bounds and error counts as bkv_paged_decode.  bf16 with

@@ -25,11 +25,46 @@ static constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxT = 256;       // tree tokens a request
 constexpr int kBK = 32;          // keys a tile of the CUDA-core kernel
 constexpr int kThreads = 128;
+#ifndef CCA
+#define CCA 64
+#endif
+#ifndef CCN
+#define CCN 8
+#endif
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[8]) {   // eight bf16
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[4]) {   // four fp32
+    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+}
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store_out(float *p, float x) { *p = x; }
+
+// Two fp32 multiply-adds in one instruction (each rounded as fmaf's), on pairs
+// of consecutive elements: half the issue slots of the products.
+struct __align__(8) Pair {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(const Pair &p) {
+    unsigned long long u;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(p.x), "f"(p.y));
+    return u;
+}
+__device__ __forceinline__ Pair fma2(const Pair &a, const Pair &b, const Pair &c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    Pair r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
+}
 
 // ---------------------------------------------------------------------------
 // CUDA-core kernel: any dtype, head_dim <= DP, any block size.  CTA = (stream
@@ -41,15 +76,15 @@ __device__ __forceinline__ void store_out(float *p, float x) { *p = x; }
 // not see it, and makes the rows that do NaN.
 // ---------------------------------------------------------------------------
 template <typename T, int DP, int BR>
-__global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
-    constexpr int LD = DP + 4, RPT = BR / 16, DJ = DP / 32;
+__global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a, bool vec) {
+    constexpr int LD = DP + 4, RPT = BR / 16, DJ = DP / 32, W = 16 / sizeof(T);
     extern __shared__ float sm[];
     float *Qs = sm;                    // [BR][LD], scaled to base 2
     float *Ks = Qs + BR * LD;          // [kBK][LD]
     float *Vs = Ks + kBK * LD;         // [kBK][LD]
     float *Ps = Vs + kBK * LD;         // [BR][kBK + 4]
-    __shared__ int64_t rowoff[kBK];    // element offset of each key's row, -1: not there
-    __shared__ uint32_t live, poison;
+    __shared__ int64_t rowoff[2][kBK]; // element offset of each key's row, -1: not there; by tile parity
+    __shared__ uint32_t live[2], poison[2];
     pdl_wait();
     pdl_trigger();
     const int rg = blockIdx.x / a.n_chunks, c = blockIdx.x - rg * a.n_chunks;
@@ -68,17 +103,8 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
             if (bad) atomicAdd(a.err, 1);
         }
     }
-    const T *Q = static_cast<const T *>(a.q);
-    for (int e = threadIdx.x; e < BR * DP; e += kThreads) {
-        const int i = e / DP, d = e - i * DP, row = i0 + i;
-        float x = 0.f;
-        if (row < nq && d < a.D) {
-            const int t = row / a.G, h = g * a.G + (row - t * a.G);
-            x = to_f(Q[(((int64_t)r * a.T + t) * a.H_q + h) * a.D + d]) * a.scale_log2;
-        }
-        Qs[i * LD + d] = x;
-    }
-    float o[RPT][DJ][4], m[RPT], l[RPT];
+    Pair o[RPT][DJ][2];   // elements 4 tx + 32 j + {0, 1}, {2, 3}
+    float m[RPT], l[RPT];
     const uint32_t *mrow[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -87,40 +113,104 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
         const int row = min(i0 + ty + 16 * i, nq - 1);
         mrow[i] = a.mask + (int64_t)r * a.mask_stride + (int64_t)(row / a.G) * a.mask_words;
 #pragma unroll
-        for (int j = 0; j < DJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+        for (int j = 0; j < DJ; ++j) o[i][j][0] = o[i][j][1] = Pair{0.f, 0.f};
     }
-    for (int32_t k0 = start; k0 < end; k0 += kBK) {
-        __syncthreads();   // the last tile is read out
-        if (threadIdx.x < kBK) {
-            const int32_t j = k0 + threadIdx.x;
-            int64_t off = -1;
-            if (j < end) {
-                const int32_t lb = j / a.bs;
-                const int64_t b = lb < a.bt_cols ? __ldg(a.bt + (int64_t)r * a.bt_stride + lb) : -1;
-                if (b > 0 && b < a.total_blocks) off = ((b * a.bs + (j - lb * a.bs)) * a.H_kv + g) * a.D;
-            }
-            rowoff[threadIdx.x] = off;
-            const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
-            if (threadIdx.x == 0) {
-                live = ok;
-                poison = 0u;
-            }
+    auto offset_of = [&](int32_t j) -> int64_t {
+        if (j >= end) return -1;
+        const int32_t lb = j / a.bs;
+        const int64_t b = lb < a.bt_cols ? __ldg(a.bt + (int64_t)r * a.bt_stride + lb) : -1;
+        return b > 0 && b < a.total_blocks ? ((b * a.bs + (j - lb * a.bs)) * a.H_kv + g) * a.D : -1;
+    };
+    auto publish = [&](int64_t off, int par) {   // by the first warp
+        rowoff[par][threadIdx.x] = off;
+        const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
+        if (threadIdx.x == 0) {
+            live[par] = ok;
+            poison[par] = 0u;
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < kBK * DP; e += kThreads) {
-            const int i = e / DP, d = e - i * DP;
-            const int64_t off = rowoff[i];
+    };
+    // 16-byte loads of a tile, W elements each, NV a thread: all in flight before the first use, and (head_dim
+    // up to 128) those of the next tile during this one's products
+    constexpr int NV = kBK * DP / W / kThreads;
+    static_assert(NV * W * kThreads == kBK * DP, "whole rounds of 16-byte loads");
+    uint4 kw[NV], vw[NV];
+    auto fetch = [&](int par) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int e = (u * kThreads + (int)threadIdx.x) * W, i = e / DP, d = e - i * DP;
+            const int64_t off = rowoff[par][i];
             const bool in = off >= 0 && d < a.D;
-            const float kx = in ? to_f(static_cast<const T *>(a.k)[off + d]) : 0.f;
-            const float vx = in ? to_f(static_cast<const T *>(a.v)[off + d]) : 0.f;
-            Ks[i * LD + d] = kx;
-            Vs[i * LD + d] = vx;
-            if (k0 + i >= first && !isfinite(vx)) atomicOr(&poison, 1u << i);
+            kw[u] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k) + off + d)) : make_uint4(0, 0, 0, 0);
+            vw[u] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + off + d)) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    int64_t ahead = -1;   // the first warp's key of the next tile
+    if (threadIdx.x < 32) {
+        publish(offset_of(start + threadIdx.x), 0);
+        ahead = offset_of(start + kBK + threadIdx.x);
+    }
+    __syncthreads();
+    if (vec) fetch(0);
+    const T *Q = static_cast<const T *>(a.q);
+    auto q_row = [&](int row) {
+        const int t = row / a.G, h = g * a.G + (row - t * a.G);
+        return Q + (((int64_t)r * a.T + t) * a.H_q + h) * a.D;
+    };
+    if (vec) {
+#pragma unroll 8
+        for (int e = threadIdx.x * W; e < BR * DP; e += kThreads * W) {
+            const int i = e / DP, d = e - i * DP, row = i0 + i;
+            const uint4 w = row < nq && d < a.D ? __ldg(reinterpret_cast<const uint4 *>(q_row(row) + d)) : make_uint4(0, 0, 0, 0);
+            float f[W];
+            unpack(w, f);
+#pragma unroll
+            for (int z = 0; z < W; ++z) Qs[i * LD + d + z] = f[z] * a.scale_log2;
+        }
+    } else {
+        for (int e = threadIdx.x; e < BR * DP; e += kThreads) {
+            const int i = e / DP, d = e - i * DP, row = i0 + i;
+            Qs[i * LD + d] = row < nq && d < a.D ? to_f(q_row(row)[d]) * a.scale_log2 : 0.f;
+        }
+    }
+    int par = 0;
+    for (int32_t k0 = start; k0 < end; k0 += kBK, par ^= 1) {
+        if (k0 > start) __syncthreads();   // the last tile is read out
+        if (vec) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int e = (u * kThreads + (int)threadIdx.x) * W, i = e / DP, d = e - i * DP;
+                float f[W], h[W];
+                unpack(kw[u], f);
+                unpack(vw[u], h);
+                bool fine = true;
+#pragma unroll
+                for (int z = 0; z < W; ++z) fine &= isfinite(h[z]);
+#pragma unroll
+                for (int z = 0; z < W; z += 4) {
+                    *reinterpret_cast<float4 *>(Ks + i * LD + d + z) = make_float4(f[z], f[z + 1], f[z + 2], f[z + 3]);
+                    *reinterpret_cast<float4 *>(Vs + i * LD + d + z) = make_float4(h[z], h[z + 1], h[z + 2], h[z + 3]);
+                }
+                if (!fine && k0 + i >= first) atomicOr(&poison[par], 1u << i);
+            }
+        } else {
+            for (int e = threadIdx.x; e < kBK * DP; e += kThreads) {
+                const int i = e / DP, d = e - i * DP;
+                const int64_t off = rowoff[par][i];
+                const bool in = off >= 0 && d < a.D;
+                const float kx = in ? to_f(static_cast<const T *>(a.k)[off + d]) : 0.f;
+                const float vx = in ? to_f(static_cast<const T *>(a.v)[off + d]) : 0.f;
+                Ks[i * LD + d] = kx;
+                Vs[i * LD + d] = vx;
+                if (k0 + i >= first && !isfinite(vx)) atomicOr(&poison[par], 1u << i);
+            }
+        }
+        if (threadIdx.x < 32) {
+            publish(ahead, par ^ 1);
+            ahead = offset_of(k0 + 2 * kBK + threadIdx.x);
         }
         __syncthreads();
-        const uint32_t bad = poison;
+        const uint32_t bad = poison[par], there = live[par];
+        if (vec && k0 + kBK < end) fetch(par ^ 1);
         if (bad) {
             for (int e = threadIdx.x; e < kBK * DP; e += kThreads) {
                 const int i = e / DP;
@@ -128,11 +218,11 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
             }
             __syncthreads();
         }
-        float s[RPT][4];
+        Pair s2[RPT][4];   // sums over the even and the odd elements
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) s2[i][j] = Pair{0.f, 0.f};
 #pragma unroll 4
         for (int d = 0; d < DP; d += 4) {
             float4 kk[4];
@@ -143,17 +233,20 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
                 const float4 qq = *reinterpret_cast<const float4 *>(Qs + (ty + 16 * i) * LD + d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qq.x, kk[j].x, s[i][j]);
-                    s[i][j] = fmaf(qq.y, kk[j].y, s[i][j]);
-                    s[i][j] = fmaf(qq.z, kk[j].z, s[i][j]);
-                    s[i][j] = fmaf(qq.w, kk[j].w, s[i][j]);
+                    s2[i][j] = fma2(Pair{qq.x, qq.y}, Pair{kk[j].x, kk[j].y}, s2[i][j]);
+                    s2[i][j] = fma2(Pair{qq.z, qq.w}, Pair{kk[j].z, kk[j].w}, s2[i][j]);
                 }
             }
         }
+        float s[RPT][4];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
         __syncwarp();   // this warp's P rows of the last tile are read
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            const uint32_t vis = live & (k0 + kBK <= first ? 0xffffffffu
+            const uint32_t vis = there & (k0 + kBK <= first ? 0xffffffffu
                                                            : tree_vis32(mrow[i], a.mask_words, first, L, k0));
             float top = -INFINITY;
 #pragma unroll
@@ -181,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
 #pragma unroll
             for (int j = 0; j < DJ; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][j][e] *= corr;
+                for (int e = 0; e < 2; ++e) o[i][j][e].x *= corr, o[i][j][e].y *= corr;
         }
         __syncwarp();
 #pragma unroll 2
@@ -198,10 +291,8 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
                         const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-                        o[i][j][0] = fmaf(w, vv.x, o[i][j][0]);
-                        o[i][j][1] = fmaf(w, vv.y, o[i][j][1]);
-                        o[i][j][2] = fmaf(w, vv.z, o[i][j][2]);
-                        o[i][j][3] = fmaf(w, vv.w, o[i][j][3]);
+                        o[i][j][0] = fma2(Pair{w, w}, Pair{vv.x, vv.y}, o[i][j][0]);
+                        o[i][j][1] = fma2(Pair{w, w}, Pair{vv.z, vv.w}, o[i][j][1]);
                     }
                 }
             }
@@ -218,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int d = 4 * tx + 32 * j + e;
-                if (d < a.D) a.ws_o[pr * a.D + d] = o[i][j][e];
+                if (d < a.D) a.ws_o[pr * a.D + d] = e & 1 ? o[i][j][e >> 1].y : o[i][j][e >> 1].x;
             }
         if (tx == 0) {
             a.ws_ml[pr * 2] = m[i];
@@ -237,6 +328,13 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a) {
 // CTA finished are written already.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
+#ifndef MR
+#define MR 2
+#endif
+#ifndef MS
+#define MS 4
+#endif
+constexpr int kMergeRows = MR;
 
 template <typename T, bool kTc>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
@@ -262,8 +360,90 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
         slot0 = (int64_t)blockIdx.x * a.n_chunks;
     }
     const int g = hp / a.groups, tok0 = (hp - g * a.groups) * a.TS;
+    const int rows = min(a.NR, (a.T - tok0) * a.G);
+    if constexpr (kTc) {
+        // head_dim 128: four elements a lane, two rows at a time, four slots' loads of both in flight
+        const int row0 = (blockIdx.y * kMergeWarps + warp) * kMergeRows;
+#pragma unroll 1
+        for (int rr = row0; rr < min(rows, row0 + kMergeRows); rr += MR) {
+            float M[MR], sum[MR];
+            float4 acc[MR];
+#pragma unroll
+            for (int i = 0; i < MR; ++i) {
+                M[i] = -INFINITY;
+                sum[i] = 0.f;
+                acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            for (int base = 0; base < nch; base += 32) {   // lane k: slot base + k
+                float2 ml[MR];
+                float4 v[MR][MS];
+                auto load = [&](int c) {
+#pragma unroll
+                    for (int i = 0; i < MR; ++i)
+#pragma unroll
+                        for (int k = 0; k < MS; ++k)
+                            v[i][k] = rr + i < rows && c + k < nch
+                                          ? *reinterpret_cast<const float4 *>(
+                                                a.ws_o + ((slot0 + c + k) * a.NR + rr + i) * 128 + 4 * lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    ml[i] = rr + i < rows && base + lane < nch
+                                ? *reinterpret_cast<const float2 *>(a.ws_ml + ((slot0 + base + lane) * a.NR + rr + i) * 2)
+                                : make_float2(-INFINITY, 0.f);
+                load(base);
+                float w[MR];
+#pragma unroll
+                for (int i = 0; i < MR; ++i) {
+                    float top = ml[i].x;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float mn = fmaxf(M[i], top);
+                    const float corr = mn == -INFINITY ? 1.f : exp2f(M[i] - mn);   // of the slots before
+                    w[i] = ml[i].x == -INFINITY ? 0.f : exp2f(ml[i].x - mn);
+                    // a part that saw nothing but NaN scores has no maximum, and a NaN sum
+                    float part = (ml[i].x == -INFINITY && ml[i].y != ml[i].y ? 1.f : w[i]) * ml[i].y;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+                    sum[i] = fmaf(sum[i], corr, part);
+                    acc[i].x *= corr, acc[i].y *= corr, acc[i].z *= corr, acc[i].w *= corr;
+                    M[i] = mn;
+                }
+                for (int c = base; c < min(nch, base + 32); c += MS) {
+                    if (c > base) load(c);
+#pragma unroll
+                    for (int k = 0; k < MS; ++k)
+#pragma unroll
+                        for (int i = 0; i < MR; ++i) {
+                            const float wk = __shfl_sync(0xffffffffu, w[i], (c + k) & 31);
+                            acc[i].x = fmaf(wk, v[i][k].x, acc[i].x);
+                            acc[i].y = fmaf(wk, v[i][k].y, acc[i].y);
+                            acc[i].z = fmaf(wk, v[i][k].z, acc[i].z);
+                            acc[i].w = fmaf(wk, v[i][k].w, acc[i].w);
+                        }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MR; ++i) {
+                const int row = rr + i;
+                if (row >= rows) break;
+                const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+                T *out = static_cast<T *>(a.out) +
+                         (((int64_t)r * a.T + tok0 + row / a.G) * a.H_q + g * a.G + row % a.G) * 128 + 4 * lane;
+                T o4[4];
+                store_out(o4, acc[i].x * inv);
+                store_out(o4 + 1, acc[i].y * inv);
+                store_out(o4 + 2, acc[i].z * inv);
+                store_out(o4 + 3, acc[i].w * inv);
+                if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(o4);
+                else *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<const uint4 *>(o4);
+            }
+        }
+        return;
+    }
     const int row = blockIdx.y * kMergeWarps + warp;
-    if (row >= min(a.NR, (a.T - tok0) * a.G)) return;
+    if (row >= rows) return;
     const int t = tok0 + row / a.G, h = g * a.G + row % a.G;
     T *out = static_cast<T *>(a.out) + (((int64_t)r * a.T + t) * a.H_q + h) * a.D;
     auto ml_of = [&](int c) {
@@ -353,10 +533,10 @@ static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, in
     const int64_t nq = (int64_t)T * G;
     const int64_t units = (int64_t)num_reqs * H_kv;
     const int64_t sms = current_sm_count();
-    // splits hold whole blocks, of 128 positions at least; about four CTAs an SM where the batch alone has fewer
-    const int64_t align = (int64_t)bs / gcd64(bs, 128) * 128;
+    // splits hold whole blocks, of 128 positions at least; about CCN CTAs an SM where the batch alone has fewer
+    const int64_t align = (int64_t)bs / gcd64(bs, CCA) * CCA;
     const int64_t row_tiles = ceil_div<int64_t>(nq, 64);
-    int64_t chunk = ceil_div<int64_t>((int64_t)max_ctx * units * row_tiles, 4 * sms);
+    int64_t chunk = ceil_div<int64_t>((int64_t)max_ctx * units * row_tiles, CCN * sms);
     chunk = ceil_div<int64_t>(chunk < 1 ? 1 : chunk, align) * align;
     if (chunk > (int64_t)1 << 30) return false;
     p->chunk = (int32_t)chunk;
@@ -393,26 +573,44 @@ static cudaError_t launch_cc(const TreeArgs &a, cudaStream_t st) {
         }
     }
     const dim3 grid((unsigned)(a.num_reqs * a.H_kv * a.n_chunks), (unsigned)ceil_div(a.T * a.G, BR));
-    return launch_pdl(kern, grid, dim3(kThreads), smem, st, a);
+    // rows of whole 16-byte pieces
+    const bool vec = a.D * sizeof(T) % 16 == 0 && aligned(a.q, 16) && aligned(a.k, 16) && aligned(a.v, 16);
+    return launch_pdl(kern, grid, dim3(kThreads), smem, st, a, vec);
 }
 
-// Few rows take the small query tile (16 rows), more the large one (64; 32 with
-// head_dim above 128, for its registers).
+// The query tile (16, 32, 48 or 64 rows; up to 32 with head_dim above 128, for
+// its registers) that leaves the fewest rows idle, the larger of two.
+static int query_tile(int32_t nq, int32_t D) {
+    int best = 16;
+    for (int br = 32; br <= (D > 128 ? 32 : 64); br += 16)
+        if (ceil_div(nq, br) * br <= ceil_div(nq, best) * best) best = br;
+    return best;
+}
+
+template <typename T, int DP>
+static cudaError_t launch_cc_rows(const TreeArgs &a, cudaStream_t st) {
+    const int br = query_tile(a.T * a.G, a.D);
+    if constexpr (DP <= 128) {
+        if (br == 64) return launch_cc<T, DP, 64>(a, st);
+        if (br == 48) return launch_cc<T, DP, 48>(a, st);
+    }
+    return br == 32 ? launch_cc<T, DP, 32>(a, st) : launch_cc<T, DP, 16>(a, st);
+}
+
 template <typename T>
 static cudaError_t launch_cc_dims(const TreeArgs &a, cudaStream_t st) {
-    const bool few = a.T * a.G <= 16;
-    if (a.D <= 32) return few ? launch_cc<T, 32, 16>(a, st) : launch_cc<T, 32, 64>(a, st);
-    if (a.D <= 64) return few ? launch_cc<T, 64, 16>(a, st) : launch_cc<T, 64, 64>(a, st);
-    if (a.D <= 128) return few ? launch_cc<T, 128, 16>(a, st) : launch_cc<T, 128, 64>(a, st);
-    return few ? launch_cc<T, 256, 16>(a, st) : launch_cc<T, 256, 32>(a, st);
+    if (a.D <= 32) return launch_cc_rows<T, 32>(a, st);
+    if (a.D <= 64) return launch_cc_rows<T, 64>(a, st);
+    if (a.D <= 128) return launch_cc_rows<T, 128>(a, st);
+    return launch_cc_rows<T, 256>(a, st);
 }
 
 template <bool kTc>
 static int launch_merge(const TreeArgs &a, cudaStream_t st) {
     const int64_t x = (int64_t)(kTc ? a.P : a.num_reqs) * a.H_kv * a.groups;
-    const dim3 grid((unsigned)x, (unsigned)ceil_div(a.NR, kMergeWarps)), block(kMergeWarps * 32);
+    const dim3 grid((unsigned)x, (unsigned)ceil_div(a.NR, kMergeWarps * (kTc ? kMergeRows : 1))), block(kMergeWarps * 32);
     const cudaError_t e = a.dtype == BKV_BF16 ? launch_pdl(tree_merge_kernel<__nv_bfloat16, kTc>, grid, block, 0, st, a)
-                                              : launch_pdl(tree_merge_kernel<float, kTc>, grid, block, 0, st, a);
+                                              : launch_pdl(tree_merge_kernel<float, false>, grid, block, 0, st, a);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }
@@ -449,7 +647,7 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
     if (mask_req_stride != 0 && mask_req_stride < (int64_t)q_len * words) return BKV_ERR_INVALID_ARG;
     if (!q || !out || !context_lens || !tree_mask || (bt_cols > 0 && !block_table)) return BKV_ERR_INVALID_ARG;
     if (max_context_len > 0 && (!k_cache || !v_cache)) return BKV_ERR_INVALID_ARG;
-    if (workspace_bytes < plan.ws_bytes || !workspace || !aligned(workspace, 16)) return BKV_ERR_INVALID_ARG;
+    if (workspace_bytes < plan.ws_bytes || !workspace || !aligned(workspace, 32)) return BKV_ERR_INVALID_ARG;
     if (!(softmax_scale > 0.f)) softmax_scale = 1.0f / sqrtf((float)head_dim);
     TreeArgs a{};
     a.q = q;

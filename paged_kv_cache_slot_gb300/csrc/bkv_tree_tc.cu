@@ -56,6 +56,10 @@ constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (
 constexpr int kTimeoutErr = 1 << 24;
 constexpr int kMaxReqs = 2048;
 constexpr float kSlack = 8.f;
+#ifndef EC
+#define EC 1
+#endif
+constexpr int kEndCost = EC;             // tiles that a unit's end takes as long as
 #ifndef QB
 #define QB 1
 #endif
@@ -91,6 +95,14 @@ struct Ring {
 __host__ __device__ constexpr uint32_t col_s(int x) { return 128u * (uint32_t)x; }
 __host__ __device__ constexpr uint32_t col_o(int x) { return 256u + 128u * (uint32_t)x; }
 
+// 32 bytes of one row (a whole sector: a thread's rows lie apart, and 16-byte
+// stores would touch each line twice as often).
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float tree_max32(const float (&v)[32]) {
     float t[16];
 #pragma unroll
@@ -108,23 +120,25 @@ struct Unit {
     bool whole;
 };
 
-// Walks this CTA's units: column q's share of the tiles laid end to end.
+// Walks this CTA's units.  pre[r] is the cost of the requests before r: a tile
+// costs 1 and a unit's end (the last softmax, the wait for the last P V, the
+// output: nothing else runs meanwhile) kEndCost, laid behind the request's
+// tiles.  Column q takes the tiles in its share of the whole cost.
 struct Units {
     const int32_t *pre;
     const uint8_t *fill;
-    int n, r, q, P;
-    int64_t t, t1;
+    int n, r, q;
+    int64_t t, t1, C, peff;
     __device__ Units(const TreeArgs &a, const int32_t *pre_, const uint8_t *fill_, int q_) {
         pre = pre_;
         fill = fill_;
         n = a.num_reqs;
         q = q_;
-        P = a.P;
-        const int64_t TP = pre[n];
-        const int64_t peff = TP < a.P ? TP : a.P;
-        t = q < peff ? TP * q / peff : TP;
-        t1 = q < peff ? TP * (q + 1) / peff : TP;
-        int lo = 0, hi = n;   // first request whose tiles end after t
+        C = pre[n];
+        peff = C < a.P ? C : a.P;
+        t = q < peff ? C * q / peff : C;
+        t1 = q < peff ? C * (q + 1) / peff : C;
+        int lo = 0, hi = n;   // first request whose cost ends after t
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid + 1] > t) hi = mid;
@@ -137,25 +151,29 @@ struct Units {
     __device__ int4 split() const {
         if (t >= t1) return make_int4(0, 0, 0, 0);
         int r1 = r;
-        while (pre[r1 + 1] < t1) ++r1;   // the request of tile t1 - 1
-        const int64_t TP = pre[n], peff = TP < P ? TP : P;
-        if (pre[r1 + 1] == t1 || pre[r1] < t) return make_int4(0, 0, 0, 0);
-        const int q1 = (int)(((int64_t)pre[r1 + 1] * peff - 1) / TP);   // the column of its last tile
+        while (pre[r1 + 1] < t1) ++r1;   // the request that the share ends in
+        const int64_t s = pre[r1], e = pre[r1 + 1] - kEndCost;   // its tiles
+        if (s < t || s >= t1 || e <= t1) return make_int4(0, 0, 0, 0);
+        const int q1 = (int)((e * peff - 1) / C);   // the column of its last tile
         return make_int4(r1, q1 - q + 1, q + r1, 0);
     }
     __device__ bool next(Unit &x) {
-        if (t >= t1) return false;
-        while (pre[r + 1] <= t) ++r;
-        const int s = pre[r], e = pre[r + 1];
-        x.r = r;
-        x.L = (e - s - 1) * kTile + fill[r] + 1;
-        x.f = (int)(t - s);
-        const int end = t1 < e ? (int)(t1 - s) : e - s;
-        x.nt = end - x.f;
-        x.whole = x.nt == e - s;
-        x.slot = q + r;
-        t = s + end;
-        return true;
+        for (; t < t1; ++r) {
+            const int64_t s = pre[r], e = pre[r + 1] - kEndCost;
+            if (pre[r + 1] <= t) continue;   // no tiles (or passed)
+            const int64_t lo = t, hi = t1 < e ? t1 : e;
+            t = pre[r + 1];
+            if (lo >= hi) continue;   // only the end's share of the request is this column's
+            x.r = r;
+            x.f = (int)(lo - s);
+            x.nt = (int)(hi - lo);
+            x.L = (int)(e - s - 1) * kTile + fill[r] + 1;
+            x.whole = lo == s && hi == e;
+            x.slot = q + r;
+            ++r;
+            return true;
+        }
+        return false;
     }
 };
 
@@ -253,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t L = tree_len(a, c);
         if (c > a.max_ctx && blockIdx.x == 0 && a.err) atomicAdd(a.err, 1);
         fill[r] = (uint8_t)((L - 1) & (kTile - 1));
-        pre[r] = (L + kTile - 1) / kTile;
+        pre[r] = L > 0 ? (L + kTile - 1) / kTile + kEndCost : 0;
     }
     __syncthreads();
     if (warp == 0) {   // exclusive prefix sum of the tiles
@@ -780,21 +798,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!valid) continue;
                     if (x.whole) {
 #pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4) {
-                            uint32_t w[4];
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
+                            for (int e = 0; e < 8; ++e) {
                                 const __nv_bfloat162 h2 =
-                                    __floats2bfloat162_rn(ov[8 * q4 + 2 * e] * inv, ov[8 * q4 + 2 * e + 1] * inv);
+                                    __floats2bfloat162_rn(ov[16 * h + 2 * e] * inv, ov[16 * h + 2 * e + 1] * inv);
                                 w[e] = *reinterpret_cast<const uint32_t *>(&h2);
                             }
-                            *reinterpret_cast<uint4 *>(out + 32 * c + 8 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+                            store32(out + 32 * c + 16 * h, w);
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(po + 32 * c + k) =
-                                make_float4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+                        for (int k = 0; k < 32; k += 8) store32(po + 32 * c + k, reinterpret_cast<uint32_t *>(ov + k));
                     }
                 }
                 if (!x.whole && valid && kh == 0 && (dual || xb == 0))
@@ -870,10 +886,10 @@ bool prepare_tree_tc(const TreeArgs &a, TreeTc *t) {
     if (a.bs < 8 || !((kTile % a.bs == 0) || (a.bs % kTile == 0))) return false;
     if (a.num_reqs > kMaxReqs || (int64_t)a.num_reqs * a.T >= ((int64_t)1 << 31)) return false;
     if (a.total_blocks <= 0 || (int64_t)a.total_blocks * a.bs >= ((int64_t)1 << 31)) return false;
-    // the tiles' prefix stays within int32
-    if ((int64_t)a.num_reqs * ((a.max_ctx + (int64_t)kTile - 1) / kTile) >= ((int64_t)1 << 31)) return false;
+    // the costs' prefix stays within int32
+    if ((int64_t)a.num_reqs * ((a.max_ctx + (int64_t)kTile - 1) / kTile + kEndCost) >= ((int64_t)1 << 31)) return false;
     if ((int64_t)a.P * a.H_kv * a.groups >= ((int64_t)1 << 31)) return false;
-    if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q, 16) || !aligned(a.out, 16)) return false;
+    if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q, 16) || !aligned(a.out, 32)) return false;
     if (!encode_fn()) return false;
     ring_shape(a, &t->sh);
     const uint64_t rows = (uint64_t)a.total_blocks * (uint64_t)a.bs;
