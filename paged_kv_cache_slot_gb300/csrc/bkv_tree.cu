@@ -25,12 +25,6 @@ static constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxT = 256;       // tree tokens a request
 constexpr int kBK = 32;          // keys a tile of the CUDA-core kernel
 constexpr int kThreads = 128;
-#ifndef CCA
-#define CCA 64
-#endif
-#ifndef CCN
-#define CCN 8
-#endif
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -328,16 +322,11 @@ __global__ void __launch_bounds__(kThreads) tree_cc_kernel(const TreeArgs a, boo
 // CTA finished are written already.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
-#ifndef MR
-#define MR 2
-#endif
-#ifndef MS
-#define MS 4
-#endif
-constexpr int kMergeRows = MR;
 
-template <typename T, bool kTc>
+// MR rows of a warp at a time, MS of their slots in flight (tensor-core kernel's streams; MR 0: the others).
+template <typename T, int MR, int MS>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
+    constexpr bool kTc = MR > 0;
     constexpr int kUnroll = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
@@ -361,11 +350,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     }
     const int g = hp / a.groups, tok0 = (hp - g * a.groups) * a.TS;
     const int rows = min(a.NR, (a.T - tok0) * a.G);
-    if constexpr (kTc) {
-        // head_dim 128: four elements a lane, two rows at a time, four slots' loads of both in flight
-        const int row0 = (blockIdx.y * kMergeWarps + warp) * kMergeRows;
+    if constexpr (MR > 0) {
+        // head_dim 128: four elements a lane
+        const int row0 = (blockIdx.y * kMergeWarps + warp) * MR;
 #pragma unroll 1
-        for (int rr = row0; rr < min(rows, row0 + kMergeRows); rr += MR) {
+        for (int rr = row0; rr < min(rows, row0 + MR); rr += MR) {
             float M[MR], sum[MR];
             float4 acc[MR];
 #pragma unroll
@@ -533,10 +522,10 @@ static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, in
     const int64_t nq = (int64_t)T * G;
     const int64_t units = (int64_t)num_reqs * H_kv;
     const int64_t sms = current_sm_count();
-    // splits hold whole blocks, of 128 positions at least; about CCN CTAs an SM where the batch alone has fewer
-    const int64_t align = (int64_t)bs / gcd64(bs, CCA) * CCA;
+    // splits hold whole blocks, of 64 positions at least; about eight CTAs an SM where the batch alone has fewer
+    const int64_t align = (int64_t)bs / gcd64(bs, 64) * 64;
     const int64_t row_tiles = ceil_div<int64_t>(nq, 64);
-    int64_t chunk = ceil_div<int64_t>((int64_t)max_ctx * units * row_tiles, CCN * sms);
+    int64_t chunk = ceil_div<int64_t>((int64_t)max_ctx * units * row_tiles, 8 * sms);
     chunk = ceil_div<int64_t>(chunk < 1 ? 1 : chunk, align) * align;
     if (chunk > (int64_t)1 << 30) return false;
     p->chunk = (int32_t)chunk;
@@ -605,12 +594,13 @@ static cudaError_t launch_cc_dims(const TreeArgs &a, cudaStream_t st) {
     return launch_cc_rows<T, 256>(a, st);
 }
 
-template <bool kTc>
+template <int MR, int MS>
 static int launch_merge(const TreeArgs &a, cudaStream_t st) {
-    const int64_t x = (int64_t)(kTc ? a.P : a.num_reqs) * a.H_kv * a.groups;
-    const dim3 grid((unsigned)x, (unsigned)ceil_div(a.NR, kMergeWarps * (kTc ? kMergeRows : 1))), block(kMergeWarps * 32);
-    const cudaError_t e = a.dtype == BKV_BF16 ? launch_pdl(tree_merge_kernel<__nv_bfloat16, kTc>, grid, block, 0, st, a)
-                                              : launch_pdl(tree_merge_kernel<float, false>, grid, block, 0, st, a);
+    const int64_t x = (int64_t)(MR ? a.P : a.num_reqs) * a.H_kv * a.groups;
+    const dim3 grid((unsigned)x, (unsigned)ceil_div(a.NR, kMergeWarps * (MR ? MR : 1))), block(kMergeWarps * 32);
+    cudaError_t e;
+    if (MR || a.dtype == BKV_BF16) e = launch_pdl(tree_merge_kernel<__nv_bfloat16, MR, MS>, grid, block, 0, st, a);
+    else e = launch_pdl(tree_merge_kernel<float, 0, 0>, grid, block, 0, st, a);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }
@@ -689,7 +679,10 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
         if (prepare_tree_tc(a, &t)) {
             set_slots(plan.slots_tc);
             const int rc = launch_tree_tc(a, t, st);
-            return rc != BKV_OK ? rc : launch_merge<true>(a, st);
+            if (rc != BKV_OK) return rc;
+            // few rows: one a warp, all its loads at once (28 rows of 8 streams 11.8 us a call, 13.1 by two
+            // rows); many: two a warp (244 rows of 128 streams 113 us a call, 117 by one)
+            return a.NR <= 32 ? launch_merge<1, 8>(a, st) : launch_merge<2, 4>(a, st);
         }
     }
     // one query-row group for all tokens: the CUDA-core kernel's slots
@@ -700,5 +693,5 @@ extern "C" int bkv_paged_decode_tree(const void *q, const void *k_cache, const v
     const cudaError_t e = dtype == BKV_BF16 ? launch_cc_dims<__nv_bfloat16>(a, st) : launch_cc_dims<float>(a, st);
     if (e != cudaSuccess) set_cuda_error(e);
     const int rc = launch_status();
-    return rc != BKV_OK ? rc : launch_merge<false>(a, st);
+    return rc != BKV_OK ? rc : launch_merge<0, 0>(a, st);
 }

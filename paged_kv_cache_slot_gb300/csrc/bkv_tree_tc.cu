@@ -19,10 +19,14 @@
 //   tensor memory), so that one stream's softmax runs beside the other's MMAs;
 //   their O are joined when the unit ends.  A group of two query tiles gives
 //   each its own stream, and every K and V tile serves both.
-// * Warp roles (608 threads): warp 0 loads Q and gathers K tiles, the last warp
-//   gathers V tiles (2-slot rings of 32 KB), warp 1 issues every MMA from one
-//   thread; eight softmax warps a stream, four lane quarters times two halves
-//   of a tile's keys, one query row a thread; quarters without rows are idle.
+// * Warp roles (352 threads): warp 0 loads Q and gathers K tiles, the last warp
+//   gathers V tiles (rings of two or three 32 KB slots each, as the queries leave
+//   room), warp 1 issues every MMA from one thread; four softmax warps a stream,
+//   one query row a thread.  A row's 128 scores stay in its thread's registers
+//   between the max and the weights: the lanes' quarters are tied to the SM's
+//   four partitions, so two warps a row would share one exponential unit anyway
+//   (128 rows of a tile take 1024 cycles of it) and pay for exchanging their
+//   maxima.  Quarters without rows mend the V tiles instead (below).
 // * P (bf16, two per column) goes over its own S columns and enters P V from
 //   tensor memory.  The running max is a lazy reference (it moves when a tile's
 //   max passes it by 8 in log2 units), so O is seldom rescaled.
@@ -50,14 +54,17 @@ constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
 constexpr int kHalfBytes = kTile * 128;
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kThreads = 608;
+constexpr int kThreads = 352;   // K producer, MMA issuer, 2 x 4 softmax warps, V producer
 constexpr int kWarpV = kThreads / 32 - 1;
 constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (128 columns each)
 constexpr int kTimeoutErr = 1 << 24;
 constexpr int kMaxReqs = 2048;
 constexpr float kSlack = 8.f;
+#ifndef TW
+#define TW 1
+#endif
 #ifndef EC
-#define EC 1
+#define EC 3
 #endif
 constexpr int kEndCost = EC;             // tiles that a unit's end takes as long as
 #ifndef QB
@@ -68,16 +75,16 @@ constexpr int kMaxStages = 3;                             // slots of a ring, at
 constexpr int kOffMask = 0;                               // 8 words: loaded segments per tile (ring)
 constexpr int kOffPoison = kOffMask + 8 * 4;              // 8 x 32 bytes: V rows of the tile that are not finite
 constexpr int kOffBar = kOffPoison + 8 * 32;
-constexpr int kNumBars = 4 * kMaxStages + 4 + 2 + 2 + 2 + 8 + 8 + 4;
+constexpr int kNumBars = 4 * kMaxStages + 4 + 2 + 2 + 2 + 8 + 4;
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 4;
-constexpr int kOffPre = (kOffAbort + 4 + 15) / 16 * 16;   // [kMaxReqs + 1] tiles before request r
+constexpr int kOffAnyBad = kOffAbort + 4;                 // a V row that was not finite has been met
+constexpr int kOffSums = kOffAnyBad + 4;                  // [warps] prefix sum's scratch
+constexpr int kOffPre = (kOffSums + kThreads / 32 * 4 + 15) / 16 * 16;   // [kMaxReqs + 1] tiles before request r
 constexpr int kOffFill = kOffPre + (kMaxReqs + 4) * 4;    // [kMaxReqs] positions of its last tile, less one
-constexpr int kOffXmax = kOffFill + kMaxReqs;             // [stream][half][tile parity][row]
-constexpr int kOffXm = kOffXmax + 2 * 2 * 2 * kTile * 4;  // [stream][row]
-constexpr int kOffXsum = kOffXm + 2 * kTile * 4;          // [stream][half][row]
+constexpr int kOffXm = kOffFill + kMaxReqs;               // [stream][row] running max, weight sum
 // queries, then the K and V rings: what a launch needs of the rest (see ring_shape)
-constexpr int kOffQ = (kOffXsum + 2 * 2 * kTile * 4 + 1023) / 1024 * 1024;
+constexpr int kOffQ = (kOffXm + 2 * kTile * 8 + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024 - 1024;               // less the slack for 1024 alignment
 
 // A ring slot and its phase parity.
@@ -103,15 +110,70 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *w) {
                  : "memory");
 }
 
-__device__ __forceinline__ float tree_max32(const float (&v)[32]) {
-    float t[16];
+// 32 fp32 columns of this thread's lane, without the wait; use32 after it keeps
+// the compiler from reading them earlier.
+__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void use32(float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = fmaxf(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// Max of 32 values, three at a time.
+__device__ __forceinline__ float max32(const float (&v)[32]) {
+    float t[11];
 #pragma unroll
-    for (int w = 8; w > 0; w >>= 1)
-#pragma unroll
-        for (int i = 0; i < w; ++i) t[i] = fmaxf(t[2 * i], t[2 * i + 1]);
-    return t[0];
+    for (int i = 0; i < 10; ++i) t[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+    t[10] = fmaxf(v[30], v[31]);
+    return max3(max3(max3(t[0], t[1], t[2]), max3(t[3], t[4], t[5]), max3(t[6], t[7], t[8])), t[9], t[10]);
+}
+
+// Two fp32 operations in one instruction, each rounded as the single one.
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// Whether a phase is over, without waiting (try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // One unit: tiles [f, f + nt) of request r.  whole: they are all of its tiles.
@@ -127,18 +189,16 @@ struct Unit {
 struct Units {
     const int32_t *pre;
     const uint8_t *fill;
-    int n, r, q;
-    int64_t t, t1, C, peff;
+    int r, q, t, t1;
     __device__ Units(const TreeArgs &a, const int32_t *pre_, const uint8_t *fill_, int q_) {
         pre = pre_;
         fill = fill_;
-        n = a.num_reqs;
         q = q_;
-        C = pre[n];
-        peff = C < a.P ? C : a.P;
-        t = q < peff ? C * q / peff : C;
-        t1 = q < peff ? C * (q + 1) / peff : C;
-        int lo = 0, hi = n;   // first request whose cost ends after t
+        const int64_t C = pre[a.num_reqs];
+        const int64_t peff = C < a.P ? C : a.P;
+        t = (int)(q < peff ? C * q / peff : C);
+        t1 = (int)(q < peff ? C * (q + 1) / peff : C);
+        int lo = 0, hi = a.num_reqs;   // first request whose cost ends after t
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid + 1] > t) hi = mid;
@@ -148,26 +208,27 @@ struct Units {
     }
     // The stream that this column begins and does not end (before next() is called): its request, how
     // many columns share it, and its first slot past the head's; all 0 without one.
-    __device__ int4 split() const {
+    __device__ int4 split(const TreeArgs &a) const {
         if (t >= t1) return make_int4(0, 0, 0, 0);
         int r1 = r;
         while (pre[r1 + 1] < t1) ++r1;   // the request that the share ends in
-        const int64_t s = pre[r1], e = pre[r1 + 1] - kEndCost;   // its tiles
+        const int s = pre[r1], e = pre[r1 + 1] - kEndCost;   // its tiles
         if (s < t || s >= t1 || e <= t1) return make_int4(0, 0, 0, 0);
+        const int64_t C = pre[a.num_reqs], peff = C < a.P ? C : a.P;
         const int q1 = (int)((e * peff - 1) / C);   // the column of its last tile
         return make_int4(r1, q1 - q + 1, q + r1, 0);
     }
     __device__ bool next(Unit &x) {
         for (; t < t1; ++r) {
-            const int64_t s = pre[r], e = pre[r + 1] - kEndCost;
+            const int s = pre[r], e = pre[r + 1] - kEndCost;
             if (pre[r + 1] <= t) continue;   // no tiles (or passed)
-            const int64_t lo = t, hi = t1 < e ? t1 : e;
+            const int lo = t, hi = t1 < e ? t1 : e;
             t = pre[r + 1];
             if (lo >= hi) continue;   // only the end's share of the request is this column's
             x.r = r;
-            x.f = (int)(lo - s);
-            x.nt = (int)(hi - lo);
-            x.L = (int)(e - s - 1) * kTile + fill[r] + 1;
+            x.f = lo - s;
+            x.nt = hi - lo;
+            x.L = (e - s - 1) * kTile + fill[r] + 1;
             x.whole = lo == s && hi == e;
             x.slot = q + r;
             ++r;
@@ -189,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *poison = smem + kOffPoison;   // [tile & 7][32], four rows a byte
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmemSlot);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
+    int32_t *warp_sums = reinterpret_cast<int32_t *>(smem + kOffSums);
+    volatile int *any_bad = reinterpret_cast<volatile int *>(smem + kOffAnyBad);
     int32_t *pre = reinterpret_cast<int32_t *>(smem + kOffPre);
     uint8_t *fill = smem + kOffFill;
     const uint32_t bar0 = sbase + kOffBar;
@@ -204,9 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar_ofull = bar0 + 8u * (kB + 8);
     const uint32_t bar_oempty = bar0 + 8u * (kB + 9);
     auto bar_mask = [&](int m) { return bar0 + 8u * (kB + 10 + m); };
-    // the two warps (one per key half) of a lane quarter of a stream; the four of a quarter of both
-    auto bar_pair = [&](int x, int qw) { return bar0 + 8u * (kB + 18 + 4 * x + qw); };
-    auto bar_quad = [&](int qw) { return bar0 + 8u * (kB + 26 + qw); };
+    // the two streams' warps of a lane quarter
+    auto bar_pair = [&](int qw) { return bar0 + 8u * (kB + 18 + qw); };
     const int seg_rows = sh.seg_rows, tok_per_tile = sh.tok_per_tile, box_tok = sh.box_tok;
     const int nK = sh.k_stages, nV = sh.v_stages;
     const int off_v = kOffQ + sh.q_bytes + nK * kTileBytes;
@@ -239,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar_qfull(x), 1);
             mbar_init(bar_qempty(x), 1);
             mbar_init(bar_sfull(x), 1);
-            mbar_init(bar_pfull(x), (!dual || x == 0) ? 8 : 2 * aq1);
-            for (int qw = 0; qw < 4; ++qw) mbar_init(bar_pair(x, qw), 2);
+            mbar_init(bar_pfull(x), (!dual || x == 0) ? 4 : aq1);
         }
         mbar_init(bar_ofull, 2);
-        mbar_init(bar_oempty, 2 * (aq0 + aq1));
+        mbar_init(bar_oempty, aq0 + aq1);
         for (int m = 0; m < 8; ++m) mbar_init(bar_mask(m), 1);
-        for (int qw = 0; qw < 4; ++qw) mbar_init(bar_quad(qw), 4);
+        for (int qw = 0; qw < 4; ++qw) mbar_init(bar_pair(qw), 2);
         *abort_flag = 0;
+        *any_bad = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0 && lane == 0) {
@@ -266,45 +328,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     pdl_wait();   // global memory is read from here on
     pdl_trigger();
-    for (int r = threadIdx.x; r < a.num_reqs; r += kThreads) {
-        const int32_t c = __ldg(a.ctx + r);
-        const int32_t L = tree_len(a, c);
-        if (c > a.max_ctx && blockIdx.x == 0 && a.err) atomicAdd(a.err, 1);
-        fill[r] = (uint8_t)((L - 1) & (kTile - 1));
-        pre[r] = L > 0 ? (L + kTile - 1) / kTile + kEndCost : 0;
-    }
-    __syncthreads();
-    if (warp == 0) {   // exclusive prefix sum of the tiles
-        const int n = a.num_reqs;
-        const int per = (n + 31) / 32;
-        const int lo = min(n, lane * per), hi = min(n, lo + per);
+    // costs of the requests and their exclusive prefix sum: a run of requests a thread
+    {
+        const int n = a.num_reqs, per = (n + kThreads - 1) / kThreads;
+        const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
         int32_t sum = 0;
-        for (int r = lo; r < hi; ++r) sum += pre[r];
+        for (int r = lo; r < hi; ++r) {
+            const int32_t c = __ldg(a.ctx + r);
+            const int32_t L = tree_len(a, c);
+            if (c > a.max_ctx && blockIdx.x == 0 && a.err) atomicAdd(a.err, 1);
+            fill[r] = (uint8_t)((L - 1) & (kTile - 1));
+            const int32_t cost = L > 0 ? (L + kTile - 1) / kTile + kEndCost : 0;
+            pre[r] = cost;
+            sum += cost;
+        }
         int32_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+            const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
         }
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
         int32_t run = inc - sum;
+        for (int w = 0; w < warp; ++w) run += warp_sums[w];
         for (int r = lo; r < hi; ++r) {
-            const int32_t t = pre[r];
+            const int32_t cost = pre[r];
             pre[r] = run;
-            run += t;
+            run += cost;
         }
-        if (lane == 31) pre[n] = inc;
+        if (threadIdx.x == kThreads - 1) pre[n] = run;
     }
     __syncthreads();
-    // the merge's table, and the rows of requests without a position
-    if (hp == 0 && threadIdx.x == 32) a.ws_split[q] = Units(a, pre, fill, q).split();
-    for (int r = q; r < a.num_reqs; r += a.P) {
-        if (pre[r + 1] > pre[r]) continue;
-        for (int e = threadIdx.x; e < ntok * G * (kD / 8); e += kThreads) {
-            const int row = e / (kD / 8), t = tok0 + row / G, h = g * G + row % G;
-            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                      (((int64_t)r * a.T + t) * a.H_q + h) * kD)[e % (kD / 8)] = make_uint4(0, 0, 0, 0);
-        }
-    }
     const uint32_t tmem = *tmem_slot;
     const int nseg = kTile / seg_rows;
     const int seg_shift = 31 - __clz(seg_rows);
@@ -346,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 4; ++h) rows |= ((m8 >> (8 * h)) & 0xffu) ? 1u << h : 0u;
                     if ((rows >> (lane >> 3)) & 1u) v0[e] = v1[e] = make_uint4(0, 0, 0, 0);
+                    if (lane == 0) *any_bad = 1;
                 }
                 if (lane == 0) bad_rows[i] = (uint8_t)rows;
             }
@@ -444,9 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t v_base = sm_v + s * kTileBytes;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk) {
-                    // P of keys 0..63 lies over S columns 0..31, of keys 64..127 over columns 64..95
-                    const uint32_t pcol = (kk < 4 ? 0u : 64u) + 8u * (uint32_t)(kk & 3);
-                    mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + pcol, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
+                    mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + 8u * (uint32_t)kk, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
                                 kIdescO, (first && kk == 0) ? 0u : 1u);
                 }
                 return true;
@@ -492,8 +546,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int b = nbuf == 2 ? uq & 1 : 0;
                     const uint32_t qphase = (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1);
                     for (int kt = 0; kt < x.nt; ++kt, xb ^= 1) {
-                        ok = settle(xb) && (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
-                             mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
+                        // operands that are there already are not waited for between P V and S: the tensor
+                        // cores run dry in the time that a barrier takes to answer
+#if TW
+                        const bool ready = (kt > 0 || mbar_test(bar_qfull(b), qphase)) && mbar_test(bar_kfull(kr.slot), kr.phase);
+#else
+                        const bool ready = false;
+#endif
+                        ok = settle(xb);
+                        if (ok && !ready)
+                            ok = (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
+                                 mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
                         if (!ok) break;
                         tc_fence_after();
                         issue_s(xb, kr.slot, b);
@@ -542,69 +605,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ====== softmax: stream xb, key half kh, lane quarter qw, one query row a thread ======
-        const int xb = (warp - 2) >> 3;
-        const int kh = ((warp - 2) >> 2) & 1;
+        // ====== softmax: stream xb, lane quarter qw, one query row a thread ======
+        // the merge's table, and the rows of requests without a position
+        if (hp == 0 && threadIdx.x == 64) a.ws_split[q] = Units(a, pre, fill, q).split(a);
+        for (int r = q; r < a.num_reqs; r += a.P) {
+            if (pre[r + 1] > pre[r]) continue;
+            for (int e = (int)threadIdx.x - 64; e < ntok * G * (kD / 8); e += 256) {
+                const int row = e / (kD / 8), t = tok0 + row / G, h = g * G + row % G;
+                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                          (((int64_t)r * a.T + t) * a.H_q + h) * kD)[e % (kD / 8)] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        const int xb = (warp - 2) >> 2;
         const int qw = warp & 3;
         const int aq = xb ? aq1 : aq0;
         const bool fixes = !dual || xb == 0;   // V serves both query tiles: the first one's stream mends it
+        Ring vr;             // the V slot of the tile at hand
+        int j = 0;           // tiles of this CTA before the unit
+        int ns = 0;          // S tiles of this stream seen so far
+        bool ok = true;
+        Units units(a, pre, fill, q);
+        Unit x;
         if (qw >= aq) {
             // a quarter without rows: it mends the stream's V tiles beside the softmax
-            if (fixes) {
-                Ring vr;
-                int j = 0, ns = 0;
-                bool ok = true;
-                Units units(a, pre, fill, q);
-                Unit x;
-                while (ok && units.next(x)) {
-                    for (int kt = 0; kt < x.nt; ++kt, ++j, vr.advance(nV)) {
-                        if (!dual && (j & 1) != xb) continue;
-                        if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
-                            !mbar_wait_warp(bar_mask(j & 7), (uint32_t)((j >> 3) & 1), abort_flag)) {
+            while (fixes && ok && units.next(x)) {
+                for (int kt = 0; kt < x.nt; ++kt, ++j, vr.advance(nV)) {
+                    if (!dual && (j & 1) != xb) continue;
+                    if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
+                        !mbar_wait_warp(bar_mask(j & 7), (uint32_t)((j >> 3) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ++ns;
+                    const uint32_t mword = mask_words[j & 7];
+                    const int k0 = (x.f + kt) * kTile;
+                    if (mword != all_seg || k0 + kTile > x.L - a.T) {
+                        if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        ++ns;
-                        const uint32_t mword = mask_words[j & 7];
-                        const int k0 = (x.f + kt) * kTile;
-                        if (mword != all_seg || k0 + kTile > x.L - a.T) {
-                            if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            fix_v(vr.slot, j, mword, x.L - a.T - k0, x.L - k0, kh * (4 - aq) + qw - aq, 2 * (4 - aq));
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_pfull(xb));
+                        fix_v(vr.slot, j, mword, x.L - a.T - k0, x.L - k0, qw - aq, 4 - aq);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_pfull(xb));
                 }
             }
         } else {
             const int row = 32 * qw + lane;
-            const bool valid = row < (xb ? rows1 : rows0);
-            const int tok = tok0 + (dual ? xb * tok_per_tile : 0) + min(row, (xb ? rows1 : rows0) - 1) / G;
+            const int nrows = xb ? rows1 : rows0;
+            const bool valid = row < nrows;
+            const int tok = tok0 + (dual ? xb * tok_per_tile : 0) + min(row, nrows - 1) / G;
             const int hh = valid ? row % G : 0;
-            const int srow = row + (dual ? xb * tok_per_tile * G : 0);   // row of the slot
-            const uint32_t lane_base = (uint32_t)(32 * qw) << 16;
-            const uint32_t s_col = tmem + lane_base + col_s(xb);
-            float *xmax = reinterpret_cast<float *>(smem + kOffXmax) + xb * (2 * 2 * kTile);   // [half][parity][row]
-            float *xm = reinterpret_cast<float *>(smem + kOffXm);                              // [stream][row]
-            float *xsum = reinterpret_cast<float *>(smem + kOffXsum);                          // [stream][half][row]
-            uint32_t pphase = 0;
-            Ring vr;             // the V slot of the tile at hand
-            int j = 0;
-            int ns = 0;          // S tiles of this stream seen so far
+            const uint32_t lanes = tmem + ((uint32_t)(32 * qw) << 16);
+            const uint32_t s_col = lanes + col_s(xb);
+            float2 *xm = reinterpret_cast<float2 *>(smem + kOffXm);   // [stream][row]
             int no = 0;          // units finished so far
-            bool ok = true;
-            auto pair_sync = [&]() -> bool {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_pair(xb, qw));
-                const bool r = mbar_wait_warp(bar_pair(xb, qw), pphase, abort_flag);
-                pphase ^= 1u;
-                return r;
-            };
-            Units units(a, pre, fill, q);
-            Unit x;
             while (ok && units.next(x)) {
                 const int first = x.L - a.T;   // position of the tree's first token
                 const uint32_t *mrow = a.mask + (int64_t)x.r * a.mask_stride + (int64_t)tok * a.mask_words;
@@ -617,25 +672,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!dual && (jj & 1) != xb) continue;
                     const int k0 = (x.f + kt) * kTile;
                     const bool near = k0 + kTile > first;    // positions of the tree, or past the cache end
-                    // what this row sees of its half's 64 keys, as bits (the mask's words are on their way
-                    // while the scores are waited for)
-                    uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+                    // what this row sees of the tile, as bits (the mask's words are on their way while the
+                    // scores are waited for)
+                    uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                     if (near) {
-                        vis[0] = tree_vis32(mrow, a.mask_words, first, x.L, k0 + 64 * kh);
-                        vis[1] = tree_vis32(mrow, a.mask_words, first, x.L, k0 + 64 * kh + 32);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) vis[c] = tree_vis32(mrow, a.mask_words, first, x.L, k0 + 32 * c);
                     }
                     if (!mbar_wait_warp(bar_sfull(xb), (uint32_t)(ns & 1), abort_flag) ||
                         !mbar_wait_warp(bar_mask(jj & 7), (uint32_t)((jj >> 3) & 1), abort_flag)) {
                         ok = false;
                         break;
                     }
+                    ++ns;
                     tc_fence_after();
                     const uint32_t mword = mask_words[jj & 7];
                     const bool full = !near && mword == all_seg;
                     if (mword != all_seg) {   // keys of entries that are not there
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t bits = mword >> ((64 * kh + 32 * h) >> seg_shift);
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t bits = mword >> ((32 * c) >> seg_shift);
                             uint32_t sb = 0u;
                             if (seg_rows >= 32) {
                                 sb = (bits & 1u) ? 0xffffffffu : 0u;
@@ -644,158 +700,111 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int i = 0; i < (32 >> seg_shift); ++i)
                                     if ((bits >> i) & 1u) sb |= ones << (i * seg_rows);
                             }
-                            vis[h] &= sb;
+                            vis[c] &= sb;
                         }
                     }
-                    // pass 1: this half's max of the raw scores, then the row's from the two halves
-                    float mraw = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float sv[32];
-                        tmem_ld32(s_col + 64u * kh + 32u * c, sv);
-                        if (!full) {
-                            const uint32_t vm = vis[c];
+                    // the row's 128 scores stay in registers: their max, then the weights
+                    float sv[4][32];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) sv[k] = (vm & (1u << k)) ? sv[k] : -INFINITY;
-                        }
-                        mraw = fmaxf(mraw, tree_max32(sv));
+                    for (int c = 0; c < 4; ++c) tmem_ld32_nw(s_col + 32u * c, sv[c]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) use32(sv[c]);
+                    if (!full) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) sv[c][k] = (vis[c] & (1u << k)) ? sv[c][k] : -INFINITY;
                     }
-                    float *xt = xmax + (ns & 1) * kTile;
-                    xt[kh * 2 * kTile + row] = mraw;
-                    if (!pair_sync()) {
-                        ok = false;
-                        break;
-                    }
-                    mraw = fmaxf(mraw, xt[(1 - kh) * 2 * kTile + row]);
-                    ++ns;
-                    const float mt = mraw * a.scale_log2;
+                    float top[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) top[c] = max32(sv[c]);
+                    const float mt = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
                     const bool bump = mt > m + kSlack;
                     const float mn = bump ? mt : m;
                     const float corr = bump ? fast_exp2(m - mn) : 1.f;
-                    // the stream's last P V completed before this S did: rescale this half's O columns
+                    // the stream's last P V completed before this S did: rescale O
                     if (any && __any_sync(0xffffffffu, corr != 1.f)) {
-                        const uint32_t o_col = tmem + lane_base + col_o(xb);
 #pragma unroll 1
-                        for (int c = 2 * kh; c < 2 * kh + 2; ++c) {
-                            float ov[32];
-                            tmem_ld32(o_col + 32u * c, ov);
+                        for (int c = 0; c < 16; ++c) {
+                            float ov[8];
+                            uint32_t ow[8];
+                            tmem_ld8(lanes + col_o(xb) + 8u * c, ov);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) ov[k] *= corr;
-                            tmem_st32(o_col + 32u * c, ov);
+                            for (int k = 0; k < 8; ++k) ow[k] = __float_as_uint(ov[k] * corr);
+                            tmem_st8(lanes + col_o(xb) + 8u * c, ow);
                         }
                     }
                     any = true;
-                    // pass 2: weights, their sum, and P over the first 32 of this half's S columns
-                    float psum = 0.f;
-                    {
-                        const float nb = -mn;
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float sv[16];
-                            tmem_ld16(s_col + 64u * kh + 16u * c, sv);
-                            if (full) {
+                    // weights 2^(s scale - mn) (a masked score is -inf: 0), their sum, and P (bf16) over the
+                    // first half of S's columns
+                    const float nb = mn == -INFINITY ? 0.f : -mn;
+                    float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) sv[k] = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
-                            } else {
-                                const uint32_t vh = (c < 2 ? vis[0] : vis[1]) >> (16 * (c & 1));
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const float e = fast_exp2(fmaf(sv[k], a.scale_log2, nb));
-                                    sv[k] = (vh & (1u << k)) ? e : 0.f;
-                                }
-                            }
-                            uint32_t pk[8];
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const __nv_bfloat162 pb = __floats2bfloat162_rn(sv[k], sv[k + 1]);
-                                pk[k >> 1] = *reinterpret_cast<const uint32_t *>(&pb);
-                                psum += sv[k] + sv[k + 1];
-                            }
-                            tmem_st8(s_col + 64u * kh + 8u * c, pk);
+                        for (int k = 0; k < 32; k += 2) {
+                            float2 e = fma2(make_float2(sv[c][k], sv[c][k + 1]), a.scale_log2, nb);
+                            e.x = fast_exp2(e.x);
+                            e.y = fast_exp2(e.y);
+                            const __nv_bfloat162 pb = __floats2bfloat162_rn(e.x, e.y);
+                            pk[k >> 1] = *reinterpret_cast<const uint32_t *>(&pb);
+                            sum2 = add2(sum2, e);
                         }
-                        tmem_st_wait();
+                        tmem_st16(s_col + 16u * c, pk);
                     }
-                    l = fmaf(l, corr, psum);
+                    tmem_st_wait();
+                    l = fmaf(l, corr, sum2.x + sum2.y);
                     m = mn;
                     if (!full && fixes && aq == 4) {
                         if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
                             ok = false;
                             break;
                         }
-                        fix_v(vr.slot, jj, mword, first - k0, x.L - k0, kh * 4 + qw, 8);
+                        fix_v(vr.slot, jj, mword, first - k0, x.L - k0, qw, 4);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_pfull(xb));
                 }
                 if (!ok) break;
-                // ---- the unit's end: O of both streams is settled ----
+                // ---- the unit's end ----
+                const int srow = row + (dual ? xb * tok_per_tile * G : 0);   // row of the slot
+                const int64_t prow = ((int64_t)hp * (a.P + a.num_reqs) + x.slot) * a.NR + srow;
+                float *po = a.ws_o + prow * kD;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                                     (((int64_t)x.r * a.T + tok) * a.H_q + (int64_t)g * G + hh) * kD;
+                float M = m, fa = 1.f, fb = 0.f, lsum = l;
+                if (!dual) {
+                    // the streams' parts of this row
+                    xm[xb * kTile + row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_pair(qw));
+                    if (!mbar_wait_warp(bar_pair(qw), (uint32_t)(no & 1), abort_flag)) break;
+                    const float2 pa = xm[row], pb = xm[kTile + row];
+                    M = fmaxf(pa.x, pb.x);
+                    fa = pa.x == -INFINITY ? 0.f : fast_exp2(pa.x - M);
+                    fb = pb.x == -INFINITY ? 0.f : fast_exp2(pb.x - M);
+                    lsum = fa * pa.y + fb * pb.y;
+                }
+                // O of both streams is settled
                 if (!mbar_wait_warp(bar_ofull, (uint32_t)(no & 1), abort_flag)) break;
                 tc_fence_after();
-                if (kh == 0) xm[xb * kTile + row] = any ? m : -INFINITY;
-                xsum[(2 * xb + kh) * kTile + row] = l;
-                if (dual) {
-                    if (!pair_sync()) break;
-                } else {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_quad(qw));
-                    if (!mbar_wait_warp(bar_quad(qw), (uint32_t)(no & 1), abort_flag)) break;
-                }
                 ++no;
-                float M, fa, fb = 0.f, lsum;
-                bool use_a = true, use_b = false;
-                if (dual) {
-                    M = m;
-                    fa = 1.f;
-                    lsum = xsum[2 * xb * kTile + row] + xsum[(2 * xb + 1) * kTile + row];
-                } else {
-                    const float ma = xm[row], mb = xm[kTile + row];
-                    M = fmaxf(ma, mb);
-                    fa = ma == -INFINITY ? 0.f : fast_exp2(ma - M);
-                    fb = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
-                    lsum = fa * (xsum[row] + xsum[kTile + row]) + fb * (xsum[2 * kTile + row] + xsum[3 * kTile + row]);
-                    use_a = x.nt > 1 || (jb & 1) == 0;   // a stream without a tile leaves its O unwritten
-                    use_b = x.nt > 1 || (jb & 1) == 1;
-                }
                 // a V row of the tree that was not finite makes the rows that see it NaN
-                for (int kt = max(0, (first >> 7) - x.f); kt < x.nt; ++kt) {
-                    const uint8_t *bad_rows = poison + ((jb + kt) & 7) * 32;
-                    const uint4 b0 = *reinterpret_cast<const uint4 *>(bad_rows);
-                    const uint4 b1 = *reinterpret_cast<const uint4 *>(bad_rows + 16);
-                    if ((b0.x | b0.y | b0.z | b0.w | b1.x | b1.y | b1.z | b1.w) == 0u) continue;
+                if (*any_bad) {
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 4 * max(0, (first >> 7) - x.f); c < 4 * x.nt; ++c) {
+                        const uint8_t *bad_rows = poison + ((jb + (c >> 2)) & 7) * 32 + 8 * (c & 3);
                         uint32_t w = 0u;
-                        for (int i = 0; i < 8; ++i) w |= (uint32_t)bad_rows[8 * c + i] << (4 * i);
-                        if (w & tree_vis32(mrow, a.mask_words, first, x.L, (x.f + kt) * kTile + 32 * c)) lsum = NAN;
+                        for (int i = 0; i < 8; ++i) w |= (uint32_t)bad_rows[i] << (4 * i);
+                        if (w && (w & tree_vis32(mrow, a.mask_words, first, x.L, x.f * kTile + 32 * c))) lsum = NAN;
                     }
                 }
                 const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-                const int64_t slot = (int64_t)hp * (a.P + a.num_reqs) + x.slot;
-                float *po = a.ws_o + (slot * a.NR + srow) * kD;
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
-                                     (((int64_t)x.r * a.T + tok) * a.H_q + (int64_t)g * G + hh) * kD;
-                // one query tile: the quarter's four warps take 32 columns each; two: a half each of its own
-                const int c0 = dual ? 2 * kh : 2 * xb + kh, c1 = dual ? c0 + 2 : c0 + 1;
-#pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    float ov[32];
-                    if (dual) {
-                        tmem_ld32(tmem + lane_base + col_o(xb) + 32u * c, ov);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t oa[16], ob[16];
-                            tmem_ld16_nw(tmem + lane_base + col_o(0) + 32u * c + 16u * h, oa);
-                            tmem_ld16_nw(tmem + lane_base + col_o(1) + 32u * c + 16u * h, ob);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)   // (columns of a stream without a tile may hold anything)
-                                ov[16 * h + k] = (use_a ? __uint_as_float(oa[k]) * fa : 0.f) +
-                                                 (use_b ? __uint_as_float(ob[k]) * fb : 0.f);
-                        }
-                    }
-                    if (!valid) continue;
+                auto put32 = [&](int c, const float (&ov)[32]) {   // columns [32 c, 32 c + 32)
+                    if (!valid) return;
                     if (x.whole) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -810,11 +819,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) store32(po + 32 * c + k, reinterpret_cast<uint32_t *>(ov + k));
+                        for (int k = 0; k < 32; k += 8) store32(po + 32 * c + k, reinterpret_cast<const uint32_t *>(ov + k));
+                    }
+                };
+                if (dual) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        float oa[32], ob[32];
+                        tmem_ld32_nw(lanes + col_o(xb) + 32u * c, oa);
+                        tmem_ld32_nw(lanes + col_o(xb) + 32u * c + 32u, ob);
+                        tmem_ld_wait();
+                        use32(oa);
+                        use32(ob);
+                        put32(c, oa);
+                        put32(c + 1, ob);
+                    }
+                } else {
+                    // the quarter's two warps take half of the columns each (those of a stream without a tile
+                    // in the unit may hold anything)
+                    const bool use_a = x.nt > 1 || (jb & 1) == 0, use_b = x.nt > 1 || (jb & 1) == 1;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float oa[32], ob[32];
+                        tmem_ld32_nw(lanes + col_o(0) + 64u * xb + 32u * h, oa);
+                        tmem_ld32_nw(lanes + col_o(1) + 64u * xb + 32u * h, ob);
+                        tmem_ld_wait();
+                        use32(oa);
+                        use32(ob);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) oa[k] = (use_a ? oa[k] * fa : 0.f) + (use_b ? ob[k] * fb : 0.f);
+                        put32(2 * xb + h, oa);
                     }
                 }
-                if (!x.whole && valid && kh == 0 && (dual || xb == 0))
-                    *reinterpret_cast<float2 *>(a.ws_ml + (slot * a.NR + srow) * 2) = make_float2(M, lsum);
+                if (!x.whole && valid && (dual || xb == 0))
+                    *reinterpret_cast<float2 *>(a.ws_ml + prow * 2) = make_float2(M, lsum);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_oempty);
