@@ -27,6 +27,12 @@ LIB_PATH = _build.LIB
 _lib = None
 _lock = threading.Lock()
 
+# The current device and its current stream's handle, without the objects that torch.cuda's functions build
+# around them (a call of a few microseconds on the GPU notices those).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = (torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
+               else lambda device: torch.cuda.current_stream(device).cuda_stream)
+
 
 class BkvError(RuntimeError):
     def __init__(self, fn: str, status: int):
@@ -41,6 +47,8 @@ class BkvError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libbkv.so (built in-tree by ``build()``); raise if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -123,14 +131,15 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:
+        return _raw_stream(_current_device())
+    return stream.cuda_stream
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None, contiguous=True):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -465,9 +474,9 @@ def bkv_merge_attn_states(outs, lses, out, lse_out=None, stream=None):
 
 def _same_device(*tensors):
     """Every tensor on the current device, whose stream the call is enqueued on."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
 
 
@@ -494,44 +503,55 @@ def bkv_qk_norm_rope_cache_write_fp8(q, k, v, q_weight, k_weight, norm_eps, cos_
 
 def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table, req_indices, positions,
                slot_mapping, q_out, k_cache, v_cache, rope_positions, interleaved, num_tokens, err_count, stream):
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    cache = k_cache.shape
+    if len(cache) != 4 or cache != v_cache.shape:
         raise ValueError("caches must be (total_blocks, block_size, H_kv, D) and equal in shape")
-    tb, bs, hkv, d = k_cache.shape
-    if q.dim() != 3 or q.shape[2] != d or k.dim() != 3 or tuple(k.shape[1:]) != (hkv, d) or k.shape != v.shape:
+    tb, bs, hkv, d = cache
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or qs[2] != d or len(ks) != 3 or ks[1] != hkv or ks[2] != d or ks != v.shape:
         raise ValueError("q must be (num_tokens, H_q, D), k / v (num_tokens, H_kv, D) matching the cache")
-    nt, hq, _ = q.shape
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.stride(2) != 1 or t.stride(1) != d:
+    nt, hq, _ = qs
+    dtype, stride = q.dtype, []
+    for t, name, heads in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv)):
+        row, head, elem = t.stride()
+        if elem != 1 or head != d:
             raise ValueError(f"{name} rows must be dense (a row stride is allowed)")
-        if t.dtype != q.dtype:
+        if t.dtype is not dtype:
             raise TypeError("mixed dtypes")
+        # a dimension of size 1 (one token) may carry any stride
+        stride.append(row if t.shape[0] > 1 else max(row, heads * d))
     dt = _kv_dtype(q)
-    cache_dtype = torch.uint8 if scales else q.dtype
-    if k_cache.dtype != cache_dtype or v_cache.dtype != cache_dtype or q_out.dtype != q.dtype:
-        raise TypeError(f"caches must be {cache_dtype} and q_out {q.dtype}")
-    if q_out.dim() != 3 or q_out.shape[0] < nt or tuple(q_out.shape[1:]) != (hq, d):
+    cache_dtype = torch.uint8 if scales else dtype
+    if k_cache.dtype is not cache_dtype or v_cache.dtype is not cache_dtype or q_out.dtype is not dtype:
+        raise TypeError(f"caches must be {cache_dtype} and q_out {dtype}")
+    os_ = q_out.shape
+    if len(os_) != 3 or os_[0] < nt or os_[1] != hq or os_[2] != d:
         raise ValueError("q_out must be (>= num_tokens, H_q, D)")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.numel() != d:
-            raise ValueError(f"{name} must have head_dim elements")
-    if cos_sin is not None and cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be (max_position, rot_dim)")
+    if (q_weight is not None and q_weight.numel() != d) or (k_weight is not None and k_weight.numel() != d):
+        raise ValueError("q_weight and k_weight must have head_dim elements")
+    max_pos, rot = 1 << 62, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be (max_position, rot_dim)")
+        max_pos, rot = cos_sin.shape
     if block_table.dim() != 2 or block_table.stride(1) != 1:
         raise ValueError("block_table must be 2-D with unit column stride")
-    n = positions.numel() if num_tokens is None else int(num_tokens)
-    if (n > nt or n > k.shape[0] or n > positions.numel() or n > req_indices.numel() or n > slot_mapping.numel() or
+    rows, cols = block_table.shape
+    n, most = positions.numel(), slot_mapping.numel()
+    if num_tokens is not None:
+        if int(num_tokens) > n:
+            raise ValueError("num_tokens exceeds positions")
+        n = int(num_tokens)
+    if (n > nt or n > ks[0] or n > req_indices.numel() or n > most or
             (rope_positions is not None and n > rope_positions.numel())):
-        raise ValueError("num_tokens exceeds q / k / positions / req_indices / slot_mapping / rope_positions")
+        raise ValueError("num_tokens exceeds q / k / req_indices / slot_mapping / rope_positions")
     ptrs = (_dev(q, "q", contiguous=False), _dev(k, "k", contiguous=False), _dev(v, "v", contiguous=False))
-    # a dimension of size 1 (one token) may carry any stride
-    stride = [t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * d) for t in (q, k, v)]
-    args = (*ptrs, *stride, _opt(q_weight, "q_weight", q.dtype), _opt(k_weight, "k_weight", q.dtype), float(norm_eps),
-            _opt(cos_sin, "cos_sin", torch.float32), 1 << 62 if cos_sin is None else cos_sin.shape[0],
-            0 if cos_sin is None else cos_sin.shape[1], int(bool(interleaved)),
-            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.shape[0], block_table.stride(0),
-            block_table.shape[1], _dev(req_indices, "req_indices", torch.int32),
+    args = (*ptrs, *stride, _opt(q_weight, "q_weight", dtype), _opt(k_weight, "k_weight", dtype), float(norm_eps),
+            _opt(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(bool(interleaved)),
+            _dev(block_table, "block_table", torch.int32, contiguous=False), rows, block_table.stride(0), cols,
+            _dev(req_indices, "req_indices", torch.int32),
             _dev(positions, "positions", torch.int64), _opt(rope_positions, "rope_positions", torch.int64), n,
-            slot_mapping.numel(), _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
+            most, _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), tb, bs, hq, hkv, d, dt, *scales,
             _opt(err_count, "err_count", torch.int32))
     _same_device(q, k_cache)
@@ -551,31 +571,31 @@ def bkv_paged_decode_tree(q, k_cache, v_cache, block_table, context_lens, max_co
     """Paged attention of drafted trees into ``out`` (num_reqs, q_len, H_q, D): a request's q_len tokens are its
     last cached positions, and bit i of token t's words in ``tree_mask`` (int32, (num_reqs, q_len, ceil(q_len /
     32)), or (q_len, ..) for one tree of all requests) lets it see token i (see include/bkv.h)."""
-    if q.dim() != 4 or out.shape != q.shape or k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    shape, cache = q.shape, k_cache.shape
+    if len(shape) != 4 or out.shape != shape or len(cache) != 4 or cache != v_cache.shape:
         raise ValueError("q/out must be (num_reqs, q_len, H_q, D); caches (total_blocks, bs, H_kv, D)")
-    nr, ql, hq, d = q.shape
-    tb, bs, hkv, d2 = k_cache.shape
+    nr, ql, hq, d = shape
+    tb, bs, hkv, d2 = cache
     if d2 != d:
         raise ValueError("head_dim mismatch")
-    if block_table.dim() != 2 or block_table.shape[0] < nr or block_table.stride(1) != 1:
+    table = block_table.shape
+    if len(table) != 2 or table[0] < nr or block_table.stride(1) != 1:
         raise ValueError("block_table must be (>= num_reqs, cols) with unit column stride")
     if context_lens.numel() < nr:
         raise ValueError("context_lens must have num_reqs elements")
-    words = (ql + 31) // 32
-    shape = tuple(tree_mask.shape)
-    if shape != (ql, words) and (len(shape) != 3 or shape[0] < nr or shape[1:] != (ql, words)):
+    words, ms = (ql + 31) // 32, tree_mask.shape
+    if ms[-2:] != (ql, words) or (len(ms) != 2 and (len(ms) != 3 or ms[0] < nr)):
         raise ValueError("tree_mask must be (num_reqs, q_len, ceil(q_len / 32)) or (q_len, ceil(q_len / 32))")
-    dt = _kv_dtype(q)
-    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype or out.dtype != q.dtype:
-        raise TypeError(f"caches and out must be {q.dtype}")
-    if workspace.dtype != torch.uint8:
+    dt, dtype = _kv_dtype(q), q.dtype
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or out.dtype is not dtype:
+        raise TypeError(f"caches and out must be {dtype}")
+    if workspace.dtype is not torch.uint8:
         raise TypeError("workspace must be a uint8 tensor")
     args = (_dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.stride(0),
-            block_table.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv,
-            d, bs, tb, float(softmax_scale), _dev(tree_mask, "tree_mask", torch.int32),
-            ql * words if len(shape) == 3 else 0, dt, _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(),
-            _opt(err_count, "err_count", torch.int32))
+            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.stride(0), table[1],
+            _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv, d, bs, tb,
+            float(softmax_scale), _dev(tree_mask, "tree_mask", torch.int32), ql * words if len(ms) == 3 else 0, dt,
+            _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(), _opt(err_count, "err_count", torch.int32))
     _same_device(q, k_cache)
     _check("bkv_paged_decode_tree", load().bkv_paged_decode_tree(*args, _stream(stream)))
     return out
@@ -588,8 +608,8 @@ def bkv_verify_draft_chain(target_probs, draft_probs, draft_tokens, accept_u, sa
     -> out_tokens int64 (num_reqs, K + 1), num_accepted int32 (num_reqs) (see include/bkv.h)."""
     nr, k1, vocab = target_probs.shape
     k = k1 - 1
-    if (tuple(draft_probs.shape) != (nr, k, vocab) or tuple(draft_tokens.shape) != (nr, k) or
-            tuple(accept_u.shape) != (nr, k) or tuple(out_tokens.shape) != (nr, k1)):
+    if (draft_probs.shape != (nr, k, vocab) or draft_tokens.shape != (nr, k) or accept_u.shape != (nr, k) or
+            out_tokens.shape != (nr, k1)):
         raise ValueError("target_probs (R, K + 1, V), draft_probs (R, K, V), draft_tokens / accept_u (R, K) and "
                          "out_tokens (R, K + 1) disagree")
     if sample_u.numel() != nr or num_accepted.numel() != nr or (draft_lens is not None and draft_lens.numel() != nr):
@@ -615,7 +635,7 @@ def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_
     nr, t, vocab = target_probs.shape
     for x, name in ((draft_tokens, "draft_tokens"), (parents, "parents"), (accept_u, "accept_u"),
                     (out_tokens, "out_tokens"), (path, "path")):
-        if tuple(x.shape) != (nr, t):
+        if x.shape != (nr, t):
             raise ValueError(f"{name} must be (num_reqs, num_nodes)")
     if sample_u.numel() != nr or num_accepted.numel() != nr:
         raise ValueError("sample_u and num_accepted must have num_reqs elements")
@@ -633,7 +653,8 @@ def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_
 
 def _row_strides(t):
     """Request and row stride of probabilities (R, rows, V); a dimension of size 1 or 0 may carry any stride."""
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    (reqs, rows, vocab), (req, row, _) = t.shape, t.stride()
+    return req if reqs > 1 else 0, row if rows > 1 else vocab
 
 
 def alloc_tree_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, device=None):

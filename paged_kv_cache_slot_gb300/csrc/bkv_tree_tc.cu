@@ -54,22 +54,14 @@ constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
 constexpr int kHalfBytes = kTile * 128;
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kThreads = 352;   // K producer, MMA issuer, 2 x 4 softmax warps, V producer
-constexpr int kWarpV = kThreads / 32 - 1;
+constexpr int kThreads = 384;   // K producer, MMA issuer, V producer and a spare warp; 2 x 4 softmax warps
+constexpr int kWarpV = 2;
+constexpr int kWarpS = 4;   // first softmax warp
 constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (128 columns each)
 constexpr int kTimeoutErr = 1 << 24;
 constexpr int kMaxReqs = 2048;
 constexpr float kSlack = 8.f;
-#ifndef TW
-#define TW 1
-#endif
-#ifndef EC
-#define EC 3
-#endif
-constexpr int kEndCost = EC;             // tiles that a unit's end takes as long as
-#ifndef QB
-#define QB 1
-#endif
+constexpr int kEndCost = 3;    // tiles that a unit's end takes as long as (see Units)
 
 constexpr int kMaxStages = 3;                             // slots of a ring, at most
 constexpr int kOffMask = 0;                               // 8 words: loaded segments per tile (ring)
@@ -409,214 +401,220 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async();
     };
 
-    if (warp == 0 || warp == kWarpV) {
-        // ================= TMA producers (warp 0: Q and K, last warp: V) =================
-        const bool is_v = warp == kWarpV;
-        const bool count = !is_v && p == 0 && a.err;   // bad entries count once a KV head
-        const int stages = is_v ? nV : nK;
-        Ring ring;
-        int j = 0, uq = 0;
-        Units units(a, pre, fill, q);
-        Unit x;
-        for (; !*abort_flag && units.next(x); ++uq) {
-            if (!is_v) {
-                const int b = nbuf == 2 ? uq & 1 : 0;
-                if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1) ^ 1u, abort_flag)) break;
-                if (lane == 0) {
-                    const uint32_t bytes = (uint32_t)(box_tok * G) * 256u;
-                    mbar_arrive_expect_tx(bar_qfull(b), dual ? 2 * bytes : bytes);
-                    for (int xb = 0; xb < (dual ? 2 : 1); ++xb) {
-                        const int tq = x.r * a.T + tok0 + xb * tok_per_tile;
-                        const uint32_t dq = sm_q + (b + xb) * 2 * sh.q_half;
-                        tma_load_3d(dq, &tmQ, bar_qfull(b), 0, g * G, tq);
-                        tma_load_3d(dq + sh.q_half, &tmQ, bar_qfull(b), 64, g * G, tq);
-                    }
-                }
-            }
-            // block entry of this lane's segment of key tile kt: the cache row to load, or -1
-            auto entry = [&](int kt) -> int64_t {
-                if (lane >= nseg) return -1;
-                const int32_t p0 = kt * kTile + lane * seg_rows;
-                if (p0 >= x.L) return -1;
-                const int32_t lb = p0 / a.bs;
-                const int32_t off = p0 - lb * a.bs;
-                const int64_t e = lb < a.bt_cols ? __ldg(a.bt + (int64_t)x.r * a.bt_stride + lb) : a.total_blocks;
-                if (e >= a.total_blocks) {
-                    if (count && off == 0) atomicAdd(a.err, 1);
-                    return -1;
-                }
-                return e > 0 ? e * a.bs + off : -1;
-            };
-            int64_t row_cur = entry(x.f);
-            for (int kt = 0; kt < x.nt; ++kt, ++j) {
-                const int64_t row_nxt = kt + 1 < x.nt ? entry(x.f + kt + 1) : -1;   // in flight meanwhile
-                const int s = ring.slot;
-                const uint32_t bar_e = is_v ? bar_vempty(s) : bar_kempty(s);
-                const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
-                if (!mbar_wait_warp(bar_e, ring.phase ^ 1u, abort_flag)) break;
-                ring.advance(stages);
-                const bool load = row_cur >= 0;
-                const uint32_t ballot = __ballot_sync(0xffffffffu, load);
-                if (lane == 0) {
-                    // a word is rewritten 8 tiles on; its readers are at most 5 tiles behind
-                    if (!is_v) {
-                        mask_words[j & 7] = ballot;
-                        mbar_arrive(bar_mask(j & 7));
-                    }
-                    mbar_arrive_expect_tx(bar_f, (uint32_t)__popc(ballot) * (uint32_t)seg_rows * 256u);
-                }
-                __syncwarp();
-                if (load) {
-                    const uint32_t dst = (is_v ? sm_v : sm_k) + s * kTileBytes + lane * seg_rows * 128;
-                    const CUtensorMap *map = is_v ? &tmV : &tmK;
-                    tma_load_3d(dst, map, bar_f, 0, g, (int)row_cur);
-                    tma_load_3d(dst + kHalfBytes, map, bar_f, 64, g, (int)row_cur);
-                }
-                __syncwarp();
-                row_cur = row_nxt;
-            }
-        }
-        if (*abort_flag) {   // let copies in flight land
-            const unsigned long long t0 = global_ns();
-            while (global_ns() - t0 < 200000ull) {
-            }
-        }
-    } else if (warp == 1) {
-        // ================= MMA issuer (one thread) =================
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);   // Q (K-major) x K (K-major)
-            constexpr uint32_t kIdescO = idesc_bf16(128, 128, 0, 1);   // P (TMEM) x V (MN-major)
-            int np[2] = {0, 0};   // P tiles consumed
-            // O_x += P_x V(next tile): `first` overwrites O_x, once the unit before has been read out
-            Ring kr, vr;          // tiles are multiplied in their order
-            auto issue_pv = [&](int xb, bool first, int unit) -> bool {
-                const int s = vr.slot;
-                if (!mbar_wait(bar_vfull(s), vr.phase, abort_flag) ||
-                    !mbar_wait(bar_pfull(xb), (uint32_t)(np[xb] & 1), abort_flag))
-                    return false;
-                ++np[xb];
-                if (first && unit > 0 && !mbar_wait(bar_oempty, (uint32_t)((unit - 1) & 1), abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t v_base = sm_v + s * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk) {
-                    mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + 8u * (uint32_t)kk, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
-                                kIdescO, (first && kk == 0) ? 0u : 1u);
-                }
-                return true;
-            };
-            auto issue_s = [&](int xb, int s, int qb) {
-                const uint32_t k_base = sm_k + s * kTileBytes;
-                const uint32_t q_base = sm_q + qb * 2 * sh.q_half;
-#pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk) {
-                    // (rows of the query tile past the group's: whatever lies there, their scores are not used)
-                    mma_bf16(tmem + col_s(xb), sdesc(q_base + (kk >> 2) * sh.q_half + (kk & 3) * 32, 16, 1024),
-                             sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(bar_sfull(xb));
-            };
-            // The unit's last P V: O is settled.  The plain arrival carries the softmax warps' own
-            // shared-memory writes (acquired with P) on to the other warps.
-            auto finish = [&]() {
-                mma_commit(bar_ofull);
-                mbar_arrive(bar_ofull);
-            };
+    // A row's scores need more registers than the launch gives each thread (168): the first warpgroup hands
+    // some of its own over (4 x 32 x 96 + 8 x 32 x 200 of 12 x 32 x 168).
+    if (warp < kWarpS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 0 || warp == kWarpV) {
+            // ================= TMA producers (warp 0: Q and K, last warp: V) =================
+            const bool is_v = warp == kWarpV;
+            const bool count = !is_v && p == 0 && a.err;   // bad entries count once a KV head
+            const int stages = is_v ? nV : nK;
+            Ring ring;
+            int j = 0, uq = 0;
             Units units(a, pre, fill, q);
             Unit x;
-            bool ok = true;
-            if (!dual) {
-                // stream j & 1 has tile j; its P V is issued before the S of tile j + 2, over the same columns
-                struct {
-                    int unit;
-                    bool on, first, last;
-                } pend[2] = {{0, false, false, false}, {0, false, false, false}};
-                auto settle = [&](int xb) -> bool {
-                    auto &w = pend[xb];
-                    if (!w.on) return true;
-                    w.on = false;
-                    if (!issue_pv(xb, w.first, w.unit)) return false;
-                    mma_commit(bar_vempty(vr.slot));
-                    vr.advance(nV);
-                    if (w.last) finish();
-                    return true;
-                };
-                int xb = 0;
-                for (int uq = 0; ok && units.next(x); ++uq) {
+            for (; !*abort_flag && units.next(x); ++uq) {
+                if (!is_v) {
                     const int b = nbuf == 2 ? uq & 1 : 0;
-                    const uint32_t qphase = (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1);
-                    for (int kt = 0; kt < x.nt; ++kt, xb ^= 1) {
-                        // operands that are there already are not waited for between P V and S: the tensor
-                        // cores run dry in the time that a barrier takes to answer
-#if TW
-                        const bool ready = (kt > 0 || mbar_test(bar_qfull(b), qphase)) && mbar_test(bar_kfull(kr.slot), kr.phase);
-#else
-                        const bool ready = false;
-#endif
-                        ok = settle(xb);
-                        if (ok && !ready)
-                            ok = (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
-                                 mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(xb, kr.slot, b);
-                        mma_commit(bar_kempty(kr.slot));
-                        kr.advance(nK);
-                        if (kt == x.nt - 1) mma_commit(bar_qempty(b));
-                        pend[xb].unit = uq;
-                        pend[xb].on = true;
-                        pend[xb].first = kt < 2;
-                        pend[xb].last = kt == x.nt - 1;
+                    if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1) ^ 1u, abort_flag)) break;
+                    if (lane == 0) {
+                        const uint32_t bytes = (uint32_t)(box_tok * G) * 256u;
+                        mbar_arrive_expect_tx(bar_qfull(b), dual ? 2 * bytes : bytes);
+                        for (int xb = 0; xb < (dual ? 2 : 1); ++xb) {
+                            const int tq = x.r * a.T + tok0 + xb * tok_per_tile;
+                            const uint32_t dq = sm_q + (b + xb) * 2 * sh.q_half;
+                            tma_load_3d(dq, &tmQ, bar_qfull(b), 0, g * G, tq);
+                            tma_load_3d(dq + sh.q_half, &tmQ, bar_qfull(b), 64, g * G, tq);
+                        }
                     }
                 }
-                if (ok) ok = settle(xb) && settle(xb ^ 1);
-            } else {
-                // per key tile: O_A += P_A V(-1), S_A; O_B += P_B V(-1), S_B
-                for (int uq = 0; ok && units.next(x); ++uq) {
-                    ok = mbar_wait(bar_qfull(0), (uint32_t)(uq & 1), abort_flag);
-                    for (int kt = 0; ok && kt <= x.nt; ++kt) {
-                        if (kt < x.nt && !mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag)) {
-                            ok = false;
-                            break;
+                // block entry of this lane's segment of key tile kt: the cache row to load, or -1
+                auto entry = [&](int kt) -> int64_t {
+                    if (lane >= nseg) return -1;
+                    const int32_t p0 = kt * kTile + lane * seg_rows;
+                    if (p0 >= x.L) return -1;
+                    const int32_t lb = p0 / a.bs;
+                    const int32_t off = p0 - lb * a.bs;
+                    const int64_t e = lb < a.bt_cols ? __ldg(a.bt + (int64_t)x.r * a.bt_stride + lb) : a.total_blocks;
+                    if (e >= a.total_blocks) {
+                        if (count && off == 0) atomicAdd(a.err, 1);
+                        return -1;
+                    }
+                    return e > 0 ? e * a.bs + off : -1;
+                };
+                int64_t row_cur = entry(x.f);
+                for (int kt = 0; kt < x.nt; ++kt, ++j) {
+                    const int64_t row_nxt = kt + 1 < x.nt ? entry(x.f + kt + 1) : -1;   // in flight meanwhile
+                    const int s = ring.slot;
+                    const uint32_t bar_e = is_v ? bar_vempty(s) : bar_kempty(s);
+                    const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
+                    if (!mbar_wait_warp(bar_e, ring.phase ^ 1u, abort_flag)) break;
+                    ring.advance(stages);
+                    const bool load = row_cur >= 0;
+                    const uint32_t ballot = __ballot_sync(0xffffffffu, load);
+                    if (lane == 0) {
+                        // a word is rewritten 8 tiles on; its readers are at most 5 tiles behind
+                        if (!is_v) {
+                            mask_words[j & 7] = ballot;
+                            mbar_arrive(bar_mask(j & 7));
                         }
-                        tc_fence_after();
-                        for (int xb = 0; xb < 2; ++xb) {
-                            if (kt > 0 && !issue_pv(xb, kt == 1, uq)) {
+                        mbar_arrive_expect_tx(bar_f, (uint32_t)__popc(ballot) * (uint32_t)seg_rows * 256u);
+                    }
+                    __syncwarp();
+                    if (load) {
+                        const uint32_t dst = (is_v ? sm_v : sm_k) + s * kTileBytes + lane * seg_rows * 128;
+                        const CUtensorMap *map = is_v ? &tmV : &tmK;
+                        tma_load_3d(dst, map, bar_f, 0, g, (int)row_cur);
+                        tma_load_3d(dst + kHalfBytes, map, bar_f, 64, g, (int)row_cur);
+                    }
+                    __syncwarp();
+                    row_cur = row_nxt;
+                }
+            }
+            if (*abort_flag) {   // let copies in flight land
+                const unsigned long long t0 = global_ns();
+                while (global_ns() - t0 < 200000ull) {
+                }
+            }
+        } else if (warp == 1) {
+            // ================= MMA issuer (one thread) =================
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);   // Q (K-major) x K (K-major)
+                constexpr uint32_t kIdescO = idesc_bf16(128, 128, 0, 1);   // P (TMEM) x V (MN-major)
+                int np[2] = {0, 0};   // P tiles consumed
+                // O_x += P_x V(next tile): `first` overwrites O_x, once the unit before has been read out
+                Ring kr, vr;          // tiles are multiplied in their order
+                auto issue_pv = [&](int xb, bool first, int unit) -> bool {
+                    const int s = vr.slot;
+                    if (!mbar_wait(bar_vfull(s), vr.phase, abort_flag) ||
+                        !mbar_wait(bar_pfull(xb), (uint32_t)(np[xb] & 1), abort_flag))
+                        return false;
+                    ++np[xb];
+                    if (first && unit > 0 && !mbar_wait(bar_oempty, (uint32_t)((unit - 1) & 1), abort_flag)) return false;
+                    tc_fence_after();
+                    const uint32_t v_base = sm_v + s * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk) {
+                        mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + 8u * (uint32_t)kk, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
+                                    kIdescO, (first && kk == 0) ? 0u : 1u);
+                    }
+                    return true;
+                };
+                auto issue_s = [&](int xb, int s, int qb) {
+                    const uint32_t k_base = sm_k + s * kTileBytes;
+                    const uint32_t q_base = sm_q + qb * 2 * sh.q_half;
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk) {
+                        // (rows of the query tile past the group's: whatever lies there, their scores are not used)
+                        mma_bf16(tmem + col_s(xb), sdesc(q_base + (kk >> 2) * sh.q_half + (kk & 3) * 32, 16, 1024),
+                                 sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar_sfull(xb));
+                };
+                // The unit's last P V: O is settled.  The plain arrival carries the softmax warps' own
+                // shared-memory writes (acquired with P) on to the other warps.
+                auto finish = [&]() {
+                    mma_commit(bar_ofull);
+                    mbar_arrive(bar_ofull);
+                };
+                Units units(a, pre, fill, q);
+                Unit x;
+                bool ok = true;
+                if (!dual) {
+                    // stream j & 1 has tile j; its P V is issued before the S of tile j + 2, over the same columns
+                    struct {
+                        int unit;
+                        bool on, first, last;
+                    } pend[2] = {{0, false, false, false}, {0, false, false, false}};
+                    auto settle = [&](int xb) -> bool {
+                        auto &w = pend[xb];
+                        if (!w.on) return true;
+                        w.on = false;
+                        if (!issue_pv(xb, w.first, w.unit)) return false;
+                        mma_commit(bar_vempty(vr.slot));
+                        vr.advance(nV);
+                        if (w.last) finish();
+                        return true;
+                    };
+                    int xb = 0;
+                    for (int uq = 0; ok && units.next(x); ++uq) {
+                        const int b = nbuf == 2 ? uq & 1 : 0;
+                        const uint32_t qphase = (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1);
+                        for (int kt = 0; kt < x.nt; ++kt, xb ^= 1) {
+                            // operands that are there already are not waited for between P V and S: the tensor
+                            // cores run dry in the time that a barrier takes to answer
+#if TW
+                            const bool ready = (kt > 0 || mbar_test(bar_qfull(b), qphase)) && mbar_test(bar_kfull(kr.slot), kr.phase);
+#else
+                            const bool ready = false;
+#endif
+                            ok = settle(xb);
+                            if (ok && !ready)
+                                ok = (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
+                                     mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_s(xb, kr.slot, b);
+                            mma_commit(bar_kempty(kr.slot));
+                            kr.advance(nK);
+                            if (kt == x.nt - 1) mma_commit(bar_qempty(b));
+                            pend[xb].unit = uq;
+                            pend[xb].on = true;
+                            pend[xb].first = kt < 2;
+                            pend[xb].last = kt == x.nt - 1;
+                        }
+                    }
+                    if (ok) ok = settle(xb) && settle(xb ^ 1);
+                } else {
+                    // per key tile: O_A += P_A V(-1), S_A; O_B += P_B V(-1), S_B
+                    for (int uq = 0; ok && units.next(x); ++uq) {
+                        ok = mbar_wait(bar_qfull(0), (uint32_t)(uq & 1), abort_flag);
+                        for (int kt = 0; ok && kt <= x.nt; ++kt) {
+                            if (kt < x.nt && !mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag)) {
                                 ok = false;
                                 break;
                             }
-                            if (kt < x.nt) issue_s(xb, kr.slot, xb);
-                        }
-                        if (!ok) break;
-                        if (kt > 0) {
-                            mma_commit(bar_vempty(vr.slot));
-                            vr.advance(nV);
-                        }
-                        if (kt < x.nt) {
-                            mma_commit(bar_kempty(kr.slot));
-                            kr.advance(nK);
-                            if (kt == x.nt - 1) mma_commit(bar_qempty(0));
-                        } else {
-                            finish();
+                            tc_fence_after();
+                            for (int xb = 0; xb < 2; ++xb) {
+                                if (kt > 0 && !issue_pv(xb, kt == 1, uq)) {
+                                    ok = false;
+                                    break;
+                                }
+                                if (kt < x.nt) issue_s(xb, kr.slot, xb);
+                            }
+                            if (!ok) break;
+                            if (kt > 0) {
+                                mma_commit(bar_vempty(vr.slot));
+                                vr.advance(nV);
+                            }
+                            if (kt < x.nt) {
+                                mma_commit(bar_kempty(kr.slot));
+                                kr.advance(nK);
+                                if (kt == x.nt - 1) mma_commit(bar_qempty(0));
+                            } else {
+                                finish();
+                            }
                         }
                     }
                 }
             }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ====== softmax: stream xb, lane quarter qw, one query row a thread ======
         // the merge's table, and the rows of requests without a position
-        if (hp == 0 && threadIdx.x == 64) a.ws_split[q] = Units(a, pre, fill, q).split(a);
+        if (hp == 0 && threadIdx.x == 32 * kWarpS) a.ws_split[q] = Units(a, pre, fill, q).split(a);
         for (int r = q; r < a.num_reqs; r += a.P) {
             if (pre[r + 1] > pre[r]) continue;
-            for (int e = (int)threadIdx.x - 64; e < ntok * G * (kD / 8); e += 256) {
+            for (int e = (int)threadIdx.x - 32 * kWarpS; e < ntok * G * (kD / 8); e += 256) {
                 const int row = e / (kD / 8), t = tok0 + row / G, h = g * G + row % G;
                 reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
                                           (((int64_t)r * a.T + t) * a.H_q + h) * kD)[e % (kD / 8)] = make_uint4(0, 0, 0, 0);
             }
         }
-        const int xb = (warp - 2) >> 2;
+        const int xb = (warp - kWarpS) >> 2;
         const int qw = warp & 3;
         const int aq = xb ? aq1 : aq0;
         const bool fixes = !dual || xb == 0;   // V serves both query tiles: the first one's stream mends it
@@ -907,7 +905,7 @@ static void ring_shape(const TreeArgs &a, TreeShape *s) {
     s->q_half = (s->box_tok * a.G + 7) / 8 * 1024;
     s->q_buffers = 2;
     auto slots = [&](int buffers) { return (kSmemMax - kOffQ - buffers * 2 * s->q_half) / kTileBytes; };
-    if (a.T <= s->tok_per_tile && slots(1) > slots(2) && slots(2) < 2 * kMaxStages) s->q_buffers = QB;
+    if (a.T <= s->tok_per_tile && slots(1) > slots(2) && slots(2) < 2 * kMaxStages) s->q_buffers = 1;
     s->q_bytes = s->q_buffers * 2 * s->q_half;
     int n = slots(s->q_buffers);
     n = n < 2 * kMaxStages ? n : 2 * kMaxStages;
