@@ -137,7 +137,7 @@ def _stream(stream) -> int:
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None, contiguous=True):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not getattr(t, "is_cuda", False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -503,29 +503,29 @@ def bkv_qk_norm_rope_cache_write_fp8(q, k, v, q_weight, k_weight, norm_eps, cos_
 
 def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block_table, req_indices, positions,
                slot_mapping, q_out, k_cache, v_cache, rope_positions, interleaved, num_tokens, err_count, stream):
-    cache = k_cache.shape
+    cache, qs, ks = k_cache.shape, q.shape, k.shape
     if len(cache) != 4 or cache != v_cache.shape:
         raise ValueError("caches must be (total_blocks, block_size, H_kv, D) and equal in shape")
     tb, bs, hkv, d = cache
-    qs, ks = q.shape, k.shape
     if len(qs) != 3 or qs[2] != d or len(ks) != 3 or ks[1] != hkv or ks[2] != d or ks != v.shape:
         raise ValueError("q must be (num_tokens, H_q, D), k / v (num_tokens, H_kv, D) matching the cache")
     nt, hq, _ = qs
-    dtype, stride = q.dtype, []
-    for t, name, heads in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv)):
-        row, head, elem = t.stride()
-        if elem != 1 or head != d:
-            raise ValueError(f"{name} rows must be dense (a row stride is allowed)")
-        if t.dtype is not dtype:
-            raise TypeError("mixed dtypes")
-        # a dimension of size 1 (one token) may carry any stride
-        stride.append(row if t.shape[0] > 1 else max(row, heads * d))
+    (q_row, qh, qe), (k_row, kh, ke), (v_row, vh, ve) = q.stride(), k.stride(), v.stride()
+    if qe != 1 or ke != 1 or ve != 1 or qh != d or kh != d or vh != d:
+        raise ValueError("q, k and v rows must be dense (a row stride is allowed)")
+    if nt <= 1:   # a dimension of size 1 may carry any stride
+        q_row = max(q_row, hq * d)
+    if ks[0] <= 1:
+        k_row, v_row = max(k_row, hkv * d), max(v_row, hkv * d)
+    dtype = q.dtype
     dt = _kv_dtype(q)
     cache_dtype = torch.uint8 if scales else dtype
+    if k.dtype is not dtype or v.dtype is not dtype:
+        raise TypeError("mixed dtypes")
     if k_cache.dtype is not cache_dtype or v_cache.dtype is not cache_dtype or q_out.dtype is not dtype:
         raise TypeError(f"caches must be {cache_dtype} and q_out {dtype}")
-    os_ = q_out.shape
-    if len(os_) != 3 or os_[0] < nt or os_[1] != hq or os_[2] != d:
+    outs = q_out.shape
+    if len(outs) != 3 or outs[0] < nt or outs[1] != hq or outs[2] != d:
         raise ValueError("q_out must be (>= num_tokens, H_q, D)")
     if (q_weight is not None and q_weight.numel() != d) or (k_weight is not None and k_weight.numel() != d):
         raise ValueError("q_weight and k_weight must have head_dim elements")
@@ -534,9 +534,11 @@ def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be (max_position, rot_dim)")
         max_pos, rot = cos_sin.shape
-    if block_table.dim() != 2 or block_table.stride(1) != 1:
+    if block_table.dim() != 2:
         raise ValueError("block_table must be 2-D with unit column stride")
-    rows, cols = block_table.shape
+    (rows, cols), (bt_row, bt_col) = block_table.shape, block_table.stride()
+    if bt_col != 1:
+        raise ValueError("block_table must be 2-D with unit column stride")
     n, most = positions.numel(), slot_mapping.numel()
     if num_tokens is not None:
         if int(num_tokens) > n:
@@ -545,15 +547,16 @@ def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block
     if (n > nt or n > ks[0] or n > req_indices.numel() or n > most or
             (rope_positions is not None and n > rope_positions.numel())):
         raise ValueError("num_tokens exceeds q / k / req_indices / slot_mapping / rope_positions")
-    ptrs = (_dev(q, "q", contiguous=False), _dev(k, "k", contiguous=False), _dev(v, "v", contiguous=False))
-    args = (*ptrs, *stride, _opt(q_weight, "q_weight", dtype), _opt(k_weight, "k_weight", dtype), float(norm_eps),
-            _opt(cos_sin, "cos_sin", torch.float32), max_pos, rot, int(bool(interleaved)),
-            _dev(block_table, "block_table", torch.int32, contiguous=False), rows, block_table.stride(0), cols,
-            _dev(req_indices, "req_indices", torch.int32),
-            _dev(positions, "positions", torch.int64), _opt(rope_positions, "rope_positions", torch.int64), n,
-            most, _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
+    args = (_dev(q, "q", None, False), _dev(k, "k", None, False), _dev(v, "v", None, False), q_row, k_row, v_row,
+            None if q_weight is None else _dev(q_weight, "q_weight", dtype),
+            None if k_weight is None else _dev(k_weight, "k_weight", dtype), norm_eps,
+            None if cos_sin is None else _dev(cos_sin, "cos_sin", torch.float32), max_pos, rot, 1 if interleaved else 0,
+            _dev(block_table, "block_table", torch.int32, False), rows, bt_row, cols,
+            _dev(req_indices, "req_indices", torch.int32), _dev(positions, "positions", torch.int64),
+            None if rope_positions is None else _dev(rope_positions, "rope_positions", torch.int64), n, most,
+            _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), tb, bs, hq, hkv, d, dt, *scales,
-            _opt(err_count, "err_count", torch.int32))
+            None if err_count is None else _dev(err_count, "err_count", torch.int32))
     _same_device(q, k_cache)
     _check(fn, getattr(load(), fn)(*args, _stream(stream)))
     return q_out, slot_mapping
