@@ -624,7 +624,9 @@ size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int
  *   workspace  device scratch of workspace_bytes >=
  *              bkv_paged_decode_tree_workspace_size(...), 32-byte aligned,
  *              used only while the call's kernels run; its contents on entry
- *              do not matter.
+ *              do not matter.  Calls that may overlap on the GPU (two captured
+ *              graphs among them) need one each.
+ *   out must not overlap q or the caches.
  *   Other arguments, bounds and error counts as bkv_paged_decode.  bf16 with
  *   head_dim 128 and at most 128 query heads per KV head runs a tcgen05
  *   kernel (block sizes from 8 that divide 128 or are multiples of it, at

@@ -531,7 +531,7 @@ static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, in
     p->chunk = (int32_t)chunk;
     p->n_chunks = max_ctx > 0 ? (int32_t)ceil_div<int64_t>(max_ctx, chunk) : 1;
     p->slots_cc = units * p->n_chunks;
-    if (p->slots_cc >= ((int64_t)1 << 31) || ceil_div<int64_t>(nq, 16) > 65535) return false;
+    if (p->slots_cc >= ((int64_t)1 << 31) || ceil_div<int64_t>(nq, kMergeWarps) > 65535) return false;   // grids
     int64_t rows = p->slots_cc * nq;
     p->slots_tc = 0;
     if (D == 128 && G <= 128) {

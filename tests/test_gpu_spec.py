@@ -227,6 +227,44 @@ def test_rope_write_no_tokens():
     assert (slots == -1).all() and not kc.any() and not vc.any() and not q_out.any()
 
 
+def test_rope_write_fewer_tokens_side_stream_and_graph():
+    """num_tokens below the buffers' length (the rest is padding), on a side stream, and replayed from a graph
+    after the projections changed in place."""
+    c = _rope_case(40, 8, 2, 128, 128, "bf16")
+    c["req"][:], c["pos"][:13], c["rpos"][:13] = np.maximum(c["req"], 0) % 3, np.arange(13), np.arange(13)
+    c["table"][c["table"] <= 0] = 1
+    c["table"][c["table"] >= c["total"]] = 1
+    q, k, v = _views(_d(c["qkv"]), 8, 2, 128)
+    kc, vc = (torch.zeros(c["total"], c["bs"], 2, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    slots = torch.full((40,), -9, dtype=torch.int64, device=DEV)
+    q_out = torch.full((40, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    args = [q, k, v, _d(c["w"][0]), _d(c["w"][1]), 1e-6, _d(c["cs"]), _d(c["table"]), _d(c["req"]), _d(c["pos"]), slots, q_out,
+            kc, vc]
+    rpos = _d(c["rpos"])
+
+    def check(qkv):
+        want, _ = oracle.norm_rope(_split(qkv, 8, 2, 128)[0], c["w"][0], 1e-6, c["cs"], c["rpos"])
+        got = _f64(q_out)
+        w = want[:25]
+        assert (np.abs(got[:25] - w) <= 2.0 ** -8 * np.abs(w) + 2e-6 * np.abs(w).max(-1, keepdims=True)).all()
+        assert (got[25:] == 7).all() and (slots[25:] == -1).all() and (slots[:25] >= 0).all()
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    bkv.bkv_qk_norm_rope_cache_write(*args, rope_positions=rpos, num_tokens=25, stream=side)
+    side.synchronize()
+    check(c["qkv"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bkv.bkv_qk_norm_rope_cache_write(*args, rope_positions=rpos, num_tokens=25)
+    new = cast(np.random.default_rng(3).standard_normal(c["qkv"].shape).astype(np.float32), "bf16")
+    for view, src in zip((q, k, v), _split(new, 8, 2, 128)):
+        view.copy_(_d(src))
+    g.replay()
+    torch.cuda.synchronize()
+    check(new)
+
+
 # ---------------------------------------------------------------------------
 # Attention of drafted trees
 # ---------------------------------------------------------------------------
@@ -448,6 +486,85 @@ def test_tree_decode_streams_and_graphs():
         assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("case", [
+    ([30, 140], 5, 160, 160, 128, 16, "bf16"),                   # more KV heads than SMs
+    ([9, 300, 70], 33, 88, 44, 128, 64, "bf16"),                 # KV heads that do not divide the SMs
+    ([12, 70], 3, 130, 1, 128, 16, "bf16"),                      # a group wider than a query tile
+    ([21, 400], 2, 128, 1, 128, 16, "bf16"),                     # one token a query tile
+    ([40, 260], 33, 100, 4, 128, 16, "bf16"),                    # pairs of query tiles of 125 rows, a part of them idle
+    ([60, 200], 3, 64, 1, 128, 32, "bf16"),                      # a pair whose second tile has one token
+    ([3, 4, 5] * 750, 3, 2, 1, 128, 8, "bf16"),                  # more requests than the tensor-core kernel's tables hold
+], ids=lambda c: f"n{len(c[0])}_t{c[1]}_h{c[2]}x{c[3]}")
+def test_tree_decode_head_and_batch_counts(case):
+    lens, t, hq, hkv, d, bs, dtype = case
+    p = Paged(lens, t, hq, hkv, d, bs, dtype)
+    mask = ancestors(parents(np.random.default_rng(6), len(lens), t))
+    want, _ = _want(p, mask)
+    check_attention(_f64(_tree(p, mask)), want, dtype)
+
+
+def test_tree_decode_nothing_cached():
+    """A bound of 0 on the lengths, and lengths of 0 under a bound: zeros everywhere."""
+    for dtype, lens, bound in (("bf16", [5, 9], 0), ("f32", [5, 9], 0), ("bf16", [0, 0], 500), ("f32", [0, 0], 500)):
+        p = Paged(lens, 4, 8, 2, 128, 16, dtype)
+        mask = np.ones((2, 4, 4), bool)
+        err = _err()
+        assert not _tree(p, mask, max_ctx=bound, err=err).any()
+        assert int(err.item()) == (2 if bound == 0 else 0)
+
+
+def test_tree_decode_very_long_context():
+    """One request of 70,001 positions over every column of CTAs, against torch in fp64."""
+    t, hq, hkv, L = 9, 8, 2, 70001
+    p = Paged([L], t, hq, hkv, 128, 64)
+    mask = ancestors(parents(np.random.default_rng(7), 1, t))
+    got = _tree(p, mask)[0].double()
+    rows = torch.from_numpy(p.rows(0, np.arange(L))).to(DEV)
+    seen = torch.ones(t, L, dtype=torch.bool, device=DEV)
+    seen[:, L - t:] = _d(mask[0])
+    q = _d(p.q)[0].double()
+    for h in range(hq):
+        k, v = (_d(c).view(-1, hkv, 128)[rows, h // 4].double() for c in (p.k, p.v))
+        s = (q[:, h] @ k.T / 128 ** 0.5).masked_fill(~seen, float("-inf"))
+        want = s.softmax(-1) @ v
+        assert ((got[:, h] - want).abs().amax(-1) <= 1e-2 * want.abs().amax(-1)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_decode_graph_replays_on_new_lengths(dtype):
+    """A captured call, replayed after lengths, table, mask and queries changed in place: nothing of the first
+    run is kept."""
+    a, b = (Paged(lens, 7, 8, 2, 128, 16, dtype, seed=s) for s, lens in ((1, [300, 20, 700]), (2, [9, 640, 0])))
+    rng = np.random.default_rng(5)
+    ma, mb = (ancestors(parents(rng, 3, 7)) for _ in range(2))
+    n = max(a.total, b.total)
+    w = max(a.table.shape[1], b.table.shape[1])
+    bufs = [torch.zeros((n,) + a.k.shape[1:], dtype=TDT[dtype], device=DEV) for _ in range(2)]
+    bufs += [torch.zeros(3, w, dtype=torch.int32, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV),
+             torch.zeros(3, 7, 1, dtype=torch.int32, device=DEV), torch.zeros(a.q.shape, dtype=TDT[dtype], device=DEV)]
+    k, v, table, lens, mask, q = bufs
+    out = torch.zeros_like(q)
+    ws = bkv.alloc_tree_workspace(3, 7, 8, 2, 128, 16, 700)
+
+    def fill(p, m):
+        k[: p.total], v[: p.total] = _d(p.k), _d(p.v)
+        table.fill_(-1)
+        table[:, : p.table.shape[1]] = _d(p.table)
+        lens.copy_(_d(p.lens))
+        mask.copy_(_i32(words(m)))
+        q.copy_(_d(p.q))
+
+    fill(a, ma)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bkv.bkv_paged_decode_tree(q, k, v, table, lens, 700, mask, out, ws)
+    for p, m in ((a, ma), (b, mb), (a, ma)):
+        fill(p, m)
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(_f64(out), _want(p, m)[0], dtype)
+
+
 # ---------------------------------------------------------------------------
 # Verification
 # ---------------------------------------------------------------------------
@@ -567,6 +684,60 @@ def test_verify_tree_bad_inputs_and_edges():
         assert np.array_equal(a, b)
     assert int(err.item()) == want[3] > 0
     assert got[0][4, 0] == -1 and got[0][5, 0] in (3, 5)
+
+
+def test_verify_shared_rows_and_streams():
+    """One set of target rows for all requests (request stride 0), on a side stream and replayed from a graph."""
+    rng = np.random.default_rng(17)
+    p = probs(rng, (1, 6, 777))
+    par = parents(rng, 20, 6)
+    tok = draws(rng, np.take_along_axis(np.repeat(p, 20, 0), np.maximum(par, 0)[..., None], 1))
+    u, us = _u(rng, 20, 6) * 0.4, _u(rng, 20)
+    want = oracle.verify_tree(np.repeat(p, 20, 0), tok, par, u, us)
+    shared = _d(p).expand(20, 6, 777)
+    for a, b in zip(_tree_verify(shared, tok, par, u, us), want):
+        assert np.array_equal(a, b)
+    args = [_d(tok), _d(par), _d(u), _d(us), torch.zeros(20, 6, dtype=torch.int64, device=DEV),
+            torch.zeros(20, 6, dtype=torch.int32, device=DEV), torch.zeros(20, dtype=torch.int32, device=DEV)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    bkv.bkv_verify_draft_tree(shared, *args, stream=side)
+    side.synchronize()
+    assert np.array_equal(args[4].cpu().numpy(), want[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bkv.bkv_verify_draft_tree(shared, *args)
+    for x in args[4:]:
+        x.fill_(-9)
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(args[4:], want):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_verify_wide_trees_and_long_chains():
+    """The most nodes and drafts: a root with 1023 children, a chain of 1024."""
+    rng = np.random.default_rng(18)
+    p = np.zeros((2, 1024, 1500), np.float32)
+    p[:] = probs(rng, (1, 1, 1500), 1.0)
+    par = np.zeros((2, 1024), np.int32)
+    par[:, 0] = -1
+    par[1, 600:] = 599
+    tok = np.stack([rng.permutation(1500)[:1024] for _ in range(2)])
+    u = np.full((2, 1024), 0.999, np.float32)
+    u[0, 1000:] = 0.0
+    us = _u(rng, 2)
+    want = oracle.verify_tree(p, tok, par, u, us)
+    for a, b in zip(_tree_verify(_d(p), tok, par, u, us), want):
+        assert np.array_equal(a, b)
+    q = p[:, :1, :].repeat(1024, 1)
+    t = np.concatenate([p, p[:, :1]], 1)
+    u = np.full((2, 1024), 0.5, np.float32)
+    u[1, 700] = 1.0
+    want = oracle.verify_chain(t, q, tok, u, us)
+    assert want[1].tolist() == [1024, 700]
+    got = _chain(_d(t), _d(q), tok, u, us)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
 
 
 def test_verify_offsets_past_32_bits():
