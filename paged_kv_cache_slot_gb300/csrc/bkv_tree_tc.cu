@@ -19,9 +19,9 @@
 //   tensor memory), so that one stream's softmax runs beside the other's MMAs;
 //   their O are joined when the unit ends.  A group of two query tiles gives
 //   each its own stream, and every K and V tile serves both.
-// * Warp roles (352 threads): warp 0 loads Q and gathers K tiles, the last warp
-//   gathers V tiles (rings of two or three 32 KB slots each, as the queries leave
-//   room), warp 1 issues every MMA from one thread; four softmax warps a stream,
+// * Warp roles (384 threads): warp 0 loads Q and gathers K tiles, warp 2 gathers
+//   V tiles (rings of two or three 32 KB slots each, as the queries leave room),
+//   warps 1 and 3 issue the MMAs, one thread each; four softmax warps a stream,
 //   one query row a thread.  A row's 128 scores stay in its thread's registers
 //   between the max and the weights: the lanes' quarters are tied to the SM's
 //   four partitions, so two warps a row would share one exponential unit anyway
@@ -36,6 +36,14 @@
 //   finite is zeroed too and remembered, and rows that see it become NaN.
 // * Every wait is bounded (~2 s), after which the CTA records 1 << 24 in
 //   err_count, frees its tensor memory and exits.
+//
+// Measured (device time of a call with its merge; 128-element heads, bf16): 256
+// requests of 9 to 8192 positions, 4 tokens of 32 / 8 heads (16 rows a group)
+// 218 us, 5.9 TB/s of K and V; 32 of 512 to 4096, 16 tokens (64 rows) 51 us, 4.6
+// TB/s: 9 us of it launches, the first tiles and the merge; 8 of 1000 to 16693,
+// 61 tokens of 64 / 8 heads (488 rows) 105 us, 0.84 PFLOP/s of the products
+// that the rows need: there the two streams' softmaxes take turns at the
+// exponential units with the products, and neither pipe is kept full.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -54,7 +62,7 @@ constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
 constexpr int kHalfBytes = kTile * 128;
 constexpr int kTileBytes = 2 * kHalfBytes;
-constexpr int kThreads = 384;   // K producer, MMA issuer, V producer and a spare warp; 2 x 4 softmax warps
+constexpr int kThreads = 384;   // K producer, MMA issuers (1 and 3), V producer; 2 x 4 softmax warps
 constexpr int kWarpV = 2;
 constexpr int kWarpS = 4;   // first softmax warp
 constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (128 columns each)
@@ -67,7 +75,7 @@ constexpr int kMaxStages = 3;                             // slots of a ring, at
 constexpr int kOffMask = 0;                               // 8 words: loaded segments per tile (ring)
 constexpr int kOffPoison = kOffMask + 8 * 4;              // 8 x 32 bytes: V rows of the tile that are not finite
 constexpr int kOffBar = kOffPoison + 8 * 32;
-constexpr int kNumBars = 4 * kMaxStages + 4 + 2 + 2 + 2 + 8 + 4;
+constexpr int kNumBars = 2 * 8 + 2 * kMaxStages + 4 + 2 + 2 + 2 + 8 + 4;
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 4;
 constexpr int kOffAnyBad = kOffAbort + 4;                 // a V row that was not finite has been met
@@ -247,11 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t *pre = reinterpret_cast<int32_t *>(smem + kOffPre);
     uint8_t *fill = smem + kOffFill;
     const uint32_t bar0 = sbase + kOffBar;
-    auto bar_kfull = [&](int s) { return bar0 + 8u * s; };
-    auto bar_kempty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-    auto bar_vfull = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };
-    auto bar_vempty = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };
-    constexpr int kB = 4 * kMaxStages;
+    // Tile j's K and V have landed: by tile, not by slot.  Where the tiles alternate, an MMA thread looks at its
+    // own stream's only, and a parity answers at once for a phase whose predecessor it has not seen end; of
+    // eight barriers each belongs to one stream (8 is even).
+    auto bar_kfull = [&](int j) { return bar0 + 8u * (j & 7); };
+    auto bar_vfull = [&](int j) { return bar0 + 8u * (8 + (j & 7)); };
+    auto phase_of = [](int j) { return (uint32_t)(j >> 3) & 1u; };
+    auto bar_kempty = [&](int s) { return bar0 + 8u * (16 + s); };
+    auto bar_vempty = [&](int s) { return bar0 + 8u * (16 + kMaxStages + s); };
+    constexpr int kB = 16 + 2 * kMaxStages;
     auto bar_qfull = [&](int b) { return bar0 + 8u * (kB + b); };
     auto bar_qempty = [&](int b) { return bar0 + 8u * (kB + 2 + b); };
     auto bar_sfull = [&](int x) { return bar0 + 8u * (kB + 4 + x); };
@@ -283,21 +295,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nbuf = dual ? 1 : sh.q_buffers;
 
     if (threadIdx.x == 0) {
+        for (int j = 0; j < 8; ++j) {
+            mbar_init(bar_kfull(j), 1);
+            mbar_init(bar_vfull(j), 1);
+            mbar_init(bar_mask(j), 1);
+        }
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(bar_kfull(s), 1);
             mbar_init(bar_kempty(s), 1);
-            mbar_init(bar_vfull(s), 1);
             mbar_init(bar_vempty(s), 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_qfull(x), 1);
-            mbar_init(bar_qempty(x), 1);
+            mbar_init(bar_qempty(x), dual ? 1 : 2);
             mbar_init(bar_sfull(x), 1);
             mbar_init(bar_pfull(x), (!dual || x == 0) ? 4 : aq1);
         }
-        mbar_init(bar_ofull, 2);
+        mbar_init(bar_ofull, dual ? 2 : 4);
         mbar_init(bar_oempty, aq0 + aq1);
-        for (int m = 0; m < 8; ++m) mbar_init(bar_mask(m), 1);
         for (int qw = 0; qw < 4; ++qw) mbar_init(bar_pair(qw), 2);
         *abort_flag = 0;
         *any_bad = 0;
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kWarpS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == 0 || warp == kWarpV) {
-            // ================= TMA producers (warp 0: Q and K, last warp: V) =================
+            // ================= TMA producers (warp 0: Q and K, warp 2: V) =================
             const bool is_v = warp == kWarpV;
             const bool count = !is_v && p == 0 && a.err;   // bad entries count once a KV head
             const int stages = is_v ? nV : nK;
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int64_t row_nxt = kt + 1 < x.nt ? entry(x.f + kt + 1) : -1;   // in flight meanwhile
                     const int s = ring.slot;
                     const uint32_t bar_e = is_v ? bar_vempty(s) : bar_kempty(s);
-                    const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
+                    const uint32_t bar_f = is_v ? bar_vfull(j) : bar_kfull(j);
                     if (!mbar_wait_warp(bar_e, ring.phase ^ 1u, abort_flag)) break;
                     ring.advance(stages);
                     const bool load = row_cur >= 0;
@@ -477,42 +491,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (global_ns() - t0 < 200000ull) {
                 }
             }
-        } else if (warp == 1) {
-            // ================= MMA issuer (one thread) =================
-            if (lane == 0) {
+        } else {
+            // ================= MMA issuers (one thread each) =================
+            // A stream's tiles in turn: O += P V of its last one, then S of the next over the same columns (one
+            // thread's MMAs run in issue order).  Where the tiles alternate each stream has its own thread, so
+            // that one's barriers are waited for while the other's products run (32 requests of 512 to 4096
+            // positions, 16 tokens of 32 / 8 heads: 51.3 us, 53.7 with one thread).  Two query tiles share every K
+            // and V tile, and two threads drift apart over them: there warp 1 issues both (8 requests of 1000 to
+            // 16693 positions, 61 tokens of 64 / 8 heads: 105 us, 118 with two threads).
+            if (lane == 0 && (!dual || warp == 1)) {
                 constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);   // Q (K-major) x K (K-major)
                 constexpr uint32_t kIdescO = idesc_bf16(128, 128, 0, 1);   // P (TMEM) x V (MN-major)
-                int np[2] = {0, 0};   // P tiles consumed
-                // O_x += P_x V(next tile): `first` overwrites O_x, once the unit before has been read out
-                Ring kr, vr;          // tiles are multiplied in their order
-                auto issue_pv = [&](int xb, bool first, int unit) -> bool {
-                    const int s = vr.slot;
-                    if (!mbar_wait(bar_vfull(s), vr.phase, abort_flag) ||
-                        !mbar_wait(bar_pfull(xb), (uint32_t)(np[xb] & 1), abort_flag))
+                uint32_t pphase = 0u;   // bit x: P of stream x
+                // O_xb += P_xb V(tile): `first` overwrites O_xb, once the unit before has been read out
+                auto issue_pv = [&](int xb, int tile, int slot, bool first, int unit) -> bool {
+                    if (!mbar_wait(bar_vfull(tile), phase_of(tile), abort_flag) ||
+                        !mbar_wait(bar_pfull(xb), (pphase >> xb) & 1u, abort_flag))
                         return false;
-                    ++np[xb];
+                    pphase ^= 1u << xb;
                     if (first && unit > 0 && !mbar_wait(bar_oempty, (uint32_t)((unit - 1) & 1), abort_flag)) return false;
                     tc_fence_after();
-                    const uint32_t v_base = sm_v + s * kTileBytes;
+                    const uint32_t v_base = sm_v + slot * kTileBytes;
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk) {
-                        mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + 8u * (uint32_t)kk, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
-                                    kIdescO, (first && kk == 0) ? 0u : 1u);
-                    }
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_bf16_ts(tmem + col_o(xb), tmem + col_s(xb) + 8u * (uint32_t)kk,
+                                    sdesc(v_base + kk * 2048, kHalfBytes, 1024), kIdescO, (first && kk == 0) ? 0u : 1u);
                     return true;
                 };
-                auto issue_s = [&](int xb, int s, int qb) {
-                    const uint32_t k_base = sm_k + s * kTileBytes;
+                auto issue_s = [&](int xb, int slot, int qb) {
+                    const uint32_t k_base = sm_k + slot * kTileBytes;
                     const uint32_t q_base = sm_q + qb * 2 * sh.q_half;
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
+                    for (int kk = 0; kk < kD / 16; ++kk)
                         // (rows of the query tile past the group's: whatever lies there, their scores are not used)
                         mma_bf16(tmem + col_s(xb), sdesc(q_base + (kk >> 2) * sh.q_half + (kk & 3) * 32, 16, 1024),
-                                 sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
-                    }
+                                 sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024), kIdescS,
+                                 kk > 0 ? 1u : 0u);
                     mma_commit(bar_sfull(xb));
                 };
-                // The unit's last P V: O is settled.  The plain arrival carries the softmax warps' own
+                // This thread's part of the unit is settled.  The plain arrival carries the softmax warps' own
                 // shared-memory writes (acquired with P) on to the other warps.
                 auto finish = [&]() {
                     mma_commit(bar_ofull);
@@ -520,64 +537,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 Units units(a, pre, fill, q);
                 Unit x;
+                Ring kr, vr;   // slots of the next K tile; of the next V tile (dual), or K's tile (alternating)
+                int j = 0;
                 bool ok = true;
                 if (!dual) {
-                    // stream j & 1 has tile j; its P V is issued before the S of tile j + 2, over the same columns
-                    struct {
-                        int unit;
-                        bool on, first, last;
-                    } pend[2] = {{0, false, false, false}, {0, false, false, false}};
-                    auto settle = [&](int xb) -> bool {
-                        auto &w = pend[xb];
-                        if (!w.on) return true;
-                        w.on = false;
-                        if (!issue_pv(xb, w.first, w.unit)) return false;
-                        mma_commit(bar_vempty(vr.slot));
-                        vr.advance(nV);
-                        if (w.last) finish();
+                    const int xb = warp == 1 ? 0 : 1;   // has the tiles j of its parity
+                    // the tile whose P V is still to come: its number, V slot, and what it is in its unit
+                    bool pend = false, pend_first = false, pend_last = false;
+                    int pend_tile = 0, pend_slot = 0, pend_unit = 0;
+                    auto settle = [&]() -> bool {
+                        if (!pend) return true;
+                        pend = false;
+                        if (!issue_pv(xb, pend_tile, pend_slot, pend_first, pend_unit)) return false;
+                        mma_commit(bar_vempty(pend_slot));
+                        if (pend_last) finish();
                         return true;
                     };
-                    int xb = 0;
                     for (int uq = 0; ok && units.next(x); ++uq) {
                         const int b = nbuf == 2 ? uq & 1 : 0;
                         const uint32_t qphase = (uint32_t)((nbuf == 2 ? uq >> 1 : uq) & 1);
-                        for (int kt = 0; kt < x.nt; ++kt, xb ^= 1) {
-                            // operands that are there already are not waited for between P V and S: the tensor
-                            // cores run dry in the time that a barrier takes to answer
-#if TW
-                            const bool ready = (kt > 0 || mbar_test(bar_qfull(b), qphase)) && mbar_test(bar_kfull(kr.slot), kr.phase);
-#else
-                            const bool ready = false;
-#endif
-                            ok = settle(xb);
-                            if (ok && !ready)
-                                ok = (kt > 0 || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
-                                     mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag);
+                        bool had = false;
+                        for (int kt = 0; kt < x.nt; ++kt, ++j, kr.advance(nK), vr.advance(nV)) {
+                            if ((j & 1) != xb) continue;
+                            ok = settle() && (had || mbar_wait(bar_qfull(b), qphase, abort_flag)) &&
+                                 mbar_wait(bar_kfull(j), phase_of(j), abort_flag);
                             if (!ok) break;
                             tc_fence_after();
                             issue_s(xb, kr.slot, b);
                             mma_commit(bar_kempty(kr.slot));
-                            kr.advance(nK);
-                            if (kt == x.nt - 1) mma_commit(bar_qempty(b));
-                            pend[xb].unit = uq;
-                            pend[xb].on = true;
-                            pend[xb].first = kt < 2;
-                            pend[xb].last = kt == x.nt - 1;
+                            pend = true;
+                            pend_first = !had;
+                            pend_last = kt + 2 >= x.nt;
+                            pend_unit = uq;
+                            pend_tile = j;
+                            pend_slot = vr.slot;
+                            had = true;
+                            if (pend_last) mma_commit(bar_qempty(b));
+                        }
+                        if (ok && !had) {   // no tile of the unit is this stream's: only its part of the barriers
+                            ok = settle() && mbar_wait(bar_qfull(b), qphase, abort_flag) &&
+                                 (uq == 0 || mbar_wait(bar_oempty, (uint32_t)((uq - 1) & 1), abort_flag));
+                            if (ok) {
+                                mbar_arrive(bar_qempty(b));
+                                finish();
+                            }
                         }
                     }
-                    if (ok) ok = settle(xb) && settle(xb ^ 1);
+                    if (ok) settle();
                 } else {
                     // per key tile: O_A += P_A V(-1), S_A; O_B += P_B V(-1), S_B
                     for (int uq = 0; ok && units.next(x); ++uq) {
                         ok = mbar_wait(bar_qfull(0), (uint32_t)(uq & 1), abort_flag);
                         for (int kt = 0; ok && kt <= x.nt; ++kt) {
-                            if (kt < x.nt && !mbar_wait(bar_kfull(kr.slot), kr.phase, abort_flag)) {
+                            if (kt < x.nt && !mbar_wait(bar_kfull(j + kt), phase_of(j + kt), abort_flag)) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
+#pragma unroll
                             for (int xb = 0; xb < 2; ++xb) {
-                                if (kt > 0 && !issue_pv(xb, kt == 1, uq)) {
+                                if (kt > 0 && !issue_pv(xb, j + kt - 1, vr.slot, kt == 1, uq)) {
                                     ok = false;
                                     break;
                                 }
@@ -596,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 finish();
                             }
                         }
+                        j += x.nt;
                     }
                 }
             }
@@ -638,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t mword = mask_words[j & 7];
                     const int k0 = (x.f + kt) * kTile;
                     if (mword != all_seg || k0 + kTile > x.L - a.T) {
-                        if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
+                        if (!mbar_wait_warp(bar_vfull(j), phase_of(j), abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -756,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = fmaf(l, corr, sum2.x + sum2.y);
                     m = mn;
                     if (!full && fixes && aq == 4) {
-                        if (!mbar_wait_warp(bar_vfull(vr.slot), vr.phase, abort_flag)) {
+                        if (!mbar_wait_warp(bar_vfull(jj), phase_of(jj), abort_flag)) {
                             ok = false;
                             break;
                         }

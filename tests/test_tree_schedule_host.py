@@ -82,16 +82,6 @@ class _Bar:
             self.pending, self.phase = self.count, self.phase + 1
 
 
-class _Ring:
-    def __init__(self, n):
-        self.n, self.slot, self.phase = n, 0, 0
-
-    def advance(self):
-        self.slot += 1
-        if self.slot == self.n:
-            self.slot, self.phase = 0, self.phase ^ 1
-
-
 def _run(rng, units, nK, nV, nbuf, dual, aq):
     now, events, count = [0], [], [0]
 
@@ -104,12 +94,13 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
         assert bar.phase in (k, k + 1), "a parity wait a phase early or late"
         return bar, k
 
-    kf, ke = [_Bar(1) for _ in range(3)], [_Bar(1) for _ in range(3)]
-    vf, ve = [_Bar(1) for _ in range(3)], [_Bar(1) for _ in range(3)]
-    qf, qe = [_Bar(1), _Bar(1)], [_Bar(1), _Bar(1)]
+    issuers = 1 if dual else 2
+    kf, ke = [_Bar(1) for _ in range(8)], [_Bar(1) for _ in range(3)]
+    vf, ve = [_Bar(1) for _ in range(8)], [_Bar(1) for _ in range(3)]
+    qf, qe = [_Bar(1), _Bar(1)], [_Bar(issuers), _Bar(issuers)]
     sf = [_Bar(1), _Bar(1)]
     pf = [_Bar(4), _Bar(aq[1] if dual else 4)]
-    of, oe = _Bar(2), _Bar(aq[0] + aq[1])
+    of, oe = _Bar(2 * issuers), _Bar(aq[0] + aq[1])
     mk, pair = [_Bar(1) for _ in range(8)], [_Bar(2) for _ in range(4)]
     K, V, Q, mask = [None] * 3, [None] * 3, [None] * 2, [None] * 8
     S, Pw, O = [None, None], [None, None], [[], []]
@@ -121,14 +112,14 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
                 own.setdefault((u, x), []).append(j)
             j += 1
     pace = [rng.randint(1, 40) for _ in range(8)]
-    free = [0]
+    free = [0, 0]
 
-    def mma(f):   # one issuing thread's products run in order
-        free[0] = max(now[0], free[0]) + 6
-        later(free[0] - now[0], f)
+    def mma(x, f):   # one issuing thread's products run in order
+        free[x] = max(now[0], free[x]) + rng.randint(5, 9)
+        later(free[x] - now[0], f)
 
-    def commit(bar):
-        later(max(now[0], free[0]) - now[0] + rng.randint(0, 3), bar.arrive)
+    def commit(x, bar):
+        later(max(now[0], free[x]) - now[0] + rng.randint(0, 3), bar.arrive)
 
     def use(k):   # a slot's or buffer's k-th use waits for the end of its (k - 1)-th
         return k - 1
@@ -157,92 +148,100 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
 
                 def land(s=s, j=j):
                     store[s] = j
-                    full[s].arrive()
+                    full[j & 7].arrive()
                 later(rng.randint(1, pace[1 + is_v]), land)
                 j += 1
                 yield rng.randint(0, 2)
 
-    def issuer():
-        done = [0, 0]   # P tiles used of each stream
-        kj = vj = 0
+    done = [0, 0]   # P tiles used of each stream
 
-        def pv(x, j, first, u):
-            nonlocal vj
-            s = j % nV
-            yield wait(vf[s], j // nV)
-            yield wait(pf[x], done[x])
-            done[x] += 1
-            if first and u:
-                yield wait(oe, u - 1)
+    def finish(i):
+        commit(i, of)
+        of.arrive()
 
-            def f():
-                assert V[s] == j and Pw[x] == j
-                Pw[x] = None
-                if first:
-                    O[x] = []
-                O[x].append(j)
-            mma(f)
+    def pv(i, x, j, first, u):
+        yield wait(vf[j & 7], j >> 3)
+        yield wait(pf[x], done[x])
+        done[x] += 1
+        if first and u:
+            yield wait(oe, u - 1)
 
-        def score(x, j, u, b):
-            def f(s=j % nK):
-                assert K[s] == j and Q[b] == u and Pw[x] is None
-                S[x] = j
-            mma(f)
-            commit(sf[x])
+        def f():
+            assert V[j % nV] == j and Pw[x] == j
+            Pw[x] = None
+            if first:
+                O[x] = []
+            O[x].append(j)
+        mma(i, f)
 
-        def finish():
-            commit(of)
-            of.arrive()
+    def score(i, x, j, u, b):
+        def f():
+            assert K[j % nK] == j and Q[b] == u and Pw[x] is None
+            S[x] = j
+        mma(i, f)
+        commit(i, sf[x])
 
-        pend = [None, None]
+    def issuer_of_both():   # two query tiles: one thread
+        j = 0
+        for u, n in enumerate(units):
+            yield wait(qf[0], u)
+            for t in range(n + 1):
+                if t < n:
+                    yield wait(kf[(j + t) & 7], (j + t) >> 3)
+                for x in range(2):
+                    if t:
+                        yield from pv(0, x, j + t - 1, t == 1, u)
+                    if t < n:
+                        score(0, x, j + t, u, 0)
+                    yield rng.randint(0, 6)
+                if t:
+                    commit(0, ve[(j + t - 1) % nV])
+                if t < n:
+                    commit(0, ke[(j + t) % nK])
+                    if t == n - 1:
+                        commit(0, qe[0])
+                else:
+                    finish(0)
+            j += n
 
-        def settle(x):
-            if pend[x]:
-                j, first, last, u = pend[x]
-                pend[x] = None
-                yield from pv(x, j, first, u)
-                commit(ve[j % nV])
-                if last:
-                    finish()
+    def issuer(x):   # one query tile: a thread a stream
+        pend = None  # the tile whose P V is to come
+
+        def settle():
+            nonlocal pend
+            if pend is None:
+                return
+            (j, first, last, u), pend = pend, None
+            yield from pv(x, x, j, first, u)
+            commit(x, ve[j % nV])
+            if last:
+                finish(x)
         j = 0
         for u, n in enumerate(units):
             b, k = (u & 1, u >> 1) if nbuf == 2 else (0, u)
-            if dual:
-                yield wait(qf[b], k)
-                for t in range(n + 1):
-                    if t < n:
-                        yield wait(kf[j % nK], j // nK)
-                    for x in range(2):
-                        if t:
-                            yield from pv(x, j - 1, t == 1, u)
-                        if t < n:
-                            score(x, j, u, b)
-                        yield rng.randint(0, 6)
-                    if t:
-                        commit(ve[(j - 1) % nV])
-                    if t < n:
-                        commit(ke[j % nK])
-                        if t == n - 1:
-                            commit(qe[b])
-                        j += 1
-                    else:
-                        finish()
-            else:
-                for t in range(n):
-                    x = j & 1
-                    yield from settle(x)
-                    if t == 0:
+            had = False
+            for t in range(n):
+                if (j & 1) == x:
+                    yield from settle()
+                    if not had:
                         yield wait(qf[b], k)
-                    yield wait(kf[j % nK], j // nK)
-                    score(x, j, u, b)
-                    commit(ke[j % nK])
-                    if t == n - 1:
-                        commit(qe[b])
-                    pend[x] = (j, t < 2, t == n - 1, u)
-                    j += 1
+                    yield wait(kf[j & 7], j >> 3)
+                    score(x, x, j, u, b)
+                    commit(x, ke[j % nK])
+                    last = t + 2 >= n
+                    pend, had = (j, not had, last, u), True
+                    if last:
+                        commit(x, qe[b])
                     yield rng.randint(0, 6)
-        yield from settle(j & 1)
-        yield from settle((j + 1) & 1)
+                j += 1
+            if not had:   # no tile of the unit is this stream's
+                yield from settle()
+                yield wait(qf[b], k)
+                if u:
+                    yield wait(oe, u - 1)
+                qe[b].arrive()
+                finish(x)
+        yield from settle()
 
     posted = {}
 
@@ -260,7 +259,7 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
                 yield rng.randint(1, pace[3 + x])
                 assert mask[j & 7] == j
                 if fixes and rng.random() < 0.5:
-                    yield wait(vf[j % nV], j // nV)
+                    yield wait(vf[j & 7], j >> 3)
                     assert V[j % nV] == j
                 yield rng.randint(1, pace[5])
                 assert S[x] == j and (not fixes or V[j % nV] in (j, None, j - nV))
@@ -280,7 +279,7 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
                 yield rng.randint(1, pace[6])
             oe.arrive()
 
-    agents = [loads(False), loads(True), issuer()] + [softmax(x, w) for x in range(2) for w in range(4)]
+    agents = [loads(False), loads(True)] + ([issuer_of_both()] if dual else [issuer(0), issuer(1)]) + [softmax(x, w) for x in range(2) for w in range(4)]
     at, blocked, alive = [0] * len(agents), [None] * len(agents), set(range(len(agents)))
     while alive:
         while events and events[0][0] <= now[0]:
@@ -303,7 +302,7 @@ def _run(rng, units, nK, nV, nbuf, dual, aq):
             now[0] = max(now[0] + 1, min(nxt))
 
 
-@pytest.mark.parametrize("seed", range(150))
+@pytest.mark.parametrize("seed", range(200))
 def test_barriers_answer_every_wait(seed):
     rng = random.Random(seed)
     dual = rng.random() < 0.4
