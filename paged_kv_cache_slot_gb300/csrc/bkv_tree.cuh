@@ -33,9 +33,10 @@ struct TreeArgs {
     // The split: a stream is (request, KV head, token group of TS tokens, NR =
     // TS * G query rows); its partials are slots of NR rows in the workspace.
     int32_t TS, NR, groups;  // groups = ceil(T / TS)
-    int32_t P;               // tensor-core kernel: CTA columns of the split (grid = P * H_kv * groups)
-    int32_t chunk, n_chunks; // CUDA-core kernel: positions a split, splits at max_ctx
-    int4 *ws_split;          // [P] the stream that column q begins and does not end: (request, slots, first slot, 0)
+    int32_t P;               // columns: each takes its share of the positions of all requests
+    // A column may end one stream that it did not begin (its partial: slot q of 2 P a KV head and group) and begin
+    // one that it does not end (slot P + q).
+    int2 *ws_split;          // [P] the latter: (request, columns that share it), (0, 0) without one
     float *ws_o;             // [slots][NR][D] unnormalised partial outputs
     float *ws_ml;            // [slots][NR][2] (running max in base 2, sum of weights)
 };

@@ -163,19 +163,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
-// Whether a phase is over, without waiting (try_wait may suspend the thread).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // One unit: tiles [f, f + nt) of request r.  whole: they are all of its tiles.
 struct Unit {
     int r, L, f, nt, slot;
@@ -189,11 +176,12 @@ struct Unit {
 struct Units {
     const int32_t *pre;
     const uint8_t *fill;
-    int r, q, t, t1;
+    int r, q, t, t1, P;
     __device__ Units(const TreeArgs &a, const int32_t *pre_, const uint8_t *fill_, int q_) {
         pre = pre_;
         fill = fill_;
         q = q_;
+        P = a.P;
         const int64_t C = pre[a.num_reqs];
         const int64_t peff = C < a.P ? C : a.P;
         t = (int)(q < peff ? C * q / peff : C);
@@ -206,17 +194,17 @@ struct Units {
         }
         r = lo;
     }
-    // The stream that this column begins and does not end (before next() is called): its request, how
-    // many columns share it, and its first slot past the head's; all 0 without one.
-    __device__ int4 split(const TreeArgs &a) const {
-        if (t >= t1) return make_int4(0, 0, 0, 0);
+    // The stream that this column begins and does not end (before next() is called): its request and how
+    // many columns share it; 0 without one.
+    __device__ int2 split(const TreeArgs &a) const {
+        if (t >= t1) return make_int2(0, 0);
         int r1 = r;
         while (pre[r1 + 1] < t1) ++r1;   // the request that the share ends in
         const int s = pre[r1], e = pre[r1 + 1] - kEndCost;   // its tiles
-        if (s < t || s >= t1 || e <= t1) return make_int4(0, 0, 0, 0);
+        if (s < t || s >= t1 || e <= t1) return make_int2(0, 0);
         const int64_t C = pre[a.num_reqs], peff = C < a.P ? C : a.P;
         const int q1 = (int)((e * peff - 1) / C);   // the column of its last tile
-        return make_int4(r1, q1 - q + 1, q + r1, 0);
+        return make_int2(r1, q1 - q + 1);
     }
     __device__ bool next(Unit &x) {
         for (; t < t1; ++r) {
@@ -230,7 +218,7 @@ struct Units {
             x.nt = hi - lo;
             x.L = (e - s - 1) * kTile + fill[r] + 1;
             x.whole = lo == s && hi == e;
-            x.slot = q + r;
+            x.slot = lo == s ? P + q : q;
             ++r;
             return true;
         }
@@ -789,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 // ---- the unit's end ----
                 const int srow = row + (dual ? xb * tok_per_tile * G : 0);   // row of the slot
-                const int64_t prow = ((int64_t)hp * (a.P + a.num_reqs) + x.slot) * a.NR + srow;
+                const int64_t prow = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR + srow;
                 float *po = a.ws_o + prow * kD;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
                                      (((int64_t)x.r * a.T + tok) * a.H_q + (int64_t)g * G + hh) * kD;

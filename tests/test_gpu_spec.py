@@ -503,6 +503,35 @@ def test_tree_decode_head_and_batch_counts(case):
     check_attention(_f64(_tree(p, mask)), want, dtype)
 
 
+@pytest.mark.parametrize("t,hq,hkv,d,bs,dtype", [
+    (3, 4, 2, 66, 12, "f32"),
+    (11, 15, 5, 64, 100, "f32"),                                 # blocks of no whole number of tiles
+    (2, 4, 4, 128, 48, "f32"),
+    (24, 3, 1, 36, 7, "bf16"),
+    (40, 4, 2, 96, 16, "bf16"),                                  # several query tiles
+    (1, 8, 1, 256, 1, "f32"),
+])
+def test_tree_decode_ragged_batches_without_tensor_cores(t, hq, hkv, d, bs, dtype):
+    """Requests from none to 2,500 positions in one batch, many of them empty, with missing and bad entries: each of
+    the bad ones counts once a KV head, however the columns share the positions."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(0, 120, 150) * (rng.random(150) < 0.6)
+    lens[[7, 80, 149]] = 2500, 1, 1300
+    p = Paged(lens, t, hq, hkv, d, bs, dtype)
+    need = -(-p.lens // bs)
+    for r in range(150):
+        for b in range(need[r]):
+            if rng.random() < 0.03:
+                p.table[r, b] = rng.choice([0, -1, p.total, p.total + 5])
+    mask = ancestors(parents(rng, 150, t))
+    want, errs = _want(p, mask)
+    err = _err()
+    got = _tree(p, mask, err=err)
+    assert errs > 0 and int(err.item()) == errs * hkv
+    check_attention(_f64(got), want, dtype)
+    assert torch.equal(got, _tree(p, mask))                      # and the same bits again
+
+
 def test_tree_decode_nothing_cached():
     """A bound of 0 on the lengths, and lengths of 0 under a bound: zeros everywhere."""
     for dtype, lens, bound in (("bf16", [5, 9], 0), ("f32", [5, 9], 0), ("bf16", [0, 0], 500), ("f32", [0, 0], 500)):

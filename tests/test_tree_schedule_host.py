@@ -2,7 +2,7 @@
 
 The schedule (which column of CTAs takes which tiles, and where partials go) is
 restated from its definition and checked for what the merge relies on: every
-tile taken once, partial slots distinct and contiguous per stream, the table of
+tile taken once, partial slots distinct and where the merge looks for them, the table of
 split streams complete.  The barrier protocol of the kernel's warps (rings of
 K and V slots, query buffers, two softmax streams, the unit's end) is run as
 agents with random delays: no wait may be left unanswered, none answered a
@@ -13,10 +13,10 @@ import random
 import numpy as np
 import pytest
 
-TILE, END_COST = 128, 3
+KERNELS = [(128, 3), (32, 1)]   # positions a tile, tiles that a unit's end takes as long as
 
 
-def _columns(lens, P):
+def _columns(lens, P, TILE, END_COST):
     """Column q's units: (request, first tile, tiles, whole, slot)."""
     tiles = [-(-n // TILE) for n in lens]
     cost = [t + END_COST if t else 0 for t in tiles]
@@ -30,28 +30,29 @@ def _columns(lens, P):
         for r, t in enumerate(tiles):
             a, b = max(lo, pre[r]), min(hi, pre[r] + t)
             if a < b:
-                units.append((r, a - pre[r], b - a, b - a == t, q + r))
-        split = (0, 0, 0)
+                units.append((r, a - pre[r], b - a, b - a == t, P + q if a == pre[r] else q))
+        split = (0, 0)
         for r, t in enumerate(tiles):   # the stream that this column begins and does not end
             s, e = pre[r], pre[r] + t
             if t and lo <= s < hi < e:
-                split = (r, (e * peff - 1) // C - q + 1, q + r)
+                split = (r, (e * peff - 1) // C - q + 1)
         out.append((units, split))
     return tiles, out
 
 
 @pytest.mark.parametrize("seed", range(40))
-def test_every_tile_once_and_slots_for_the_merge(seed):
+@pytest.mark.parametrize("TILE,END_COST", KERNELS)
+def test_every_tile_once_and_slots_for_the_merge(seed, TILE, END_COST):
     rng = random.Random(seed)
     P = rng.choice([1, 2, 5, 9, 19, 76, 152])
     lens = [rng.choice([0, 1, 127, 128, 129, rng.randint(1, 20000), rng.randint(1, 700)]) for _ in range(rng.randint(1, 60))]
-    tiles, cols = _columns(lens, P)
+    tiles, cols = _columns(lens, P, TILE, END_COST)
     seen = [np.zeros(t, int) for t in tiles]
     parts, slots = {}, set()
     for q, (units, split) in enumerate(cols):
         for r, f, n, whole, slot in units:
             seen[r][f:f + n] += 1
-            assert slot < P + len(lens)
+            assert slot < 2 * P
             if whole:
                 assert n == tiles[r]
             else:
@@ -59,11 +60,11 @@ def test_every_tile_once_and_slots_for_the_merge(seed):
                 slots.add(slot)
                 parts.setdefault(r, []).append(slot)
     assert all((s == 1).all() for s in seen)
-    table = {s[0]: s for _, s in cols if s[1]}
+    table = {s[0]: (q, s[1]) for q, (_, s) in enumerate(cols) if s[1]}
     assert set(table) == set(parts)              # every split stream, once
     for r, got in parts.items():
-        _, n, first = table[r]
-        assert got == list(range(first, first + n)) and n >= 2
+        q, n = table[r]
+        assert got == [P + q] + list(range(q + 1, q + n)) and n >= 2
     load = [sum(n for _, _, n, _, _ in u) + END_COST * len(u) for u, _ in cols]
     assert max(load) <= sum(tiles + [END_COST for t in tiles if t]) / P + 2 + 2 * END_COST or P > sum(tiles)
 
