@@ -40,15 +40,17 @@ constexpr int kUnroll = 16;       // elements of each row in flight a lane
 
 // CTA size, the CTAs an SM is built to hold, and how many of them an SM a launch
 // may ask for before its clusters get narrower.  Chains stream two rows and are
-// bound by bandwidth: small CTAs, several waves (100003 tokens: 256 requests 44.6
-// us, 61.7 with 512 threads and one wave; 100 requests of 90001 22.3 and 20.4).
-// Trees walk before they stream: large CTAs, one wave (64 requests of 131072
-// 14.6 us, 22.2 with 256 threads).
+// bound by bandwidth: small CTAs, about two waves, so that one's walk and border
+// run beside another's sums (256 requests of 100003 tokens: 41 us, 5.0 TB/s; 45
+// with one wave or four, 44 with three CTAs an SM, 58 with six and half of the
+// loads in flight; 61.7 with 512 threads, before the sums by pairs).  Trees walk
+// before they stream: large CTAs, one wave (64 requests of 131072 14.1 us, 18.2
+// with three an SM; 22.2 with 256 threads, before the sums by pairs).
 template <bool kChain>
 struct Shape {
     static constexpr int kThreads = kChain ? 256 : 512;
     static constexpr int kWarps = kThreads / 32;
-    static constexpr int kBuilt = kChain ? 3 : 2;
+    static constexpr int kBuilt = kChain ? 4 : 2;
     static constexpr int kAsked = kChain ? 7 : 2;
 };
 
@@ -79,15 +81,15 @@ struct Args {
 struct Limbs {
     int32_t h, l, m;
 };
+constexpr float kC1 = 2.f, kC2 = 0x1.8p-21f, kC3 = 0x1.8p-33f;
 __device__ __forceinline__ Limbs limbs(float x) {
-    constexpr float c1 = 2.f, c2 = 0x1.8p-21f, c3 = 0x1.8p-33f;
-    const float a = __fadd_rn(x, c1);
-    const float x1 = __fsub_rn(x, __fsub_rn(a, c1));
-    const float b = __fadd_rn(x1, c2);
-    const float x2 = __fsub_rn(x1, __fsub_rn(b, c2));
-    const float c = __fadd_rn(x2, c3);
-    return {__float_as_int(a) - __float_as_int(c1), __float_as_int(b) - __float_as_int(c2),
-            __float_as_int(c) - __float_as_int(c3)};
+    const float a = __fadd_rn(x, kC1);
+    const float x1 = __fsub_rn(x, __fsub_rn(a, kC1));
+    const float b = __fadd_rn(x1, kC2);
+    const float x2 = __fsub_rn(x1, __fsub_rn(b, kC2));
+    const float c = __fadd_rn(x2, kC3);
+    return {__float_as_int(a) - __float_as_int(kC1), __float_as_int(b) - __float_as_int(kC2),
+            __float_as_int(c) - __float_as_int(kC3)};
 }
 __device__ __forceinline__ long long whole_of(const Limbs &v) {
     return ((long long)v.h << 34) + ((long long)v.l << 12) + v.m;
@@ -108,50 +110,104 @@ __device__ __forceinline__ unsigned long long weight(float p, float q) {
     return w > 0 ? w : 0;
 }
 
+// limbs() of two values in one instruction each step (every operation rounds
+// as the single one): the sums' bits, with the constants still in them.
+struct Limbs2 {
+    uint32_t h[2], l[2], m[2];
+};
+__device__ __forceinline__ unsigned long long pair_of(float x, float y) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, float c) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(pair_of(c, c)));
+    return r;
+}
+__device__ __forceinline__ unsigned long long sub2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(pair_of(-1.f, -1.f)), "l"(a));
+    return r;
+}
+__device__ __forceinline__ void split2(unsigned long long a, uint32_t (&w)[2]) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(w[0]), "=r"(w[1]) : "l"(a));
+}
+__device__ __forceinline__ Limbs2 limbs2(float x, float y) {
+    Limbs2 r;
+    const unsigned long long v = pair_of(x, y);
+    const unsigned long long a = add2(v, kC1);
+    const unsigned long long v1 = sub2(v, add2(a, -kC1));
+    const unsigned long long b = add2(v1, kC2);
+    const unsigned long long v2 = sub2(v1, add2(b, -kC2));
+    split2(a, r.h);
+    split2(b, r.l);
+    split2(add2(v2, kC3), r.m);
+    return r;
+}
+
+// The weights of one round: N tokens of this lane from v, below v1 (all of
+// them: kFull).  Their limbs fit 32 bits.
+template <bool kResidual, int kVec, int N, bool kFull>
+__device__ __forceinline__ long long round_sum(const float *pr, const float *qr, uint32_t v, uint32_t v1) {
+    float x[N], y[N];
+#pragma unroll
+    for (int k = 0; k < N; k += kVec) {
+        const bool in = kFull || v + 32 * k < v1;
+        if constexpr (kVec == 4) {
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(x + k) = in ? __ldg(reinterpret_cast<const float4 *>(pr + v + 32 * k)) : z;
+            if (kResidual)
+                *reinterpret_cast<float4 *>(y + k) = in ? __ldg(reinterpret_cast<const float4 *>(qr + v + 32 * k)) : z;
+        } else {
+            x[k] = in ? __ldg(pr + v + 32 * k) : 0.f;
+            if (kResidual) y[k] = in ? __ldg(qr + v + 32 * k) : 0.f;
+        }
+    }
+    uint32_t h = 0, l = 0, m = 0;
+    if constexpr (kResidual) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float xs = __saturatef(x[k]), ys = __saturatef(y[k]);
+            const Limbs2 t = limbs2(xs, ys);
+            if (xs > ys) {   // rounding keeps the order
+                h += t.h[0] - t.h[1];
+                l += t.l[0] - t.l[1];
+                m += t.m[0] - t.m[1];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const Limbs2 t = limbs2(__saturatef(x[k]), __saturatef(x[k + 1]));
+            h += t.h[0] + t.h[1];
+            l += t.l[0] + t.l[1];
+            m += t.m[0] + t.m[1];
+        }
+        h -= N * __float_as_uint(kC1);
+        l -= N * __float_as_uint(kC2);
+        m -= N * __float_as_uint(kC3);
+    }
+    return whole_of({(int32_t)h, (int32_t)l, (int32_t)m});
+}
+
 // The weights of tokens [v0, v1), a warp's part, of this lane: four at a time
 // where both rows start on 16 bytes (and v0 and v1 are whole fours), one
 // otherwise; the elements of a round are loaded before the first is used, and
-// their limbs fit 32 bits.
+// what is left below a round takes no more of one than it needs.  (256 chains of
+// 100003 tokens: 40.9 us, 44.6 with a value an instruction and a test a load.)
 template <bool kResidual, int kVec>
 __device__ __forceinline__ unsigned long long part_sum(const float *pr, const float *qr, int64_t v0, int64_t v1,
                                                        int lane) {
     long long sum = 0;
-    for (int64_t v = v0 + lane * kVec; v < v1; v += 32 * kUnroll) {
-        float x[kUnroll], y[kUnroll];
-#pragma unroll
-        for (int k = 0; k < kUnroll; k += kVec) {
-            const int64_t at = v + 32 * k;
-            if constexpr (kVec == 4) {
-                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                *reinterpret_cast<float4 *>(x + k) = at < v1 ? __ldg(reinterpret_cast<const float4 *>(pr + at)) : z;
-                if (kResidual)
-                    *reinterpret_cast<float4 *>(y + k) = at < v1 ? __ldg(reinterpret_cast<const float4 *>(qr + at)) : z;
-            } else {
-                x[k] = at < v1 ? __ldg(pr + at) : 0.f;
-                if (kResidual) y[k] = at < v1 ? __ldg(qr + at) : 0.f;
-            }
-        }
-        Limbs t{0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const float xs = __saturatef(x[k]);
-            const Limbs p = limbs(xs);
-            if (kResidual) {
-                const float ys = __saturatef(y[k]);
-                const Limbs q = limbs(ys);
-                if (xs > ys) {   // rounding keeps the order
-                    t.h += p.h - q.h;
-                    t.l += p.l - q.l;
-                    t.m += p.m - q.m;
-                }
-            } else {
-                t.h += p.h;
-                t.l += p.l;
-                t.m += p.m;
-            }
-        }
-        sum += whole_of(t);
-    }
+    uint32_t v = (uint32_t)min(v0, v1) + lane * kVec;   // (below 2^31 + 2^12)
+    const uint32_t end = (uint32_t)v1;
+    for (; v - lane * kVec + 32 * kUnroll <= end; v += 32 * kUnroll)
+        sum += round_sum<kResidual, kVec, kUnroll, true>(pr, qr, v, end);
+    const uint32_t rest = end - min(v - lane * kVec, end);
+    if (rest > 32 * kUnroll / 2) sum += round_sum<kResidual, kVec, kUnroll, false>(pr, qr, v, end);
+    else if (rest > 32 * kUnroll / 4) sum += round_sum<kResidual, kVec, kUnroll / 2, false>(pr, qr, v, end);
+    else if (rest > 0) sum += round_sum<kResidual, kVec, kUnroll / 4, false>(pr, qr, v, end);
     return (unsigned long long)sum;
 }
 

@@ -637,6 +637,28 @@ def test_verify_chain(reqs, k, v):
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and int(err.item()) == want[2] == 0
 
 
+@pytest.mark.parametrize("v", [127, 128, 2047, 2049, 4100, 6145, 8191, 8192, 10239, 12292, 16385, 20480])
+def test_verify_parts_of_every_length(v):
+    """Vocabularies whose parts of a warp end in every share of a round, rows aligned and not: the same tokens as the
+    oracle's, bit for bit, in chains and trees."""
+    rng = np.random.default_rng(v)
+    p, q = probs(rng, (280, 2, v)), probs(rng, (280, 1, v))
+    tok = draws(rng, q)
+    u, us = np.ones((280, 1), np.float32), _u(rng, 280)          # every draft refused: the residual's sample
+    u[::2] = 0.0                                                 # or taken: the row's own
+    want = oracle.verify_chain(p, q, tok, u, us)
+    got = _chain(_d(p), _d(q), tok, u, us)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    t = 3
+    p = probs(rng, (100, t, v))
+    par = parents(rng, 100, t)
+    tok = rng.integers(0, v, (100, t))
+    u, us = _u(rng, 100, t), _u(rng, 100)
+    want = oracle.verify_tree(p, tok, par, u, us)
+    got = _tree_verify(_d(p), tok, par, u, us)
+    assert all(np.array_equal(g, w) for g, w in zip(got, want))
+
+
 def test_verify_chain_bad_inputs_and_edges():
     rng = np.random.default_rng(12)
     p, q = probs(rng, (6, 4, 500)), probs(rng, (6, 3, 500))
