@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(128) rope_write_any_kernel(const Args a, bool 
 // head; a lane holds two pieces of 8 elements that rotate with one another:
 // [8 l, ..) and [rot / 2 + 8 l, ..), or, interleaved and past the rotated part,
 // 16 consecutive ones, so a pair never leaves its lane and both layouts use
-// table entries 8 l .. 8 l + 7.  A CTA takes a token at a time, 128 / LPH heads
-// a round, U rounds' loads in flight before the token's own answers (table
+// table entries 8 l .. 8 l + 7.  A CTA takes a token at a time, a head by LPH
+// lanes a round, U rounds' loads in flight before the token's own answers (table
 // entry, rotation row) are needed.
 // ---------------------------------------------------------------------------
-// CTAs an SM is built to hold: fewer leave too few loads in flight, more spill rows (8752 tokens of 32 + 2 x 8
-// heads of 128, bf16: 47.4, 45.6, 49.4 and 56.4 us with 4, 5, 6 and 8; 4.8 TB/s of the bytes that it has to move).
+// CTAs of 128 threads an SM is built to hold: fewer leave too few loads in flight, more spill rows (8752 tokens of 32 +
+// 2 x 8 heads of 128, bf16: 47.4, 45.6, 49.4 and 56.4 us with 4, 5, 6 and 8; 4.8 TB/s of the bytes that it has to move).
 constexpr int kPerSm = 5;
 
 template <typename T>
@@ -239,10 +239,11 @@ __device__ __forceinline__ void put8(uint8_t *p, const float (&f)[8], float scal
     *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
 }
 
-template <typename T, typename C, int LPH, int U>
-__global__ void __launch_bounds__(128, kPerSm) rope_write_kernel(const Args a, bool inter) {
-    constexpr int D = 16 * LPH, NG = 128 / LPH;
-    const int l = threadIdx.x % LPH, grp = threadIdx.x / LPH;
+// B: threads of the CTA, 0: any up to 160 (the registers of as many warps an SM).
+template <typename T, typename C, int LPH, int U, int B>
+__global__ void __launch_bounds__(B ? B : 160, B ? kPerSm : 4) rope_write_kernel(const Args a, bool inter) {
+    constexpr int D = 16 * LPH;
+    const int NG = (B ? B : blockDim.x) / LPH, l = threadIdx.x % LPH, grp = threadIdx.x / LPH;
     const int heads = a.hq + 2 * a.hkv, half = a.rot / 2;
     const bool turns = 16 * l < a.rot;
     const int ea = inter || !turns ? 16 * l : 8 * l;        // this lane's two pieces
@@ -371,16 +372,22 @@ template <typename T, typename C, int LPH>
 static cudaError_t launch_pieces(const Args &a, bool inter, cudaStream_t st) {
     // three rounds of 16-bit rows in flight (48 heads of 128 elements), two of 32-bit ones: registers
     constexpr int U = sizeof(T) == 2 ? 3 : 2;
-    const int rounds = ceil_div(a.hq + 2 * a.hkv, 128 / LPH);
-    // fewer tokens than CTAs fit: a token's heads over several (1021 tokens, E4M3: 11.2 -> 10.2 us)
+    const int heads = a.hq + 2 * a.hkv, rounds = ceil_div(heads, 128 / LPH);
     const int64_t sms = current_sm_count();
+    // fewer tokens than CTAs fit: a token's heads over several (1021 tokens, E4M3: 11.2 -> 10.2 us)
     const int64_t room = 16 * sms / (a.max_n < 1 ? 1 : a.max_n);
-    const int64_t tokens = a.max_n < sms * 2 * kPerSm ? a.max_n : sms * 2 * kPerSm;
     if (room >= 2 && rounds > 1) {
         const unsigned y = (unsigned)(room < rounds ? room : rounds);
-        return launch_pdl(rope_write_kernel<T, C, LPH, 1>, dim3((unsigned)tokens, y), dim3(128), 0, st, a, inter);
+        return launch_pdl(rope_write_kernel<T, C, LPH, 1, 128>, dim3((unsigned)a.max_n, y), dim3(128), 0, st, a, inter);
     }
-    return launch_pdl(rope_write_kernel<T, C, LPH, U>, dim3((unsigned)tokens), dim3(128), 0, st, a, inter);
+    // a CTA as wide as a token's heads, so that no round is left half empty (E4M3 caches, 128 threads against what this
+    // gives: 15 + 2 x 5 heads of 256, bf16, 54.0 and 47.0 us; 4 + 2 x 1, fp32, 58.2 and 42.5)
+    const int lanes = ceil_div(heads * LPH, U), steps = ceil_div(lanes, 160);
+    const int threads = ceil_div(ceil_div(lanes, steps), 32) * 32;
+    const int64_t ctas = sms * 2 * (kPerSm * 128 / threads);
+    const dim3 grid((unsigned)(a.max_n < ctas ? a.max_n : ctas)), block(threads);
+    if (threads == 128) return launch_pdl(rope_write_kernel<T, C, LPH, U, 128>, grid, block, 0, st, a, inter);
+    return launch_pdl(rope_write_kernel<T, C, LPH, U, 0>, grid, block, 0, st, a, inter);
 }
 
 static bool in_pieces(const Args &a, int e, int ec) {

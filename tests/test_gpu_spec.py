@@ -162,6 +162,21 @@ def test_rope_write_row_strides(extra):
     _check_rope(_rope_case(40, 8, 2, 128, 128, "bf16", extra=extra), 8, 2, 128, "bf16", False, True, False)
 
 
+@pytest.mark.parametrize("hq,hkv,d,rot,dtype,fp8", [
+    (1, 1, 32, 32, "bf16", False),                               # two lanes' work in a warp
+    (4, 1, 256, 128, "f32", True),                               # a warp a token
+    (15, 5, 256, 256, "bf16", True),                             # five warps
+    (64, 8, 128, 128, "bf16", False),                            # more heads than a CTA takes at once
+    (40, 8, 64, 64, "f32", False),
+    (33, 11, 64, 32, "bf16", True),
+])
+def test_rope_write_more_tokens_than_ctas(hq, hkv, d, rot, dtype, fp8):
+    """Enough tokens that a CTA takes a token's heads together, several tokens in turn."""
+    c = _rope_case(3500, hq, hkv, d, rot, dtype, reqs=40, bs=16, pad=3)
+    for inter in (False, True):
+        _check_rope(c, hq, hkv, d, dtype, fp8, True, inter)
+
+
 def test_rope_write_many_tokens():
     c = _rope_case(3000, 32, 8, 128, 128, "bf16", reqs=40, bs=16)
     _check_rope(c, 32, 8, 128, "bf16", False, True, False)
