@@ -632,7 +632,7 @@ size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int
  *   kernel (block sizes from 8 that divide 128 or are multiples of it, at
  *   most 2048 requests); anything else a CUDA-core kernel.
  *   INVALID_ARG: as bkv_paged_decode, or mask_req_stride neither 0 nor at
- *   least q_len * words, or tree_mask null.
+ *   least q_len * words, or tree_mask null, or max_context_len above 2^30.
  *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd, q_len
  *   > 256.
  */

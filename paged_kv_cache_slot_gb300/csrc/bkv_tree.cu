@@ -23,6 +23,7 @@ namespace tree {
 
 static constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxT = 256;       // tree tokens a request
+constexpr int kMaxCtx = 1 << 30; // positions a request: sums of one and a tile or a block stay within int32
 constexpr int kBK = 32;          // keys a tile of the CUDA-core kernel
 constexpr int kThreads = 128;
 constexpr int kCcEnd = 1;        // tiles of the CUDA-core kernel that a unit's start and end take as long as
@@ -640,7 +641,7 @@ static int32_t cc_columns(int32_t nq, int32_t D, int32_t H_kv) {
 static bool make_plan(int32_t num_reqs, int32_t T, int32_t H_q, int32_t H_kv, int32_t D, int32_t bs, int32_t max_ctx,
                       Plan *p) {
     if (num_reqs <= 0 || T <= 0 || T > kMaxT || H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || D <= 0 || D > 256 ||
-        D % 2 != 0 || bs <= 0 || bs > 65536 || max_ctx < 0)
+        D % 2 != 0 || bs <= 0 || bs > 65536 || max_ctx < 0 || max_ctx > kMaxCtx)
         return false;
     const int32_t G = H_q / H_kv;
     const int64_t nq = (int64_t)T * G;

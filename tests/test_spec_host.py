@@ -64,6 +64,15 @@ def test_tree_decode_refusals(lib):
         assert size(*bad) == 0, bad
 
 
+def test_tree_decode_longest_context(lib):
+    size = lib.bkv_paged_decode_tree_workspace_size
+    assert size(2, 5, 32, 8, 128, 16, 1 << 30) > 0
+    for bound in ((1 << 30) + 1, (1 << 31) - 1):
+        assert size(2, 5, 32, 8, 128, 16, bound) == 0
+    # what a call needs does not grow with the lengths or the batch
+    assert size(2, 5, 32, 8, 128, 16, 100) == size(4000, 5, 32, 8, 128, 16, 1 << 20)
+
+
 def test_verify_refusals(lib):
     def chain(**kw):
         a = dict(p=NULL, pr=400, prow=100, q=NULL, qr=300, qrow=100, tok=NULL, lens=NULL, u=NULL, us=NULL, nr=1, k=3, v=100,
