@@ -715,13 +715,15 @@ static int launch_merge(const TreeArgs &a, cudaStream_t st) {
     return launch_status();
 }
 
-// Few rows: one a warp, all its loads at once (28 rows of 8 streams 11.8 us a call, 13.1 by two rows); many: two a
-// warp (244 rows of 128 streams 113 us a call, 117 by one).
+// Few rows, or streams in many parts: one row a warp, eight of its parts at once (28 rows of 8 streams: 1.3 us a call
+// less than by two rows; 3 requests of up to 13459 positions, 96 rows over 46 columns: 16.5 us, 18.3).  Else two rows a
+// warp (32 requests of up to 4096, 64 rows over 19 columns: 51.4 us, 53.2 by one).
 static int merge(const TreeArgs &a, cudaStream_t st) {
     const bool fours = a.D <= 128 && a.D % 4 == 0 && aligned(a.out, a.dtype == BKV_BF16 ? 8 : 16);
     if (!fours) return launch_merge<0, 0, 0>(a, st);
-    if (a.D == 128) return a.NR <= 32 ? launch_merge<1, 8, 128>(a, st) : launch_merge<2, 4, 128>(a, st);
-    return a.NR <= 32 ? launch_merge<1, 8, 0>(a, st) : launch_merge<2, 4, 0>(a, st);
+    const bool one = a.NR <= 32 || a.P > 2 * (int64_t)a.num_reqs;
+    if (a.D == 128) return one ? launch_merge<1, 8, 128>(a, st) : launch_merge<2, 4, 128>(a, st);
+    return one ? launch_merge<1, 8, 0>(a, st) : launch_merge<2, 4, 0>(a, st);
 }
 
 }  // namespace tree

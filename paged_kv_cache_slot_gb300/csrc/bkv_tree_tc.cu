@@ -39,7 +39,7 @@
 //
 // Measured (device time of a call with its merge; 128-element heads, bf16): 256
 // requests of 9 to 8192 positions, 4 tokens of 32 / 8 heads (16 rows a group)
-// 218 us, 5.9 TB/s of K and V; 32 of 512 to 4096, 16 tokens (64 rows) 51 us, 4.6
+// 217 us, 5.9 TB/s of K and V; 32 of 512 to 4096, 16 tokens (64 rows) 51 us, 4.6
 // TB/s: 9 us of it launches, the first tiles and the merge; 8 of 1000 to 16693,
 // 61 tokens of 64 / 8 heads (488 rows) 105 us, 0.84 PFLOP/s of the products
 // that the rows need: there the two streams' softmaxes take turns at the
@@ -69,7 +69,10 @@ constexpr int kTmemCols = 512;   // S and P of streams 0, 1, O of streams 0, 1 (
 constexpr int kTimeoutErr = 1 << 24;
 constexpr int kMaxReqs = 2048;
 constexpr float kSlack = 8.f;
-constexpr int kEndCost = 3;    // tiles that a unit's end takes as long as (see Units)
+// Tiles that a unit's end takes as long as, and what a column takes of both at least (fewer columns leave fewer
+// partials): 256 requests of 9 to 8192 positions 217 us, 221 with 3 or without the least, 227 with 1 or 4; 3 requests
+// of up to 13459, 12 tokens of 16 / 2 heads: 18.3 us, 22.8 without the least.
+constexpr int kEndCost = 2, kMinCost = 2;
 
 constexpr int kMaxStages = 3;                             // slots of a ring, at most
 constexpr int kOffMask = 0;                               // 8 words: loaded segments per tile (ring)
@@ -177,13 +180,18 @@ struct Units {
     const int32_t *pre;
     const uint8_t *fill;
     int r, q, t, t1, P;
+    // Columns that share a cost of C.
+    __device__ static int64_t columns(int64_t C, int64_t P) {
+        const int64_t most = (C + kMinCost - 1) / kMinCost;
+        return most < P ? most : P;
+    }
     __device__ Units(const TreeArgs &a, const int32_t *pre_, const uint8_t *fill_, int q_) {
         pre = pre_;
         fill = fill_;
         q = q_;
         P = a.P;
         const int64_t C = pre[a.num_reqs];
-        const int64_t peff = C < a.P ? C : a.P;
+        const int64_t peff = columns(C, a.P);
         t = (int)(q < peff ? C * q / peff : C);
         t1 = (int)(q < peff ? C * (q + 1) / peff : C);
         int lo = 0, hi = a.num_reqs;   // first request whose cost ends after t
@@ -202,7 +210,7 @@ struct Units {
         while (pre[r1 + 1] < t1) ++r1;   // the request that the share ends in
         const int s = pre[r1], e = pre[r1 + 1] - kEndCost;   // its tiles
         if (s < t || s >= t1 || e <= t1) return make_int2(0, 0);
-        const int64_t C = pre[a.num_reqs], peff = C < a.P ? C : a.P;
+        const int64_t C = pre[a.num_reqs], peff = columns(C, a.P);
         const int q1 = (int)((e * peff - 1) / C);   // the column of its last tile
         return make_int2(r1, q1 - q + 1);
     }

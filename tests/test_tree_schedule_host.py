@@ -13,16 +13,16 @@ import random
 import numpy as np
 import pytest
 
-KERNELS = [(128, 3), (32, 1)]   # positions a tile, tiles that a unit's end takes as long as
+KERNELS = [(128, 2, 2), (32, 1, 1)]   # positions a tile, tiles that a unit's end takes as long as, a column's least cost
 
 
-def _columns(lens, P, TILE, END_COST):
+def _columns(lens, P, TILE, END_COST, MIN_COST):
     """Column q's units: (request, first tile, tiles, whole, slot)."""
     tiles = [-(-n // TILE) for n in lens]
     cost = [t + END_COST if t else 0 for t in tiles]
     pre = np.concatenate([[0], np.cumsum(cost)]).tolist()
     C = pre[-1]
-    peff = min(C, P)
+    peff = min(-(-C // MIN_COST), P)
     out = []
     for q in range(P):
         lo, hi = (C * q // peff, C * (q + 1) // peff) if q < peff else (C, C)
@@ -41,12 +41,12 @@ def _columns(lens, P, TILE, END_COST):
 
 
 @pytest.mark.parametrize("seed", range(40))
-@pytest.mark.parametrize("TILE,END_COST", KERNELS)
-def test_every_tile_once_and_slots_for_the_merge(seed, TILE, END_COST):
+@pytest.mark.parametrize("TILE,END_COST,MIN_COST", KERNELS)
+def test_every_tile_once_and_slots_for_the_merge(seed, TILE, END_COST, MIN_COST):
     rng = random.Random(seed)
     P = rng.choice([1, 2, 5, 9, 19, 76, 152])
     lens = [rng.choice([0, 1, 127, 128, 129, rng.randint(1, 20000), rng.randint(1, 700)]) for _ in range(rng.randint(1, 60))]
-    tiles, cols = _columns(lens, P, TILE, END_COST)
+    tiles, cols = _columns(lens, P, TILE, END_COST, MIN_COST)
     seen = [np.zeros(t, int) for t in tiles]
     parts, slots = {}, set()
     for q, (units, split) in enumerate(cols):
@@ -66,7 +66,7 @@ def test_every_tile_once_and_slots_for_the_merge(seed, TILE, END_COST):
         q, n = table[r]
         assert got == [P + q] + list(range(q + 1, q + n)) and n >= 2
     load = [sum(n for _, _, n, _, _ in u) + END_COST * len(u) for u, _ in cols]
-    assert max(load) <= sum(tiles + [END_COST for t in tiles if t]) / P + 2 + 2 * END_COST or P > sum(tiles)
+    assert max(load) <= sum(tiles + [END_COST for t in tiles if t]) / P + 2 + 2 * END_COST or MIN_COST * P > sum(tiles)
 
 
 class _Bar:
