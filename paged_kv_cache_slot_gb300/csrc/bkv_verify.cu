@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
     const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int64_t r = blockIdx.x / cs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // a CTA's shared memory may be written by the others only once it runs: the wait is behind the walk
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
     pdl_wait();
     pdl_trigger();
     const int64_t *tokens = a.tokens + r * a.nodes;
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
     const int64_t v1 = min((int64_t)a.V, v0 + part);
     const float us = __ldg(a.us + r);
     const unsigned long long U = unit64(us);
+    asm volatile("barrier.cluster.wait;" ::: "memory");   // every CTA of the cluster has started
     // pass 0: the residual weights; where they are all 0, pass 1: the row itself
     for (int pass = 0; pass < 2; ++pass) {
         const bool plain = pass == 1;
