@@ -85,9 +85,14 @@ constexpr int kOffAnyBad = kOffAbort + 4;                 // a V row that was no
 constexpr int kOffSums = kOffAnyBad + 4;                  // [warps] prefix sum's scratch
 constexpr int kOffPre = (kOffSums + kThreads / 32 * 4 + 15) / 16 * 16;   // [kMaxReqs + 1] tiles before request r
 constexpr int kOffFill = kOffPre + (kMaxReqs + 4) * 4;    // [kMaxReqs] positions of its last tile, less one
-constexpr int kOffXm = kOffFill + kMaxReqs;               // [stream][row] running max, weight sum
+// Sets of the streams' exchange at a unit's end, used in turn: a stream with no tile of the next unit, or one, writes
+// its next entries while its partner may still read the last; before it writes the ones after those, the barrier of the
+// unit between has seen the partner past them.  (A second barrier phase in place of the second set: 256 requests of 9 to
+// 8192 positions 217 -> 220 us, 700 of 9 to 200 194 -> 200.)
+constexpr int kXmSets = 2;
+constexpr int kOffXm = kOffFill + kMaxReqs;               // [set][stream][row] running max, weight sum
 // queries, then the K and V rings: what a launch needs of the rest (see ring_shape)
-constexpr int kOffQ = (kOffXm + 2 * kTile * 8 + 1023) / 1024 * 1024;
+constexpr int kOffQ = (kOffXm + kXmSets * 2 * kTile * 8 + 1023) / 1024 * 1024;
 constexpr int kSmemMax = 227 * 1024 - 1024;               // less the slack for 1024 alignment
 
 // A ring slot and its phase parity.
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar_ofull = bar0 + 8u * (kB + 8);
     const uint32_t bar_oempty = bar0 + 8u * (kB + 9);
     auto bar_mask = [&](int m) { return bar0 + 8u * (kB + 10 + m); };
-    // the two streams' warps of a lane quarter
+    // the two streams' warps of a lane quarter: their entries of a unit are written
     auto bar_pair = [&](int qw) { return bar0 + 8u * (kB + 18 + qw); };
     const int seg_rows = sh.seg_rows, tok_per_tile = sh.tok_per_tile, box_tok = sh.box_tok;
     const int nK = sh.k_stages, nV = sh.v_stages;
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hh = valid ? row % G : 0;
             const uint32_t lanes = tmem + ((uint32_t)(32 * qw) << 16);
             const uint32_t s_col = lanes + col_s(xb);
-            float2 *xm = reinterpret_cast<float2 *>(smem + kOffXm);   // [stream][row]
+            float2 *xm = reinterpret_cast<float2 *>(smem + kOffXm);   // [set][stream][row]
             int no = 0;          // units finished so far
             while (ok && units.next(x)) {
                 const int first = x.L - a.T;   // position of the tree's first token
@@ -792,11 +797,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float M = m, fa = 1.f, fb = 0.f, lsum = l;
                 if (!dual) {
                     // the streams' parts of this row
-                    xm[xb * kTile + row] = make_float2(m, l);
+                    float2 *xu = xm + no % kXmSets * 2 * kTile;
+                    xu[xb * kTile + row] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_pair(qw));
                     if (!mbar_wait_warp(bar_pair(qw), (uint32_t)(no & 1), abort_flag)) break;
-                    const float2 pa = xm[row], pb = xm[kTile + row];
+                    const float2 pa = xu[row], pb = xu[kTile + row];
                     M = fmaxf(pa.x, pb.x);
                     fa = pa.x == -INFINITY ? 0.f : fast_exp2(pa.x - M);
                     fb = pb.x == -INFINITY ? 0.f : fast_exp2(pb.x - M);
