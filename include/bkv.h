@@ -615,9 +615,12 @@ size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int
  *   V, 0 where no key is seen.  Causal bits give bkv_paged_decode's causal
  *   mask, all bits its BKV_MASK_ALL.  Bits from q_len on are ignored.
  *   Cache memory at positions a token does not see does not reach its output
- *   (it may hold NaN or infinities).  An element of K or V that is not finite
- *   at a position of the tree that a token sees makes the token's output row
- *   NaN (for V: the whole row of head_dim values).
+ *   (it may hold NaN or infinities).  At a position that a token sees, a score
+ *   of NaN or +inf (NaN or infinite elements of K) makes the token's output row
+ *   of that query head NaN, and a score of -inf weighs nothing; a row that sees
+ *   nothing but scores of -inf is 0, as one that sees no key.  An element of V
+ *   that is not finite at a position of the tree that a token sees makes all
+ *   head_dim values of the token's output row NaN.
  *
  *   tree_mask  words of 32 bits as above; mask_req_stride words between the
  *              requests' masks, or 0: one tree for all requests.

@@ -352,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, cc_ctas(DP, BR)) tree_cc_kernel(cons
                 for (int w = 4; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
                 const float mn = fmaxf(m[i], top);
                 const float corr = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+                const float base = mn == -INFINITY ? 0.f : mn;   // nothing but scores of -inf so far: weights of 0
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // a seen NaN score stays NaN (fmaxf dropped it from the maximum)
-                    const float p = (vis >> (tx + 8 * j)) & 1u ? exp2f(s[j] - mn) : 0.f;
+                    const float p = (vis >> (tx + 8 * j)) & 1u ? exp2f(s[j] - base) : 0.f;
                     prow[8 * j] = p;
                     sum += p;
                 }

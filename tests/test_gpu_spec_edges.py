@@ -55,3 +55,42 @@ def test_tree_decode_many_short_requests(t, hq, hkv, seed):
     for r in rng.permutation(700)[:60]:
         want, _ = oracle.paged_decode_tree_request(r, p.q, p.k, p.v, p.table, p.lens, words(mask))
         check_attention(got[r], want, "bf16")
+
+
+@pytest.mark.parametrize("t,hq,hkv,d,dtype", [
+    (6, 8, 2, 128, "bf16"), (40, 8, 2, 128, "bf16"), (6, 8, 2, 64, "bf16"), (6, 6, 3, 64, "f32"), (20, 4, 1, 128, "f32")])
+def test_tree_decode_infinite_keys(t, hq, hkv, d, dtype):
+    """An infinite key element makes scores of -inf (a weight of 0) or, by the query's sign, of +inf (a NaN row): among
+    the committed positions (a first tile of nothing else included), in the tree, and where a row sees nothing else."""
+    lens = [t + 300, t + 500, t + 90, t]
+    p = Paged(lens, t, hq, hkv, d, 16, dtype)
+    mask = ancestors(parents(np.random.default_rng(4), 4, t))
+    mask[3, 4] = False
+    mask[3, 4, 2] = True                                        # sees one key, and that one is infinite
+    where = [(0, np.arange(5, 21)), (1, np.arange(0, 160)), (2, np.array([90 + 3])), (3, np.array([2]))]
+    k = p.k.reshape(-1, hkv, d)
+    for i, (r, pos) in enumerate(where):
+        k[p.rows(r, pos), :, 3] = cast(np.array([-np.inf if i % 2 else np.inf], np.float32), dtype)[0]
+    got = _f64(_tree(p, mask))
+    finite = nans = empty = 0
+    for r, n in enumerate(lens):
+        rows = p.rows(r, np.arange(n))
+        kr, vr = (wl.to_f32(c).reshape(-1, hkv, d)[rows].astype(np.float64) for c in (p.k, p.v))
+        q = wl.to_f32(p.q[r]).astype(np.float64)
+        for i in range(t):
+            seen = np.ones(n, bool)
+            seen[n - t:] = mask[r, i]
+            for h in range(hq):
+                s = (kr[seen, h // (hq // hkv)] @ q[i, h]) / np.sqrt(d)
+                row = got[r, i, h]
+                if np.isposinf(s).any():
+                    assert np.isnan(row).all()
+                    nans += 1
+                elif np.isneginf(s).all():
+                    assert not row.any()                        # nothing weighs anything
+                    empty += 1
+                else:
+                    w = np.exp(s - s.max())
+                    check_attention(row[None], (w @ vr[seen, h // (hq // hkv)] / w.sum())[None], dtype)
+                    finite += 1
+    assert finite and nans and empty
