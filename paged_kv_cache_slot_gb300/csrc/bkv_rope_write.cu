@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(128) rope_write_any_kernel(const Args a, bool 
                 ss = fmaf(x[u], x[u], ss);
             }
         }
+        __syncwarp();   // q_out may be q: no lane stores before the others have read what turns with their elements
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float inv = w ? rsqrtf(ss / (float)a.d + a.eps) : 1.f;

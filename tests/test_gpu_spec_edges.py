@@ -94,3 +94,32 @@ def test_tree_decode_infinite_keys(t, hq, hkv, d, dtype):
                     check_attention(row[None], (w @ vr[seen, h // (hq // hkv)] / w.sum())[None], dtype)
                     finite += 1
     assert finite and nans and empty
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,d,rot,dtype,norm", [
+    (70, 4, 2, 80, 80, "bf16", True), (33, 3, 1, 10, 6, "f32", True), (50, 8, 2, 128, 24, "bf16", False),
+    (41, 5, 1, 256, 250, "f32", False), (900, 7, 7, 96, 72, "bf16", True), (60, 8, 2, 64, 64, "bf16", True)])
+def test_rope_write_in_place(n, hq, hkv, d, rot, dtype, norm, inter):
+    """q_out may be q: the shapes whose elements turn with another lane's included."""
+    rng = np.random.default_rng(7)
+    q, k, v = (cast(rng.standard_normal((n, h, d)).astype(np.float32) * 2, dtype) for h in (hq, hkv, hkv))
+    w = cast(1 + 0.3 * rng.standard_normal(d).astype(np.float32), dtype)
+    cs, pos = rope_table(n, rot), np.arange(n)
+    table = np.arange(1, -(-n // 16) + 1, dtype=np.int32).reshape(1, -1)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    outs = []
+    for in_place in (False, True):
+        tq = _d(q)
+        qo = tq if in_place else torch.zeros_like(tq)
+        kc, vc = (torch.zeros(table.size + 1, 16, hkv, d, dtype=td, device=DEV) for _ in range(2))
+        slots = torch.zeros(n, dtype=torch.int64, device=DEV)
+        bkv.bkv_qk_norm_rope_cache_write(tq, _d(k), _d(v), _d(w) if norm else None, None, 1e-6, _d(cs), _d(table),
+                                         torch.zeros(n, dtype=torch.int32, device=DEV), _d(pos), slots, qo, kc, vc,
+                                         interleaved=inter)
+        outs.append((qo, kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    want, bad = oracle.norm_rope(q, w if norm else None, 1e-6, cs, pos, inter)
+    assert bad == 0
+    step = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype]
+    assert (np.abs(_f64(outs[1][0]) - want) <= step * np.abs(want) + 2e-6 * np.abs(want).max(-1, keepdims=True)).all()
