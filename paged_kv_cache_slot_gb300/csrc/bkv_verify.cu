@@ -97,12 +97,22 @@ __device__ __forceinline__ long long whole_of(const Limbs &v) {
 // Below 0 and NaN: 0; above 1: 1.
 __device__ __forceinline__ long long fixed(float p) { return whole_of(limbs(__saturatef(p))); }
 
-// A random number u in [0, 1) in units of 2^-64, exactly: floor(u n) is then the
-// high word of a product, and u n < m for integers is floor(u n) < m.  From 1 on
-// (and NaN) the largest, below 0 none.
-__device__ __forceinline__ unsigned long long unit64(float u) {
-    return u < 1.f ? __float2ull_rz(fmaxf(u, 0.f) * 18446744073709551616.f) : ~0ull;
-}
+// floor(u n) of a random number u in [0, 1), exactly: u n < m for integers is
+// floor(u n) < m.  From 1 on (and NaN) u is the largest number below, 2^-64 off;
+// below 0 it is 0.  u in units of 2^-64 makes floor(u n) the high word of a
+// product.  Below 2^-40 the last of its 24 bits would fall out of those units:
+// there they are of 2^-104, which hold every bit down to 2^-80, and below that
+// u n < 2^-16 is 0 either way.
+struct Unit {
+    unsigned long long u;
+    int shift;
+    __device__ __forceinline__ explicit Unit(float x) {
+        const bool tiny = x < 0x1p-40f;
+        shift = tiny ? 40 : 0;
+        u = x < 1.f ? __float2ull_rz(fmaxf(x, 0.f) * (tiny ? 0x1p104f : 0x1p64f)) : ~0ull;
+    }
+    __device__ __forceinline__ unsigned long long times(unsigned long long n) const { return __umul64hi(u, n) >> shift; }
+};
 
 // What token v weighs: its probability p, less the draft's q in a chain.
 __device__ __forceinline__ unsigned long long weight(float p, float q) {
@@ -308,7 +318,7 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
                 const long long rem = max((1ll << 56) - out_of_it, 0ll);
                 const float u = s.u[c];
                 // (fp64 runs at 2 a clock and SM here; a u outside [0, 1) and NaN take it)
-                const bool ok = u >= 0.f && u < 1.f ? (long long)__umul64hi(unit64(u), rem) < s.fx[c]
+                const bool ok = u >= 0.f && u < 1.f ? (long long)Unit(u).times(rem) < s.fx[c]
                                                     : (double)u * (double)rem < (double)s.fx[c];
                 if (ok) atomicMin(&s.next[par], c);
             }
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
     const int64_t v0 = ((int64_t)rank * kWarps + warp) * part;
     const int64_t v1 = min((int64_t)a.V, v0 + part);
     const float us = __ldg(a.us + r);
-    const unsigned long long U = unit64(us);
+    const Unit U(us);
     asm volatile("barrier.cluster.wait;" ::: "memory");   // every CTA of the cluster has started
     // pass 0: the residual weights; where they are all 0, pass 1: the row itself
     for (int pass = 0; pass < 2; ++pass) {
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
             if (pass == 1 && rank == 0 && threadIdx.x == 0 && a.err) atomicAdd(a.err, 1);   // a row without any weight
             continue;
         }
-        const unsigned long long border = __umul64hi(U, whole);   // floor(u * whole) < whole
+        const unsigned long long border = U.times(whole);   // floor(u * whole) < whole
         // the CTA whose part holds the border: its threads scan the warp's part that does, together
         if (border < before || border - before >= s.tot[pass][rank]) break;
         int w = 0;

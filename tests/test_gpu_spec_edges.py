@@ -4,6 +4,9 @@ place, batches of short contexts, the smallest random numbers.
 Tolerances as in tests/test_gpu_spec.py: attention by tests/_parity.py; norm and
 rotation the output's rounding plus 2e-6 of the row's largest value; tokens,
 paths and counts equal."""
+import itertools
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -123,3 +126,40 @@ def test_rope_write_in_place(n, hq, hkv, d, rot, dtype, norm, inter):
     assert bad == 0
     step = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype]
     assert (np.abs(_f64(outs[1][0]) - want) <= step * np.abs(want) + 2e-6 * np.abs(want).max(-1, keepdims=True)).all()
+
+
+# 2^-42 (1 + 2^-23) of a whole of 2^56 - 1 units of 2^-56 is just above 2^14 of them; without its last bit, just below
+TINY = np.float32(2.0 ** -42 * (1 + 2.0 ** -23))
+
+
+def test_verify_chain_smallest_numbers():
+    """A sample by a number whose last bit lies below 2^-64: the running sum is compared with the exact product."""
+    w = np.array([2.0 ** -42] + [2.0 ** (i - 56) for i in range(56) if i != 14], np.float32)
+    us = np.array([TINY, 2.0 ** -42, np.nextafter(np.float32(2.0 ** -42), np.float32(0)), 2.0 ** -100, 2.0 ** -149, 0.0],
+                  np.float32)
+    p = np.broadcast_to(w, (6, 1, 56)).copy()
+    out = torch.full((6, 1), -5, dtype=torch.int64, device=DEV)
+    n = torch.full((6,), -5, dtype=torch.int32, device=DEV)
+    none = torch.zeros(6, 0, device=DEV)
+    bkv.bkv_verify_draft_chain(_d(p), torch.zeros(6, 0, 56, device=DEV), none.long(), none, _d(us), out, n)
+    # u (2^56 - 1) against 2^14 units: above; 2^14 - 2^-42 and what is smaller: below
+    assert out[:, 0].tolist() == [1, 0, 0, 0, 0, 0]
+    # the definition in rational numbers (the whole has 56 bits: more than a double holds)
+    weights = [Fraction(float(x)) for x in w]
+    runs = list(itertools.accumulate(weights))
+    assert out[:, 0].tolist() == [next(v for v, c in enumerate(runs) if c > Fraction(float(u)) * runs[-1]) for u in us]
+
+
+def test_verify_tree_smallest_numbers():
+    """A child against what its rejected sibling, of one unit, left: the product exact for a number below 2^-40."""
+    v = 8
+    p = np.zeros((3, 3, v), np.float32)
+    p[:] = 0.1
+    p[:, 0, 2], p[:, 0, 3] = 2.0 ** -56, 2.0 ** -42
+    tok, par = np.array([[0, 2, 3]] * 3), np.array([[-1, 0, 0]] * 3, np.int32)
+    u = np.array([[0, 0.5, TINY], [0, 0.5, 2.0 ** -42], [0, 0.5, 2.0 ** -120]], np.float32)
+    out = torch.zeros(3, 3, dtype=torch.int64, device=DEV)
+    path = torch.zeros(3, 3, dtype=torch.int32, device=DEV)
+    n = torch.zeros(3, dtype=torch.int32, device=DEV)
+    bkv.bkv_verify_draft_tree(_d(p), _d(tok), _d(par), _d(u), torch.full((3,), 0.5, device=DEV), out, path, n)
+    assert n.tolist() == [0, 1, 1] and path[1:, 1].tolist() == [2, 2]
