@@ -1126,6 +1126,11 @@ int64_t orc_verify_tree(const float *target, const int64_t *tokens, const int32_
             for (int32_t c = cur + 1; c < T && taken < 0; ++c) {
                 if (par[c] != cur || tok[c] < 0 || tok[c] >= V)
                     continue;
+                int met = 0;
+                for (int32_t b = cur + 1; b < c; ++b)
+                    met |= par[b] == cur && tok[b] == tok[c];
+                if (met)
+                    continue;
                 if ((double)u[r * T + c] * (rem > 0.0 ? rem : 0.0) < w[tok[c]]) {
                     taken = c;
                 } else {

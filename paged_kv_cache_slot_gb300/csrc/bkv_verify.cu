@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
             s.par[i] = node ? par : -1;
             s.next[i] = kMaxNodes;
             s.tok[i] = in ? (int32_t)x : -1;
-            s.u[i] = u;
+            s.u[i] = in ? u : INFINITY;   // no child: its test fails whatever its number
             s.fx[i] = node && in ? fixed(P[par * a.p_row + x]) : 0;
         }
     }
@@ -303,7 +303,10 @@ __global__ void __launch_bounds__(Shape<kChain>::kThreads, Shape<kChain>::kBuilt
             if (par >= 0)
                 for (int j = 1 + sub; j < c; j += 8) dup |= (s.par[j] == par) & (s.tok[j] == x);
             const unsigned any = __ballot_sync(0xffffffffu, dup);
-            if (sub == 0 && ((any >> lane) & 0xffu)) s.fx[c] = 0;   // it is never taken and weighs nothing
+            if (sub == 0 && ((any >> lane) & 0xffu)) {   // it is never taken and weighs nothing
+                s.fx[c] = 0;
+                s.u[c] = INFINITY;
+            }
         }
         __syncthreads();
         for (int c0 = 0; c0 < len; c0 += kThreads / 8) {

@@ -163,3 +163,20 @@ def test_verify_tree_smallest_numbers():
     n = torch.zeros(3, dtype=torch.int32, device=DEV)
     bkv.bkv_verify_draft_tree(_d(p), _d(tok), _d(par), _d(u), torch.full((3,), 0.5, device=DEV), out, path, n)
     assert n.tolist() == [0, 1, 1] and path[1:, 1].tolist() == [2, 2]
+
+
+def test_verify_tree_never_takes_what_is_no_child():
+    """A token outside the vocabulary or met before is rejected whatever its number."""
+    rng = np.random.default_rng(3)
+    p = probs(rng, (4, 4, 50), 1.0)
+    p[:, 0, 7] = 0.0
+    tok = np.array([[0, 50, -3, 9], [0, 7, 7, 7], [0, 9, 9, 9], [0, 11, 11, -1]])
+    par = np.array([[-1, 0, 0, 0]] * 4, np.int32)
+    u = np.array([[0, -1, -1, 0.999], [0, 0.5, -1, -1], [0, 0.999, -1, -1], [0, 0.999, -0.5, -1]], np.float32)
+    out = torch.zeros(4, 4, dtype=torch.int64, device=DEV)
+    path = torch.zeros(4, 4, dtype=torch.int32, device=DEV)
+    n = torch.zeros(4, dtype=torch.int32, device=DEV)
+    bkv.bkv_verify_draft_tree(_d(p), _d(tok), _d(par), _d(u), _d(np.float32([0.1, 0.3, 0.5, 0.9])), out, path, n)
+    for got, want in zip((out, path, n), oracle.verify_tree(p, tok, par, u, np.float32([0.1, 0.3, 0.5, 0.9]))):
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert n.tolist() == [0, 0, 0, 0] and (path[:, 1:] == -1).all() and (out[:, 0] >= 0).all()
