@@ -557,7 +557,8 @@ def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block
             _dev(slot_mapping, "slot_mapping", torch.int64), _dev(q_out, "q_out"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), tb, bs, hq, hkv, d, dt, *scales,
             None if err_count is None else _dev(err_count, "err_count", torch.int32))
-    _same_device(q, k_cache)
+    _same_device(q, k, v, q_weight, k_weight, cos_sin, block_table, req_indices, positions, rope_positions, slot_mapping,
+                 q_out, k_cache, v_cache, err_count)
     _check(fn, getattr(load(), fn)(*args, _stream(stream)))
     return q_out, slot_mapping
 
@@ -599,7 +600,7 @@ def bkv_paged_decode_tree(q, k_cache, v_cache, block_table, context_lens, max_co
             _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv, d, bs, tb,
             float(softmax_scale), _dev(tree_mask, "tree_mask", torch.int32), ql * words if len(ms) == 3 else 0, dt,
             _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(), _opt(err_count, "err_count", torch.int32))
-    _same_device(q, k_cache)
+    _same_device(q, k_cache, v_cache, block_table, context_lens, tree_mask, out, workspace, err_count)
     _check("bkv_paged_decode_tree", load().bkv_paged_decode_tree(*args, _stream(stream)))
     return out
 
@@ -625,7 +626,8 @@ def bkv_verify_draft_chain(target_probs, draft_probs, draft_tokens, accept_u, sa
             _dev(accept_u, "accept_u", torch.float32), _dev(sample_u, "sample_u", torch.float32), nr, k, vocab,
             _dev(out_tokens, "out_tokens", torch.int64), _dev(num_accepted, "num_accepted", torch.int32),
             _opt(err_count, "err_count", torch.int32))
-    _same_device(target_probs, out_tokens)
+    _same_device(target_probs, draft_probs, draft_tokens, draft_lens, accept_u, sample_u, out_tokens, num_accepted,
+                 err_count)
     _check("bkv_verify_draft_chain", load().bkv_verify_draft_chain(*args, _stream(stream)))
     return out_tokens, num_accepted
 
@@ -649,7 +651,7 @@ def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_
             _dev(accept_u, "accept_u", torch.float32), _dev(sample_u, "sample_u", torch.float32), nr, t, vocab,
             _dev(out_tokens, "out_tokens", torch.int64), _dev(path, "path", torch.int32),
             _dev(num_accepted, "num_accepted", torch.int32), _opt(err_count, "err_count", torch.int32))
-    _same_device(target_probs, out_tokens)
+    _same_device(target_probs, draft_tokens, parents, accept_u, sample_u, out_tokens, path, num_accepted, err_count)
     _check("bkv_verify_draft_tree", load().bkv_verify_draft_tree(*args, _stream(stream)))
     return out_tokens, path, num_accepted
 
