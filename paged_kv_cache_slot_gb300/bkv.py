@@ -511,9 +511,10 @@ def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block
         raise ValueError("q must be (num_tokens, H_q, D), k / v (num_tokens, H_kv, D) matching the cache")
     nt, hq, _ = qs
     (q_row, qh, qe), (k_row, kh, ke), (v_row, vh, ve) = q.stride(), k.stride(), v.stride()
-    if qe != 1 or ke != 1 or ve != 1 or qh != d or kh != d or vh != d:
+    # (a dimension of size 1 may carry any stride)
+    if qe != 1 or ke != 1 or ve != 1 or (qh != d and hq > 1) or (hkv > 1 and (kh != d or vh != d)):
         raise ValueError("q, k and v rows must be dense (a row stride is allowed)")
-    if nt <= 1:   # a dimension of size 1 may carry any stride
+    if nt <= 1:
         q_row = max(q_row, hq * d)
     if ks[0] <= 1:
         k_row, v_row = max(k_row, hkv * d), max(v_row, hkv * d)
@@ -537,8 +538,10 @@ def _norm_rope(fn, scales, q, k, v, q_weight, k_weight, norm_eps, cos_sin, block
     if block_table.dim() != 2:
         raise ValueError("block_table must be 2-D with unit column stride")
     (rows, cols), (bt_row, bt_col) = block_table.shape, block_table.stride()
-    if bt_col != 1:
+    if bt_col != 1 and cols > 1:
         raise ValueError("block_table must be 2-D with unit column stride")
+    if rows <= 1:
+        bt_row = max(bt_row, cols)
     n, most = positions.numel(), slot_mapping.numel()
     if num_tokens is not None:
         if int(num_tokens) > n:
@@ -583,8 +586,9 @@ def bkv_paged_decode_tree(q, k_cache, v_cache, block_table, context_lens, max_co
     if d2 != d:
         raise ValueError("head_dim mismatch")
     table = block_table.shape
-    if len(table) != 2 or table[0] < nr or block_table.stride(1) != 1:
+    if len(table) != 2 or table[0] < nr or (block_table.stride(1) != 1 and table[1] > 1):
         raise ValueError("block_table must be (>= num_reqs, cols) with unit column stride")
+    bt_row = block_table.stride(0) if table[0] > 1 else max(block_table.stride(0), table[1])
     if context_lens.numel() < nr:
         raise ValueError("context_lens must have num_reqs elements")
     words, ms = (ql + 31) // 32, tree_mask.shape
@@ -596,7 +600,7 @@ def bkv_paged_decode_tree(q, k_cache, v_cache, block_table, context_lens, max_co
     if workspace.dtype is not torch.uint8:
         raise TypeError("workspace must be a uint8 tensor")
     args = (_dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(block_table, "block_table", torch.int32, contiguous=False), block_table.stride(0), table[1],
+            _dev(block_table, "block_table", torch.int32, contiguous=False), bt_row, table[1],
             _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv, d, bs, tb,
             float(softmax_scale), _dev(tree_mask, "tree_mask", torch.int32), ql * words if len(ms) == 3 else 0, dt,
             _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(), _opt(err_count, "err_count", torch.int32))
@@ -618,7 +622,7 @@ def bkv_verify_draft_chain(target_probs, draft_probs, draft_tokens, accept_u, sa
                          "out_tokens (R, K + 1) disagree")
     if sample_u.numel() != nr or num_accepted.numel() != nr or (draft_lens is not None and draft_lens.numel() != nr):
         raise ValueError("sample_u, num_accepted and draft_lens must have num_reqs elements")
-    if target_probs.stride(2) != 1 or (k > 0 and draft_probs.stride(2) != 1):
+    if vocab > 1 and (target_probs.stride(2) != 1 or (k > 0 and draft_probs.stride(2) != 1)):
         raise ValueError("probability rows must be dense")
     args = (_dev(target_probs, "target_probs", torch.float32, contiguous=False), *_row_strides(target_probs),
             _dev(draft_probs, "draft_probs", torch.float32, contiguous=False), *_row_strides(draft_probs),
@@ -644,7 +648,7 @@ def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_
             raise ValueError(f"{name} must be (num_reqs, num_nodes)")
     if sample_u.numel() != nr or num_accepted.numel() != nr:
         raise ValueError("sample_u and num_accepted must have num_reqs elements")
-    if target_probs.stride(2) != 1:
+    if vocab > 1 and target_probs.stride(2) != 1:
         raise ValueError("probability rows must be dense")
     args = (_dev(target_probs, "target_probs", torch.float32, contiguous=False), *_row_strides(target_probs),
             _dev(draft_tokens, "draft_tokens", torch.int64), _dev(parents, "parents", torch.int32),

@@ -50,3 +50,28 @@ def test_every_tensor_is_looked_at_for_its_device(fake, monkeypatch, at):  # noq
 
 
 SAME_DEVICE = bkv._same_device
+
+
+def test_dimensions_of_size_one_may_carry_any_stride(fake):  # noqa: F811
+    """One head taken out of a (heads, tokens, D) layout, a table of one row or one column: dense, whatever torch calls
+    the strides of those dimensions."""
+    a = _rope_inputs(hq=1, hkv=1)
+    heads = torch.zeros(3, 5, 64, dtype=torch.bfloat16)
+    a.update(q=heads[:1].transpose(0, 1), k=heads[1:2].transpose(0, 1), v=heads[2:].transpose(0, 1),
+             block_table=torch.zeros(7, dtype=torch.int32).as_strided((1, 7), (0, 1)))
+    assert a["k"].stride() == (64, 320, 1)
+    bkv.bkv_qk_norm_rope_cache_write(**a)
+    got = fake.calls["bkv_qk_norm_rope_cache_write"]
+    assert got[3:6] == (64, 64, 64) and got[14:17] == (1, 7, 7)
+    for table, want in ((torch.zeros(6, dtype=torch.int32).as_strided((1, 6), (0, 1)), (6, 6)),
+                        (torch.zeros(3, 4, dtype=torch.int32).as_strided((1, 1), (4, 4)), (4, 1)),
+                        (torch.zeros(6, dtype=torch.int32).as_strided((3, 1), (2, 2)), (2, 1))):
+        t = _tree_inputs(nr=min(3, len(table)))
+        bkv.bkv_paged_decode_tree(**dict(t, block_table=table))
+        assert fake.calls["bkv_paged_decode_tree"][4:6] == want
+    one = torch.zeros(3, 1, 4).transpose(1, 2)                   # a vocabulary of one token
+    bkv.bkv_verify_draft_chain(one, one[:, :3], torch.zeros(3, 3, dtype=I64), torch.zeros(3, 3), torch.zeros(3),
+                               torch.zeros(3, 4, dtype=I64), torch.zeros(3, dtype=I32))
+    assert fake.calls["bkv_verify_draft_chain"][1:3] == (4, 1) and fake.calls["bkv_verify_draft_chain"][4:6] == (4, 1)
+    with pytest.raises(ValueError):
+        bkv.bkv_qk_norm_rope_cache_write(**dict(_rope_inputs(), k=torch.zeros(2, 5, 64, dtype=torch.bfloat16).transpose(0, 1)))
