@@ -472,8 +472,16 @@ def bkv_merge_attn_states(outs, lses, out, lse_out=None, stream=None):
     return out
 
 
+_gpus = None   # GPUs of this process, once a call has asked
+
+
 def _same_device(*tensors):
-    """Every tensor on the current device, whose stream the call is enqueued on."""
+    """Every tensor on the current device, whose stream the call is enqueued on (with one GPU there is no other)."""
+    global _gpus
+    if _gpus is None:
+        _gpus = torch.cuda.device_count()
+    if _gpus == 1:
+        return
     dev = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:

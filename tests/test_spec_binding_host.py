@@ -38,6 +38,7 @@ def test_every_tensor_is_looked_at_for_its_device(fake, monkeypatch, at):  # noq
     fn, kw = list(_calls())[at]
     monkeypatch.setattr(bkv, "_same_device", SAME_DEVICE)
     monkeypatch.setattr(bkv, "_current_device", lambda: -1)      # the device that host tensors say they are on
+    monkeypatch.setattr(bkv, "_gpus", 2)
     fn(**kw)
     assert len(fake.calls) == 1
     names = [n for n, x in kw.items() if isinstance(x, torch.Tensor)]
