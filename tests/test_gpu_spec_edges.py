@@ -180,3 +180,28 @@ def test_verify_tree_never_takes_what_is_no_child():
     for got, want in zip((out, path, n), oracle.verify_tree(p, tok, par, u, np.float32([0.1, 0.3, 0.5, 0.9]))):
         assert np.array_equal(got.cpu().numpy(), want)
     assert n.tolist() == [0, 0, 0, 0] and (path[:, 1:] == -1).all() and (out[:, 0] >= 0).all()
+
+
+@pytest.mark.parametrize("lens,t,hq,hkv,d,bs,dtype", [
+    ([3, 70, 400], 5, 4, 2, 2, 16, "bf16"), ([3, 70, 400], 5, 4, 2, 8, 16, "f32"), ([40, 900], 9, 6, 2, 32, 16, "f32"),
+    ([40, 900], 33, 6, 2, 32, 32, "bf16"), ([1, 31, 33, 257], 1, 2, 2, 24, 4, "bf16"),
+    ([2, 3, 130] * 682 + [77, 1], 2, 2, 1, 128, 16, "bf16")],    # as many requests as the tensor-core kernel takes
+    ids=lambda x: str(len(x)) if isinstance(x, list) else str(x))
+def test_tree_decode_small_heads_and_full_tables(lens, t, hq, hkv, d, bs, dtype):
+    p = Paged(lens, t, hq, hkv, d, bs, dtype)
+    mask = ancestors(parents(np.random.default_rng(6), len(lens), t))
+    want = np.stack([oracle.paged_decode_tree_request(r, p.q, p.k, p.v, p.table, p.lens, words(mask))[0]
+                     for r in range(len(lens))])
+    check_attention(_f64(_tree(p, mask)), want, dtype)
+
+
+@pytest.mark.parametrize("bs", [128, 256])
+@pytest.mark.parametrize("t,hq", [(6, 8), (50, 8)])
+def test_tree_decode_tiles_that_are_not_there(bs, t, hq):
+    """Null entries that leave whole tiles unloaded: the first, the last, one between, all."""
+    p = Paged([700, 900, 1100, 520], t, hq, 2, 128, bs, holes=[(0, 0), (1, 2), (2, -(-1100 // bs) - 1)] +
+              [(3, b) for b in range(-(-520 // bs))])
+    mask = ancestors(parents(np.random.default_rng(6), 4, t))
+    want = np.stack([oracle.paged_decode_tree_request(r, p.q, p.k, p.v, p.table, p.lens, words(mask))[0] for r in range(4)])
+    assert not want[3].any()
+    check_attention(_f64(_tree(p, mask)), want, "bf16")

@@ -3,7 +3,8 @@ two softmax streams: a lane quarter's two warps (one a stream) exchange a row's
 maximum and sum through shared memory, an entry a stream, by a barrier of two
 arrivals; sets of entries are used in turn.  Run as agents at random paces: what
 a warp reads must be both streams' entries of its own unit, whatever the units'
-lengths."""
+lengths.  And the constants that the model of the schedule was written with, against
+the sources'."""
 import os
 import random
 import re
@@ -11,7 +12,7 @@ import re
 import pytest
 
 from paged_kv_cache_slot_gb300 import build as bkv_build
-from test_tree_schedule_host import _Bar
+from test_tree_schedule_host import KERNELS, _Bar
 
 
 def _source(name):
@@ -139,3 +140,15 @@ def test_the_model_sees_a_single_set():
             assert "another unit" in str(e)
             bad += 1
     assert bad > 0
+
+
+def test_the_schedules_model_has_the_kernels_constants():
+    cc, tc, shared = (_source(n) for n in ("bkv_tree.cu", "bkv_tree_tc.cu", "bkv_tree.cuh"))
+
+    def value(src, name):
+        return int(re.search(rf"\b{name} = (\d+)[,;]", src).group(1))
+    assert re.search(r"kTile = kTreeTile;", tc)
+    # the CUDA-core kernel's columns: at least a cost of one each
+    assert re.search(r"peff = C < a\.P \? C : a\.P;", cc)
+    assert KERNELS == [(value(shared, "kTreeTile"), value(tc, "kEndCost"), value(tc, "kMinCost")),
+                       (value(cc, "kBK"), value(cc, "kCcEnd"), 1)]
