@@ -666,7 +666,7 @@ int bkv_paged_decode_tree(const void *q, const void *k_cache, const void *v_cach
  *   their sum; the sums are exact in units of 2^-56, to which each
  *   probability (clamped to [0, 1], NaN: 0) is rounded.  Weights that are all
  *   0 fall back to the row p itself; a row without any weight gives token -1
- *   and counts in *err_count.  A row may sum to 256 at most.
+ *   and counts in *err_count.  A row has to sum to less than 256.
  *   A draft outside [0, vocab_size) among the first len is rejected and
  *   counted; a length outside [0, K] is clamped and counted.
  *

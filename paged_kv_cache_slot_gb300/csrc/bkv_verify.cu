@@ -17,7 +17,7 @@
 // rounding errors of one another, so weights are summed as integers in units
 // of 2^-56: exact for probabilities from 2^-32 up (24 significant bits) and
 // within 2^-57 below, associative, so the answer depends on no order, and
-// sums up to 256 fit 64 bits.
+// sums below 256 fit 64 bits.
 //
 // Memory-bound: one row of p (chain: of q too) of V fp32 a request.  A
 // cluster of CTAs shares a request's row; every CTA walks the drafts itself

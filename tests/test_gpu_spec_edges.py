@@ -205,3 +205,17 @@ def test_tree_decode_tiles_that_are_not_there(bs, t, hq):
     want = np.stack([oracle.paged_decode_tree_request(r, p.q, p.k, p.v, p.table, p.lens, words(mask))[0] for r in range(4)])
     assert not want[3].any()
     check_attention(_f64(_tree(p, mask)), want, "bf16")
+
+
+def test_verify_rows_that_sum_to_just_below_256():
+    """The largest sum that the units of 2^-56 hold: 255 weights of 1 and one of 1 - 2^-24."""
+    p = np.ones((3, 1, 256), np.float32)
+    p[:, 0, 255] = 1 - 2.0 ** -24
+    us = np.array([0.0, 0.5, 1 - 2.0 ** -24], np.float32)
+    out = torch.full((3, 1), -5, dtype=torch.int64, device=DEV)
+    n, none, err = torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros(3, 0, device=DEV), torch.zeros(
+        1, dtype=torch.int32, device=DEV)
+    bkv.bkv_verify_draft_chain(_d(p), torch.zeros(3, 0, 256, device=DEV), none.long(), none, _d(us), out, n, err_count=err)
+    runs = list(itertools.accumulate(Fraction(float(w)) for w in p[0, 0]))
+    assert out[:, 0].tolist() == [next(v for v, c in enumerate(runs) if c > Fraction(float(u)) * runs[-1]) for u in us]
+    assert out[:, 0].tolist() == [0, 127, 255] and int(err.item()) == 0
