@@ -633,7 +633,9 @@ size_t bkv_paged_decode_tree_workspace_size(int32_t num_reqs, int32_t q_len, int
  *   Other arguments, bounds and error counts as bkv_paged_decode.  bf16 with
  *   head_dim 128 and at most 128 query heads per KV head runs a tcgen05
  *   kernel (block sizes from 8 that divide 128 or are multiples of it, at
- *   most 2048 requests); anything else a CUDA-core kernel.
+ *   most 2048 requests); anything else a CUDA-core kernel.  The former rounds
+ *   the softmax's weights to bf16 for their product with V, as
+ *   bkv_paged_decode does; sums and partial results are fp32 in both.
  *   INVALID_ARG: as bkv_paged_decode, or mask_req_stride neither 0 nor at
  *   least q_len * words, or tree_mask null, or max_context_len above 2^30.
  *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd, q_len

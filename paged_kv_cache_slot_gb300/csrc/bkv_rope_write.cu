@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(B ? B : 160, B ? kPerSm : 4) rope_write_kernel
                     wa.get(fa);
                     wb.get(fb);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 8; ++e) {   // (two fp32 roundings, as (x inv) w has)
                         x[e] *= inv * fa[e];
                         y[e] *= inv * fb[e];
                     }
@@ -375,7 +375,7 @@ static cudaError_t launch_pieces(const Args &a, bool inter, cudaStream_t st) {
     constexpr int U = sizeof(T) == 2 ? 3 : 2;
     const int heads = a.hq + 2 * a.hkv, rounds = ceil_div(heads, 128 / LPH);
     const int64_t sms = current_sm_count();
-    // fewer tokens than CTAs fit: a token's heads over several (1021 tokens, E4M3: 11.2 -> 10.2 us)
+    // fewer tokens than CTAs fit: a token's heads over several (1016 tokens, E4M3: 11.2 -> 10.5 us)
     const int64_t room = 16 * sms / (a.max_n < 1 ? 1 : a.max_n);
     if (room >= 2 && rounds > 1) {
         const unsigned y = (unsigned)(room < rounds ? room : rounds);

@@ -83,7 +83,7 @@ __device__ __forceinline__ Pair fma2(const Pair &a, const Pair &b, const Pair &c
 // Bound by shared memory and the multiply-adds in turn (a few warps an SM, by
 // their registers; with more rows a thread they would balance) and, in small
 // calls, by the chain length -> table -> keys.  13 requests of 33 to 2500
-// positions, 11 tokens of 15 / 5 heads of 64, fp32: 30.7 us (32.3 with the keys
+// positions, 11 tokens of 15 / 5 heads of 64, fp32: 28.4 us (32.3 with the keys
 // of a tile shared by no warps and equal runs of positions; 16 of 35 to 268
 // positions, 4 tokens of 15 / 5 heads of 128: 12.6, 22.4).
 // A V row of the tree that is not finite is taken as 0 for the rows that do
