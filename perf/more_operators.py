@@ -239,7 +239,7 @@ class _Workspace:
 
     def get(self, bkv):
         if self.mem is None:
-            self.mem = bkv.alloc_workspace(*self.sizes)
+            self.mem = bkv.alloc_window_workspace(*self.sizes)
         return self.mem
 
 
