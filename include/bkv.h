@@ -5,7 +5,9 @@
  * with a split-KV merge, mixed-step attention, the context-parallel
  * slot filter and merge, and the speculative step around them: query / key
  * norm and rotation fused with the cache write, attention of drafted trees,
- * verification of drafts.
+ * verification of drafts.  Beside them: a step's block tables and slots built
+ * from the requests' lengths, E4M3 caches with a scale for each block of tokens
+ * and head, and windows whose first tokens stay visible.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -718,6 +720,160 @@ int bkv_verify_draft_tree(const float *target_probs, int64_t target_req_stride, 
                           const float *sample_u, int32_t num_reqs, int32_t num_nodes, int32_t vocab_size,
                           int64_t *out_tokens, int32_t *path, int32_t *num_accepted, int32_t *err_count,
                           bkv_stream_t stream);
+
+/*
+ * bkv_build_step
+ *   A step's block tables, token list and slots from the requests' lengths, on
+ *   the GPU: the blocks that the new tokens need are taken from a free list
+ *   ("ブロック表" 設計動機: append_row and compute_slot_mapping, done on the host
+ *   there; the slots are bkv_compute_slot_mapping's, "Padding and Batching with
+ *   Block KV", The Core Formula).
+ *
+ *   Request r has c = cached_lens[r] tokens and have = ceil(c / block_size)
+ *   blocks in its row, and gets n = new_lens[r] tokens:
+ *     blocks  = min(ceil((c + n) / block_size), bt_cols); it takes
+ *     f = max(blocks - have, 0) of the free list, behind those of the requests
+ *     before it: block_table[r][have + j] = free_blocks[F + j], j < f, F the sum
+ *     of f over the requests before; the entries behind them, up to bt_cols, are -1;
+ *     context_lens[r] = c + n;  query_start_loc[r] = Q, the sum of n before r;
+ *     token Q + i (i < n): req_indices = r, positions = c + i, slot_mapping =
+ *     the slot of that position in the new row, or -1 where it has no block.
+ *   query_start_loc[num_reqs] is the step's number of tokens; the entries of
+ *   req_indices, positions and slot_mapping from there on are -1, 0 and -1.
+ *   *blocks_used is the sum of f (at most num_free): the caller's free list goes
+ *   on behind them.  A padded row is one with c = n = 0.  Every result is exact.
+ *   The call may be repeated: it reads the first `have` entries of a row only.
+ *
+ *   cached_lens, new_lens, context_lens int32 [num_reqs]; query_start_loc int32
+ *             [num_reqs + 1]; free_blocks int32 [num_free]; block_table int32
+ *             [num_reqs, bt_stride], in and out; req_indices int32, positions and
+ *             slot_mapping int64 [max_num_tokens]; blocks_used int32 [1].
+ *             No output may overlap an input or another output.
+ *   Counted in *err_count: a negative length (taken as 0) or c + n above
+ *   INT32_MAX (n cut), once a request; a request whose new tokens pass bt_cols
+ *   blocks, once (those tokens get slot -1); every block that the free list lacks
+ *   (-1); a step of more than max_num_tokens tokens, once (those past it are not
+ *   listed).
+ *   INVALID_ARG: block_size <= 0, negative sizes, bt_stride < bt_cols, null
+ *   pointers, context_lens the same array as an input.
+ */
+int bkv_build_step(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs, const int32_t *free_blocks,
+                   int32_t num_free, int32_t block_size, int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
+                   int64_t max_num_tokens, int32_t *context_lens, int32_t *query_start_loc, int32_t *req_indices,
+                   int64_t *positions, int64_t *slot_mapping, int32_t *blocks_used, int32_t *err_count,
+                   bkv_stream_t stream);
+
+/*
+ * bkv_cache_write_fp8_blocks
+ *   A step's K and V rows into E4M3 caches with one scale for each block of
+ *   tokens and KV head, k_scales and v_scales [total_blocks][num_kv_heads]: a
+ *   code c of block b and head h stands for e4m3(c) * scale[b][h].  The pages
+ *   name a non-FP8 pathway only ("Padding and Batching with Block KV", Block ID
+ *   0 vs. Sentinel -1); the format is this library's reading.
+ *
+ *   Request r's new tokens are rows [query_start_loc[r], query_start_loc[r + 1])
+ *   of k_new and v_new and its last cached positions, ending at context_lens[r]
+ *   (as bkv_build_step lists them).  For a block that some of them fall into, a
+ *   head, and K or V, with x those rows:
+ *     s' = 2^e, the smallest with max |x| <= 448 * 2^e over the finite x, e held
+ *          to [-40, 40];
+ *     the block's scale s becomes s' if its first row is among the new ones (what
+ *          the block held before is void), else max(s', its scale so far);
+ *     where it grew, the rows before the new ones keep their values:
+ *          code = E4M3(e4m3(code) * (old scale / s));
+ *     x is stored as E4M3(x / s): nearest, ties to the even code, magnitudes above
+ *          448 (and infinities) saturated, NaN kept NaN.
+ *   Rows behind the new ones are left as they were.  Powers of two make the
+ *   quotients exact and cost E4M3 no precision.  Two requests that write one
+ *   block in a call are invalid input: either's rows and scale may land.
+ *
+ *   k_new, v_new  [num_tokens, new_token_stride] of src_dtype, the first
+ *             num_kv_heads * head_dim of each row.
+ *   query_start_loc int32 [num_reqs + 1], non-decreasing, last <= num_tokens;
+ *             context_lens int32 [num_reqs]; block_table as in
+ *             bkv_compute_slot_mapping.  Scales of blocks that hold earlier rows
+ *             are those that this call wrote (one that is not a positive finite
+ *             number is taken as absent, and the earlier rows stay as they are).
+ *   Counted in *err_count: a request with more new tokens than its length (none
+ *   of them is written), a block past the table's columns or the cache.  A null
+ *   entry (<= 0) writes nothing.
+ *   INVALID_ARG: negative or zero sizes, new_token_stride < num_kv_heads *
+ *   head_dim, block_size or head_dim above 65536, null pointers.  UNSUPPORTED:
+ *   src_dtype not BKV_BF16 / BKV_F32.
+ */
+int bkv_cache_write_fp8_blocks(const void *k_new, const void *v_new, int64_t num_tokens, int64_t new_token_stride,
+                               const int32_t *query_start_loc, const int32_t *context_lens, int32_t num_reqs,
+                               const int32_t *block_table, int64_t bt_stride, int32_t bt_cols, uint8_t *k_cache,
+                               uint8_t *v_cache, float *k_scales, float *v_scales, int64_t total_blocks,
+                               int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int src_dtype,
+                               int32_t *err_count, bkv_stream_t stream);
+
+/*
+ * bkv_paged_decode_window_workspace_size
+ *   Bytes of device workspace bkv_paged_decode_sink and
+ *   bkv_paged_decode_fp8_blocks need for these sizes on the CURRENT device; 0
+ *   for invalid sizes.
+ */
+size_t bkv_paged_decode_window_workspace_size(int32_t num_reqs, int32_t q_len, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                              int32_t max_context_len);
+
+/*
+ * bkv_paged_decode_sink
+ *   bkv_paged_decode_swa with the first num_sinks positions of every request
+ *   visible beside the window ("KV Caching with vLLM", Layer-specific cache
+ *   specification, for the window; the first tokens that stay have no counterpart
+ *   on the pages).  Query t, at position p = L - q_len + t, sees key j < L iff
+ *     j <= p (BKV_MASK_CAUSAL only), and
+ *     sliding_window W = 0, or j > p - W, or j < num_sinks,
+ *   and its block entry is a real block.  out = softmax-weighted V, 0 where no
+ *   key is seen.  Only the blocks that hold [0, num_sinks) or overlap some
+ *   query's window are read: the entries between them may be null (-1) and their
+ *   memory reused.  num_sinks 0 is bkv_paged_decode_swa's operation.
+ *   Cache memory at positions that a token does not see does not reach its
+ *   output.  At a position that it sees, a score of NaN or +inf makes its output
+ *   row of that query head NaN, a score of -inf weighs nothing, and an element of
+ *   V that is not finite may make the whole row NaN.
+ *
+ *   workspace  device scratch of workspace_bytes >=
+ *              bkv_paged_decode_window_workspace_size(...), 32-byte aligned, used
+ *              only while the call's kernels run; its contents on entry do not
+ *              matter.  Calls that may overlap on the GPU (two captured graphs
+ *              among them) need one each.
+ *   Bad table entries among the blocks that are read (an id >= total_blocks, or a
+ *   block past bt_cols) are masked and count once per KV head in *err_count; a
+ *   context_lens[r] above max_context_len is clamped to it and counted once.
+ *   out must not overlap q or the caches.  Other arguments as
+ *   bkv_paged_decode_swa.
+ *   INVALID_ARG: as bkv_paged_decode_swa, or num_sinks < 0, max_context_len above
+ *   2^26, or q_len * (num_q_heads / num_kv_heads) above 65536.
+ *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd.
+ */
+int bkv_paged_decode_sink(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                          int64_t bt_stride, int32_t bt_cols, const int32_t *context_lens, int32_t max_context_len,
+                          int32_t num_reqs, int32_t q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t block_size, int64_t total_blocks, float softmax_scale,
+                          int mask_mode, int32_t sliding_window, int32_t num_sinks, int dtype, void *out,
+                          void *workspace, size_t workspace_bytes, int32_t *err_count, bkv_stream_t stream);
+
+/*
+ * bkv_paged_decode_fp8_blocks
+ *   bkv_paged_decode_sink over E4M3 caches with a scale for each block of tokens
+ *   and KV head, as bkv_cache_write_fp8_blocks writes them: an element of K with
+ *   code c of block b and head h stands for e4m3(c) * k_scales[b][h], of V for
+ *   e4m3(c) * v_scales[b][h] (sliding_window 0: full attention).  Any positive
+ *   scales are read, not powers of two alone; one of V outside [2^-40, 2^40] is
+ *   taken as the nearer end.
+ *   k_scales, v_scales fp32 [total_blocks][num_kv_heads]; dtype: the type of q and
+ *   out.  Other arguments, masks, errors and workspace as bkv_paged_decode_sink.
+ */
+int bkv_paged_decode_fp8_blocks(const void *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scales,
+                                const float *v_scales, const int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
+                                const int32_t *context_lens, int32_t max_context_len, int32_t num_reqs, int32_t q_len,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int64_t total_blocks, float softmax_scale, int mask_mode, int32_t sliding_window,
+                                int32_t num_sinks, int dtype, void *out, void *workspace, size_t workspace_bytes,
+                                int32_t *err_count, bkv_stream_t stream);
 
 #ifdef __cplusplus
 }

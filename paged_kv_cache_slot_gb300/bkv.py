@@ -121,6 +121,18 @@ def load() -> ctypes.CDLL:
         lib.bkv_verify_draft_chain.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
         lib.bkv_verify_draft_tree.restype = cint
         lib.bkv_verify_draft_tree.argtypes = [vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        lib.bkv_build_step.restype = cint
+        lib.bkv_build_step.argtypes = [vp, vp, i32, vp, i32, i32, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.bkv_cache_write_fp8_blocks.restype = cint
+        lib.bkv_cache_write_fp8_blocks.argtypes = [vp, vp, i64, i64, vp, vp, i32, vp, i64, i32, vp, vp, vp, vp, i64, i32,
+                                                   i32, i32, cint, vp, vp]
+        lib.bkv_paged_decode_window_workspace_size.restype = sz
+        lib.bkv_paged_decode_window_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        win = [vp, i64, i32, vp, i32, i32, i32, i32, i32, i32, i32, i64, f32, cint, i32, i32, cint, vp, vp, sz, vp, vp]
+        lib.bkv_paged_decode_sink.restype = cint
+        lib.bkv_paged_decode_sink.argtypes = [vp, vp, vp] + win
+        lib.bkv_paged_decode_fp8_blocks.restype = cint
+        lib.bkv_paged_decode_fp8_blocks.argtypes = [vp, vp, vp, vp, vp] + win
         _lib = lib
         return lib
 
@@ -668,6 +680,135 @@ def bkv_verify_draft_tree(target_probs, draft_tokens, parents, accept_u, sample_
     return out_tokens, path, num_accepted
 
 
+def _table(block_table, rows):
+    """Columns and row stride of a block table of at least ``rows`` rows (a dimension of size 1 may carry any stride)."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D with unit column stride")
+    (n, cols), (row, col) = block_table.shape, block_table.stride()
+    if n < rows or (col != 1 and cols > 1):
+        raise ValueError("block_table must be (>= num_reqs, cols) with unit column stride")
+    return cols, row if n > 1 else max(row, cols)
+
+
+def bkv_build_step(cached_lens, new_lens, free_blocks, block_size, block_table, context_lens, query_start_loc, req_indices,
+                   positions, slot_mapping, blocks_used, err_count=None, stream=None):
+    """A step's tables, token list and slots from the requests' lengths: blocks for ``new_lens`` (num_reqs) tokens behind
+    ``cached_lens`` are taken from ``free_blocks`` in request order and put into ``block_table`` (entries behind them -1);
+    context_lens (num_reqs), query_start_loc (num_reqs + 1), req_indices / positions / slot_mapping (all as long as
+    slot_mapping) and blocks_used (1) are written (see include/bkv.h).  Returns (block_table, context_lens,
+    query_start_loc, req_indices, positions, slot_mapping, blocks_used)."""
+    nr, most = cached_lens.numel(), slot_mapping.numel()
+    if new_lens.numel() != nr or context_lens.numel() != nr or query_start_loc.numel() != nr + 1 or blocks_used.numel() != 1:
+        raise ValueError("new_lens and context_lens must have num_reqs elements, query_start_loc num_reqs + 1, blocks_used 1")
+    if req_indices.numel() != most or positions.numel() != most:
+        raise ValueError("req_indices, positions and slot_mapping must have one length")
+    cols, bt_row = _table(block_table, nr)
+    i32 = torch.int32
+    args = (_dev(cached_lens, "cached_lens", i32), _dev(new_lens, "new_lens", i32), nr, _dev(free_blocks, "free_blocks", i32),
+            free_blocks.numel(), int(block_size), _dev(block_table, "block_table", i32, False), bt_row, cols, most,
+            _dev(context_lens, "context_lens", i32), _dev(query_start_loc, "query_start_loc", i32),
+            _dev(req_indices, "req_indices", i32), _dev(positions, "positions", torch.int64),
+            _dev(slot_mapping, "slot_mapping", torch.int64), _dev(blocks_used, "blocks_used", i32),
+            None if err_count is None else _dev(err_count, "err_count", i32))
+    _same_device(cached_lens, new_lens, free_blocks, block_table, context_lens, query_start_loc, req_indices, positions,
+                 slot_mapping, blocks_used, err_count)
+    _check("bkv_build_step", load().bkv_build_step(*args, _stream(stream)))
+    return block_table, context_lens, query_start_loc, req_indices, positions, slot_mapping, blocks_used
+
+
+def bkv_cache_write_fp8_blocks(k_new, v_new, query_start_loc, context_lens, block_table, k_cache, v_cache, k_scales,
+                               v_scales, err_count=None, stream=None):
+    """Quantises the step's rows k_new / v_new (num_tokens, H_kv, D; bf16 or fp32), request r's at [query_start_loc[r],
+    query_start_loc[r + 1]) and its last cached positions, into uint8 E4M3 caches with fp32 scales (total_blocks, H_kv)
+    for each block and head, which grow with what the block holds (see include/bkv.h)."""
+    cache, ks = k_cache.shape, k_new.shape
+    if len(cache) != 4 or cache != v_cache.shape:
+        raise ValueError("caches must be (total_blocks, block_size, H_kv, D) and equal in shape")
+    tb, bs, hkv, d = cache
+    if len(ks) != 3 or ks[1] != hkv or ks[2] != d or ks != v_new.shape:
+        raise ValueError("k_new/v_new must be (num_tokens, H_kv, D) matching the cache")
+    (row, kh, ke), (v_row, vh, ve) = k_new.stride(), v_new.stride()
+    # (a dimension of size 1 may carry any stride)
+    if (d > 1 and (ke != 1 or ve != 1)) or (hkv > 1 and (kh != d or vh != d)) or (ks[0] > 1 and row != v_row):
+        raise ValueError("k_new/v_new rows must be dense (a row stride is allowed)")
+    if ks[0] <= 1:
+        row = max(row, hkv * d)
+    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
+        raise TypeError("FP8 caches are uint8 tensors of E4M3 codes")
+    if k_new.dtype is not v_new.dtype:
+        raise TypeError("mixed dtypes")
+    if k_scales.shape != (tb, hkv) or v_scales.shape != (tb, hkv):
+        raise ValueError("scales must be (total_blocks, H_kv)")
+    dt, nr = _kv_dtype(k_new), query_start_loc.numel() - 1
+    if nr < 0 or context_lens.numel() < nr:
+        raise ValueError("query_start_loc must have num_reqs + 1 elements, context_lens num_reqs")
+    cols, bt_row = _table(block_table, nr)
+    args = (_dev(k_new, "k_new", None, False), _dev(v_new, "v_new", None, False), ks[0], row,
+            _dev(query_start_loc, "query_start_loc", torch.int32), _dev(context_lens, "context_lens", torch.int32), nr,
+            _dev(block_table, "block_table", torch.int32, False), bt_row, cols, _dev(k_cache, "k_cache"),
+            _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32), _dev(v_scales, "v_scales", torch.float32),
+            tb, bs, hkv, d, dt, None if err_count is None else _dev(err_count, "err_count", torch.int32))
+    _same_device(k_new, v_new, query_start_loc, context_lens, block_table, k_cache, v_cache, k_scales, v_scales, err_count)
+    _check("bkv_cache_write_fp8_blocks", load().bkv_cache_write_fp8_blocks(*args, _stream(stream)))
+
+
+def bkv_paged_decode_window_workspace_size(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                           max_context_len) -> int:
+    return int(load().bkv_paged_decode_window_workspace_size(int(num_reqs), int(q_len), int(num_q_heads),
+                                                             int(num_kv_heads), int(head_dim), int(block_size),
+                                                             int(max_context_len)))
+
+
+def bkv_paged_decode_sink(q, k_cache, v_cache, block_table, context_lens, max_context_len, out, workspace, sliding_window,
+                          num_sinks, softmax_scale=0.0, mask_mode=BKV_MASK_CAUSAL, err_count=None, stream=None):
+    """bkv_paged_decode_swa whose first ``num_sinks`` positions stay visible beside the window (see include/bkv.h)."""
+    return _window("bkv_paged_decode_sink", q, k_cache, v_cache, None, block_table, context_lens, max_context_len, out,
+                   workspace, sliding_window, num_sinks, softmax_scale, mask_mode, err_count, stream)
+
+
+def bkv_paged_decode_fp8_blocks(q, k_cache, v_cache, k_scales, v_scales, block_table, context_lens, max_context_len, out,
+                                workspace, sliding_window=0, num_sinks=0, softmax_scale=0.0, mask_mode=BKV_MASK_CAUSAL,
+                                err_count=None, stream=None):
+    """Decode attention over uint8 E4M3 caches with fp32 scales (total_blocks, H_kv) for each block and head, with or
+    without a window and first tokens that stay visible (see include/bkv.h)."""
+    return _window("bkv_paged_decode_fp8_blocks", q, k_cache, v_cache, (k_scales, v_scales), block_table, context_lens,
+                   max_context_len, out, workspace, sliding_window, num_sinks, softmax_scale, mask_mode, err_count, stream)
+
+
+def _window(fn, q, k_cache, v_cache, scales, block_table, context_lens, max_context_len, out, workspace, sliding_window,
+            num_sinks, softmax_scale, mask_mode, err_count, stream):
+    shape, cache = q.shape, k_cache.shape
+    if len(shape) != 4 or out.shape != shape or len(cache) != 4 or cache != v_cache.shape:
+        raise ValueError("q/out must be (num_reqs, q_len, H_q, D); caches (total_blocks, bs, H_kv, D)")
+    nr, ql, hq, d = shape
+    tb, bs, hkv, d2 = cache
+    if d2 != d:
+        raise ValueError("head_dim mismatch")
+    cols, bt_row = _table(block_table, nr)
+    if context_lens.numel() < nr:
+        raise ValueError("context_lens must have num_reqs elements")
+    dt, dtype = _kv_dtype(q), q.dtype
+    cache_dtype = dtype if scales is None else torch.uint8
+    if k_cache.dtype is not cache_dtype or v_cache.dtype is not cache_dtype or out.dtype is not dtype:
+        raise TypeError(f"caches must be {cache_dtype} and out {dtype}")
+    if workspace.dtype is not torch.uint8:
+        raise TypeError("workspace must be a uint8 tensor")
+    ptrs = ()
+    if scales is not None:
+        if scales[0].shape != (tb, hkv) or scales[1].shape != (tb, hkv):
+            raise ValueError("scales must be (total_blocks, H_kv)")
+        ptrs = (_dev(scales[0], "k_scales", torch.float32), _dev(scales[1], "v_scales", torch.float32))
+    args = (_dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), *ptrs,
+            _dev(block_table, "block_table", torch.int32, False), bt_row, cols,
+            _dev(context_lens, "context_lens", torch.int32), int(max_context_len), nr, ql, hq, hkv, d, bs, tb,
+            float(softmax_scale), int(mask_mode), int(sliding_window), int(num_sinks), dt, _dev(out, "out"),
+            _dev(workspace, "workspace"), workspace.numel(),
+            None if err_count is None else _dev(err_count, "err_count", torch.int32))
+    _same_device(q, k_cache, v_cache, *(scales or ()), block_table, context_lens, out, workspace, err_count)
+    _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+    return out
+
+
 def _row_strides(t):
     """Request and row stride of probabilities (R, rows, V); a dimension of size 1 or 0 may carry any stride."""
     (reqs, rows, vocab), (req, row, _) = t.shape, t.stride()
@@ -679,6 +820,13 @@ def alloc_tree_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, b
     n = bkv_paged_decode_tree_workspace_size(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
                                              max_context_len)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def alloc_window_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, device=None):
+    """Convenience: a uint8 device tensor of the size bkv_paged_decode_sink and bkv_paged_decode_fp8_blocks need."""
+    n = bkv_paged_decode_window_workspace_size(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                               max_context_len)
+    return torch.empty(max(n, 32), dtype=torch.uint8, device=device or "cuda")
 
 
 def alloc_workspace(num_reqs, q_len, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len, device=None):
