@@ -1,7 +1,8 @@
 // bkv_window.cu -- attention over paged caches in two forms beside
 // bkv_paged_decode's: E4M3 caches with a scale for each block of tokens and KV
 // head, and sliding windows whose first tokens stay visible.  Entry points,
-// planner, the CUDA-core kernel and the merge of shared streams.
+// planner, the CUDA-core kernel and the merge of shared streams (bf16 queries of
+// head_dim 128 run the tcgen05 kernel of bkv_window_tc.cu).
 //
 // For a query row at position p of a request of length L ("Padding and
 // Batching with Block KV", Cache Masking; a null or sentinel block entry
@@ -359,7 +360,7 @@ static Split make_split(int64_t nq, int64_t H_kv, int most, int64_t resident) {
 constexpr int kCcRows = 8;
 
 struct Plan {
-    Split cc;
+    Split tc, cc;
     size_t o_off, ml_off, ws_bytes;
 };
 
@@ -373,9 +374,15 @@ static bool make_plan(int32_t num_reqs, int32_t q_len, int32_t num_q_heads, int3
     const int64_t nq = (int64_t)q_len * (num_q_heads / num_kv_heads);
     const int64_t sms = current_sm_count();
     if (nq > 65536 || nq * num_kv_heads > (1 << 24)) return false;
+    p->tc = make_split(nq, num_kv_heads, kTcRows, sms);
     p->cc = make_split(nq, num_kv_heads, kCcRows, kCcPerSm * sms);
-    const int64_t rows = p->cc.rows() * num_kv_heads;
-    p->ml_off = (size_t)ceil_div<int64_t>((int64_t)p->cc.P * 8, 256) * 256;
+    int64_t rows = p->cc.rows(), P = p->cc.P;
+    if (head_dim == 128) {
+        rows = p->tc.rows() > rows ? p->tc.rows() : rows;
+        P = p->tc.P > P ? p->tc.P : P;
+    }
+    rows *= num_kv_heads;
+    p->ml_off = (size_t)ceil_div<int64_t>(P * 8, 256) * 256;
     p->o_off = p->ml_off + (size_t)ceil_div<int64_t>(rows * 8, 256) * 256;
     p->ws_bytes = p->o_off + (size_t)rows * head_dim * 4;
     return true;
@@ -402,7 +409,7 @@ static int launch_cc_rows(const Args &a, cudaStream_t st) {
     return a.NR <= 4 ? launch_cc_lanes<T, KV, 4>(a, vec, st) : launch_cc_lanes<T, KV, kCcRows>(a, vec, st);
 }
 
-static int partition(const Args &a, cudaStream_t st) {
+static int partition_cc(const Args &a, cudaStream_t st) {
     if (a.ks) {
         return a.dtype == BKV_BF16 ? launch_cc_rows<__nv_bfloat16, __nv_fp8_e4m3>(a, st)
                                    : launch_cc_rows<float, __nv_fp8_e4m3>(a, st);
@@ -471,12 +478,21 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, const
         a.out = static_cast<char *>(out) + (size_t)r0 * req_elems * e;
         a.bt = block_table ? block_table + r0 * bt_stride : nullptr;
         a.ctx = context_lens + r0;
-        a.seg = 1;
-        a.tile = kCcTile;
-        a.NR = plan.cc.NR;
-        a.groups = plan.cc.groups;
-        a.P = plan.cc.P;
-        int rc = partition(a, stream);
+        TcLaunch t;
+        a.seg = block_size < 128 ? block_size : 128;
+        a.tile = 128;
+        a.NR = plan.tc.NR;
+        a.groups = plan.tc.groups;
+        a.P = plan.tc.P;
+        const bool tc = prepare_tc(a, &t);
+        if (!tc) {
+            a.seg = 1;
+            a.tile = kCcTile;
+            a.NR = plan.cc.NR;
+            a.groups = plan.cc.groups;
+            a.P = plan.cc.P;
+        }
+        int rc = tc ? launch_tc(a, t, stream) : partition_cc(a, stream);
         if (rc != BKV_OK) return rc;
         rc = merge(a, stream);
         if (rc != BKV_OK) return rc;

@@ -2,6 +2,8 @@
 // a scale a block and head, and over windows whose first tokens stay visible.
 #pragma once
 
+#include <cuda.h>
+
 #include "bkv_internal.cuh"
 
 namespace bkv {
@@ -178,6 +180,14 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 
 // Scales of values that the writes make; others are held to this range.
 constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;   // 2^-40, 2^40
+
+// tcgen05 / TMA kernel (bkv_window_tc.cu): bf16 queries of head_dim 128.
+struct TcLaunch {
+    CUtensorMap mk, mv;
+};
+constexpr int kTcRows = 16;   // query rows a group, at most
+bool prepare_tc(const Args &a, TcLaunch *t);
+int launch_tc(const Args &a, const TcLaunch &t, cudaStream_t stream);
 
 }  // namespace win
 }  // namespace bkv

@@ -1,0 +1,761 @@
+// bkv_window_tc.cu -- tensor-core (tcgen05 + TMA) kernel of the attention over
+// E4M3 caches with a scale a block and head, and over windows whose first
+// tokens stay visible: bf16 queries of head_dim 128, bf16 or E4M3 caches.
+//
+// For a stream (request, KV head, row group of at most 16 query rows) and a run
+// of 128-position tiles of the request's span: an online softmax over s_j =
+// scale q . k_j and o += p_j v_j ("Padding and Batching with Block KV", Cache
+// Masking; Special Block and Slot Values).  A stream that one CTA finishes is
+// written to `out` there; one that several share leaves partials for the merge.
+//
+// Design (sm_103a):
+// * Schedule: the grid is P columns of one CTA per (KV head, row group); a column
+//   takes an equal share of the requests' cost (bkv_window.cuh), its CTAs the same
+//   positions of all heads together.
+// * Keys are the MMA's rows: S^T[128 x 16] = K . Q^T and O^T[128 x 16] = V^T .
+//   P^T, so that a decode step's few query rows fill the N side and a position is
+//   a thread's.  With a position a thread, the scales of its block are two
+//   registers: k's joins the score's factor, and v's the exponent: with s'_j =
+//   s_j + log2 vs_j the weights that enter P V are p'_j = 2^(s'_j - m'), m' their
+//   running maximum, and the row sum is sum_j p'_j / vs_j.  The value tile stays
+//   the codes that TMA brought, and the weights are rounded relative to what
+//   matters most to the output, whatever the blocks' scales.
+// * E4M3 caches: both products in kind::f8f6f4 on the codes.  A query row is
+//   divided by a power of two and split into two E4M3 parts (exact for elements
+//   down to 2^-10 of the row's largest, within 2^-17 of it below), P into two
+//   (within 2^-10 of the largest weight); the parts are columns [0, 16) and [16,
+//   32) of one MMA, summed as they are read.  Row sums take fp32 weights.
+//   bf16 caches: weights are rounded to bf16 (2^-8 of each), and the row sums take
+//   the rounded ones.
+// * Warp roles (384 threads): 0 gathers K tiles, 2 V tiles through the block table
+//   by 3-D TMA boxes (head_dim half, one head, rows of a block), 1 and 3 issue the
+//   MMAs of S and of P V, 4-7 and 8-11 are two softmax warpgroups on alternate
+//   tiles.  Warp 2 also brings the queries, and splits them, so that no launch has
+//   to come before this one.  K and V have rings of 96 KB each.  Block entries are
+//   loaded 32 segments ahead, a lane each, and a unit's queries with its first
+//   ones; the scales follow by cp.async, whose arrival the tile's mask barrier
+//   counts.
+// * V rows that no query row of the group sees, and segments that were not loaded,
+//   are zeroed before P V; a row that only some see is, too, if it is not finite,
+//   and those that see it become NaN.
+// * Every wait is bounded (~2 s), after which the CTA records 1 << 24 in
+//   err_count, frees its tensor memory and exits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "bkv_tc_cols.cuh"
+#include "bkv_window.cuh"
+
+namespace bkv {
+namespace win {
+
+using namespace tc;
+
+constexpr int kTcTile = 128;
+constexpr int kD = 128;
+constexpr int kN = kTcRows;
+constexpr int kTcThreads = 384;
+constexpr int kWarpV = 2, kWarpS = 4;                // (1 and 3 issue MMAs)
+constexpr int kHalfBytes = kTcTile * 128;            // a bf16 tile's half of head_dim
+constexpr int kRing = 16;                            // tiles whose segment words and scales are kept
+constexpr int kSets = 4;                             // units whose query scales, and exchanges that, are kept
+constexpr int kTmemCols = 256;                       // S at 0 and 32, O at 64 and 96, exchanges at 128 + 16 i
+constexpr int kTimeoutErr = 1 << 24;
+constexpr int kPExp = 8;                             // E4M3 weights are p' 2^8: at most 256 < 448
+
+template <bool kF8>
+struct TcCfg {
+    static constexpr int kStages = kF8 ? 6 : 3;
+    static constexpr int kSlot = kF8 ? kTcTile * 128 : 2 * kHalfBytes;
+    static constexpr int kQBytes = 2 * kN * 128;                      // two halves (bf16) or parts (E4M3) of 16 rows
+    static constexpr int kOffV = kStages * kSlot;
+    static constexpr int kOffQ = 2 * kStages * kSlot;
+    static constexpr int kOffP = kOffQ + 2 * kQBytes;
+    static constexpr int kOffMax = kOffP + 2 * kQBytes;               // [warpgroup][2][16][4] floats
+    static constexpr int kOffSum = kOffMax + 4 * kN * 4 * 4;          // [warpgroup][2][16][4]
+    static constexpr int kOffXm = kOffSum + 4 * kN * 4 * 4;           // [set][16] (max, sum)
+    static constexpr int kOffQs = kOffXm + kSets * kN * 8;            // [set][16] scores' factors
+    static constexpr int kOffScale = kOffQs + kSets * kN * 4;         // [kRing][2][16 segments]
+    static constexpr int kOffMask = kOffScale + (kF8 ? kRing * 2 * 16 * 4 : 0);   // [kRing] loaded segments
+    static constexpr int kOffBar = kOffMask + kRing * 4;
+    static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 * kSets + 8 + 2 + kRing;
+    static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+    static constexpr int kOffAbort = kOffTmem + 4;
+    static constexpr int kOffSums = kOffAbort + 4;                    // a word a warp: prefix sum's scratch
+    static constexpr int kOffPre = (kOffSums + kTcThreads / 32 * 4 + 15) / 16 * 16;
+    static constexpr int kOffLens = kOffPre + (kMaxReqs + 4) * 4;
+    static constexpr int kSmem = kOffLens + kMaxReqs * 4 + 1024;      // slack for 1024 alignment
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
+    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
+    static_assert(kStages + 2 < kRing, "a ring word is rewritten behind its readers");
+};
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+template <int NQ>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[NQ]) {
+    uint32_t w[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) w[i] = __float_as_uint(v[i]);
+    if constexpr (NQ == 16) tmem_st16(taddr, w);
+    else if constexpr (NQ == 8) tmem_st8(taddr, w);
+    else tmem_st4(taddr, w);
+}
+
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives when this thread's copies so far have landed (one of the barrier's count).
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int NQ, bool kF8>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    window_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
+    using C = TcCfg<kF8>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *qs = reinterpret_cast<float *>(smem + C::kOffQs);
+    volatile uint32_t *mask_words = reinterpret_cast<uint32_t *>(smem + C::kOffMask);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffTmem);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffAbort);
+    int32_t *pre = reinterpret_cast<int32_t *>(smem + C::kOffPre);
+    int32_t *lens = reinterpret_cast<int32_t *>(smem + C::kOffLens);
+    const uint32_t bar0 = sbase + C::kOffBar;
+    auto bar_kfull = [&](int s) { return bar0 + 8u * s; };
+    auto bar_kempty = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto bar_vfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
+    auto bar_vempty = [&](int s) { return bar0 + 8u * (3 * kStages + s); };
+    constexpr int kB = 4 * kStages;
+    auto bar_qfull = [&](int b) { return bar0 + 8u * (kB + b); };
+    auto bar_qempty = [&](int b) { return bar0 + 8u * (kB + 2 + b); };
+    auto bar_sfull = [&](int b) { return bar0 + 8u * (kB + 4 + b); };
+    auto bar_sfree = [&](int b) { return bar0 + 8u * (kB + 6 + b); };
+    auto bar_pfull = [&](int b) { return bar0 + 8u * (kB + 8 + b); };
+    auto bar_ofull = [&](int b) { return bar0 + 8u * (kB + 10 + b); };
+    auto bar_group = [&](int k) { return bar0 + 8u * (kB + 12 + k); };
+    auto bar_qscale = [&](int i) { return bar0 + 8u * (kB + 14 + i); };
+    auto bar_x = [&](int i) { return bar0 + 8u * (kB + 14 + kSets + i); };
+    auto bar_mask = [&](int m) { return bar0 + 8u * (kB + 14 + 2 * kSets + m); };
+    const uint32_t sm_k = sbase, sm_v = sbase + C::kOffV, sm_q = sbase + C::kOffQ, sm_p = sbase + C::kOffP;
+
+    // what this CTA is: column q, KV head g, row group grp, and its rows
+    const int HP = a.H_kv * a.groups;
+    const int q = (int)blockIdx.x / HP, hp = (int)blockIdx.x - q * HP;
+    const int g = hp / a.groups, grp = hp - g * a.groups;
+    const int i0 = grp * a.NR;
+    const int rows = min(a.NR, a.q_len * a.G - i0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_kfull(s), 1);
+            mbar_init(bar_kempty(s), 1);
+            mbar_init(bar_vfull(s), 1);
+            mbar_init(bar_vempty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_qfull(b), 1);
+            mbar_init(bar_qempty(b), 1);
+            mbar_init(bar_sfull(b), 1);
+            mbar_init(bar_sfree(b), 4);
+            mbar_init(bar_pfull(b), 4);
+            mbar_init(bar_ofull(b), 1);
+            mbar_init(bar_group(b), 4);
+        }
+        for (int i = 0; i < kSets; ++i) {
+            mbar_init(bar_qscale(i), 1);
+            mbar_init(bar_x(i), 4);
+        }
+        for (int m = 0; m < kRing; ++m) mbar_init(bar_mask(m), kF8 ? 33 : 1);   // the word, and the lanes' copies
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    {
+        // query rows past the group's, and P, start at zero
+        uint4 *z = reinterpret_cast<uint4 *>(smem + C::kOffQ);
+        for (int i = threadIdx.x; i < 4 * C::kQBytes / 16; i += kTcThreads) z[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();   // global memory is read from here on
+    pdl_trigger();
+    lay_out<kTcThreads>(a, pre, lens, reinterpret_cast<int32_t *>(smem + C::kOffSums));
+    const uint32_t tmem = *tmem_slot;
+    const int seg_rows = a.seg;                      // a power of two, 8 to 128
+    const int nseg = kTcTile / seg_rows;
+    const int seg_shift = 31 - __clz(seg_rows);
+    Units units(pre, a.num_reqs, q, a.P);
+    Unit x;
+    auto out_row = [&](int r, int n) {
+        const int t = (i0 + n) / a.G;
+        return (((int64_t)r * a.q_len + t) * a.H_q + g * a.G + (i0 + n - t * a.G)) * kD;
+    };
+
+    if (warp == 0 || warp == kWarpV) {
+        // ================= TMA producers =================
+        const bool is_v = warp == kWarpV;
+        const bool count = !is_v && grp == 0 && a.err;   // bad entries count once a KV head
+        // ---- queries (warp 2): unit us's rows, four elements a lane ----
+        uint2 raw[kN];
+        auto load_q = [&](int r) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+                raw[n] = n < rows ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + out_row(r, n)) + lane)
+                                  : make_uint2(0, 0);
+        };
+        auto put_q = [&](int us) -> bool {
+            const int b = us & 1;
+            if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((us >> 1) & 1) ^ 1u, abort_flag)) return false;
+            uint8_t *dst = smem + C::kOffQ + b * C::kQBytes;
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                if (n >= rows) break;
+                if constexpr (kF8) {
+                    // scaled by 2^-e, e = floor(log2 max) - 7, then x = hi + lo in E4M3: x has at most 8 significant
+                    // bits, so the remainder is exact where |x| >= 2^-2 and within 2^-10 (2^-17 of the largest) below
+                    const float2 x01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[n].x));
+                    const float2 x23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[n].y));
+                    // the largest as bits: NaN and infinity come out above every number
+                    uint32_t top = max(max(__float_as_uint(x01.x) & 0x7fffffffu, __float_as_uint(x01.y) & 0x7fffffffu),
+                                       max(__float_as_uint(x23.x) & 0x7fffffffu, __float_as_uint(x23.y) & 0x7fffffffu));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    // (a row whose largest is subnormal is left as it is: its scores are 0 to fp32's own rounding)
+                    const int e = top >= 0x00800000u && top < 0x7f800000u ? min(max((int)(top >> 23) - 127 - 7, -126), 126) : 0;
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    const float2 s01 = make_float2(x01.x * down, x01.y * down), s23 = make_float2(x23.x * down, x23.y * down);
+                    const __nv_fp8x2_storage_t h01 = __nv_cvt_float2_to_fp8x2(s01, __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t h23 = __nv_cvt_float2_to_fp8x2(s23, __NV_SATFINITE, __NV_E4M3);
+                    const float2 f01 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h01, __NV_E4M3)));
+                    const float2 f23 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h23, __NV_E4M3)));
+                    const __nv_fp8x2_storage_t l01 =
+                        __nv_cvt_float2_to_fp8x2(make_float2(s01.x - f01.x, s01.y - f01.y), __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t l23 =
+                        __nv_cvt_float2_to_fp8x2(make_float2(s23.x - f23.x, s23.y - f23.y), __NV_SATFINITE, __NV_E4M3);
+                    uint8_t *at = dst + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t *>(at) = (uint32_t)h01 | ((uint32_t)h23 << 16);
+                    *reinterpret_cast<uint32_t *>(at + kN * 128) = (uint32_t)l01 | ((uint32_t)l23 << 16);
+                    // a row that is not finite makes its scores NaN
+                    if (lane == 0)
+                        qs[(us & (kSets - 1)) * kN + n] = top < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
+                                                                            : __uint_as_float(0x7fffffffu);
+                } else {
+                    // 64 elements a half; 16-byte chunk c of row n at c ^ (n & 7)
+                    uint8_t *at = dst + (lane >> 4) * (kN * 128) + n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
+                    *reinterpret_cast<uint2 *>(at) = raw[n];
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar_qfull(b));
+                if constexpr (kF8) mbar_arrive(bar_qscale(us & (kSets - 1)));
+            }
+            return true;
+        };
+        // A chunk is 32 segments of a unit, a lane each: the cache row that its segment begins at (-1: nothing to
+        // load) and its block.  The next one's entries are loaded while this one's tiles are issued.
+        struct Chunk {
+            int r, f, nt, c;   // the unit; the chunk's number in it
+            int32_t row, blk;
+        };
+        const int tiles = 32 / nseg;   // tiles a chunk
+        auto fetch = [&](Chunk &w) {
+            w.row = -1;
+            w.blk = 0;
+            const Span s = span_of(a, lens[w.r]);
+            const int32_t seg = w.f * nseg + w.c * 32 + lane, v = seg << seg_shift;
+            if (w.c * 32 + lane < w.nt * nseg && v < s.len) {
+                const int32_t p = s.pos(v), lb = p / a.bs, off = p - lb * a.bs;
+                const int64_t e = lb < a.bt_cols ? __ldg(a.bt + (int64_t)w.r * a.bt_stride + lb) : a.total_blocks;
+                if (e >= a.total_blocks) {
+                    // at the block's first segment in the span
+                    if (count && (off == 0 || (s.gap > 0 && v == s.sb && (s.sb == 0 || lb != (s.sb - 1) / a.bs))))
+                        atomicAdd(a.err, 1);
+                } else if (e > 0) {
+                    w.blk = (int32_t)e;
+                    w.row = (int32_t)(e * a.bs + off);
+                }
+            }
+        };
+        auto next = [&](const Chunk &w, Chunk &n) -> bool {
+            if ((w.c + 1) * tiles < w.nt) {
+                n = w;
+                ++n.c;
+            } else {
+                if (!units.next(x)) return false;
+                n.r = x.r;
+                n.f = x.f;
+                n.nt = x.nt;
+                n.c = 0;
+                if (is_v) load_q(x.r);
+            }
+            fetch(n);
+            return true;
+        };
+        if (is_v) {
+            if (hp == 0 && lane == 0) a.ws_split[q] = units.split();
+            // requests without a cached position
+            for (int r = q; r < a.num_reqs; r += a.P)
+                if (pre[r + 1] == pre[r])
+                    for (int n = 0; n < rows; ++n)
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row(r, n) + 4 * lane) = make_uint2(0, 0);
+        }
+        Chunk cur{0, 0, 0, 0, -1, 0}, nxt;
+        bool have = next(cur, cur);
+        Ring ring;
+        int j = 0, us = 0;
+        while (have && !*abort_flag) {
+            if (is_v && cur.c == 0 && !put_q(us++)) break;   // (its registers go to the next unit's below)
+            const bool more = next(cur, nxt);
+            const int nt = min(tiles, cur.nt - cur.c * tiles);
+            for (int kt = 0; kt < nt; ++kt, ++j, ring.advance(kStages)) {
+                const int s = ring.slot;
+                const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
+                const int32_t row = __shfl_sync(0xffffffffu, cur.row, (kt * nseg + lane) & 31);
+                const int32_t blk = __shfl_sync(0xffffffffu, cur.blk, (kt * nseg + lane) & 31);
+                const bool load = lane < nseg && row >= 0;
+                const uint32_t ballot = __ballot_sync(0xffffffffu, load);
+                if (!mbar_wait_warp(is_v ? bar_vempty(s) : bar_kempty(s), ring.phase ^ 1u, abort_flag)) break;
+                if (!is_v) {
+                    // Tile j's word and scales: written only after the S MMA of tile j - kStages completed, which was
+                    // issued after the softmax had read tile j - kStages - 2's, so that the writer is at most
+                    // kStages + 2 < kRing tiles ahead of the readers.
+                    const int m = j & (kRing - 1);
+                    if constexpr (kF8) {
+                        if (load) {
+                            const uint32_t dst = sbase + C::kOffScale + (uint32_t)(m * 32 + lane) * 4u;
+                            const int64_t at = (int64_t)blk * a.H_kv + g;
+                            copy4_async(dst, a.ks + at);
+                            copy4_async(dst + 64u, a.vs + at);
+                        }
+                        copies_arrive(bar_mask(m));
+                    }
+                    if (lane == 0) {
+                        mask_words[m] = ballot;
+                        mbar_arrive(bar_mask(m));
+                    }
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bar_f, (uint32_t)__popc(ballot) * (uint32_t)seg_rows * (kF8 ? 128u : 256u));
+                __syncwarp();
+                if (load) {
+                    const CUtensorMap *map = is_v ? &tmV : &tmK;
+                    const uint32_t dst = (is_v ? sm_v : sm_k) + s * C::kSlot + lane * seg_rows * 128;
+                    tma_load_3d(dst, map, bar_f, 0, g, row);
+                    if constexpr (!kF8) tma_load_3d(dst + kHalfBytes, map, bar_f, 64, g, row);
+                }
+                __syncwarp();
+            }
+            cur = nxt;
+            have = more;
+        }
+        if (*abort_flag) {   // let copies in flight land
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            const unsigned long long t0 = global_ns();
+            while (global_ns() - t0 < 200000ull) {
+            }
+        }
+    } else if (warp == 1 || warp == 3) {
+        // ================= MMA issuers (one thread each) =================
+        constexpr int kNM = kF8 ? 2 * kN : kN;
+        if (lane == 0 && warp == 1) {
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kNM, 0, 0) : idesc_bf16(128, kNM, 0, 0);
+            int j = 0, us = 0;
+            Ring ring;
+            bool ok = true;
+            for (; ok && units.next(x); ++us) {
+                const int qb = us & 1;
+                if (!mbar_wait(bar_qfull(qb), (uint32_t)(us >> 1) & 1u, abort_flag)) break;
+                const uint32_t q_base = sm_q + qb * C::kQBytes;
+                for (int jt = 0; jt < x.nt; ++jt, ++j, ring.advance(kStages)) {
+                    const int b = j & 1;
+                    // K landed, and the softmax has read S tile b of tile j - 2
+                    if (!mbar_wait(bar_kfull(ring.slot), ring.phase, abort_flag) ||
+                        (j >= 2 && !mbar_wait(bar_sfree(b), (uint32_t)((j >> 1) & 1) ^ 1u, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + 32u * (uint32_t)b, k_base = sm_k + ring.slot * C::kSlot;
+                    if constexpr (kF8) {
+#pragma unroll
+                        for (int kk = 0; kk < kD / 32; ++kk)
+                            mma_f8(d, sdesc(k_base + kk * 32, 16, 1024), sdesc(q_base + kk * 32, 16, 1024), kIdesc, kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < kD / 16; ++kk)
+                            mma_bf16(d, sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
+                                     sdesc(q_base + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0);
+                    }
+                    mma_commit(bar_sfull(b));
+                    mma_commit(bar_kempty(ring.slot));
+                    if (jt == x.nt - 1) mma_commit(bar_qempty(qb));
+                }
+            }
+        } else if (lane == 0) {
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kNM, 1, 0) : idesc_bf16(128, kNM, 1, 0);
+            int j = 0;
+            Ring ring;
+            bool ok = true;
+            while (ok && units.next(x)) {
+                for (int jt = 0; jt < x.nt; ++jt, ++j, ring.advance(kStages)) {
+                    const int b = j & 1;
+                    if (!mbar_wait(bar_vfull(ring.slot), ring.phase, abort_flag) ||
+                        !mbar_wait(bar_pfull(b), (uint32_t)((j >> 1) & 1), abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + 64u + 32u * (uint32_t)b, v_base = sm_v + ring.slot * C::kSlot;
+                    const uint32_t p_base = sm_p + b * C::kQBytes;
+                    if constexpr (kF8) {
+                        // V^T MN-major: a row's 128 codes are one 128-byte span, 8-row groups 1024 bytes apart
+#pragma unroll
+                        for (int kk = 0; kk < kTcTile / 32; ++kk)
+                            mma_f8(d, sdesc(v_base + kk * 4096, 16, 1024), sdesc(p_base + kk * 32, 16, 1024), kIdesc, kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < kTcTile / 16; ++kk)
+                            mma_bf16(d, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
+                                     sdesc(p_base + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0);
+                    }
+                    mma_commit(bar_ofull(b));
+                    mma_commit(bar_vempty(ring.slot));
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================= softmax and output (two warpgroups of 128 threads) =================
+        const int wg = (warp - kWarpS) >> 2, wq = warp & 3;
+        const int row = 32 * wq + lane;                  // TMEM lane: position in the tile, and head_dim row
+        const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+        constexpr float kOutScale = kF8 ? 1.f / (float)(1 << kPExp) : 1.f;
+        const int p_off = kF8 ? (row & 15) : (row >> 6) * (kN * 128) + (row & 7) * 2;
+        const int p_chunk = kF8 ? (row >> 4) : (row & 63) >> 3;
+        const int red_row = reduced_row<NQ>(lane);
+        const bool red_writer = reduced_writer<NQ>(lane);
+        uint8_t *p_dst = smem + C::kOffP + wg * C::kQBytes + p_off;
+        uint32_t gphase = 0;
+        // Bounded barrier of the warpgroup's four warps.
+        auto group_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_group(wg));
+            const bool r = mbar_wait_warp(bar_group(wg), gphase, abort_flag);
+            gphase ^= 1u;
+            return r;
+        };
+        int j = 0, xs = 0, mu = 0;   // tile, exchange and own unit number
+        Ring vring;
+        bool ok = true;
+        for (int us = 0; ok && units.next(x); ++us) {
+            const bool both = x.nt > 1;   // a unit of one tile is one warpgroup's alone
+            if (!both && (j & 1) != wg) {
+                ++j;
+                vring.advance(kStages);
+                continue;
+            }
+            const Span s = span_of(a, lens[x.r]);
+            // Positions at or below last_lo (and from first_hi on, or below `sinks`) are seen by every row of the
+            // group, those past last_hi (or before first_lo) by none.
+            const int32_t t_lo = s.L - a.q_len + i0 / a.G, t_hi = s.L - a.q_len + (i0 + rows - 1) / a.G;
+            const int32_t last_lo = a.causal ? t_lo : s.L - 1, last_hi = a.causal ? t_hi : s.L - 1;
+            const int32_t first_lo = a.window > 0 ? t_lo - a.window + 1 : INT32_MIN;
+            const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
+            float o[NQ], lsum[NQ], mrun[NQ], cs[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                o[n] = 0.f;
+                lsum[n] = 0.f;
+                mrun[n] = -INFINITY;
+                cs[n] = a.scale_log2;
+            }
+            if constexpr (kF8) {
+                // a set is rewritten four units on, behind the S MMAs of the unit after the next, which wait until this
+                // unit's tiles have been read
+                if (!mbar_wait_warp(bar_qscale(us & (kSets - 1)), (uint32_t)(us >> 2) & 1u, abort_flag)) break;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? qs[(us & (kSets - 1)) * kN + n] : 0.f;
+            }
+            for (int jt = 0; jt < x.nt; ++jt, ++j, vring.advance(kStages)) {
+                if ((j & 1) != wg) continue;
+                const uint32_t par = (uint32_t)(j >> 1) & 1u;
+                const int m = j & (kRing - 1);
+                if (!mbar_wait_warp(bar_sfull(wg), par, abort_flag) ||
+                    !mbar_wait_warp(bar_mask(m), (uint32_t)(j / kRing) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int seg = row >> seg_shift;
+                const bool loaded = (mask_words[m] >> seg) & 1u;
+                float ks = 1.f, lv = 0.f, rv = 1.f;
+                if constexpr (kF8) {
+                    const float *sc = reinterpret_cast<const float *>(smem + C::kOffScale) + m * 32 + seg;
+                    ks = sc[0];
+                    const float vs = fminf(fmaxf(sc[16], kScaleMin), kScaleMax);
+                    lv = __log2f(vs);
+                    rv = __fdividef(1.f, vs);
+                }
+                tc_fence_after();
+                float sv[NQ];
+                if constexpr (kF8) tmem_ld_sum2<NQ>(tmem + lane_base + 32u * wg, sv);
+                else tmem_ld_cols<NQ>(tmem + lane_base + 32u * wg, sv);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sfree(wg));   // S tile may be overwritten (by tile j + 2's)
+                const int32_t v = (x.f + jt) * kTcTile + row;
+                const int32_t p = s.pos(v);
+                const bool in = loaded && v < s.len, sink = p < a.sinks;
+                const bool any = in && p <= last_hi && (p >= first_lo || sink);
+                const bool all = in && p <= last_lo && (p >= first_hi || sink);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) sv[n] = kF8 ? fmaf(sv[n], cs[n] * ks, lv) : sv[n] * cs[n];
+                const bool tile_all = __all_sync(0xffffffffu, all);
+                const int vslot = vring.slot;
+                if (!tile_all) {
+                    // rows that see a position, one by one
+                    if (!all) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const int32_t t = s.L - a.q_len + (i0 + min(n, rows - 1)) / a.G;
+                            const bool see = any && p <= (a.causal ? t : s.L - 1) &&
+                                             (a.window == 0 || p > t - a.window || sink);
+                            if (!see) sv[n] = -INFINITY;
+                        }
+                    }
+                    // V rows that must not reach P V (the tile has to be there)
+                    if (!mbar_wait_warp(bar_vfull(vslot), vring.phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!all) {
+                        uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
+                        constexpr int kParts = kF8 ? 1 : 2;
+                        bool clear = !any;
+                        if (any) {
+                            // seen by some rows and not by others: not finite?
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 w = vr[h * (kHalfBytes / 16) + ((c + lane) & 7)];
+                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        if constexpr (kF8) clear |= (__vcmpeq4(ws[i] & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0u;
+                                        else clear |= (ws[i] & 0x7f80u) == 0x7f80u || (ws[i] & 0x7f800000u) == 0x7f800000u;
+                                    }
+                                }
+                            if (clear) {
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n)
+                                    if (sv[n] != -INFINITY) lsum[n] = __uint_as_float(0x7fffffffu);
+                            }
+                        }
+                        if (clear) {
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) vr[h * (kHalfBytes / 16) + ((c + lane) & 7)] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+                // tile max per query row across the warpgroup's 128 threads
+                const float wmax = warp_reduce_rows<true, NQ>(sv, lane);
+                float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + (wg * 2 + (int)par) * (kN * 4);
+                if (red_writer) rm[red_row * 4 + wq] = wmax;
+                if (!group_sync()) {
+                    ok = false;
+                    break;
+                }
+                float corr[NQ];
+                auto weight = [&](int n) -> float {
+                    const float4 t4 = *reinterpret_cast<const float4 *>(rm + n * 4);
+                    const float mn = fmaxf(mrun[n], fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)));
+                    corr[n] = mn == -INFINITY ? 1.f : fast_exp2(mrun[n] - mn);
+                    mrun[n] = mn;
+                    return sv[n] == -INFINITY ? 0.f : fast_exp2(sv[n] - mn);
+                };
+                if constexpr (kF8) {
+                    // p' 2^8 = hi + lo, two E4M3 codes a weight (absolute error at most 2^-10)
+#pragma unroll
+                    for (int n = 0; n < NQ; n += 2) {
+                        const float p0 = weight(n), p1 = weight(n + 1);
+                        lsum[n] = fmaf(lsum[n], corr[n], p0 * rv);
+                        lsum[n + 1] = fmaf(lsum[n + 1], corr[n + 1], p1 * rv);
+                        const float2 x2 = make_float2(p0 * (float)(1 << kPExp), p1 * (float)(1 << kPExp));
+                        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(x2, __NV_SATFINITE, __NV_E4M3);
+                        const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
+                        const __nv_fp8x2_storage_t lo =
+                            __nv_cvt_float2_to_fp8x2(make_float2(x2.x - hf.x, x2.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+                        uint8_t *d0 = p_dst + n * 128 + ((p_chunk ^ (n & 7)) << 4);
+                        uint8_t *d1 = p_dst + (n + 1) * 128 + ((p_chunk ^ ((n + 1) & 7)) << 4);
+                        d0[0] = (uint8_t)(hi & 0xFF);
+                        d1[0] = (uint8_t)(hi >> 8);
+                        d0[kN * 128] = (uint8_t)(lo & 0xFF);
+                        d1[kN * 128] = (uint8_t)(lo >> 8);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const __nv_bfloat16 pb = __float2bfloat16_rn(weight(n));
+                        lsum[n] = fmaf(lsum[n], corr[n], __bfloat162float(pb));
+                        *reinterpret_cast<__nv_bfloat16 *>(p_dst + n * 128 + ((p_chunk ^ (n & 7)) << 4)) = pb;
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pfull(wg));
+                // this tile's P V (the other warpgroup works meanwhile)
+                if (!mbar_wait_warp(bar_ofull(wg), par, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float ot[NQ];
+                if constexpr (kF8) tmem_ld_sum2<NQ>(tmem + lane_base + 64u + 32u * wg, ot);
+                else tmem_ld_cols<NQ>(tmem + lane_base + 64u + 32u * wg, ot);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) o[n] = fmaf(o[n], corr[n], ot[n]);
+            }
+            if (!ok) break;
+            // row sums across the warpgroup, in two buffers in turn: one is written again behind the next unit's
+            // barrier, which all passed after reading it
+            float *sums = reinterpret_cast<float *>(smem + C::kOffSum) + (wg * 2 + (mu & 1)) * (kN * 4);
+            ++mu;
+            const float wsum = warp_reduce_rows<false, NQ>(lsum, lane);
+            if (red_writer) sums[red_row * 4 + wq] = wsum;
+            if (!group_sync()) break;
+            auto total = [&](int n) {
+                const float4 t4 = *reinterpret_cast<const float4 *>(sums + n * 4);
+                return (t4.x + t4.y) + (t4.z + t4.w);
+            };
+            // The second warpgroup hands its part to the first, through tensor memory.  Exchange e + 1 is written
+            // behind a P V of the second that follows one of the first's later tiles, so at most two are not yet read
+            // when a third is written: four sets are enough.
+            const int set = xs & (kSets - 1);
+            const uint32_t x_col = tmem + lane_base + 128u + 16u * (uint32_t)set;
+            float2 *xm = reinterpret_cast<float2 *>(smem + C::kOffXm) + set * kN;
+            const uint32_t x_par = (uint32_t)(xs >> 2) & 1u;
+            if (both) ++xs;
+            if (both && wg == 1) {
+                tmem_st_cols<NQ>(x_col, o);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    if (row == n) xm[n] = make_float2(mrun[n], total(n));
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_x(set));
+                continue;
+            }
+            float l[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) l[n] = total(n);
+            if (both) {
+                if (!mbar_wait_warp(bar_x(set), x_par, abort_flag)) break;
+                tc_fence_after();
+                float o1[NQ];
+                tmem_ld_cols<NQ>(x_col, o1);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    const float2 ml = xm[n];
+                    const float mn = fmaxf(mrun[n], ml.x);
+                    const float f0 = mn == -INFINITY ? 1.f : fast_exp2(mrun[n] - mn);
+                    const float f1 = mn == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+                    o[n] = o[n] * f0 + o1[n] * f1;
+                    l[n] = l[n] * f0 + ml.y * f1;
+                    mrun[n] = mn;
+                }
+            }
+            if (x.whole) {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    if (n < rows) out[out_row(x.r, n) + row] = __float2bfloat16_rn(o[n] * kOutScale * inverse(l[n]));
+            } else {
+                const int64_t at = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    if (n >= rows) break;
+                    a.ws_o[(at + n) * kD + row] = o[n] * kOutScale;
+                    if (row == n) *reinterpret_cast<float2 *>(a.ws_ml + (at + n) * 2) = make_float2(mrun[n], l[n]);
+                }
+            }
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0 && a.err) atomicAdd(a.err, kTimeoutErr);
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+bool prepare_tc(const Args &a, TcLaunch *t) {
+    if (a.dtype != BKV_BF16 || a.D != kD || a.NR > kN || a.max_ctx <= 0) return false;
+    if (a.bs < 8 || !((kTcTile % a.bs == 0) || (a.bs % kTcTile == 0)) || a.H_kv > 65535) return false;
+    if (a.total_blocks <= 0 || a.total_blocks * a.bs >= ((int64_t)1 << 31)) return false;
+    if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q, 16) || !aligned(a.out, 8)) return false;
+    if (!encode_fn()) return false;
+    const uint64_t rows = (uint64_t)a.total_blocks * (uint64_t)a.bs;
+    if (a.ks) {
+        const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+        return encode_3d(&t->mk, a.k, kD, a.H_kv, rows, kD, (uint64_t)a.H_kv * kD, 128, 1, a.seg, u8) &&
+               encode_3d(&t->mv, a.v, kD, a.H_kv, rows, kD, (uint64_t)a.H_kv * kD, 128, 1, a.seg, u8);
+    }
+    return encode_3d(&t->mk, a.k, kD, a.H_kv, rows, kD * 2, (uint64_t)a.H_kv * kD * 2, 64, 1, a.seg) &&
+           encode_3d(&t->mv, a.v, kD, a.H_kv, rows, kD * 2, (uint64_t)a.H_kv * kD * 2, 64, 1, a.seg);
+}
+
+template <int NQ, bool kF8>
+static int launch(const Args &a, const TcLaunch &t, cudaStream_t st) {
+    auto kern = window_tc_kernel<NQ, kF8>;
+    constexpr int smem = TcCfg<kF8>::kSmem;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return launch_status();
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const cudaError_t e =
+        launch_pdl(kern, dim3((unsigned)(a.P * a.H_kv * a.groups)), dim3(kTcThreads), smem, st, t.mk, t.mv, a);
+    if (e != cudaSuccess) set_cuda_error(e);
+    return launch_status();
+}
+
+// The softmax handles only the query rows that exist (4, 8 or 16 columns).
+int launch_tc(const Args &a, const TcLaunch &t, cudaStream_t st) {
+    if (a.ks) return a.NR <= 4 ? launch<4, true>(a, t, st) : a.NR <= 8 ? launch<8, true>(a, t, st) : launch<16, true>(a, t, st);
+    return a.NR <= 4 ? launch<4, false>(a, t, st) : a.NR <= 8 ? launch<8, false>(a, t, st) : launch<16, false>(a, t, st);
+}
+
+}  // namespace win
+}  // namespace bkv
