@@ -62,7 +62,11 @@ constexpr int kRing = 16;                            // tiles whose segment word
 constexpr int kSets = 4;                             // units whose query scales, and exchanges that, are kept
 constexpr int kTmemCols = 256;                       // S at 0 and 32, O at 64 and 96, exchanges at 128 + 16 i
 constexpr int kTimeoutErr = 1 << 24;
-constexpr int kPExp = 8;                             // E4M3 weights are p' 2^8: at most 256 < 448
+// The softmax's reference is a power 2^kPExp below the maximum it was taken from and moves when a weight passes
+// 2^kPMax, so that O is seldom rescaled: weights are at most 256 < 448, E4M3's largest value.
+constexpr float kPMax = 8.f;
+template <bool kF8>
+constexpr float kPExp = kF8 ? 5.f : 0.f;
 
 template <bool kF8>
 struct TcCfg {
@@ -71,9 +75,11 @@ struct TcCfg {
     static constexpr int kQBytes = 2 * kN * 128;                      // two halves (bf16) or parts (E4M3) of 16 rows
     static constexpr int kOffV = kStages * kSlot;
     static constexpr int kOffQ = 2 * kStages * kSlot;
+    static constexpr int kPBytes = kTcTile * 32;                      // a position's weights: 16 bf16, or 16 + 16 E4M3 parts
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
-    static constexpr int kOffMax = kOffP + 2 * kQBytes;               // [warpgroup][2][16][4] floats
-    static constexpr int kOffSum = kOffMax + 4 * kN * 4 * 4;          // [warpgroup][2][16][4]
+    static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][4 warps][16] floats
+    static constexpr int kOffFlag = kOffMax + 2 * 4 * kN * 4;         // [warpgroup][2][4 warps] words
+    static constexpr int kOffSum = kOffFlag + 2 * 2 * 4 * 4;          // [warpgroup][2][16][4] floats
     static constexpr int kOffXm = kOffSum + 4 * kN * 4 * 4;           // [set][16] (max, sum)
     static constexpr int kOffQs = kOffXm + kSets * kN * 8;            // [set][16] scores' factors
     static constexpr int kOffScale = kOffQs + kSets * kN * 4;         // [kRing][2][16 segments]
@@ -104,6 +110,41 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[NQ
     if constexpr (NQ == 16) tmem_st16(taddr, w);
     else if constexpr (NQ == 8) tmem_st8(taddr, w);
     else tmem_st4(taddr, w);
+}
+
+// Shared-memory descriptor of an MN-major operand with spans of 32 bytes (32-byte swizzle): 8 spans 256 bytes apart.
+__device__ __forceinline__ uint64_t sdesc32(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)6 << 61;
+}
+
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// Two weights (at most 256) as E4M3 codes hi, hi' and the remainders' lo, lo', in half precision: x to 11 bits, hi to 4
+// of them, lo to 4 of the rest.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const __nv_fp8x2_storage_t a = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
+    hi = a;
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The first NQ weights of a position, as one span of 32 bytes; chunk c of 16 bytes stands at c ^ (position / 4 & 1).
+template <int W>
+__device__ __forceinline__ void put_words(uint8_t *at, const uint32_t (&w)[W]) {
+    if constexpr (W == 1) *reinterpret_cast<uint32_t *>(at) = w[0];
+    else if constexpr (W == 2) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float *src) {
@@ -185,7 +226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     {
         // query rows past the group's, and P, start at zero
         uint4 *z = reinterpret_cast<uint4 *>(smem + C::kOffQ);
-        for (int i = threadIdx.x; i < 4 * C::kQBytes / 16; i += kTcThreads) z[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < (C::kOffMax - C::kOffQ) / 16; i += kTcThreads) z[i] = make_uint4(0, 0, 0, 0);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -376,9 +417,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp == 1 || warp == 3) {
         // ================= MMA issuers (one thread each) =================
-        constexpr int kNM = kF8 ? 2 * kN : kN;
         if (lane == 0 && warp == 1) {
-            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kNM, 0, 0) : idesc_bf16(128, kNM, 0, 0);
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kN, 0, 0) : idesc_bf16(128, kN, 0, 0);
             int j = 0, us = 0;
             Ring ring;
             bool ok = true;
@@ -398,8 +438,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t d = tmem + 32u * (uint32_t)b, k_base = sm_k + ring.slot * C::kSlot;
                     if constexpr (kF8) {
 #pragma unroll
-                        for (int kk = 0; kk < kD / 32; ++kk)
-                            mma_f8(d, sdesc(k_base + kk * 32, 16, 1024), sdesc(q_base + kk * 32, 16, 1024), kIdesc, kk > 0);
+                        for (int kk = 0; kk < kD / 32; ++kk) {
+                            const uint64_t k = sdesc(k_base + kk * 32, 16, 1024);
+                            mma_f8(d, k, sdesc(q_base + kk * 32, 16, 1024), kIdesc, kk > 0);
+                            mma_f8(d, k, sdesc(q_base + kN * 128 + kk * 32, 16, 1024), kIdesc, 1);
+                        }
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < kD / 16; ++kk)
@@ -412,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         } else if (lane == 0) {
-            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kNM, 1, 0) : idesc_bf16(128, kNM, 1, 0);
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, 2 * kN, 1, 1) : idesc_bf16(128, kN, 1, 1);
             int j = 0;
             Ring ring;
             bool ok = true;
@@ -426,17 +469,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + 64u + 32u * (uint32_t)b, v_base = sm_v + ring.slot * C::kSlot;
-                    const uint32_t p_base = sm_p + b * C::kQBytes;
+                    const uint32_t p_base = sm_p + b * C::kPBytes;
+                    const uint32_t more = jt >= 2;   // a warpgroup's first tile of a unit begins its O
+                    // V^T and P^T MN-major: a row's 128 codes (64 bf16) are one 128-byte span, a position's weights one
+                    // of 32 bytes
                     if constexpr (kF8) {
-                        // V^T MN-major: a row's 128 codes are one 128-byte span, 8-row groups 1024 bytes apart
 #pragma unroll
                         for (int kk = 0; kk < kTcTile / 32; ++kk)
-                            mma_f8(d, sdesc(v_base + kk * 4096, 16, 1024), sdesc(p_base + kk * 32, 16, 1024), kIdesc, kk > 0);
+                            mma_f8(d, sdesc(v_base + kk * 4096, 16, 1024), sdesc32(p_base + kk * 1024), kIdesc, more | (kk > 0));
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < kTcTile / 16; ++kk)
-                            mma_bf16(d, sdesc(v_base + kk * 2048, kHalfBytes, 1024),
-                                     sdesc(p_base + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0);
+                            mma_bf16(d, sdesc(v_base + kk * 2048, kHalfBytes, 1024), sdesc32(p_base + kk * 512), kIdesc,
+                                     more | (kk > 0));
                     }
                     mma_commit(bar_ofull(b));
                     mma_commit(bar_vempty(ring.slot));
@@ -449,12 +494,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int wg = (warp - kWarpS) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                  // TMEM lane: position in the tile, and head_dim row
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-        constexpr float kOutScale = kF8 ? 1.f / (float)(1 << kPExp) : 1.f;
-        const int p_off = kF8 ? (row & 15) : (row >> 6) * (kN * 128) + (row & 7) * 2;
-        const int p_chunk = kF8 ? (row >> 4) : (row & 63) >> 3;
+        const uint32_t s_col = tmem + lane_base + 32u * (uint32_t)wg, o_col = s_col + 64u;
         const int red_row = reduced_row<NQ>(lane);
         const bool red_writer = reduced_writer<NQ>(lane);
-        uint8_t *p_dst = smem + C::kOffP + wg * C::kQBytes + p_off;
+        const int flip = (row >> 2) & 1;
+        uint8_t *p_hi = smem + C::kOffP + wg * C::kPBytes + row * 32 + 16 * flip, *p_lo = p_hi + 16 - 32 * flip;
+        float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + wg * 4 * kN;
         uint32_t gphase = 0;
         // Bounded barrier of the warpgroup's four warps.
         auto group_sync = [&]() -> bool {
@@ -463,6 +508,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool r = mbar_wait_warp(bar_group(wg), gphase, abort_flag);
             gphase ^= 1u;
             return r;
+        };
+        auto load_o = [&](float (&v)[NQ]) {
+            if constexpr (kF8) tmem_ld_sum2<NQ>(o_col, v);
+            else tmem_ld_cols<NQ>(o_col, v);
         };
         int j = 0, xs = 0, mu = 0;   // tile, exchange and own unit number
         Ring vring;
@@ -481,12 +530,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int32_t last_lo = a.causal ? t_lo : s.L - 1, last_hi = a.causal ? t_hi : s.L - 1;
             const int32_t first_lo = a.window > 0 ? t_lo - a.window + 1 : INT32_MIN;
             const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
-            float o[NQ], lsum[NQ], mrun[NQ], cs[NQ];
+            // A row's weights are 2^(s - ref): ref is set at the first tile in which the row sees a key (bit n of
+            // `have`) and moved when a weight passes 2^kPMax.
+            float lsum[NQ], ref[NQ], cs[NQ];
+            uint32_t have = 0u;
+            const uint32_t every = (1u << rows) - 1u;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                o[n] = 0.f;
                 lsum[n] = 0.f;
-                mrun[n] = -INFINITY;
+                ref[n] = 0.f;
                 cs[n] = a.scale_log2;
             }
             if constexpr (kF8) {
@@ -517,8 +569,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_after();
                 float sv[NQ];
-                if constexpr (kF8) tmem_ld_sum2<NQ>(tmem + lane_base + 32u * wg, sv);
-                else tmem_ld_cols<NQ>(tmem + lane_base + 32u * wg, sv);
+                tmem_ld_cols<NQ>(s_col, sv);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_sfree(wg));   // S tile may be overwritten (by tile j + 2's)
@@ -528,26 +579,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool any = in && p <= last_hi && (p >= first_lo || sink);
                 const bool all = in && p <= last_lo && (p >= first_hi || sink);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) sv[n] = kF8 ? fmaf(sv[n], cs[n] * ks, lv) : sv[n] * cs[n];
-                const bool tile_all = __all_sync(0xffffffffu, all);
-                const int vslot = vring.slot;
-                if (!tile_all) {
-                    // rows that see a position, one by one
-                    if (!all) {
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            const int32_t t = s.L - a.q_len + (i0 + min(n, rows - 1)) / a.G;
-                            const bool see = any && p <= (a.causal ? t : s.L - 1) &&
-                                             (a.window == 0 || p > t - a.window || sink);
-                            if (!see) sv[n] = -INFINITY;
-                        }
-                    }
-                    // V rows that must not reach P V (the tile has to be there)
-                    if (!mbar_wait_warp(bar_vfull(vslot), vring.phase, abort_flag)) {
+                for (int n = 0; n < NQ; ++n) sv[n] = kF8 ? fmaf(sv[n], cs[n] * ks, lv - ref[n]) : fmaf(sv[n], cs[n], -ref[n]);
+                if (!__all_sync(0xffffffffu, all)) {
+                    // V rows that must not reach P V (the tile has to be there).  The P V of the warpgroup's last tile
+                    // first: behind it the slot's tile before this one has been consumed, so that the parity below
+                    // cannot be answered by a phase before that.
+                    const int vslot = vring.slot;
+                    if ((j >= 2 && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) ||
+                        !mbar_wait_warp(bar_vfull(vslot), vring.phase, abort_flag)) {
                         ok = false;
                         break;
                     }
                     if (!all) {
+                        // rows that see a position, one by one: row n's token is at position t
+                        int32_t t = t_lo, h = i0 % a.G;
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const bool see = any && p <= (a.causal ? t : s.L - 1) &&
+                                             (a.window == 0 || p > t - a.window || sink);
+                            if (!see) sv[n] = -INFINITY;
+                            if (++h == a.G) {
+                                h = 0;
+                                ++t;
+                            }
+                        }
                         uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
                         constexpr int kParts = kF8 ? 1 : 2;
                         bool clear = !any;
@@ -561,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) {
-                                        if constexpr (kF8) clear |= (__vcmpeq4(ws[i] & 0x7f7f7f7fu, 0x7f7f7f7fu)) != 0u;
+                                        if constexpr (kF8) clear |= __vcmpeq4(ws[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
                                         else clear |= (ws[i] & 0x7f80u) == 0x7f80u || (ws[i] & 0x7f800000u) == 0x7f800000u;
                                     }
                                 }
@@ -579,64 +634,112 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
-                // tile max per query row across the warpgroup's 128 threads
-                const float wmax = warp_reduce_rows<true, NQ>(sv, lane);
-                float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + (wg * 2 + (int)par) * (kN * 4);
-                if (red_writer) rm[red_row * 4 + wq] = wmax;
-                if (!group_sync()) {
+                // Does a reference have to be set or moved?  The warpgroup's warps agree on it.
+                bool move = (have & every) != every;
+                if (!move) {
+                    float top = fmaxf(sv[0], sv[1]);
+#pragma unroll
+                    for (int n = 2; n < NQ; n += 2) top = max3(top, sv[n], sv[n + 1]);
+                    const bool up = __any_sync(0xffffffffu, top > kPMax);
+                    uint32_t *flags = reinterpret_cast<uint32_t *>(smem + C::kOffFlag) + (wg * 2 + (int)par) * 4;
+                    if (lane == 0) flags[wq] = up;
+                    if (!group_sync()) {
+                        ok = false;
+                        break;
+                    }
+                    const uint4 f = *reinterpret_cast<const uint4 *>(flags);
+                    move = (f.x | f.y | f.z | f.w) != 0u;
+                }
+                if (move) {
+                    float top[NQ];
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) top[n] = redux_max(sv[n]);
+                    // (the last reading of these maxima lies behind a barrier below)
+                    if (lane == 0) {
+#pragma unroll
+                        for (int n = 0; n < NQ; n += 4)
+                            *reinterpret_cast<float4 *>(rm + wq * kN + n) = make_float4(top[n], top[n + 1], top[n + 2], top[n + 3]);
+                    }
+                    if (!group_sync()) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) top[n] = fmaxf(max3(rm[n], rm[kN + n], rm[2 * kN + n]), rm[3 * kN + n]);
+                    const bool first = jt < 2;   // nothing in O yet
+                    // the last P V into O, and the readers of the maxima
+                    if ((!first && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) || !group_sync()) {
+                        ok = false;
+                        break;
+                    }
+                    float corr[NQ];
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const bool had = (have >> n) & 1u;
+                        const bool to = had ? top[n] > kPMax : top[n] > -INFINITY;
+                        const float by = to ? top[n] - kPExp<kF8> : 0.f;
+                        corr[n] = had ? fast_exp2(-by) : 1.f;
+                        ref[n] += by;
+                        sv[n] -= by;
+                        lsum[n] *= corr[n];
+                        have |= to ? 1u << n : 0u;
+                    }
+                    if (!first) {
+                        tc_fence_after();
+                        float o[NQ];
+#pragma unroll
+                        for (int h = 0; h < (kF8 ? 2 : 1); ++h) {
+                            tmem_ld_cols<NQ>(o_col + 16u * h, o);
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) o[n] *= corr[n];
+                            tmem_st_cols<NQ>(o_col + 16u * h, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // P, once the last P V has read its buffer
+                if (j >= 2 && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
-                float corr[NQ];
-                auto weight = [&](int n) -> float {
-                    const float4 t4 = *reinterpret_cast<const float4 *>(rm + n * 4);
-                    const float mn = fmaxf(mrun[n], fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)));
-                    corr[n] = mn == -INFINITY ? 1.f : fast_exp2(mrun[n] - mn);
-                    mrun[n] = mn;
-                    return sv[n] == -INFINITY ? 0.f : fast_exp2(sv[n] - mn);
-                };
                 if constexpr (kF8) {
-                    // p' 2^8 = hi + lo, two E4M3 codes a weight (absolute error at most 2^-10)
+                    uint32_t hi[NQ / 4], lo[NQ / 4];
+#pragma unroll
+                    for (int n = 0; n < NQ; n += 4) {
+                        float w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            w[i] = fast_exp2(sv[n + i]);
+                            lsum[n + i] = fmaf(w[i], rv, lsum[n + i]);
+                        }
+                        uint32_t h0, h1, l0, l1;
+                        split2(w[0], w[1], h0, l0);
+                        split2(w[2], w[3], h1, l1);
+                        hi[n / 4] = __byte_perm(h0, h1, 0x5410);
+                        lo[n / 4] = __byte_perm(l0, l1, 0x5410);
+                    }
+                    put_words(p_hi, hi);
+                    put_words(p_lo, lo);
+                } else {
+                    uint32_t w[NQ / 2];
 #pragma unroll
                     for (int n = 0; n < NQ; n += 2) {
-                        const float p0 = weight(n), p1 = weight(n + 1);
-                        lsum[n] = fmaf(lsum[n], corr[n], p0 * rv);
-                        lsum[n + 1] = fmaf(lsum[n + 1], corr[n + 1], p1 * rv);
-                        const float2 x2 = make_float2(p0 * (float)(1 << kPExp), p1 * (float)(1 << kPExp));
-                        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(x2, __NV_SATFINITE, __NV_E4M3);
-                        const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
-                        const __nv_fp8x2_storage_t lo =
-                            __nv_cvt_float2_to_fp8x2(make_float2(x2.x - hf.x, x2.y - hf.y), __NV_SATFINITE, __NV_E4M3);
-                        uint8_t *d0 = p_dst + n * 128 + ((p_chunk ^ (n & 7)) << 4);
-                        uint8_t *d1 = p_dst + (n + 1) * 128 + ((p_chunk ^ ((n + 1) & 7)) << 4);
-                        d0[0] = (uint8_t)(hi & 0xFF);
-                        d1[0] = (uint8_t)(hi >> 8);
-                        d0[kN * 128] = (uint8_t)(lo & 0xFF);
-                        d1[kN * 128] = (uint8_t)(lo >> 8);
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(fast_exp2(sv[n]), fast_exp2(sv[n + 1]));
+                        w[n / 2] = *reinterpret_cast<const uint32_t *>(&b2);
+                        lsum[n] += __uint_as_float(w[n / 2] << 16);
+                        lsum[n + 1] += __uint_as_float(w[n / 2] & 0xffff0000u);
                     }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const __nv_bfloat16 pb = __float2bfloat16_rn(weight(n));
-                        lsum[n] = fmaf(lsum[n], corr[n], __bfloat162float(pb));
-                        *reinterpret_cast<__nv_bfloat16 *>(p_dst + n * 128 + ((p_chunk ^ (n & 7)) << 4)) = pb;
+                    if constexpr (NQ == 16) {
+                        put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(w[0]));
+                        put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(w[4]));
+                    } else {
+                        put_words(p_hi, w);
                     }
                 }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_pfull(wg));
-                // this tile's P V (the other warpgroup works meanwhile)
-                if (!mbar_wait_warp(bar_ofull(wg), par, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                float ot[NQ];
-                if constexpr (kF8) tmem_ld_sum2<NQ>(tmem + lane_base + 64u + 32u * wg, ot);
-                else tmem_ld_cols<NQ>(tmem + lane_base + 64u + 32u * wg, ot);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) o[n] = fmaf(o[n], corr[n], ot[n]);
             }
             if (!ok) break;
             // row sums across the warpgroup, in two buffers in turn: one is written again behind the next unit's
@@ -645,11 +748,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++mu;
             const float wsum = warp_reduce_rows<false, NQ>(lsum, lane);
             if (red_writer) sums[red_row * 4 + wq] = wsum;
-            if (!group_sync()) break;
+            // the warpgroup's last tile here is j - 1 or j - 2
+            const int last = (j - 1 - wg) >> 1;
+            if (!group_sync() || !mbar_wait_warp(bar_ofull(wg), (uint32_t)last & 1u, abort_flag)) break;
+            tc_fence_after();
+            float o[NQ];
+            load_o(o);
             auto total = [&](int n) {
                 const float4 t4 = *reinterpret_cast<const float4 *>(sums + n * 4);
                 return (t4.x + t4.y) + (t4.z + t4.w);
             };
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+                if (!((have >> n) & 1u)) ref[n] = -INFINITY;   // no key, or none whose score is a number
             // The second warpgroup hands its part to the first, through tensor memory.  Exchange e + 1 is written
             // behind a P V of the second that follows one of the first's later tiles, so at most two are not yet read
             // when a third is written: four sets are enough.
@@ -662,7 +773,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_st_cols<NQ>(x_col, o);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    if (row == n) xm[n] = make_float2(mrun[n], total(n));
+                    if (row == n) xm[n] = make_float2(ref[n], total(n));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -680,26 +791,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     const float2 ml = xm[n];
-                    const float mn = fmaxf(mrun[n], ml.x);
-                    const float f0 = mn == -INFINITY ? 1.f : fast_exp2(mrun[n] - mn);
+                    const float mn = fmaxf(ref[n], ml.x);
+                    const float f0 = mn == -INFINITY ? 1.f : fast_exp2(ref[n] - mn);
                     const float f1 = mn == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
                     o[n] = o[n] * f0 + o1[n] * f1;
                     l[n] = l[n] * f0 + ml.y * f1;
-                    mrun[n] = mn;
+                    ref[n] = mn;
                 }
             }
             if (x.whole) {
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    if (n < rows) out[out_row(x.r, n) + row] = __float2bfloat16_rn(o[n] * kOutScale * inverse(l[n]));
+                    if (n < rows) out[out_row(x.r, n) + row] = __float2bfloat16_rn(o[n] * inverse(l[n]));
             } else {
                 const int64_t at = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     if (n >= rows) break;
-                    a.ws_o[(at + n) * kD + row] = o[n] * kOutScale;
-                    if (row == n) *reinterpret_cast<float2 *>(a.ws_ml + (at + n) * 2) = make_float2(mrun[n], l[n]);
+                    a.ws_o[(at + n) * kD + row] = o[n];
+                    if (row == n) *reinterpret_cast<float2 *>(a.ws_ml + (at + n) * 2) = make_float2(ref[n], l[n]);
                 }
             }
         }

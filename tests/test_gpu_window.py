@@ -13,6 +13,7 @@ from _parity import check_attention
 from _spec import cast
 from _window import Blocks, attend, build_step, write_blocks
 from paged_kv_cache_slot_gb300 import bkv
+from paged_kv_cache_slot_gb300 import workloads as wl
 
 pytestmark = pytest.mark.gpu
 
@@ -177,6 +178,49 @@ def test_many_short_requests_have_the_same_bits_in_every_run(fp8, d):
         c.out.fill_(3.0)
         c.run()
         assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("t,bs", [(4, 16), (1, 16), (4, 64)])
+def test_long_and_one_tile_requests_in_turn(fp8, t, bs):
+    """Units of one tile before, between and behind units of many, whose tiles are then at different stages in the two
+    softmax streams: every request's rows, and the same bits in every run."""
+    rng = np.random.default_rng(t)
+    lens = np.where(rng.random(160) < 0.5, rng.integers(t, 100, 160), rng.integers(600, 2600, 160))
+    p = Blocks(lens, t, 32, 8, 128, bs, fp8=fp8, seed=t, window=2048, sinks=4)
+    c = _check(p, rows=rng.permutation(160)[:60])
+    first = c.out.clone()
+    for _ in range(10):
+        c.out.fill_(3.0)
+        c.run()
+        assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rising", [True, False])
+def test_scores_that_rise_or_fall_along_the_cache(fp8, rising):
+    """Scores from -60 to 60 in base e along a request, so that the softmax's reference moves again and again, or never
+    behind the first tile."""
+    p = Blocks([1500, 900, 130], 2, 8, 2, 128, 16, fp8=fp8)
+    for r in range(3):
+        L = int(p.lens[r])
+        u = np.zeros(128, np.float32)
+        u[:8] = 1.0
+        p.q[r] = cast(np.broadcast_to(u, p.q[r].shape).copy(), "bf16")
+        along = np.linspace(-1, 1, L) * (1 if rising else -1) * 60 * 128 ** 0.5 / 8
+        for pos in range(L):
+            b, i = p.table[r, pos // 16], pos % 16
+            row = np.zeros((2, 128), np.float32)
+            row[:, :8] = along[pos]
+            if fp8:
+                if i == 0:
+                    p.ks[b] = 0.25
+                p.k[b, i] = oracle.e4m3_encode(row / np.float32(0.25))
+                p.keys[r][pos] = oracle.e4m3_decode(p.k[b, i]) * 0.25
+            else:
+                p.k[b, i] = cast(row, "bf16")
+                p.keys[r][pos] = wl.to_f32(p.k[b, i])
+    _check(p)
 
 
 @pytest.mark.parametrize("fp8,d", [(False, 128), (True, 128), (False, 64), (True, 64)])
