@@ -91,7 +91,8 @@ struct TcCfg {
     static constexpr int kOffSums = kOffAbort + 4;                    // a word a warp: prefix sum's scratch
     static constexpr int kOffPre = (kOffSums + kTcThreads / 32 * 4 + 15) / 16 * 16;
     static constexpr int kOffLens = kOffPre + (kMaxReqs + 4) * 4;
-    static constexpr int kSmem = kOffLens + kMaxReqs * 4 + 1024;      // slack for 1024 alignment
+    static constexpr int kOffRow = kOffLens + kMaxReqs * 4;           // [16] where a group's rows stand in their request
+    static constexpr int kSmem = kOffRow + kN * 4 + 1024;             // slack for 1024 alignment
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
     static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
     static_assert(kStages + 2 < kRing, "a ring word is rewritten behind its readers");
@@ -129,7 +130,7 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
-// Two weights (at most 256) as E4M3 codes hi, hi' and the remainders' lo, lo', in half precision: x to 11 bits, hi to 4
+// Two numbers of at most 256 as E4M3 codes hi, hi' and the remainders' lo, lo', in half precision: x to 11 bits, hi to 4
 // of them, lo to 4 of the rest.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x0, x1);
@@ -234,6 +235,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    int32_t *row_at = reinterpret_cast<int32_t *>(smem + C::kOffRow);
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + kN) {
+        const int i = i0 + min((int)threadIdx.x - 64, rows - 1), t = i / a.G;
+        row_at[threadIdx.x - 64] = (t * a.H_q + g * a.G + (i - t * a.G)) * kD;
+    }
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
@@ -247,62 +253,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int seg_shift = 31 - __clz(seg_rows);
     Units units(pre, a.num_reqs, q, a.P);
     Unit x;
-    auto out_row = [&](int r, int n) {
-        const int t = (i0 + n) / a.G;
-        return (((int64_t)r * a.q_len + t) * a.H_q + g * a.G + (i0 + n - t * a.G)) * kD;
-    };
+    const int64_t req_elems = (int64_t)a.q_len * a.H_q * kD;   // of q and out
 
     if (warp == 0 || warp == kWarpV) {
         // ================= TMA producers =================
         const bool is_v = warp == kWarpV;
         const bool count = !is_v && grp == 0 && a.err;   // bad entries count once a KV head
-        // ---- queries (warp 2): unit us's rows, four elements a lane ----
-        uint2 raw[kN];
-        auto load_q = [&](int r) {
+        // ---- queries (warp 2): unit us's rows, eight elements a lane, two rows at a time ----
+        constexpr int kPairs = (NQ + 1) / 2;
+        uint4 raw[kPairs];
+        int32_t raw_at[kPairs];   // where this lane's eight elements stand in their request
+        const int half = lane >> 4, col = lane & 15;
+        if (is_v) {
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
-                raw[n] = n < rows ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + out_row(r, n)) + lane)
-                                  : make_uint2(0, 0);
+            for (int i = 0; i < kPairs; ++i) raw_at[i] = row_at[2 * i + half] + 8 * col;
+        }
+        auto load_q = [&](int r) {
+            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + r * req_elems;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                if (2 * i < rows) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + raw_at[i]));
         };
         auto put_q = [&](int us) -> bool {
             const int b = us & 1;
             if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((us >> 1) & 1) ^ 1u, abort_flag)) return false;
             uint8_t *dst = smem + C::kOffQ + b * C::kQBytes;
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                if (n >= rows) break;
+            for (int i = 0; i < kPairs; ++i) {
+                if (2 * i >= rows) break;
+                const int n = 2 * i + half;   // (an odd group's last row is written twice, to rows n and n + 1 < 16)
+                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                 if constexpr (kF8) {
                     // scaled by 2^-e, e = floor(log2 max) - 7, then x = hi + lo in E4M3: x has at most 8 significant
                     // bits, so the remainder is exact where |x| >= 2^-2 and within 2^-10 (2^-17 of the largest) below
-                    const float2 x01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[n].x));
-                    const float2 x23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&raw[n].y));
-                    // the largest as bits: NaN and infinity come out above every number
-                    uint32_t top = max(max(__float_as_uint(x01.x) & 0x7fffffffu, __float_as_uint(x01.y) & 0x7fffffffu),
-                                       max(__float_as_uint(x23.x) & 0x7fffffffu, __float_as_uint(x23.y) & 0x7fffffffu));
-                    top = __reduce_max_sync(0xffffffffu, top);
+                    uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                             __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
+                    // the largest as fp32 bits: NaN and infinity come out above every number
+                    const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
                     // (a row whose largest is subnormal is left as it is: its scores are 0 to fp32's own rounding)
-                    const int e = top >= 0x00800000u && top < 0x7f800000u ? min(max((int)(top >> 23) - 127 - 7, -126), 126) : 0;
+                    const int e = top >= 0x00800000u && top < 0x7f800000u ? max((int)(top >> 23) - 127 - 7, -126) : 0;
                     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    const float2 s01 = make_float2(x01.x * down, x01.y * down), s23 = make_float2(x23.x * down, x23.y * down);
-                    const __nv_fp8x2_storage_t h01 = __nv_cvt_float2_to_fp8x2(s01, __NV_SATFINITE, __NV_E4M3);
-                    const __nv_fp8x2_storage_t h23 = __nv_cvt_float2_to_fp8x2(s23, __NV_SATFINITE, __NV_E4M3);
-                    const float2 f01 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h01, __NV_E4M3)));
-                    const float2 f23 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h23, __NV_E4M3)));
-                    const __nv_fp8x2_storage_t l01 =
-                        __nv_cvt_float2_to_fp8x2(make_float2(s01.x - f01.x, s01.y - f01.y), __NV_SATFINITE, __NV_E4M3);
-                    const __nv_fp8x2_storage_t l23 =
-                        __nv_cvt_float2_to_fp8x2(make_float2(s23.x - f23.x, s23.y - f23.y), __NV_SATFINITE, __NV_E4M3);
-                    uint8_t *at = dst + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t *>(at) = (uint32_t)h01 | ((uint32_t)h23 << 16);
-                    *reinterpret_cast<uint32_t *>(at + kN * 128) = (uint32_t)l01 | ((uint32_t)l23 << 16);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t h0, h1, l0, l1;
+                        split2(__uint_as_float(w[2 * k] << 16) * down, __uint_as_float(w[2 * k] & 0xffff0000u) * down, h0, l0);
+                        split2(__uint_as_float(w[2 * k + 1] << 16) * down, __uint_as_float(w[2 * k + 1] & 0xffff0000u) * down,
+                               h1, l1);
+                        hi[k] = __byte_perm(h0, h1, 0x5410);
+                        lo[k] = __byte_perm(l0, l1, 0x5410);
+                    }
+                    uint8_t *at = dst + n * 128 + (((col >> 1) ^ (n & 7)) << 4) + (col & 1) * 8;
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(at + kN * 128) = make_uint2(lo[0], lo[1]);
                     // a row that is not finite makes its scores NaN
-                    if (lane == 0)
+                    if (col == 0)
                         qs[(us & (kSets - 1)) * kN + n] = top < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
                                                                             : __uint_as_float(0x7fffffffu);
                 } else {
                     // 64 elements a half; 16-byte chunk c of row n at c ^ (n & 7)
-                    uint8_t *at = dst + (lane >> 4) * (kN * 128) + n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
-                    *reinterpret_cast<uint2 *>(at) = raw[n];
+                    *reinterpret_cast<uint4 *>(dst + (col >> 3) * (kN * 128) + n * 128 + (((col & 7) ^ (n & 7)) << 4)) = raw[i];
                 }
             }
             fence_proxy_async();
@@ -313,29 +325,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             return true;
         };
-        // A chunk is 32 segments of a unit, a lane each: the cache row that its segment begins at (-1: nothing to
-        // load) and its block.  The next one's entries are loaded while this one's tiles are issued.
+        // A chunk is 32 segments of a unit, a lane each.  The next one's block entries are loaded while this one's tiles
+        // are issued: nothing looks at an entry before its chunk's turn.
         struct Chunk {
             int r, f, nt, c;   // the unit; the chunk's number in it
-            int32_t row, blk;
+            int32_t entry;     // the segment's block entry, as it is in the table; INT32_MAX: past its columns
+            int32_t off;       // the segment's first row in the block, and, in bit 31, that the block begins here in the
+                               // span; -1: no segment
         };
         const int tiles = 32 / nseg;   // tiles a chunk
         auto fetch = [&](Chunk &w) {
-            w.row = -1;
-            w.blk = 0;
+            w.entry = 0;
+            w.off = -1;
             const Span s = span_of(a, lens[w.r]);
             const int32_t seg = w.f * nseg + w.c * 32 + lane, v = seg << seg_shift;
             if (w.c * 32 + lane < w.nt * nseg && v < s.len) {
                 const int32_t p = s.pos(v), lb = p / a.bs, off = p - lb * a.bs;
-                const int64_t e = lb < a.bt_cols ? __ldg(a.bt + (int64_t)w.r * a.bt_stride + lb) : a.total_blocks;
-                if (e >= a.total_blocks) {
-                    // at the block's first segment in the span
-                    if (count && (off == 0 || (s.gap > 0 && v == s.sb && (s.sb == 0 || lb != (s.sb - 1) / a.bs))))
-                        atomicAdd(a.err, 1);
-                } else if (e > 0) {
-                    w.blk = (int32_t)e;
-                    w.row = (int32_t)(e * a.bs + off);
-                }
+                const bool begins = off == 0 || (s.gap > 0 && v == s.sb && (s.sb == 0 || lb != (s.sb - 1) / a.bs));
+                w.off = off | (begins ? INT32_MIN : 0);
+                w.entry = lb < a.bt_cols ? __ldg(a.bt + (int64_t)w.r * a.bt_stride + lb) : INT32_MAX;
             }
         };
         auto next = [&](const Chunk &w, Chunk &n) -> bool {
@@ -359,21 +367,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int r = q; r < a.num_reqs; r += a.P)
                 if (pre[r + 1] == pre[r])
                     for (int n = 0; n < rows; ++n)
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row(r, n) + 4 * lane) = make_uint2(0, 0);
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + r * req_elems + row_at[n] + 4 * lane) =
+                            make_uint2(0, 0);
         }
-        Chunk cur{0, 0, 0, 0, -1, 0}, nxt;
+        Chunk cur{0, 0, 0, 0, 0, -1}, nxt;
         bool have = next(cur, cur);
         Ring ring;
         int j = 0, us = 0;
         while (have && !*abort_flag) {
             if (is_v && cur.c == 0 && !put_q(us++)) break;   // (its registers go to the next unit's below)
+            // the cache row that this lane's segment begins at (-1: nothing to load) and its block
+            int32_t seg_row = -1, seg_blk = 0;
+            if (cur.off != -1) {
+                if (cur.entry >= a.total_blocks) {
+                    if (count && cur.off < 0) atomicAdd(a.err, 1);   // at the block's first segment in the span
+                } else if (cur.entry > 0) {
+                    seg_blk = cur.entry;
+                    seg_row = cur.entry * a.bs + (cur.off & INT32_MAX);
+                }
+            }
             const bool more = next(cur, nxt);
             const int nt = min(tiles, cur.nt - cur.c * tiles);
             for (int kt = 0; kt < nt; ++kt, ++j, ring.advance(kStages)) {
                 const int s = ring.slot;
                 const uint32_t bar_f = is_v ? bar_vfull(s) : bar_kfull(s);
-                const int32_t row = __shfl_sync(0xffffffffu, cur.row, (kt * nseg + lane) & 31);
-                const int32_t blk = __shfl_sync(0xffffffffu, cur.blk, (kt * nseg + lane) & 31);
+                const int32_t row = __shfl_sync(0xffffffffu, seg_row, (kt * nseg + lane) & 31);
+                const int32_t blk = __shfl_sync(0xffffffffu, seg_blk, (kt * nseg + lane) & 31);
                 const bool load = lane < nseg && row >= 0;
                 const uint32_t ballot = __ballot_sync(0xffffffffu, load);
                 if (!mbar_wait_warp(is_v ? bar_vempty(s) : bar_kempty(s), ring.phase ^ 1u, abort_flag)) break;
@@ -513,6 +532,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if constexpr (kF8) tmem_ld_sum2<NQ>(o_col, v);
             else tmem_ld_cols<NQ>(o_col, v);
         };
+        const int tok_lo = i0 / a.G, tok_hi = (i0 + rows - 1) / a.G, head0 = i0 % a.G;
         int j = 0, xs = 0, mu = 0;   // tile, exchange and own unit number
         Ring vring;
         bool ok = true;
@@ -526,7 +546,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Span s = span_of(a, lens[x.r]);
             // Positions at or below last_lo (and from first_hi on, or below `sinks`) are seen by every row of the
             // group, those past last_hi (or before first_lo) by none.
-            const int32_t t_lo = s.L - a.q_len + i0 / a.G, t_hi = s.L - a.q_len + (i0 + rows - 1) / a.G;
+            const int32_t t_lo = s.L - a.q_len + tok_lo, t_hi = s.L - a.q_len + tok_hi;
             const int32_t last_lo = a.causal ? t_lo : s.L - 1, last_hi = a.causal ? t_hi : s.L - 1;
             const int32_t first_lo = a.window > 0 ? t_lo - a.window + 1 : INT32_MIN;
             const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
@@ -592,7 +612,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     if (!all) {
                         // rows that see a position, one by one: row n's token is at position t
-                        int32_t t = t_lo, h = i0 % a.G;
+                        int32_t t = t_lo, h = head0;
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
                             const bool see = any && p <= (a.causal ? t : s.L - 1) &&
@@ -800,10 +820,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (x.whole) {
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + x.r * req_elems + row;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    if (n < rows) out[out_row(x.r, n) + row] = __float2bfloat16_rn(o[n] * inverse(l[n]));
+                    if (n < rows) out[row_at[n]] = __float2bfloat16_rn(o[n] * inverse(l[n]));
             } else {
                 const int64_t at = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR;
 #pragma unroll
