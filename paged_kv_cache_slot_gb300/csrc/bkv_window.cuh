@@ -25,7 +25,7 @@ struct Args {
     float scale_log2;         // softmax_scale * log2(e): scores are kept in base 2
     int32_t causal;
     int32_t window, sinks;    // window 0: none
-    int32_t seg;              // positions that are read together (see Span)
+    int32_t seg;              // positions that are read together, a power of two (see Span)
     int32_t tile;             // span positions a tile
     int32_t NR, groups;       // query rows a group, groups a KV head
     int32_t P;                // columns: each takes its share of the cost of all requests
@@ -54,12 +54,12 @@ __host__ __device__ inline Span span_of(const Args &a, int32_t ctx) {
     if (a.window > 0) {
         const int64_t lo = (int64_t)s.L - a.q_len - a.window + 1;   // first position in the first token's window
         if (lo > 0) {
-            const int32_t w = (int32_t)(lo / a.seg) * a.seg;
+            const int32_t w = (int32_t)lo & -a.seg;
             const int32_t keep = a.sinks < s.L ? a.sinks : s.L;
-            const int64_t sb = ((int64_t)keep + a.seg - 1) / a.seg * a.seg;
+            const int32_t sb = (keep + a.seg - 1) & -a.seg;
             if (sb < w) {
-                s.sb = (int32_t)sb;
-                s.gap = w - s.sb;
+                s.sb = sb;
+                s.gap = w - sb;
             }
         }
     }
@@ -176,7 +176,7 @@ __device__ __forceinline__ void lay_out(const Args &a, int32_t *pre, int32_t *le
 
 // The reciprocal that turns a row's sums into its output: a row that saw no
 // key is 0, one whose sum is NaN stays NaN.
-__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
 
 // Scales of values that the writes make; others are held to this range.
 constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;   // 2^-40, 2^40

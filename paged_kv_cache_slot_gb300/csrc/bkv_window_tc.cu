@@ -77,7 +77,7 @@ struct TcCfg {
     static constexpr int kOffQ = 2 * kStages * kSlot;
     static constexpr int kPBytes = kTcTile * 32;                      // a position's weights: 16 bf16, or 16 + 16 E4M3 parts
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
-    static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][4 warps][16] floats
+    static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][16][4 warps] floats
     static constexpr int kOffFlag = kOffMax + 2 * 4 * kN * 4;         // [warpgroup][2][4 warps] words
     static constexpr int kOffSum = kOffFlag + 2 * 2 * 4 * 4;          // [warpgroup][2][16][4] floats
     static constexpr int kOffXm = kOffSum + 4 * kN * 4 * 4;           // [set][16] (max, sum)
@@ -119,11 +119,6 @@ __device__ __forceinline__ uint64_t sdesc32(uint32_t saddr) {
            (uint64_t)6 << 61;
 }
 
-__device__ __forceinline__ float redux_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -266,7 +261,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int half = lane >> 4, col = lane & 15;
         if (is_v) {
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) raw_at[i] = row_at[2 * i + half] + 8 * col;
+            for (int i = 0; i < kPairs; ++i) {
+                raw_at[i] = row_at[2 * i + half] + 8 * col;
+                raw[i] = make_uint4(0, 0, 0, 0);
+            }
         }
         auto load_q = [&](int r) {
             const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + r * req_elems;
@@ -278,22 +276,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int b = us & 1;
             if (!mbar_wait_warp(bar_qempty(b), (uint32_t)((us >> 1) & 1) ^ 1u, abort_flag)) return false;
             uint8_t *dst = smem + C::kOffQ + b * C::kQBytes;
+            if constexpr (kF8) {
+                // A row is scaled by 2^-e, e = floor(log2 max) - 7, then x = hi + lo in E4M3: x has at most 8 significant
+                // bits, so the remainder is exact where |x| >= 2^-2 and within 2^-10 (2^-17 of the largest) below.
+                // (All pairs of rows side by side: one after the other is a chain of 700 cycles each.)
+                uint32_t top[kPairs];
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                if (2 * i >= rows) break;
-                const int n = 2 * i + half;   // (an odd group's last row is written twice, to rows n and n + 1 < 16)
-                const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                if constexpr (kF8) {
-                    // scaled by 2^-e, e = floor(log2 max) - 7, then x = hi + lo in E4M3: x has at most 8 significant
-                    // bits, so the remainder is exact where |x| >= 2^-2 and within 2^-10 (2^-17 of the largest) below
-                    uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                             __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                for (int i = 0; i < kPairs; ++i)
+                    top[i] = __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                      __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int n = 2 * i + half;   // (an odd group's last row is written twice, to rows n and n + 1 < 16)
+                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                     // the largest as fp32 bits: NaN and infinity come out above every number
-                    const uint32_t top = max(top2 & 0xffffu, top2 >> 16) << 16;
+                    const uint32_t t = max(top[i] & 0xffffu, top[i] >> 16) << 16;
                     // (a row whose largest is subnormal is left as it is: its scores are 0 to fp32's own rounding)
-                    const int e = top >= 0x00800000u && top < 0x7f800000u ? max((int)(top >> 23) - 127 - 7, -126) : 0;
+                    const int e = t >= 0x00800000u && t < 0x7f800000u ? max((int)(t >> 23) - 127 - 7, -126) : 0;
                     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
                     uint32_t hi[2], lo[2];
 #pragma unroll
@@ -310,10 +313,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     *reinterpret_cast<uint2 *>(at + kN * 128) = make_uint2(lo[0], lo[1]);
                     // a row that is not finite makes its scores NaN
                     if (col == 0)
-                        qs[(us & (kSets - 1)) * kN + n] = top < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
-                                                                            : __uint_as_float(0x7fffffffu);
-                } else {
-                    // 64 elements a half; 16-byte chunk c of row n at c ^ (n & 7)
+                        qs[(us & (kSets - 1)) * kN + n] = t < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
+                                                                          : __uint_as_float(0x7fffffffu);
+                }
+            } else {
+                // 64 elements a half; 16-byte chunk c of row n at c ^ (n & 7)
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int n = 2 * i + half;
                     *reinterpret_cast<uint4 *>(dst + (col >> 3) * (kN * 128) + n * 128 + (((col & 7) ^ (n & 7)) << 4)) = raw[i];
                 }
             }
@@ -340,8 +347,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const Span s = span_of(a, lens[w.r]);
             const int32_t seg = w.f * nseg + w.c * 32 + lane, v = seg << seg_shift;
             if (w.c * 32 + lane < w.nt * nseg && v < s.len) {
-                const int32_t p = s.pos(v), lb = p / a.bs, off = p - lb * a.bs;
-                const bool begins = off == 0 || (s.gap > 0 && v == s.sb && (s.sb == 0 || lb != (s.sb - 1) / a.bs));
+                const int32_t p = s.pos(v);
+                // (a block is one segment, or, above 128 positions, several)
+                const int32_t lb = a.bs == seg_rows ? p >> seg_shift : p / a.bs, off = p - lb * a.bs;
+                const bool begins = off == 0 || (s.gap > 0 && v == s.sb && (s.sb == 0 || (s.sb - 1) / a.bs != lb));
                 w.off = off | (begins ? INT32_MIN : 0);
                 w.entry = lb < a.bt_cols ? __ldg(a.bt + (int64_t)w.r * a.bt_stride + lb) : INT32_MAX;
             }
@@ -600,57 +609,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool all = in && p <= last_lo && (p >= first_hi || sink);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) sv[n] = kF8 ? fmaf(sv[n], cs[n] * ks, lv - ref[n]) : fmaf(sv[n], cs[n], -ref[n]);
-                if (!__all_sync(0xffffffffu, all)) {
-                    // V rows that must not reach P V (the tile has to be there).  The P V of the warpgroup's last tile
-                    // first: behind it the slot's tile before this one has been consumed, so that the parity below
-                    // cannot be answered by a phase before that.
-                    const int vslot = vring.slot;
-                    if ((j >= 2 && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) ||
-                        !mbar_wait_warp(bar_vfull(vslot), vring.phase, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!all) {
-                        // rows that see a position, one by one: row n's token is at position t
-                        int32_t t = t_lo, h = head0;
+                const bool tile_all = __all_sync(0xffffffffu, all);
+                if (!tile_all && !all) {
+                    // rows that see a position, one by one: row n's token is at position t
+                    int32_t t = t_lo, h = head0;
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            const bool see = any && p <= (a.causal ? t : s.L - 1) &&
-                                             (a.window == 0 || p > t - a.window || sink);
-                            if (!see) sv[n] = -INFINITY;
-                            if (++h == a.G) {
-                                h = 0;
-                                ++t;
-                            }
-                        }
-                        uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
-                        constexpr int kParts = kF8 ? 1 : 2;
-                        bool clear = !any;
-                        if (any) {
-                            // seen by some rows and not by others: not finite?
-#pragma unroll
-                            for (int h = 0; h < kParts; ++h)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const uint4 w = vr[h * (kHalfBytes / 16) + ((c + lane) & 7)];
-                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        if constexpr (kF8) clear |= __vcmpeq4(ws[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
-                                        else clear |= (ws[i] & 0x7f80u) == 0x7f80u || (ws[i] & 0x7f800000u) == 0x7f800000u;
-                                    }
-                                }
-                            if (clear) {
-#pragma unroll
-                                for (int n = 0; n < NQ; ++n)
-                                    if (sv[n] != -INFINITY) lsum[n] = __uint_as_float(0x7fffffffu);
-                            }
-                        }
-                        if (clear) {
-#pragma unroll
-                            for (int h = 0; h < kParts; ++h)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c) vr[h * (kHalfBytes / 16) + ((c + lane) & 7)] = make_uint4(0, 0, 0, 0);
+                    for (int n = 0; n < NQ; ++n) {
+                        const bool see = any && p <= (a.causal ? t : s.L - 1) && (a.window == 0 || p > t - a.window || sink);
+                        if (!see) sv[n] = -INFINITY;
+                        if (++h == a.G) {
+                            h = 0;
+                            ++t;
                         }
                     }
                 }
@@ -671,21 +640,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     move = (f.x | f.y | f.z | f.w) != 0u;
                 }
                 if (move) {
-                    float top[NQ];
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) top[n] = redux_max(sv[n]);
                     // (the last reading of these maxima lies behind a barrier below)
-                    if (lane == 0) {
-#pragma unroll
-                        for (int n = 0; n < NQ; n += 4)
-                            *reinterpret_cast<float4 *>(rm + wq * kN + n) = make_float4(top[n], top[n + 1], top[n + 2], top[n + 3]);
-                    }
+                    const float wmax = warp_reduce_rows<true, NQ>(sv, lane);
+                    if (red_writer) rm[red_row * 4 + wq] = wmax;
                     if (!group_sync()) {
                         ok = false;
                         break;
                     }
+                    float top[NQ];
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) top[n] = fmaxf(max3(rm[n], rm[kN + n], rm[2 * kN + n]), rm[3 * kN + n]);
+                    for (int n = 0; n < NQ; ++n) {
+                        const float4 t4 = *reinterpret_cast<const float4 *>(rm + n * 4);
+                        top[n] = fmaxf(max3(t4.x, t4.y, t4.z), t4.w);
+                    }
                     const bool first = jt < 2;   // nothing in O yet
                     // the last P V into O, and the readers of the maxima
                     if ((!first && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) || !group_sync()) {
@@ -756,6 +723,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         put_words(p_hi, w);
                     }
                 }
+                if (!tile_all) {
+                    // V rows that must not reach P V, once the tile is there.  (Behind the wait for the warpgroup's last
+                    // P V, above: the slot's tile before this one has been consumed by then, so that the parity cannot be
+                    // answered by a phase before that.)
+                    const int vslot = vring.slot;
+                    if (!mbar_wait_warp(bar_vfull(vslot), vring.phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!all) {
+                        uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
+                        constexpr int kParts = kF8 ? 1 : 2;
+                        bool clear = !any;
+                        if (any) {
+                            // seen by some rows and not by others: not finite?
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 w = vr[h * (kHalfBytes / 16) + ((c + lane) & 7)];
+                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        if constexpr (kF8) clear |= __vcmpeq4(ws[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+                                        else clear |= (ws[i] & 0x7f80u) == 0x7f80u || (ws[i] & 0x7f800000u) == 0x7f800000u;
+                                    }
+                                }
+                            if (clear) {
+#pragma unroll
+                                for (int n = 0; n < NQ; ++n)
+                                    if (sv[n] != -INFINITY) lsum[n] = __uint_as_float(0x7fffffffu);
+                            }
+                        }
+                        if (clear) {
+#pragma unroll
+                            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) vr[h * (kHalfBytes / 16) + ((c + lane) & 7)] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
@@ -781,15 +789,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
                 if (!((have >> n) & 1u)) ref[n] = -INFINITY;   // no key, or none whose score is a number
-            // The second warpgroup hands its part to the first, through tensor memory.  Exchange e + 1 is written
-            // behind a P V of the second that follows one of the first's later tiles, so at most two are not yet read
-            // when a third is written: four sets are enough.
+            // The warpgroup of the unit's last tile finishes it; the other hands its part over through tensor memory and
+            // goes on.  A set is written again four exchanges on, behind a P V that follows one of the other's tiles of
+            // the exchange after this one, which it begins when it has read this.
+            const bool finish = ((j - 1) & 1) == wg;
             const int set = xs & (kSets - 1);
             const uint32_t x_col = tmem + lane_base + 128u + 16u * (uint32_t)set;
             float2 *xm = reinterpret_cast<float2 *>(smem + C::kOffXm) + set * kN;
             const uint32_t x_par = (uint32_t)(xs >> 2) & 1u;
             if (both) ++xs;
-            if (both && wg == 1) {
+            if (!finish) {
                 tmem_st_cols<NQ>(x_col, o);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
@@ -823,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + x.r * req_elems + row;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
-                    if (n < rows) out[row_at[n]] = __float2bfloat16_rn(o[n] * inverse(l[n]));
+                    if (n < rows) out[row_at[n]] = __float2bfloat16_rn(l[n] == 0.f ? 0.f : __fdividef(o[n], l[n]));
             } else {
                 const int64_t at = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR;
 #pragma unroll
