@@ -798,8 +798,9 @@ int bkv_build_step(const int32_t *cached_lens, const int32_t *new_lens, int32_t 
  *   of them is written), a block past the table's columns or the cache.  A null
  *   entry (<= 0) writes nothing.
  *   INVALID_ARG: negative or zero sizes, new_token_stride < num_kv_heads *
- *   head_dim, block_size or head_dim above 65536, null pointers.  UNSUPPORTED:
- *   src_dtype not BKV_BF16 / BKV_F32.
+ *   head_dim, block_size or head_dim above 65536, (num_tokens / block_size + 2
+ *   num_reqs) * num_kv_heads from 2^30 on, null pointers.  UNSUPPORTED: src_dtype
+ *   not BKV_BF16 / BKV_F32.
  */
 int bkv_cache_write_fp8_blocks(const void *k_new, const void *v_new, int64_t num_tokens, int64_t new_token_stride,
                                const int32_t *query_start_loc, const int32_t *context_lens, int32_t num_reqs,

@@ -14,15 +14,16 @@
 // the scale), makes both quotients exact, and an old code only loses bits that
 // leave the subnormal end.
 //
-// The work of one (touched block, KV head) is a group's: K and V rows are read
-// once into registers, their maxima reduced, and the codes written.  The blocks
-// a step touches are numbered floor(start_r / bs) + 2 r + j, j the request's
-// own count: the numbers of different requests never meet (a request of n
-// tokens touches at most n / bs + 2 blocks), gaps are skipped, and no scan over
-// the requests has to come first.
+// The work of one (touched block, KV head) is a group's: its K rows, then its V
+// rows, are read once into registers, their maximum reduced, and the codes
+// written; the next rows are loaded while these are worked on.  The blocks a step
+// touches are numbered floor(start_r / bs) + 2 r + j, j the request's own count:
+// the numbers of different requests never meet (a request of n tokens touches at
+// most n / bs + 2 blocks), gaps are skipped, and no scan over the requests has to
+// come first.
 //
-// Memory-bound for prompts (e + 1 bytes an element); a decode step is the
-// chain request -> table entry -> scale, with the row's loads beside it.
+// Memory-bound for prompts (e + 1 bytes an element); a decode step is the chain
+// request -> row, table entry -> scale -> store behind a launch.
 #include <math.h>
 
 #include "bkv_eight.cuh"
@@ -51,53 +52,59 @@ struct Args {
 };
 
 // Where the token rows of request r begin in the step, within [0, num_tokens].
-__device__ __forceinline__ int64_t start_of(const Args &a, int r) {
-    const int64_t t = __ldg(a.qsl + r);
-    return t < 0 ? 0 : (t > a.num_tokens ? a.num_tokens : t);
+__device__ __forceinline__ int32_t start_of(const Args &a, int r) {
+    return max(0, min(__ldg(a.qsl + r), (int32_t)a.num_tokens));
+}
+// The number of request r's first block.
+__device__ __forceinline__ int32_t number_of(const Args &a, int r) {
+    return (int32_t)((uint32_t)start_of(a, r) / (uint32_t)a.bs) + 2 * r;
 }
 
-// A touched block's rows: `cnt` tokens from `tok` on go to rows `first` on of
-// block `id`; cnt 0: nothing.
+// A touched block's rows: `cnt` tokens from `tok` on go to rows `first` on of the
+// block whose table entry is `entry` (INT32_MAX: past the table's columns); cnt
+// 0: nothing.
 struct Part {
-    int64_t id, tok;
-    int32_t first, cnt;
+    int32_t tok, first, cnt, entry;
 };
 
 // Block number u of the step, by one warp.  count: this warp counts errors.
-__device__ __forceinline__ Part part_of(const Args &a, int64_t u, bool count) {
+// Nothing here looks at the entry, so that its load and the rows' overlap.
+__device__ __forceinline__ Part part_of(const Args &a, int32_t u, bool count) {
     const int lane = threadIdx.x & 31;
     Part p{0, 0, 0, 0};
-    // the last request whose numbers begin at or before u: 32 probes a round
+    // the last request whose numbers begin at or before u: 32 probes a round, and 256 in the last
     int lo = 0, n = a.num_reqs;
-    while (n > 1) {
-        const int step = (int)(((int64_t)n + 31) / 32);
-        const bool in = (int64_t)lane * step < n && start_of(a, lo + lane * step) / a.bs + 2 * (int64_t)(lo + lane * step) <= u;
+    while (n > 256) {
+        const int step = (n + 31) / 32;
+        const bool in = lane * step < n && number_of(a, lo + lane * step) <= u;
         const uint32_t m = __ballot_sync(0xffffffffu, in);
         const int last = m ? 31 - __clz(m) : 0;
         lo += last * step;
         n = min(step, n - last * step);
     }
-    const int64_t t0 = start_of(a, lo), t1 = start_of(a, lo + 1);
-    const int64_t L = __ldg(a.ctx + lo);
-    const int64_t j = u - (t0 / a.bs + 2 * (int64_t)lo), start = L - (t1 - t0);
+    int32_t at[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at[i] = 32 * i + lane < n ? number_of(a, lo + 32 * i + lane) : INT32_MAX;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) before += __popc(__ballot_sync(0xffffffffu, at[i] <= u));
+    lo += max(before - 1, 0);
+    const int32_t t0 = start_of(a, lo), t1 = start_of(a, lo + 1);
+    const int32_t L = __ldg(a.ctx + lo);
+    const int32_t j = u - ((int32_t)((uint32_t)t0 / (uint32_t)a.bs) + 2 * lo);
     if (t1 <= t0 || j < 0) return p;
-    if (start < 0) {   // more new tokens than the request's length
+    if (L < t1 - t0) {   // more new tokens than the request's length
         if (count && j == 0 && lane == 0 && a.err) atomicAdd(a.err, 1);
         return p;
     }
-    const int64_t lb = start / a.bs + j;
-    const int64_t p0 = max(start, lb * a.bs), p1 = min(L, (lb + 1) * a.bs);
-    if (p0 >= p1) return p;
-    const int64_t id = lb < a.bt_cols ? __ldg(a.bt + (int64_t)lo * a.bt_stride + lb) : a.total_blocks;
-    if (id >= a.total_blocks) {
-        if (count && lane == 0 && a.err) atomicAdd(a.err, 1);
-        return p;
-    }
-    if (id <= 0) return p;
-    p.id = id;
+    const int32_t start = L - (t1 - t0), lb = (int32_t)((uint32_t)start / (uint32_t)a.bs) + j;
+    const int64_t b0 = (int64_t)lb * a.bs;
+    const int32_t p0 = (int32_t)max((int64_t)start, b0), p1 = (int32_t)min((int64_t)L, b0 + a.bs);
+    if (b0 >= L) return p;
+    p.entry = lb < a.bt_cols ? __ldg(a.bt + (int64_t)lo * a.bt_stride + lb) : INT32_MAX;
     p.tok = t0 + (p0 - start);
-    p.first = (int32_t)(p0 - lb * a.bs);
-    p.cnt = (int32_t)(p1 - p0);
+    p.first = (int32_t)(p0 - b0);
+    p.cnt = p1 - p0;
     return p;
 }
 
@@ -149,121 +156,157 @@ __device__ __forceinline__ void put_codes(uint8_t *dst, uint2 w, int n, bool vec
     }
 }
 
-// Groups of W warps, as many as fit into 128 threads a CTA; PT pieces of K and
-// of V a thread in registers.  Rows that do not fit are read again for their codes.
+// Groups of W warps, as many as fit into 128 threads a CTA; PT pieces a thread in
+// registers, twice: one set is loaded while the other is worked on.  Rows that do
+// not fit are read again for their codes.
 template <int W>
 constexpr int kThreadsOf = W < 4 ? 128 : 32 * W;
 
 template <typename T, int W, int PT>
-__global__ void __launch_bounds__(kThreadsOf<W>) write_blocks_kernel(const Args a, int64_t items) {
+__global__ void __launch_bounds__(kThreadsOf<W>, 512 / kThreadsOf<W>) write_blocks_kernel(const Args a, int32_t items) {
     constexpr int kGroups = kThreadsOf<W> / (32 * W);
     constexpr int kLanes = 32 * W;
-    __shared__ float red[2][kGroups][W][2];
+    __shared__ float red[2][kGroups][W];
     const int group = threadIdx.x / kLanes, gl = threadIdx.x % kLanes, gw = gl >> 5, lane = threadIdx.x & 31;
+    // this thread's first piece of a group's rows, and how far apart its pieces are
+    const int row0 = gl / a.pieces, col0 = gl - row0 * a.pieces, drow = kLanes / a.pieces, dcol = kLanes - drow * a.pieces;
+    auto each_piece = [&](int rows, int from, int to, auto &&f) {   // f(number, row, column) of pieces [from, to)
+        int row = row0 + from * drow, col = col0 + from * dcol;
+        row += col / a.pieces, col %= a.pieces;
+        for (int i = from; i < to && row < rows; ++i) {
+            f(i, row, col * 8);
+            row += drow, col += dcol;
+            if (col >= a.pieces) col -= a.pieces, ++row;
+        }
+    };
     pdl_wait();
     pdl_trigger();
     int turn = 0;
-    for (int64_t it = (int64_t)blockIdx.x * kGroups + group; it < items; it += (int64_t)gridDim.x * kGroups) {
-        const int64_t u = it / a.hkv;
-        const int h = (int)(it - u * a.hkv);
-        const Part p = part_of(a, u, h == 0 && gw == 0);
-        if (p.cnt == 0) continue;
-        const int np = p.cnt * a.pieces;
-        const T *src[2] = {static_cast<const T *>(a.k), static_cast<const T *>(a.v)};
-        uint8_t *dst[2] = {a.kc, a.vc};
-        float *scales[2] = {a.ks, a.vs};
-        const int64_t sc = p.id * a.hkv + h;
-        float old[2] = {0.f, 0.f};
-        if (p.first > 0) {
-            old[0] = a.ks[sc];
-            old[1] = a.vs[sc];
+    auto src_of = [&](int kv, const Part &p, int h) {
+        return static_cast<const T *>(kv ? a.v : a.k) + p.tok * a.stride + (int64_t)h * a.d;
+    };
+    auto load = [&](Eight<T> (&x)[PT], int kv, const Part &p, int h) {
+        const T *src = src_of(kv, p, h);
+        int row = row0, col = col0;
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            x[i].zero();
+            if (row < p.cnt) x[i].load(src + row * a.stride + col * 8, min(a.d - col * 8, 8), a.vec);
+            row += drow, col += dcol;
+            if (col >= a.pieces) col -= a.pieces, ++row;
         }
-        // piece x of the group's rows
-        auto load = [&](Eight<T> &e, int kv, int x) {
-            const int row = x / a.pieces, col = (x - row * a.pieces) * 8;
-            e.load(src[kv] + (p.tok + row) * a.stride + (int64_t)h * a.d + col, min(a.d - col, 8), a.vec);
-        };
-        Eight<T> x[2][PT];
-        float top[2] = {0.f, 0.f};
+    };
+    // maximum, scale, and codes of K's or V's rows of a part
+    auto work = [&](const Eight<T> (&x)[PT], int kv, const Part &p, int h, int64_t id, float old) {
+        const T *src = src_of(kv, p, h);
+        float top = 0.f;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-            for (int i = 0; i < PT; ++i) {
-                x[kv][i].zero();
-                if (gl + i * kLanes < np) load(x[kv][i], kv, gl + i * kLanes);
-            }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-            for (int i = 0; i < PT; ++i) top[kv] = fmaxf(top[kv], top_of(x[kv][i]));
-            for (int y = gl + PT * kLanes; y < np; y += kLanes) {
-                Eight<T> e;
-                load(e, kv, y);
-                top[kv] = fmaxf(top[kv], top_of(e));
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top[kv] = fmaxf(top[kv], __shfl_xor_sync(0xffffffffu, top[kv], o));
-        }
+        for (int i = 0; i < PT; ++i) top = fmaxf(top, top_of(x[i]));
+        each_piece(p.cnt, PT, INT32_MAX, [&](int, int row, int col) {
+            Eight<T> e;
+            e.load(src + row * a.stride + col, min(a.d - col, 8), a.vec);
+            top = fmaxf(top, top_of(e));
+        });
+        // (not negative: as integers they are in the same order)
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         if constexpr (W > 1) {
             // two sets in turn: a warp writes one again only behind the barrier that all passed after reading it.
-            // Behind this barrier every warp has read the old scales, too.
-            float(*r)[2] = red[turn][group];
+            // Behind this barrier every warp has read the old scale, too.
+            float *r = red[turn][group];
             turn ^= 1;
-            if (lane == 0) r[gw][0] = top[0], r[gw][1] = top[1];
+            if (lane == 0) r[gw] = top;
             asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(kLanes) : "memory");
 #pragma unroll
-            for (int w = 0; w < W; ++w) top[0] = fmaxf(top[0], r[w][0]), top[1] = fmaxf(top[1], r[w][1]);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, r[w]);
         }
+        uint8_t *dst = (kv ? a.vc : a.kc) + (id * a.bs * a.hkv + h) * a.d;   // the block's first row
+        const int64_t pitch = (int64_t)a.hkv * a.d;
+        float s = two_to(exponent_of(top));
+        if (old > 0.f && old <= kMaxFloat) {
+            if (old >= s) {
+                s = old;
+            } else {
+                const float by = old / s;
+                each_piece(p.first, 0, INT32_MAX, [&](int, int row, int col) {
+                    uint8_t *at = dst + row * pitch + col;
+                    const int n = min(a.d - col, 8);
+                    Eight<__nv_fp8_e4m3> e;
+                    e.zero();
+                    if (a.vec) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(at);
+                        e.w[0] = w.x, e.w[1] = w.y;
+                    } else {
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            float s = two_to(exponent_of(top[kv]));
-            if (old[kv] > 0.f && old[kv] <= kMaxFloat) {
-                if (old[kv] >= s) {
-                    s = old[kv];
-                } else {
-                    const float by = old[kv] / s;
-                    for (int y = gl; y < p.first * a.pieces; y += kLanes) {
-                        const int row = y / a.pieces, col = (y - row * a.pieces) * 8, n = min(a.d - col, 8);
-                        uint8_t *at = dst[kv] + ((p.id * a.bs + row) * a.hkv + h) * a.d + col;
-                        Eight<__nv_fp8_e4m3> e;
-                        e.zero();
-                        if (a.vec) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(at);
-                            e.w[0] = w.x, e.w[1] = w.y;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c < n) e.w[c / 4] |= (uint32_t)at[c] << (8 * (c % 4));
-                        }
-                        put_codes(at, codes_of(e, by), n, a.vec);
+                        for (int c = 0; c < 8; ++c)
+                            if (c < n) e.w[c / 4] |= (uint32_t)at[c] << (8 * (c % 4));
                     }
-                }
-            }
-            if (gl == 0 && s != old[kv]) scales[kv][sc] = s;
-            const float inv = 1.f / s;
-            auto store = [&](const Eight<T> &e, int y) {
-                const int row = y / a.pieces, col = (y - row * a.pieces) * 8;
-                put_codes(dst[kv] + ((p.id * a.bs + p.first + row) * a.hkv + h) * a.d + col, codes_of(e, inv),
-                          min(a.d - col, 8), a.vec);
-            };
-#pragma unroll
-            for (int i = 0; i < PT; ++i)
-                if (gl + i * kLanes < np) store(x[kv][i], gl + i * kLanes);
-            for (int y = gl + PT * kLanes; y < np; y += kLanes) {
-                Eight<T> e;
-                load(e, kv, y);
-                store(e, y);
+                    put_codes(at, codes_of(e, by), n, a.vec);
+                });
             }
         }
+        if (gl == 0 && s != old) (kv ? a.vs : a.ks)[id * a.hkv + h] = s;
+        const float inv = 1.f / s;
+        dst += p.first * pitch;
+        int row = row0, col = col0;
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            if (row < p.cnt) put_codes(dst + row * pitch + col * 8, codes_of(x[i], inv), min(a.d - col * 8, 8), a.vec);
+            row += drow, col += dcol;
+            if (col >= a.pieces) col -= a.pieces, ++row;
+        }
+        each_piece(p.cnt, PT, INT32_MAX, [&](int, int row, int col) {
+            Eight<T> e;
+            e.load(src + row * a.stride + col, min(a.d - col, 8), a.vec);
+            put_codes(dst + row * pitch + col, codes_of(e, inv), min(a.d - col, 8), a.vec);
+        });
+    };
+
+    // items (u, head): the next one that has rows
+    int32_t it = (int32_t)blockIdx.x * kGroups + group;
+    const int32_t step = (int32_t)gridDim.x * kGroups;
+    int h = 0;
+    auto find = [&](Part &p) -> bool {
+        for (; it < items; it += step) {
+            const int32_t u = it / a.hkv;
+            h = it - u * a.hkv;
+            p = part_of(a, u, h == 0 && gw == 0);
+            if (p.cnt > 0) {
+                it += step;
+                return true;
+            }
+        }
+        return false;
+    };
+    Eight<T> xk[PT], xv[PT];
+    Part p, next;
+    bool have = find(p);
+    if (have) load(xk, 0, p, h);
+    while (have) {
+        const int hp = h;
+        load(xv, 1, p, hp);
+        // a real block, and its scales so far
+        const bool real = p.entry > 0 && p.entry < a.total_blocks;
+        if (p.entry >= a.total_blocks && hp == 0 && gl == 0 && a.err) atomicAdd(a.err, 1);
+        float old_k = 0.f, old_v = 0.f;
+        if (real && p.first > 0) {
+            old_k = a.ks[(int64_t)p.entry * a.hkv + hp];
+            old_v = a.vs[(int64_t)p.entry * a.hkv + hp];
+        }
+        have = find(next);
+        if (real) work(xk, 0, p, hp, p.entry, old_k);
+        if (have) load(xk, 0, next, h);
+        if (real) work(xv, 1, p, hp, p.entry, old_v);
+        p = next;
     }
 }
 
 template <typename T, int W>
-static int launch(const Args &a, int64_t items, cudaStream_t st) {
+static int launch(const Args &a, int32_t items, cudaStream_t st) {
     constexpr int PT = sizeof(T) == 2 ? 8 : 4;
     constexpr int threads = kThreadsOf<W>;
+    // as many CTAs as are resident at once: a group loads its next rows while it works
     const int64_t blocks = ceil_div<int64_t>(items, threads / (32 * W));
-    const int64_t most = (int64_t)current_sm_count() * 64;
+    const int64_t most = (int64_t)current_sm_count() * (512 / threads);
     const cudaError_t e = launch_pdl(write_blocks_kernel<T, W, PT>, dim3((unsigned)(blocks < most ? blocks : most)),
                                      dim3(threads), 0, st, a, items);
     if (e != cudaSuccess) set_cuda_error(e);
@@ -271,7 +314,7 @@ static int launch(const Args &a, int64_t items, cudaStream_t st) {
 }
 
 template <typename T>
-static int launch_warps(const Args &a, int64_t items, cudaStream_t st) {
+static int launch_warps(const Args &a, int32_t items, cudaStream_t st) {
     // the warps whose registers hold the rows that a block gets on average
     const int64_t mean = ceil_div<int64_t>(a.num_tokens, a.num_reqs);
     const int64_t pieces = (mean < a.bs ? mean : a.bs) * a.pieces;
@@ -309,6 +352,7 @@ extern "C" int bkv_cache_write_fp8_blocks(const void *k_new, const void *v_new, 
                        bt_stride, bt_cols, k_cache, v_cache, k_scales, v_scales, total_blocks, block_size, num_kv_heads,
                        head_dim, (head_dim + 7) / 8, err_count, vec};
     const int64_t items = (num_tokens / block_size + 2 * (int64_t)num_reqs) * num_kv_heads;
-    return src_dtype == BKV_BF16 ? wblk::launch_warps<__nv_bfloat16>(a, items, (cudaStream_t)stream)
-                                 : wblk::launch_warps<float>(a, items, (cudaStream_t)stream);
+    if (items >= ((int64_t)1 << 30)) return BKV_ERR_INVALID_ARG;
+    return src_dtype == BKV_BF16 ? wblk::launch_warps<__nv_bfloat16>(a, (int32_t)items, (cudaStream_t)stream)
+                                 : wblk::launch_warps<float>(a, (int32_t)items, (cudaStream_t)stream);
 }

@@ -35,7 +35,9 @@ struct Args {
     int32_t *ctx, *qsl, *req;
     int64_t *pos, *slots;
     int32_t *used, *err;
-    bool vec;   // table rows begin at 16-byte boundaries
+    int32_t shift;   // log2 of bs, or -1
+    bool vec;        // table rows begin at 16-byte boundaries
+    __device__ __forceinline__ int32_t block_of(uint32_t x) const { return (int32_t)(shift >= 0 ? x >> shift : x / (uint32_t)bs); }
 };
 
 constexpr int kThreads = 512;
@@ -52,8 +54,8 @@ struct Len {
             c = c > 0 ? c : 0;
             n = n < 0 ? 0 : (n > INT32_MAX - c ? INT32_MAX - c : n);
         }
-        have = (int32_t)(((int64_t)c + a.bs - 1) / a.bs);
-        all = (int32_t)(((int64_t)c + n + a.bs - 1) / a.bs);
+        have = a.block_of((uint32_t)c + (uint32_t)(a.bs - 1));
+        all = a.block_of((uint32_t)c + (uint32_t)n + (uint32_t)(a.bs - 1));
     }
     // blocks taken from the free list
     __device__ __forceinline__ int32_t take(const Args &a) const { return max(min(all, a.cols) - have, 0); }
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const Args a) {
             const Len x(a, r);
             if (t < x.n) {
                 const int64_t p = x.c + t;
-                const int32_t lb = (int32_t)(p / a.bs);
+                const int32_t lb = a.block_of((uint32_t)p);
                 int32_t id = -1;
                 if (lb < a.cols) {
                     if (lb < x.have) {
@@ -210,7 +212,8 @@ extern "C" int bkv_build_step(const int32_t *cached_lens, const int32_t *new_len
     if (num_reqs > 0 && (context_lens == cached_lens || context_lens == new_lens)) return BKV_ERR_INVALID_ARG;
     step::Args a{cached_lens, new_lens, num_reqs, free_blocks, num_free, block_size, block_table, bt_stride, bt_cols,
                  max_num_tokens, context_lens, query_start_loc, req_indices, positions, slot_mapping, blocks_used,
-                 err_count, aligned(block_table, 16) && bt_stride % 4 == 0};
+                 err_count, (block_size & (block_size - 1)) == 0 ? __builtin_ctz((unsigned)block_size) : -1,
+                 aligned(block_table, 16) && bt_stride % 4 == 0};
     int64_t grid = ceil_div<int64_t>(num_reqs, step::kThreads / 32);
     const int64_t by_tokens = ceil_div<int64_t>(max_num_tokens, step::kThreads);
     if (by_tokens > grid) grid = by_tokens;

@@ -59,8 +59,11 @@ constexpr int kTcThreads = 384;
 constexpr int kWarpV = 2, kWarpS = 4;                // (1 and 3 issue MMAs)
 constexpr int kHalfBytes = kTcTile * 128;            // a bf16 tile's half of head_dim
 constexpr int kRing = 16;                            // tiles whose segment words and scales are kept
-constexpr int kSets = 4;                             // units whose query scales, and exchanges that, are kept
-constexpr int kTmemCols = 256;                       // S at 0 and 32, O at 64 and 96, exchanges at 128 + 16 i
+constexpr int kSTiles = 4;                           // S tiles in tensor memory, two a warpgroup
+constexpr int kSets = 4, kQSets = 8;                 // exchanges, and units whose query scales are kept
+constexpr int kTmemCols = 256;
+constexpr uint32_t kColO = 32 * kSTiles, kColX = kColO + 64;   // S tiles, O of both warpgroups, exchanges (16 columns each)
+static_assert(kColX + 16 * kSets <= kTmemCols, "tensor memory");
 constexpr int kTimeoutErr = 1 << 24;
 // The softmax's reference is a power 2^kPExp below the maximum it was taken from and moves when a weight passes
 // 2^kPMax, so that O is seldom rescaled: weights are at most 256 < 448, E4M3's largest value.
@@ -82,10 +85,10 @@ struct TcCfg {
     static constexpr int kOffSum = kOffFlag + 2 * 2 * 4 * 4;          // [warpgroup][2][16][4] floats
     static constexpr int kOffXm = kOffSum + 4 * kN * 4 * 4;           // [set][16] (max, sum)
     static constexpr int kOffQs = kOffXm + kSets * kN * 8;            // [set][16] scores' factors
-    static constexpr int kOffScale = kOffQs + kSets * kN * 4;         // [kRing][2][16 segments]
+    static constexpr int kOffScale = kOffQs + kQSets * kN * 4;         // [kRing][2][16 segments]
     static constexpr int kOffMask = kOffScale + (kF8 ? kRing * 2 * 16 * 4 : 0);   // [kRing] loaded segments
     static constexpr int kOffBar = kOffMask + kRing * 4;
-    static constexpr int kNumBars = 4 * kStages + 2 + 2 + 2 * kSets + 8 + 2 + kRing;
+    static constexpr int kNumBars = 4 * kStages + 4 + 2 * kSTiles + 6 + kQSets + kSets + kRing;
     static constexpr int kOffTmem = kOffBar + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmem + 4;
     static constexpr int kOffSums = kOffAbort + 4;                    // a word a warp: prefix sum's scratch
@@ -95,7 +98,7 @@ struct TcCfg {
     static constexpr int kSmem = kOffRow + kN * 4 + 1024;             // slack for 1024 alignment
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
     static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
-    static_assert(kStages + 2 < kRing, "a ring word is rewritten behind its readers");
+    static_assert(kStages + kSTiles < kRing, "a ring word is rewritten behind its readers");
 };
 
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *v) {
@@ -113,10 +116,28 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[NQ
     else tmem_st4(taddr, w);
 }
 
-// Shared-memory descriptor of an MN-major operand with spans of 32 bytes (32-byte swizzle): 8 spans 256 bytes apart.
-__device__ __forceinline__ uint64_t sdesc32(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)6 << 61;
+// Shared-memory descriptors by their words: the upper ones are constants (128-byte swizzle with 8-row groups 1024 bytes
+// apart; 32-byte swizzle with groups of 8 spans 256 bytes apart), the lower hold the address, so that an operand's next
+// piece is an addition away.
+constexpr uint32_t kDesc128 = 1024 >> 4 | 1u << 14 | 2u << 29, kDesc32 = 256 >> 4 | 1u << 14 | 6u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return saddr >> 4 | (lbo >> 4) << 16; }
+
+template <bool kF8, uint32_t kHiA, uint32_t kHiB>
+__device__ __forceinline__ void mma_words(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (kF8)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+            : "memory");
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -141,6 +162,19 @@ __device__ __forceinline__ void put_words(uint8_t *at, const uint32_t (&w)[W]) {
     if constexpr (W == 1) *reinterpret_cast<uint32_t *>(at) = w[0];
     else if constexpr (W == 2) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Whether a phase is over, without mbarrier.try_wait's suspension.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float *src) {
@@ -174,14 +208,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int kB = 4 * kStages;
     auto bar_qfull = [&](int b) { return bar0 + 8u * (kB + b); };
     auto bar_qempty = [&](int b) { return bar0 + 8u * (kB + 2 + b); };
-    auto bar_sfull = [&](int b) { return bar0 + 8u * (kB + 4 + b); };
-    auto bar_sfree = [&](int b) { return bar0 + 8u * (kB + 6 + b); };
-    auto bar_pfull = [&](int b) { return bar0 + 8u * (kB + 8 + b); };
-    auto bar_ofull = [&](int b) { return bar0 + 8u * (kB + 10 + b); };
-    auto bar_group = [&](int k) { return bar0 + 8u * (kB + 12 + k); };
-    auto bar_qscale = [&](int i) { return bar0 + 8u * (kB + 14 + i); };
-    auto bar_x = [&](int i) { return bar0 + 8u * (kB + 14 + kSets + i); };
-    auto bar_mask = [&](int m) { return bar0 + 8u * (kB + 14 + 2 * kSets + m); };
+    auto bar_sfull = [&](int i) { return bar0 + 8u * (kB + 4 + i); };
+    auto bar_sfree = [&](int i) { return bar0 + 8u * (kB + 4 + kSTiles + i); };
+    constexpr int kB2 = kB + 4 + 2 * kSTiles;
+    auto bar_pfull = [&](int b) { return bar0 + 8u * (kB2 + b); };
+    auto bar_ofull = [&](int b) { return bar0 + 8u * (kB2 + 2 + b); };
+    auto bar_group = [&](int k) { return bar0 + 8u * (kB2 + 4 + k); };
+    auto bar_qscale = [&](int i) { return bar0 + 8u * (kB2 + 6 + i); };
+    auto bar_x = [&](int i) { return bar0 + 8u * (kB2 + 6 + kQSets + i); };
+    auto bar_mask = [&](int m) { return bar0 + 8u * (kB2 + 6 + kQSets + kSets + m); };
     const uint32_t sm_k = sbase, sm_v = sbase + C::kOffV, sm_q = sbase + C::kOffQ, sm_p = sbase + C::kOffP;
 
     // what this CTA is: column q, KV head g, row group grp, and its rows
@@ -201,16 +236,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_qfull(b), 1);
             mbar_init(bar_qempty(b), 1);
-            mbar_init(bar_sfull(b), 1);
-            mbar_init(bar_sfree(b), 4);
             mbar_init(bar_pfull(b), 4);
             mbar_init(bar_ofull(b), 1);
             mbar_init(bar_group(b), 4);
         }
-        for (int i = 0; i < kSets; ++i) {
-            mbar_init(bar_qscale(i), 1);
-            mbar_init(bar_x(i), 4);
+        for (int i = 0; i < kSTiles; ++i) {
+            mbar_init(bar_sfull(i), 1);
+            mbar_init(bar_sfree(i), 4);
         }
+        for (int i = 0; i < kQSets; ++i) mbar_init(bar_qscale(i), 1);
+        for (int i = 0; i < kSets; ++i) mbar_init(bar_x(i), 4);
         for (int m = 0; m < kRing; ++m) mbar_init(bar_mask(m), kF8 ? 33 : 1);   // the word, and the lanes' copies
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -313,7 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     *reinterpret_cast<uint2 *>(at + kN * 128) = make_uint2(lo[0], lo[1]);
                     // a row that is not finite makes its scores NaN
                     if (col == 0)
-                        qs[(us & (kSets - 1)) * kN + n] = t < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
+                        qs[(us & (kQSets - 1)) * kN + n] = t < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
                                                                           : __uint_as_float(0x7fffffffu);
                 }
             } else {
@@ -328,7 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar_qfull(b));
-                if constexpr (kF8) mbar_arrive(bar_qscale(us & (kSets - 1)));
+                if constexpr (kF8) mbar_arrive(bar_qscale(us & (kQSets - 1)));
             }
             return true;
         };
@@ -407,8 +442,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!mbar_wait_warp(is_v ? bar_vempty(s) : bar_kempty(s), ring.phase ^ 1u, abort_flag)) break;
                 if (!is_v) {
                     // Tile j's word and scales: written only after the S MMA of tile j - kStages completed, which was
-                    // issued after the softmax had read tile j - kStages - 2's, so that the writer is at most
-                    // kStages + 2 < kRing tiles ahead of the readers.
+                    // issued after the softmax had read tile j - kStages - kSTiles's, so that the writer is at most
+                    // kStages + kSTiles < kRing tiles ahead of the readers.
                     const int m = j & (kRing - 1);
                     if constexpr (kF8) {
                         if (load) {
@@ -446,36 +481,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == 1 || warp == 3) {
         // ================= MMA issuers (one thread each) =================
         if (lane == 0 && warp == 1) {
-            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, kN, 0, 0) : idesc_bf16(128, kN, 0, 0);
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, 2 * kN, 0, 0) : idesc_bf16(128, kN, 0, 0);
+            const uint32_t k_lo = desc_lo(sm_k, 16);
             int j = 0, us = 0;
             Ring ring;
             bool ok = true;
             for (; ok && units.next(x); ++us) {
                 const int qb = us & 1;
                 if (!mbar_wait(bar_qfull(qb), (uint32_t)(us >> 1) & 1u, abort_flag)) break;
-                const uint32_t q_base = sm_q + qb * C::kQBytes;
+                const uint32_t q_lo = desc_lo(sm_q + qb * C::kQBytes, 16);
                 for (int jt = 0; jt < x.nt; ++jt, ++j, ring.advance(kStages)) {
-                    const int b = j & 1;
-                    // K landed, and the softmax has read S tile b of tile j - 2
+                    const int b = j & (kSTiles - 1);
+                    // K landed, and the softmax has read what was in this S tile
                     if (!mbar_wait(bar_kfull(ring.slot), ring.phase, abort_flag) ||
-                        (j >= 2 && !mbar_wait(bar_sfree(b), (uint32_t)((j >> 1) & 1) ^ 1u, abort_flag))) {
+                        (j >= kSTiles && !mbar_wait(bar_sfree(b), (uint32_t)(j / kSTiles - 1) & 1u, abort_flag))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem + 32u * (uint32_t)b, k_base = sm_k + ring.slot * C::kSlot;
+                    const uint32_t d = tmem + 32u * (uint32_t)b, k = k_lo + ring.slot * (C::kSlot >> 4);
                     if constexpr (kF8) {
 #pragma unroll
-                        for (int kk = 0; kk < kD / 32; ++kk) {
-                            const uint64_t k = sdesc(k_base + kk * 32, 16, 1024);
-                            mma_f8(d, k, sdesc(q_base + kk * 32, 16, 1024), kIdesc, kk > 0);
-                            mma_f8(d, k, sdesc(q_base + kN * 128 + kk * 32, 16, 1024), kIdesc, 1);
-                        }
+                        for (int kk = 0; kk < kD / 32; ++kk)
+                            mma_words<kF8, kDesc128, kDesc128>(d, k + 2 * kk, q_lo + 2 * kk, kIdesc, kk > 0);
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < kD / 16; ++kk)
-                            mma_bf16(d, sdesc(k_base + (kk >> 2) * kHalfBytes + (kk & 3) * 32, 16, 1024),
-                                     sdesc(q_base + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024), kIdesc, kk > 0);
+                            mma_words<kF8, kDesc128, kDesc128>(d, k + (kk >> 2) * (kHalfBytes >> 4) + (kk & 3) * 2,
+                                                               q_lo + (kk >> 2) * (kN * 8) + (kk & 3) * 2, kIdesc, kk > 0);
                     }
                     mma_commit(bar_sfull(b));
                     mma_commit(bar_kempty(ring.slot));
@@ -484,6 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         } else if (lane == 0) {
             constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, 2 * kN, 1, 1) : idesc_bf16(128, kN, 1, 1);
+            const uint32_t v_lo = desc_lo(sm_v, kF8 ? 16 : kHalfBytes), p_lo = desc_lo(sm_p, 16);
             int j = 0;
             Ring ring;
             bool ok = true;
@@ -496,21 +530,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem + 64u + 32u * (uint32_t)b, v_base = sm_v + ring.slot * C::kSlot;
-                    const uint32_t p_base = sm_p + b * C::kPBytes;
+                    const uint32_t d = tmem + kColO + 32u * (uint32_t)b, v = v_lo + ring.slot * (C::kSlot >> 4);
+                    const uint32_t p = p_lo + b * (C::kPBytes >> 4);
                     const uint32_t more = jt >= 2;   // a warpgroup's first tile of a unit begins its O
                     // V^T and P^T MN-major: a row's 128 codes (64 bf16) are one 128-byte span, a position's weights one
                     // of 32 bytes
-                    if constexpr (kF8) {
 #pragma unroll
-                        for (int kk = 0; kk < kTcTile / 32; ++kk)
-                            mma_f8(d, sdesc(v_base + kk * 4096, 16, 1024), sdesc32(p_base + kk * 1024), kIdesc, more | (kk > 0));
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < kTcTile / 16; ++kk)
-                            mma_bf16(d, sdesc(v_base + kk * 2048, kHalfBytes, 1024), sdesc32(p_base + kk * 512), kIdesc,
-                                     more | (kk > 0));
-                    }
+                    for (int kk = 0; kk < (kF8 ? kTcTile / 32 : kTcTile / 16); ++kk)
+                        mma_words<kF8, kDesc128, kDesc32>(d, v + kk * (kF8 ? 256 : 128), p + kk * (kF8 ? 64 : 32), kIdesc,
+                                                          more | (kk > 0));
                     mma_commit(bar_ofull(b));
                     mma_commit(bar_vempty(ring.slot));
                 }
@@ -522,7 +550,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int wg = (warp - kWarpS) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                  // TMEM lane: position in the tile, and head_dim row
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-        const uint32_t s_col = tmem + lane_base + 32u * (uint32_t)wg, o_col = s_col + 64u;
+        const uint32_t o_col = tmem + lane_base + kColO + 32u * (uint32_t)wg;
         const int red_row = reduced_row<NQ>(lane);
         const bool red_writer = reduced_writer<NQ>(lane);
         const int flip = (row >> 2) & 1;
@@ -533,7 +561,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto group_sync = [&]() -> bool {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_group(wg));
-            const bool r = mbar_wait_warp(bar_group(wg), gphase, abort_flag);
+            bool r = false;
+            for (int i = 0; i < 64 && !r; ++i) r = __all_sync(0xffffffffu, mbar_test(bar_group(wg), gphase));
+            if (!r) r = mbar_wait_warp(bar_group(wg), gphase, abort_flag);
             gphase ^= 1u;
             return r;
         };
@@ -571,17 +601,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 cs[n] = a.scale_log2;
             }
             if constexpr (kF8) {
-                // a set is rewritten four units on, behind the S MMAs of the unit after the next, which wait until this
-                // unit's tiles have been read
-                if (!mbar_wait_warp(bar_qscale(us & (kSets - 1)), (uint32_t)(us >> 2) & 1u, abort_flag)) break;
+                // A set is rewritten eight units on, behind the S MMAs of the sixth unit after this one: its last tile is at
+                // least six behind this unit's last, and its S tile's last reader this warpgroup, past this unit.
+                if (!mbar_wait_warp(bar_qscale(us & (kQSets - 1)), (uint32_t)(us / kQSets) & 1u, abort_flag)) break;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? qs[(us & (kSets - 1)) * kN + n] : 0.f;
+                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? qs[(us & (kQSets - 1)) * kN + n] : 0.f;
             }
             for (int jt = 0; jt < x.nt; ++jt, ++j, vring.advance(kStages)) {
                 if ((j & 1) != wg) continue;
                 const uint32_t par = (uint32_t)(j >> 1) & 1u;
-                const int m = j & (kRing - 1);
-                if (!mbar_wait_warp(bar_sfull(wg), par, abort_flag) ||
+                const int m = j & (kRing - 1), sb = j & (kSTiles - 1);
+                if (!mbar_wait_warp(bar_sfull(sb), (uint32_t)(j / kSTiles) & 1u, abort_flag) ||
                     !mbar_wait_warp(bar_mask(m), (uint32_t)(j / kRing) & 1u, abort_flag)) {
                     ok = false;
                     break;
@@ -598,10 +628,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_after();
                 float sv[NQ];
-                tmem_ld_cols<NQ>(s_col, sv);
+                if constexpr (kF8) tmem_ld_sum2<NQ>(tmem + lane_base + 32u * (uint32_t)sb, sv);
+                else tmem_ld_cols<NQ>(tmem + lane_base + 32u * (uint32_t)sb, sv);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfree(wg));   // S tile may be overwritten (by tile j + 2's)
+                if (lane == 0) mbar_arrive(bar_sfree(sb));   // S tile may be overwritten (by tile j + 4's)
                 const int32_t v = (x.f + jt) * kTcTile + row;
                 const int32_t p = s.pos(v);
                 const bool in = loaded && v < s.len, sink = p < a.sinks;
@@ -794,7 +825,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the exchange after this one, which it begins when it has read this.
             const bool finish = ((j - 1) & 1) == wg;
             const int set = xs & (kSets - 1);
-            const uint32_t x_col = tmem + lane_base + 128u + 16u * (uint32_t)set;
+            const uint32_t x_col = tmem + lane_base + kColX + 16u * (uint32_t)set;
             float2 *xm = reinterpret_cast<float2 *>(smem + C::kOffXm) + set * kN;
             const uint32_t x_par = (uint32_t)(xs >> 2) & 1u;
             if (both) ++xs;
