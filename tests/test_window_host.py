@@ -1,6 +1,8 @@
 """Host-side checks of step building, block-scaled E4M3 caches and windows whose
 first tokens stay visible: the C ABI's refusals (before any CUDA call), the
 binding's checks and argument marshalling, the plain forms of the GPU tests."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -21,12 +23,25 @@ def lib():
     return bkv.load()
 
 
+class _Entry:
+    """A C entry point under the argument types of include/bkv.h (the binding passes records instead)."""
+
+    def __init__(self, f, types):
+        c = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "q": ctypes.c_int64, "f": ctypes.c_float, "n": ctypes.c_size_t}
+        self.f = ctypes.CFUNCTYPE(ctypes.c_int, *[c[x] for x in types])(ctypes.cast(f, ctypes.c_void_p).value)
+
+    def __call__(self, *args):
+        return self.f(*args)
+
+
 def test_build_step_refusals(lib):
+    entry = _Entry(lib.bkv_build_step, "ppipiipqiqpppppppp")
+
     base = dict(cached=NULL, new=NULL, nr=2, free=NULL, nf=3, bs=16, bt=NULL, st=4, cols=4, mx=5, ctx=NULL, qsl=NULL,
                 req=NULL, pos=NULL, slots=NULL, used=NULL, err=NULL, stream=NULL)
 
     def call(**kw):
-        return lib.bkv_build_step(*dict(base, **kw).values())
+        return entry(*dict(base, **kw).values())
 
     some = {n: 64 * (i + 1) for i, n in enumerate(("cached", "new", "free", "bt", "ctx", "qsl", "req", "pos", "slots", "used"))}
     for bad in (dict(nr=-1), dict(nf=-1), dict(bs=0), dict(cols=-1), dict(st=3), dict(mx=-1), dict(ctx=some["cached"]),
@@ -35,11 +50,12 @@ def test_build_step_refusals(lib):
 
 
 def test_write_refusals(lib):
+    entry = _Entry(lib.bkv_cache_write_fp8_blocks, "ppqqppipqippppqiiiipp")
     base = dict(k=NULL, v=NULL, n=4, stride=1024, qsl=NULL, ctx=NULL, nr=2, bt=NULL, st=4, cols=4, kc=NULL, vc=NULL, ks=NULL,
                 vs=NULL, tb=9, bs=16, hkv=8, d=128, dt=0, err=NULL, stream=NULL)
 
     def call(**kw):
-        return lib.bkv_cache_write_fp8_blocks(*dict(base, **kw).values())
+        return entry(*dict(base, **kw).values())
 
     assert call(dt=3) == bkv.BKV_ERR_UNSUPPORTED
     some = {n: 64 * (i + 1) for i, n in enumerate(("k", "v", "qsl", "ctx", "bt", "kc", "vc", "ks", "vs"))}
@@ -56,7 +72,8 @@ def test_decode_refusals(lib, fp8):
         base.update(ks=NULL, vs=NULL)
     base.update(bt=NULL, st=4, cols=4, ctx=NULL, mx=16, nr=2, ql=1, hq=32, hkv=8, d=128, bs=16, tb=8, scale=0.0, mode=0,
                 window=8, sinks=4, dt=0, out=NULL, ws=NULL, wsb=0, err=NULL, stream=NULL)
-    f = lib.bkv_paged_decode_fp8_blocks if fp8 else lib.bkv_paged_decode_sink
+    types = "pqipiiiiiiiqfiiiippnpp"
+    f = (_Entry(lib.bkv_paged_decode_fp8_blocks, "ppppp" + types) if fp8 else _Entry(lib.bkv_paged_decode_sink, "ppp" + types))
 
     def call(**kw):
         return f(*dict(base, **kw).values())
@@ -110,22 +127,61 @@ def _attn_fn(fp8):
     return bkv.bkv_paged_decode_fp8_blocks if fp8 else bkv.bkv_paged_decode_sink
 
 
+def _sent(fake, fn):  # noqa: F811
+    """The arguments of a call, out of its record."""
+    (record,) = fake.calls[fn + "_record"]
+    return bkv._RECORDS[fn].unpack(record)
+
+
 def test_marshalling(fake):  # noqa: F811
     bkv.bkv_build_step(**_step())
     p = fake.ptrs
-    assert fake.calls["bkv_build_step"] == (
+    assert _sent(fake, "bkv_build_step") == (
         p["cached_lens"], p["new_lens"], 3, p["free_blocks"], 7, 16, p["block_table"], 9, 5, 11, p["context_lens"],
-        p["query_start_loc"], p["req_indices"], p["positions"], p["slot_mapping"], p["blocks_used"], None, 999)
+        p["query_start_loc"], p["req_indices"], p["positions"], p["slot_mapping"], p["blocks_used"], 0, 999)
     bkv.bkv_cache_write_fp8_blocks(**_write())
-    assert fake.calls["bkv_cache_write_fp8_blocks"] == (
+    assert _sent(fake, "bkv_cache_write_fp8_blocks") == (
         p["k_new"], p["v_new"], 6, 272, p["query_start_loc"], p["context_lens"], 3, p["block_table"], 5, 5, p["k_cache"],
-        p["v_cache"], p["k_scales"], p["v_scales"], 8, 16, 2, 64, bkv.BKV_BF16, None, 999)
+        p["v_cache"], p["k_scales"], p["v_scales"], 8, 16, 2, 64, bkv.BKV_BF16, 0, 999)
     for fp8 in (False, True):
         fn = "bkv_paged_decode_fp8_blocks" if fp8 else "bkv_paged_decode_sink"
         _attn_fn(fp8)(**_attn(fp8), softmax_scale=0.5, mask_mode=bkv.BKV_MASK_ALL)
-        scales = (p["k_scales"], p["v_scales"]) if fp8 else ()
-        assert fake.calls[fn] == (p["q"], p["k_cache"], p["v_cache"], *scales, p["block_table"], 5, 5, p["context_lens"], 70,
-                                  3, 2, 8, 2, 64, 16, 8, 0.5, 1, 33, 4, bkv.BKV_BF16, p["out"], p["workspace"], 99, None, 999)
+        scales = (p["k_scales"], p["v_scales"]) if fp8 else (0, 0)
+        assert _sent(fake, fn) == (p["q"], p["k_cache"], p["v_cache"], *scales, p["block_table"], 5, 5, p["context_lens"], 70,
+                                   3, 2, 8, 2, 64, 16, 8, 0.5, 1, 33, 4, bkv.BKV_BF16, p["out"], p["workspace"], 99, 0, 999)
+    with pytest.raises(ValueError, match="C type"):              # no argument is cut to fit
+        bkv.bkv_paged_decode_sink(**dict(_attn(False), sliding_window=1 << 33))
+
+
+def test_records_are_the_entry_points_arguments(lib):
+    """A record read by the library refuses exactly what its entry point refuses: every field sits where the C struct has
+    it (a wrong size before it would move what is refused)."""
+    good = dict(step=[64, 64, 2, 64, 3, 16, 64, 4, 4, 5, 128, 64, 64, 64, 64, 64, 0, 0],
+                write=[64, 64, 4, 1024, 64, 64, 2, 64, 4, 4, 64, 64, 64, 64, 9, 16, 8, 128, 0, 0, 0],
+                attn=[64, 64, 64, 64, 64, 64, 4, 4, 64, 16, 2, 1, 32, 8, 128, 16, 8, 0.0, 0, 8, 4, 0, 64, 64,
+                      lib.bkv_paged_decode_window_workspace_size(2, 1, 32, 8, 128, 16, 16), 0, 0])
+
+    def refused(fn, args, at, value, status=bkv.BKV_ERR_INVALID_ARG):
+        args = list(args)
+        args[at] = value
+        got = getattr(lib, fn + "_record")(bkv._RECORDS[fn].pack(*args))
+        assert got == status, (fn, at, value, got)
+
+    for at, value in ((0, 0), (1, 0), (2, -1), (3, 0), (4, -1), (5, 0), (6, 0), (7, 3), (8, -1), (9, -1), (10, 64), (11, 0),
+                      (12, 0), (13, 0), (14, 0), (15, 0)):
+        refused("bkv_build_step", good["step"], at, value)
+    for at, value in ((0, 0), (1, 0), (2, -1), (3, 1023), (4, 0), (5, 0), (6, -1), (7, 0), (8, 3), (9, -1), (10, 0), (11, 0),
+                      (12, 0), (13, 0), (14, -1), (15, 0), (16, 0), (17, 0)):
+        refused("bkv_cache_write_fp8_blocks", good["write"], at, value)
+    refused("bkv_cache_write_fp8_blocks", good["write"], 18, 7, bkv.BKV_ERR_UNSUPPORTED)
+    for fn in ("bkv_paged_decode_sink", "bkv_paged_decode_fp8_blocks"):
+        for at, value in ((0, 0), (1, 0), (2, 0), (5, 0), (6, 3), (7, -1), (8, 0), (9, -1), (10, 0), (11, 0), (12, 30), (13, 0),
+                          (15, 0), (16, -1), (18, 3), (19, -1), (20, -1), (22, 0), (23, 0), (23, 16), (24, 100)):
+            refused(fn, good["attn"], at, value)
+        refused(fn, good["attn"], 14, 63, bkv.BKV_ERR_UNSUPPORTED)
+        refused(fn, good["attn"], 21, 3, bkv.BKV_ERR_UNSUPPORTED)
+    refused("bkv_paged_decode_fp8_blocks", good["attn"], 3, 0)
+    refused("bkv_paged_decode_fp8_blocks", good["attn"], 4, 0)
 
 
 STEP_BAD = [(dict(new_lens=torch.zeros(2, dtype=I32)), ValueError), (dict(context_lens=torch.zeros(4, dtype=I32)), ValueError),
@@ -195,11 +251,11 @@ def test_dimensions_of_size_one_may_carry_any_stride(fake):  # noqa: F811
     one = torch.zeros(5, dtype=I32).as_strided((1, 5), (0, 1))
     a = _attn(True, nr=1)
     bkv.bkv_paged_decode_fp8_blocks(**dict(a, block_table=one))
-    assert fake.calls["bkv_paged_decode_fp8_blocks"][6:8] == (5, 5)
+    assert _sent(fake, "bkv_paged_decode_fp8_blocks")[6:8] == (5, 5)
     heads = torch.zeros(2, 6, 64, dtype=torch.bfloat16)
     w = dict(_write(hkv=1), k_new=heads[:1].transpose(0, 1), v_new=heads[1:].transpose(0, 1))
     bkv.bkv_cache_write_fp8_blocks(**w)
-    assert fake.calls["bkv_cache_write_fp8_blocks"][3] == 64
+    assert _sent(fake, "bkv_cache_write_fp8_blocks")[3] == 64
 
 
 def test_plain_forms():
