@@ -35,28 +35,75 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 //
 // A CTA of four warps walks its column's units for one (KV head, row group).
 // LP lanes hold a position's row, eight elements each, so a warp takes 32 / LP
-// positions at a time and U of those at once (their loads in flight together;
-// the positions' block entries come one step ahead).  Each set of LP lanes
-// keeps its own running maximum, sum and output for the NR query rows, and the
-// sets are joined when the unit ends.
+// positions at a time and U of those a step.  Each set of LP lanes keeps its own
+// running maximum, sum and output for the NR query rows, and the sets are joined
+// when the unit ends.
 //
-// Bound by the loads in flight and, from 8 query rows on, by issue slots: a
-// position costs 16 multiply-adds a lane and row, log2(LP) shuffles and an
-// exponential.
+// Rows come by cp.async through a ring of kStages steps in shared memory, each
+// lane copying exactly what it reads itself, so that the only wait is its own:
+// 12 KB a warp are in flight however many registers the rows' arithmetic takes
+// (with the rows in registers, one step at a time, 16 requests of 3000 positions,
+// 15 / 5 heads of 64, fp32: 57 us; 32 / 8 of 64, E4M3: 90).  Block entries are
+// loaded a step before their rows.  Multiply-adds go two an instruction.
 // ---------------------------------------------------------------------------
 constexpr int kCcThreads = 128;
 constexpr int kCcTile = 64;
-constexpr int kCcPerSm = 2;   // CTAs an SM is laid out for
+
+template <int NR>
+constexpr int kCcPerSm = NR <= 4 ? 3 : 2;   // CTAs an SM is laid out for
+
+// What a warp's ring holds a step, and a CTA's shared memory: the rings, and over them (a unit's steps are all read by
+// then) the warps' outputs.
+template <typename KV, int NR>
+struct CcShape {
+    static constexpr int U = NR <= 4 ? 4 : 2;
+    static constexpr int kStages = sizeof(KV) * U == 16 ? 2 : 4;         // steps in a warp's ring
+    static constexpr int kChunk = 8 * (int)sizeof(KV);                   // a lane's piece of a row
+    static constexpr int kStep = U * 2 * kChunk * 32 + (sizeof(KV) == 1 ? U * 2 * 4 * 32 : 0);   // rows, and scales
+    static constexpr int kRing = 4 * kStages * kStep;
+};
+template <typename KV, int NR, int LP>
+constexpr int kCcSmem = CcShape<KV, NR>::kRing > 4 * NR * 8 * LP * 4 ? CcShape<KV, NR>::kRing : 4 * NR * 8 * LP * 4;
+
+__device__ __forceinline__ float two_to(float x) {   // 2^x, 2 units in the last place
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t shared_at(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+// n bytes of `size` come from src, the others are 0.
+template <int size>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int n) {
+    if constexpr (size == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(size), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 
 template <typename T, typename KV, int NR, int LP>
-__global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const Args a, const bool vec) {
-    constexpr int U = sizeof(KV) == 4 || NR > 4 ? 2 : 4;
+__global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(const Args a, const bool vec) {
+    using S = CcShape<KV, NR>;
+    constexpr int U = S::U, kStages = S::kStages;
     constexpr int PW = 32 / LP;          // positions a warp holds at once
     constexpr int DP = 8 * LP;
     constexpr bool kF8 = sizeof(KV) == 1;
+    constexpr int kPiece = S::kChunk > 16 ? 16 : S::kChunk, kPieces = S::kChunk / kPiece;   // a copy, copies a chunk
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int32_t pre[kMaxReqs + 1], lens[kMaxReqs], sums[kCcThreads / 32];
-    __shared__ float so[4][NR][DP], sm[4][NR], sl[4][NR];
+    __shared__ float sm[4][NR], sl[4][NR];
+    float(*so)[NR][DP] = reinterpret_cast<float(*)[NR][DP]>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = smem + warp * (kStages * S::kStep) + lane * kPiece;   // this lane's part of the warp's ring
+    const uint32_t ring_s = shared_at(ring);
     const int sub = lane / LP, e0 = (lane % LP) * 8;   // this lane's position of PW, and elements
     const int ne = min(max(a.D - e0, 0), 8);
     const int HP = a.H_kv * a.groups;
@@ -64,6 +111,8 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const A
     const int g = hp / a.groups, grp = hp - g * a.groups;
     const int i0 = grp * a.NR;
     const int rows = min(a.NR, a.q_len * a.G - i0);
+    const int tok_lo = i0 / a.G, tok_hi = (i0 + rows - 1) / a.G;
+    const int shift = (a.bs & (a.bs - 1)) == 0 ? 31 - __clz(a.bs) : -1;
     pdl_wait();
     pdl_trigger();
     lay_out<kCcThreads>(a, pre, lens, sums);
@@ -83,148 +132,235 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const A
     while (units.next(x)) {
         const Span s = span_of(a, lens[x.r]);
         const int v_end = min((x.f + x.nt) * kCcTile, s.len);
-        float qv[NR][8], o[NR][8], m[NR], l[NR];
-        int32_t tp[NR];   // a row's own position
+        const int32_t *table = a.bt + (int64_t)x.r * a.bt_stride;
+        const int v_first = x.f * kCcTile + warp * PW * U + sub;
+        constexpr int kStepPos = 4 * PW * U;   // positions the CTA takes a step
+        const int steps = (v_end - x.f * kCcTile + kStepPos - 1) / kStepPos;
+        auto block_of = [&](int32_t p) { return shift >= 0 ? p >> shift : p / a.bs; };
+        // this lane's position u of step i: its block entry (0 where there is none) as it is in the table
+        auto fetch = [&](int i, int32_t (&ent)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = v_first + i * kStepPos + u * PW;
+                ent[u] = 0;
+                if (i < steps && v < v_end) {
+                    const int32_t lb = block_of(s.pos(v));
+                    if (lb < a.bt_cols) ent[u] = __ldg(table + lb);
+                }
+            }
+        };
+        // the rows (and scales) of step i into its ring slot; which of them are there, as bits
+        auto issue = [&](int i, const int32_t (&ent)[U]) -> uint32_t {
+            const uint32_t slot = (uint32_t)(i % kStages) * S::kStep;
+            uint32_t bits = 0u;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool there = ent[u] > 0 && ent[u] < a.total_blocks;
+                const int32_t p = s.pos(v_first + i * kStepPos + u * PW);
+                const int32_t b = there ? ent[u] : 0, off = there ? p - block_of(p) * a.bs : 0;
+                const int64_t at = (((int64_t)b * a.bs + off) * a.H_kv + g) * a.D + (ne > 0 ? e0 : 0);
+                bits |= there ? 1u << u : 0u;
+                const int n = there && ne > 0 ? kPiece : 0;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const KV *src = static_cast<const KV *>(kv ? a.v : a.k) + at;
+                    constexpr int kRow = kPieces * 32 * kPiece;
+                    if (vec) {
+#pragma unroll
+                        for (int c = 0; c < kPieces; ++c)
+                            copy_async<kPiece>(ring_s + slot + (u * 2 + kv) * kRow + c * (32 * kPiece),
+                                               reinterpret_cast<const uint8_t *>(src) + c * kPiece, n);
+                    } else {
+                        Eight<KV> e;
+                        e.zero();
+                        if (n > 0) e.load(src, ne, false);
+#pragma unroll
+                        for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+                            for (int w = 0; w < kPiece / 4; ++w)
+                                reinterpret_cast<uint32_t *>(ring + slot + (u * 2 + kv) * kRow + c * (32 * kPiece))[w] =
+                                    e.w[c * (kPiece / 4) + w];
+                    }
+                    if constexpr (kF8)   // (behind the rows, a word a lane)
+                        copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((u * 2 + kv) * 32 + lane) * 4,
+                                      (kv ? a.vs : a.ks) + (int64_t)b * a.H_kv + g, there ? 4 : 0);
+                }
+            }
+            return bits;
+        };
+        uint32_t there = 0u;   // U bits a ring slot
+        {
+            int32_t ent[kStages - 1][U];
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) fetch(i, ent[i]);
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) {
+                there |= issue(i, ent[i]) << (U * i);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        }
+        int32_t ent[U];
+        fetch(kStages - 1, ent);
+        float2 qv[NR][4], o[NR][4];
+        float m[NR], l[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const int nn = min(n, rows - 1);
-            tp[n] = s.L - a.q_len + (i0 + nn) / a.G;
             Eight<T> raw;
             raw.zero();
             if (n < rows && ne > 0) raw.load(static_cast<const T *>(a.q) + out_row(x.r, n) + e0, ne, vec);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = raw.two(i);
-                qv[n][2 * i] = f.x * a.scale_log2;
-                qv[n][2 * i + 1] = f.y * a.scale_log2;
+                qv[n][i] = make_float2(f.x * a.scale_log2, f.y * a.scale_log2);
+                o[n][i] = make_float2(0.f, 0.f);
             }
             m[n] = -INFINITY;
             l[n] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[n][i] = 0.f;
         }
         // Bad entries among the blocks that the unit begins, counted once a KV head: every block that the span
         // reads begins once in it, at its first position there.
         if (a.err && grp == 0) {
             for (int v = x.f * kCcTile + (int)threadIdx.x; v < v_end; v += kCcThreads) {
-                const int32_t p = s.pos(v);
-                if (p % a.bs != 0 && !(s.gap > 0 && v == s.sb && (s.sb == 0 || p / a.bs != (s.sb - 1) / a.bs))) continue;
-                const int32_t lb = p / a.bs;
-                if (lb >= a.bt_cols || __ldg(a.bt + (int64_t)x.r * a.bt_stride + lb) >= a.total_blocks) atomicAdd(a.err, 1);
+                const int32_t p = s.pos(v), lb = block_of(p);
+                if (p != lb * a.bs && !(s.gap > 0 && v == s.sb && (s.sb == 0 || lb != block_of(s.sb - 1)))) continue;
+                if (lb >= a.bt_cols || __ldg(table + lb) >= a.total_blocks) atomicAdd(a.err, 1);
             }
         }
+        // Positions at or below last_lo (and from first_hi on, or below `sinks`) are seen by every row of the group.
+        const int32_t t_lo = s.L - a.q_len + tok_lo, t_hi = s.L - a.q_len + tok_hi;
+        const int32_t last_lo = a.causal ? t_lo : s.L - 1;
+        const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
+        const uint32_t full = (1u << rows) - 1u;
         // which of the rows see position p, as bits
         auto seen = [&](int32_t p) {
             uint32_t b = 0u;
+            int32_t t = t_lo, h = i0 - tok_lo * a.G;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                const bool last = p <= (a.causal ? tp[n] : s.L - 1);
-                const bool near = a.window == 0 || p > tp[n] - a.window || p < a.sinks;
+                const bool last = p <= (a.causal ? t : s.L - 1);
+                const bool near = a.window == 0 || p > t - a.window || p < a.sinks;
                 b |= (last && near && n < rows) ? 1u << n : 0u;
+                if (++h == a.G) {
+                    h = 0;
+                    ++t;
+                }
             }
             return b;
         };
-        // where position v of the span is cached: row of the cache, or -1
-        auto entry = [&](int v, int32_t &p) -> int64_t {
-            p = -1;
-            if (v >= v_end) return -1;
-            p = s.pos(v);
-            const int32_t lb = p / a.bs;
-            const int64_t b = lb < a.bt_cols ? __ldg(a.bt + (int64_t)x.r * a.bt_stride + lb) : 0;
-            return b > 0 && b < a.total_blocks ? b * a.bs + (p - lb * a.bs) : -1;
-        };
-        const int step = 4 * PW * U;
-        int v0 = x.f * kCcTile + warp * PW * U;
-        int64_t row[U];
-        int32_t pos[U];
+        for (int i = 0; i < steps; ++i) {
+            {
+                const int j = i + kStages - 1, at = U * (j % kStages);
+                there = (there & ~(((1u << U) - 1u) << at)) | issue(j, ent) << at;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                fetch(j + 1, ent);
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            const uint8_t *slot = ring + (i % kStages) * S::kStep;
+            const uint32_t here = there >> (U * (i % kStages));
+            auto held = [&](int u, int kv) {
+                Eight<KV> e;
+                const uint8_t *src = slot + (u * 2 + kv) * kPieces * (32 * kPiece);
+                if constexpr (kPiece == 8) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                    e.w[0] = w.x, e.w[1] = w.y;
+                } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) row[u] = entry(v0 + u * PW + sub, pos[u]);
-        for (; v0 < v_end; v0 += step) {
-            Eight<KV> kr[U], vr[U];
-            float ks[U], vs[U];
-            uint32_t see[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                see[u] = row[u] >= 0 ? seen(pos[u]) : 0u;
-                kr[u].zero();
-                vr[u].zero();
-                ks[u] = vs[u] = 1.f;
-                if (see[u]) {
-                    const int64_t at = (row[u] * a.H_kv + g) * a.D + e0;
-                    if (ne > 0) {
-                        kr[u].load(static_cast<const KV *>(a.k) + at, ne, vec);
-                        vr[u].load(static_cast<const KV *>(a.v) + at, ne, vec);
-                    }
-                    if constexpr (kF8) {
-                        const int64_t b = row[u] / a.bs * a.H_kv + g;
-                        ks[u] = __ldg(a.ks + b);
-                        vs[u] = fminf(fmaxf(__ldg(a.vs + b), kScaleMin), kScaleMax);
+                    for (int c = 0; c < kPieces; ++c) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + c * (32 * kPiece));
+                        e.w[4 * c] = w.x, e.w[4 * c + 1] = w.y, e.w[4 * c + 2] = w.z, e.w[4 * c + 3] = w.w;
                     }
                 }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) row[u] = entry(v0 + step + u * PW + sub, pos[u]);
-            float sc[U][NR];
+                return e;
+            };
+            float sc[U][NR], vs[U];
+            uint32_t see[U];
+            bool every = true;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                const int v = v_first + i * kStepPos + u * PW;
+                const int32_t p = s.pos(v);
+                const bool in = (here >> u) & 1u;
+                see[u] = in && p <= last_lo && (p >= first_hi || p < a.sinks) ? full : 0u;
+                if (in && see[u] == 0u) see[u] = seen(p);
+                every &= see[u] == full;
+                const Eight<KV> k = held(u, 0);
+                float2 acc[NR];
 #pragma unroll
-                for (int n = 0; n < NR; ++n) sc[u][n] = 0.f;
+                for (int n = 0; n < NR; ++n) acc[n] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = kr[u].two(i);
+                for (int c = 0; c < 4; ++c) {
+                    const float2 f = k.two(c);
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) sc[u][n] = fmaf(qv[n][2 * i + 1], f.y, fmaf(qv[n][2 * i], f.x, sc[u][n]));
+                    for (int n = 0; n < NR; ++n) acc[n] = fma2(qv[n][c], f, acc[n]);
+                }
+                float ks = 1.f;
+                vs[u] = 1.f;
+                if constexpr (kF8) {
+                    const float *sp = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32) + u * 64 + lane;
+                    ks = sp[0];
+                    vs[u] = fminf(fmaxf(sp[32], kScaleMin), kScaleMax);
                 }
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
+                    float d = acc[n].x + acc[n].y;
 #pragma unroll
-                    for (int w = LP / 2; w > 0; w >>= 1) sc[u][n] += __shfl_xor_sync(0xffffffffu, sc[u][n], w);
-                    sc[u][n] = (see[u] >> n) & 1u ? sc[u][n] * ks[u] : -INFINITY;
+                    for (int w = LP / 2; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
+                    sc[u][n] = (see[u] >> n) & 1u ? (kF8 ? d * ks : d) : -INFINITY;
                 }
             }
-            // a value that some rows see and others do not reaches only the former, whatever it is
-            const uint32_t full = (1u << rows) - 1u;
-            bool mixed = false;
-#pragma unroll
-            for (int u = 0; u < U; ++u) mixed |= see[u] != 0u && see[u] != full;
-            mixed = __any_sync(0xffffffffu, mixed);
+            // a new maximum anywhere in the warp: all rescale (seldom, behind the first steps)
+            float mn[NR];
+            bool up = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                float mn = m[n];
+                mn[n] = m[n];
 #pragma unroll
-                for (int u = 0; u < U; ++u) mn = fmaxf(mn, sc[u][n]);
-                const float corr = mn == -INFINITY ? 1.f : exp2f(m[n] - mn);
-                m[n] = mn;
-                l[n] *= corr;
+                for (int u = 0; u < U; ++u) mn[n] = fmaxf(mn[n], sc[u][n]);
+                up |= mn[n] != m[n];
+            }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const float corr = mn[n] == -INFINITY ? 1.f : two_to(m[n] - mn[n]);
+                    m[n] = mn[n];
+                    l[n] *= corr;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[n][c].x *= corr, o[n][c].y *= corr;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    sc[u][n] = sc[u][n] == -INFINITY ? 0.f : exp2f(sc[u][n] - mn);
+                    sc[u][n] = sc[u][n] == -INFINITY ? 0.f : two_to(sc[u][n] - m[n]);
                     l[n] += sc[u][n];
                     if constexpr (kF8) sc[u][n] *= vs[u];
                 }
+            // a value that some rows do not see reaches only those that do, whatever it is
+            if (__all_sync(0xffffffffu, every)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[n][i] *= corr;
-            }
+                for (int u = 0; u < U; ++u) {
+                    const Eight<KV> val = held(u, 1);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 f = val.two(c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = vr[u].two(i);
-                    if (!mixed) {
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) {
-                            o[n][2 * i] = fmaf(sc[u][n], f.x, o[n][2 * i]);
-                            o[n][2 * i + 1] = fmaf(sc[u][n], f.y, o[n][2 * i + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < NR; ++n)
-                            if ((see[u] >> n) & 1u) {
-                                o[n][2 * i] = fmaf(sc[u][n], f.x, o[n][2 * i]);
-                                o[n][2 * i + 1] = fmaf(sc[u][n], f.y, o[n][2 * i + 1]);
-                            }
+                        for (int n = 0; n < NR; ++n) o[n][c] = fma2(make_float2(sc[u][n], sc[u][n]), f, o[n][c]);
                     }
                 }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const Eight<KV> val = held(u, 1);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 f = val.two(c);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            if ((see[u] >> n) & 1u) o[n][c] = fma2(make_float2(sc[u][n], sc[u][n]), f, o[n][c]);
+                    }
+                }
+            }
         }
         // join the warp's sets of lanes, then the warps
         auto join = [](float m0, float m1, float &f0, float &f1) {
@@ -233,7 +369,8 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const A
             f1 = mn == -INFINITY ? 1.f : exp2f(m1 - mn);
             return mn;
         };
-        __syncthreads();   // the last unit's sums have been read
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();   // every warp is through with its ring
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
@@ -242,12 +379,15 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const A
                 const float mn = join(m[n], __shfl_xor_sync(0xffffffffu, m[n], w), f0, f1);
                 l[n] = l[n] * f0 + __shfl_xor_sync(0xffffffffu, l[n], w) * f1;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[n][i] = o[n][i] * f0 + __shfl_xor_sync(0xffffffffu, o[n][i], w) * f1;
+                for (int c = 0; c < 4; ++c) {
+                    o[n][c].x = o[n][c].x * f0 + __shfl_xor_sync(0xffffffffu, o[n][c].x, w) * f1;
+                    o[n][c].y = o[n][c].y * f0 + __shfl_xor_sync(0xffffffffu, o[n][c].y, w) * f1;
+                }
                 m[n] = mn;
             }
             if (lane < LP) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) so[warp][n][e0 + i] = o[n][i];
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<float2 *>(&so[warp][n][e0 + 2 * c]) = o[n][c];
             }
             if (lane == 0) {
                 sm[warp][n] = m[n];
@@ -276,37 +416,76 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm) window_cc_kernel(const A
                 }
             }
         }
+        __syncthreads();   // the rings are filled again
     }
 }
 
 // ---------------------------------------------------------------------------
 // Merge of the streams that several columns share, one (column, KV head, row
 // group) a CTA row: the at most one stream that column q begins and does not
-// end.  A warp a query row; the lanes hold the parts' maxima and sums, then
-// the row's elements.  Bound by its launch and one chain of loads.
+// end.  A warp a query row.  Up to 32 parts and a head_dim of fours up to 128:
+// lane k holds part k's maximum and sum, and four elements of eight parts at a
+// time, so that up to 8 parts cost one round of loads behind the split's.  Bound
+// by its launch and those two rounds.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kMergeWarps * 32) window_merge_kernel(const Args a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_trigger();
     const int HP = a.H_kv * a.groups;
     const int q = (int)blockIdx.x / HP, hp = (int)blockIdx.x - q * HP;
+    const int g = hp / a.groups, i0 = (hp - g * a.groups) * a.NR;
+    const int n = blockIdx.y * kMergeWarps + warp, t = (i0 + n) / a.G;
+    const int64_t in_req = ((int64_t)t * a.H_q + g * a.G + (i0 + n - t * a.G)) * a.D, req = (int64_t)a.q_len * a.H_q * a.D;
+    const bool there = n < min(a.NR, a.q_len * a.G - i0);
+    pdl_wait();
+    pdl_trigger();
     const int2 e = a.ws_split[q];
     const int r = e.x, nch = e.y;
-    if (nch == 0) return;
-    const int g = hp / a.groups, i0 = (hp - g * a.groups) * a.NR;
-    const int n = blockIdx.y * kMergeWarps + warp;
-    if (n >= min(a.NR, a.q_len * a.G - i0)) return;
+    if (nch == 0 || !there) return;
     auto at = [&](int c) { return ((int64_t)hp * (2 * a.P) + (c == 0 ? a.P + q : q + c)) * a.NR + n; };
+    T *out = static_cast<T *>(a.out) + r * req + in_req;
+    if (nch <= 32 && a.D <= 128 && a.D % 4 == 0) {
+        const bool act = 4 * lane < a.D;
+        const float2 ml = lane < nch ? *reinterpret_cast<const float2 *>(a.ws_ml + at(lane) * 2) : make_float2(-INFINITY, 0.f);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float w = 0.f, inv = 0.f;
+        for (int c = 0; c < nch; c += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = act && c + k < nch ? *reinterpret_cast<const float4 *>(a.ws_o + at(c + k) * a.D + 4 * lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c == 0) {
+                float M = ml.x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                w = M == -INFINITY ? 1.f : exp2f(ml.x - M);
+                float l = w * ml.y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                inv = inverse(l);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, (c + k) & 31);
+                acc.x = fmaf(wk, v[k].x, acc.x), acc.y = fmaf(wk, v[k].y, acc.y);
+                acc.z = fmaf(wk, v[k].z, acc.z), acc.w = fmaf(wk, v[k].w, acc.w);
+            }
+        }
+        if (act) {
+            put(out + 4 * lane, acc.x * inv);
+            put(out + 4 * lane + 1, acc.y * inv);
+            put(out + 4 * lane + 2, acc.z * inv);
+            put(out + 4 * lane + 3, acc.w * inv);
+        }
+        return;
+    }
     float M = -INFINITY;
     for (int c = lane; c < nch; c += 32) M = fmaxf(M, a.ws_ml[at(c) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const int t = (i0 + n) / a.G;
-    T *out = static_cast<T *>(a.out) + (((int64_t)r * a.q_len + t) * a.H_q + g * a.G + (i0 + n - t * a.G)) * a.D;
     for (int d0 = 0; d0 < a.D; d0 += 128) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
         for (int c0 = 0; c0 < nch; c0 += 32) {
@@ -375,7 +554,8 @@ static bool make_plan(int32_t num_reqs, int32_t q_len, int32_t num_q_heads, int3
     const int64_t sms = current_sm_count();
     if (nq > 65536 || nq * num_kv_heads > (1 << 24)) return false;
     p->tc = make_split(nq, num_kv_heads, kTcRows, sms);
-    p->cc = make_split(nq, num_kv_heads, kCcRows, kCcPerSm * sms);
+    const int64_t per_sm = nq <= 4 ? kCcPerSm<4> : kCcPerSm<kCcRows>;
+    p->cc = make_split(nq, num_kv_heads, kCcRows, per_sm * sms);
     int64_t rows = p->cc.rows(), P = p->cc.P;
     if (head_dim == 128) {
         rows = p->tc.rows() > rows ? p->tc.rows() : rows;
@@ -390,8 +570,16 @@ static bool make_plan(int32_t num_reqs, int32_t q_len, int32_t num_q_heads, int3
 
 template <typename T, typename KV, int NR, int LP>
 static int launch_cc(const Args &a, bool vec, cudaStream_t st) {
-    const cudaError_t e = launch_pdl(window_cc_kernel<T, KV, NR, LP>, dim3((unsigned)(a.P * a.H_kv * a.groups)),
-                                     dim3(kCcThreads), 0, st, a, vec);
+    auto kern = window_cc_kernel<T, KV, NR, LP>;
+    constexpr int smem = kCcSmem<KV, NR, LP>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return launch_status();
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)(a.P * a.H_kv * a.groups)), dim3(kCcThreads), smem, st, a, vec);
     if (e != cudaSuccess) set_cuda_error(e);
     return launch_status();
 }
