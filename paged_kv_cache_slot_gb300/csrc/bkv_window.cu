@@ -42,9 +42,11 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 // Rows come by cp.async through a ring of kStages steps in shared memory, each
 // lane copying exactly what it reads itself, so that the only wait is its own:
 // 12 KB a warp are in flight however many registers the rows' arithmetic takes
-// (with the rows in registers, one step at a time, 16 requests of 3000 positions,
-// 15 / 5 heads of 64, fp32: 57 us; 32 / 8 of 64, E4M3: 90).  Block entries are
-// loaded a step before their rows.  Multiply-adds go two an instruction.
+// (with the rows in registers, one step at a time, 64 requests of 6000 positions,
+// 32 / 8 heads of 64, bf16: 505 us in place of 275).  Where the rows stand is worked
+// out for 32 positions at a time, a lane each, their block entries loaded that much
+// ahead, and handed to the lanes that copy them by shuffles.  Multiply-adds go two
+// an instruction.
 // ---------------------------------------------------------------------------
 constexpr int kCcThreads = 128;
 constexpr int kCcTile = 64;
@@ -133,37 +135,54 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         const Span s = span_of(a, lens[x.r]);
         const int v_end = min((x.f + x.nt) * kCcTile, s.len);
         const int32_t *table = a.bt + (int64_t)x.r * a.bt_stride;
-        const int v_first = x.f * kCcTile + warp * PW * U + sub;
-        constexpr int kStepPos = 4 * PW * U;   // positions the CTA takes a step
+        constexpr int kStepPos = 4 * PW * U, kMine = PW * U;   // positions the CTA, and a warp of it, takes a step
+        constexpr int kBatch = 32 / kMine;                      // steps whose places are worked out together
+        const int v_first = x.f * kCcTile + warp * kMine;
         const int steps = (v_end - x.f * kCcTile + kStepPos - 1) / kStepPos;
         auto block_of = [&](int32_t p) { return shift >= 0 ? p >> shift : p / a.bs; };
-        // this lane's position u of step i: its block entry (0 where there is none) as it is in the table
-        auto fetch = [&](int i, int32_t (&ent)[U]) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v_first + i * kStepPos + u * PW;
-                ent[u] = 0;
-                if (i < steps && v < v_end) {
-                    const int32_t lb = block_of(s.pos(v));
-                    if (lb < a.bt_cols) ent[u] = __ldg(table + lb);
-                }
-            }
+        // Positions at or below last_lo (and from first_hi on, or below `sinks`) are seen by every row of the group.
+        const int32_t t_lo = s.L - a.q_len + tok_lo, t_hi = s.L - a.q_len + tok_hi;
+        const int32_t last_lo = a.causal ? t_lo : s.L - 1;
+        const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
+        // lane k of batch b: position k % kMine of step b kBatch + k / kMine
+        auto span_at = [&](int b) { return v_first + (b * kBatch + lane / kMine) * kStepPos + lane % kMine; };
+        auto fetch = [&](int b) -> int32_t {   // its block entry as it is in the table, 0 where there is none
+            const int v = span_at(b);
+            if (v >= v_end) return 0;
+            const int32_t lb = block_of(s.pos(v));
+            return lb < a.bt_cols ? __ldg(table + lb) : 0;
         };
-        // the rows (and scales) of step i into its ring slot; which of them are there, as bits
-        auto issue = [&](int i, const int32_t (&ent)[U]) -> uint32_t {
+        // where batch `b` stands: the row's first element of this head (-1: nothing there) and, E4M3, its scales; and,
+        // as bits by lane, which positions are there, and are seen by every row
+        int64_t place = -1;
+        int32_t scale_at = 0;
+        uint32_t there_bits = 0u, all_bits = 0u;
+        auto locate = [&](int b, int32_t ent) {
+            const bool there = ent > 0 && ent < a.total_blocks;
+            const int32_t p = s.pos(span_at(b));
+            place = -1;
+            if (there) {
+                place = (((int64_t)ent * a.bs + (p - block_of(p) * a.bs)) * a.H_kv + g) * a.D;
+                scale_at = ent * a.H_kv + g;
+            }
+            there_bits = __ballot_sync(0xffffffffu, there);
+            all_bits = __ballot_sync(0xffffffffu, there && p <= last_lo && (p >= first_hi || p < a.sinks));
+        };
+        // the rows (and scales) of step i, of the batch that was located last, into its ring slot; its positions that
+        // are there, and, from bit 16 on, that every row sees
+        auto issue = [&](int i) -> uint32_t {
             const uint32_t slot = (uint32_t)(i % kStages) * S::kStep;
-            uint32_t bits = 0u;
+            const int from = (i % kBatch) * kMine;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool there = ent[u] > 0 && ent[u] < a.total_blocks;
-                const int32_t p = s.pos(v_first + i * kStepPos + u * PW);
-                const int32_t b = there ? ent[u] : 0, off = there ? p - block_of(p) * a.bs : 0;
-                const int64_t at = (((int64_t)b * a.bs + off) * a.H_kv + g) * a.D + (ne > 0 ? e0 : 0);
-                bits |= there ? 1u << u : 0u;
-                const int n = there && ne > 0 ? kPiece : 0;
+                const int64_t at = __shfl_sync(0xffffffffu, place, from + u * PW + sub);
+                const int n = at >= 0 && ne > 0 ? kPiece : 0;
+                const int64_t mine = n > 0 ? at + e0 : 0;
+                int32_t sc = 0;
+                if constexpr (kF8) sc = __shfl_sync(0xffffffffu, scale_at, from + u * PW + sub);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const KV *src = static_cast<const KV *>(kv ? a.v : a.k) + at;
+                    const KV *src = static_cast<const KV *>(kv ? a.v : a.k) + mine;
                     constexpr int kRow = kPieces * 32 * kPiece;
                     if (vec) {
 #pragma unroll
@@ -183,24 +202,25 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                     }
                     if constexpr (kF8)   // (behind the rows, a word a lane)
                         copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((u * 2 + kv) * 32 + lane) * 4,
-                                      (kv ? a.vs : a.ks) + (int64_t)b * a.H_kv + g, there ? 4 : 0);
+                                      (kv ? a.vs : a.ks) + (at >= 0 ? sc : 0), at >= 0 ? 4 : 0);
                 }
             }
-            return bits;
+            constexpr uint32_t kBits = (1u << kMine) - 1u;
+            return ((there_bits >> from) & kBits) | ((all_bits >> from) & kBits) << 16;
         };
-        uint32_t there = 0u;   // U bits a ring slot
-        {
-            int32_t ent[kStages - 1][U];
+        // bits of the steps in the ring, the next one to work on first
+        uint32_t fifo[kStages];
+        int32_t ent = fetch(0), ent_next = fetch(1);
 #pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) fetch(i, ent[i]);
-#pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) {
-                there |= issue(i, ent[i]) << (U * i);
-                asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (i % kBatch == 0) {
+                locate(i / kBatch, ent);
+                ent = ent_next;
+                ent_next = fetch(i / kBatch + 2);
             }
+            fifo[i] = issue(i);
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        int32_t ent[U];
-        fetch(kStages - 1, ent);
         float2 qv[NR][4], o[NR][4];
         float m[NR], l[NR];
 #pragma unroll
@@ -226,10 +246,6 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 if (lb >= a.bt_cols || __ldg(table + lb) >= a.total_blocks) atomicAdd(a.err, 1);
             }
         }
-        // Positions at or below last_lo (and from first_hi on, or below `sinks`) are seen by every row of the group.
-        const int32_t t_lo = s.L - a.q_len + tok_lo, t_hi = s.L - a.q_len + tok_hi;
-        const int32_t last_lo = a.causal ? t_lo : s.L - 1;
-        const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
         const uint32_t full = (1u << rows) - 1u;
         // which of the rows see position p, as bits
         auto seen = [&](int32_t p) {
@@ -249,14 +265,23 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         };
         for (int i = 0; i < steps; ++i) {
             {
-                const int j = i + kStages - 1, at = U * (j % kStages);
-                there = (there & ~(((1u << U) - 1u) << at)) | issue(j, ent) << at;
+                const int j = i + kStages - 1;
+                if (j % kBatch == 0) {
+                    locate(j / kBatch, ent);
+                    ent = ent_next;
+                    ent_next = fetch(j / kBatch + 2);
+                }
+                fifo[kStages - 1] = issue(j);
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                fetch(j + 1, ent);
             }
+            const uint32_t here = fifo[0];
+#pragma unroll
+            for (int k = 0; k < kStages - 1; ++k) fifo[k] = fifo[k + 1];
+            // every position of the step is there, and every row sees it
+            constexpr uint32_t kBits = (1u << kMine) - 1u;
+            const bool every = here == (kBits | kBits << 16);
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
             const uint8_t *slot = ring + (i % kStages) * S::kStep;
-            const uint32_t here = there >> (U * (i % kStages));
             auto held = [&](int u, int kv) {
                 Eight<KV> e;
                 const uint8_t *src = slot + (u * 2 + kv) * kPieces * (32 * kPiece);
@@ -274,15 +299,14 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             };
             float sc[U][NR], vs[U];
             uint32_t see[U];
-            bool every = true;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int v = v_first + i * kStepPos + u * PW;
-                const int32_t p = s.pos(v);
-                const bool in = (here >> u) & 1u;
-                see[u] = in && p <= last_lo && (p >= first_hi || p < a.sinks) ? full : 0u;
-                if (in && see[u] == 0u) see[u] = seen(p);
-                every &= see[u] == full;
+                see[u] = full;
+                if (!every) {
+                    const int k = u * PW + sub;
+                    if (!((here >> k) & 1u)) see[u] = 0u;
+                    else if (!((here >> (16 + k)) & 1u)) see[u] = seen(s.pos(v_first + i * kStepPos + k));
+                }
                 const Eight<KV> k = held(u, 0);
                 float2 acc[NR];
 #pragma unroll
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                     if constexpr (kF8) sc[u][n] *= vs[u];
                 }
             // a value that some rows do not see reaches only those that do, whatever it is
-            if (__all_sync(0xffffffffu, every)) {
+            if (every) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const Eight<KV> val = held(u, 1);
