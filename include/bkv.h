@@ -754,8 +754,8 @@ int bkv_verify_draft_tree(const float *target_probs, int64_t target_req_stride, 
  *   blocks, once (those tokens get slot -1); every block that the free list lacks
  *   (-1); a step of more than max_num_tokens tokens, once (those past it are not
  *   listed).
- *   INVALID_ARG: block_size <= 0, negative sizes, bt_stride < bt_cols, null
- *   pointers, context_lens the same array as an input.
+ *   INVALID_ARG: block_size <= 0, negative sizes, num_reqs above 2^30, bt_stride <
+ *   bt_cols, null pointers, context_lens the same array as an input.
  */
 int bkv_build_step(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs, const int32_t *free_blocks,
                    int32_t num_free, int32_t block_size, int32_t *block_table, int64_t bt_stride, int32_t bt_cols,
@@ -847,7 +847,8 @@ size_t bkv_paged_decode_window_workspace_size(int32_t num_reqs, int32_t q_len, i
  *   out must not overlap q or the caches.  Other arguments as
  *   bkv_paged_decode_swa.
  *   INVALID_ARG: as bkv_paged_decode_swa, or num_sinks < 0, max_context_len above
- *   2^26, or q_len * (num_q_heads / num_kv_heads) above 65536.
+ *   2^26, block_size or q_len * (num_q_heads / num_kv_heads) above 65536, or
+ *   q_len * num_q_heads above 2^24.
  *   UNSUPPORTED: dtype not BKV_BF16 / BKV_F32, head_dim > 256 or odd.
  */
 int bkv_paged_decode_sink(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         // where batch `b` stands: the row's first element of this head (-1: nothing there) and, E4M3, its scales; and,
         // as bits by lane, which positions are there, and are seen by every row
         int64_t place = -1;
-        int32_t scale_at = 0;
+        int64_t scale_at = 0;
         uint32_t there_bits = 0u, all_bits = 0u;
         auto locate = [&](int b, int32_t ent) {
             const bool there = ent > 0 && ent < a.total_blocks;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             place = -1;
             if (there) {
                 place = (((int64_t)ent * a.bs + (p - block_of(p) * a.bs)) * a.H_kv + g) * a.D;
-                scale_at = ent * a.H_kv + g;
+                scale_at = (int64_t)ent * a.H_kv + g;
             }
             there_bits = __ballot_sync(0xffffffffu, there);
             all_bits = __ballot_sync(0xffffffffu, there && p <= last_lo && (p >= first_hi || p < a.sinks));
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 const int64_t at = __shfl_sync(0xffffffffu, place, from + u * PW + sub);
                 const int n = at >= 0 && ne > 0 ? kPiece : 0;
                 const int64_t mine = n > 0 ? at + e0 : 0;
-                int32_t sc = 0;
+                int64_t sc = 0;
                 if constexpr (kF8) sc = __shfl_sync(0xffffffffu, scale_at, from + u * PW + sub);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
@@ -673,7 +673,7 @@ static int attend(const void *q, const void *k_cache, const void *v_cache, const
     a.total_blocks = total_blocks;
     a.scale_log2 = softmax_scale * kLog2e;
     a.causal = mask_mode == BKV_MASK_CAUSAL;
-    a.window = sliding_window;
+    a.window = sliding_window < max_context_len ? sliding_window : 0;   // (a window that reaches every position is none)
     a.sinks = num_sinks;
     a.dtype = dtype;
     a.err = err_count;

@@ -109,6 +109,15 @@ def test_masks_and_scales(fp8, causal, window, sinks):
         assert bool((c.out[1, :3] == 0).all()) and bool((c.out[2, :1] == 0).all())
 
 
+@pytest.mark.parametrize("fp8,d", [(False, 128), (True, 128), (False, 64), (True, 64)])
+@pytest.mark.parametrize("window", [300, 299, (1 << 31) - 1])
+def test_windows_as_long_as_any_request(fp8, d, window):
+    """A window that reaches every position is none: query tokens before the request's first position, whose window
+    begins far below zero, see what the mask mode leaves."""
+    _check(Blocks([1, 2, 8, 150, 300], 9, 4, 2, d, 16, fp8=fp8, window=window, sinks=0), causal=False)
+    _check(Blocks([1, 2, 8, 150, 300], 9, 4, 2, d, 16, fp8=fp8, window=window, sinks=3))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_null_entries_and_errors(fp8):
     """Null entries in the window and among the first tokens' blocks, whole requests of them; ids past the cache, tables

@@ -44,8 +44,8 @@ def test_build_step_refusals(lib):
         return entry(*dict(base, **kw).values())
 
     some = {n: 64 * (i + 1) for i, n in enumerate(("cached", "new", "free", "bt", "ctx", "qsl", "req", "pos", "slots", "used"))}
-    for bad in (dict(nr=-1), dict(nf=-1), dict(bs=0), dict(cols=-1), dict(st=3), dict(mx=-1), dict(ctx=some["cached"]),
-                dict(ctx=some["new"]), *({n: NULL} for n in some)):
+    for bad in (dict(nr=-1), dict(nr=(1 << 30) + 1), dict(nf=-1), dict(bs=0), dict(cols=-1), dict(st=3), dict(mx=-1),
+                dict(ctx=some["cached"]), dict(ctx=some["new"]), *({n: NULL} for n in some)):
         assert call(**dict(some, **bad)) == bkv.BKV_ERR_INVALID_ARG, bad
 
 
