@@ -27,19 +27,32 @@
 //   32) of one MMA, summed as they are read.  Row sums take fp32 weights.
 //   bf16 caches: weights are rounded to bf16 (2^-8 of each), and the row sums take
 //   the rounded ones.
+// * O stays in tensor memory over a unit, one of each softmax warpgroup (even and
+//   odd tiles), joined at the unit's end.  The reference that weights are taken
+//   from, ref, is not the running maximum: it moves when a weight passes 2^8 (and
+//   O is rescaled then), which a unit's first tiles do and few others.  A tile's
+//   warps agree on it by a vote over a barrier, and work out their weights while
+//   the others arrive.  (E4M3 weights of a fresh reference are at most 2^5, so that
+//   what grows later stays below 448, and 2^-14 of the largest is still a code.)
+// * P is MN-major: a position's 16 weights are one 32-byte span, one or two stores
+//   a thread, with no transposition and no bank conflicts.
+// * Four S tiles let the S issuer run two tiles ahead of each warpgroup.
 // * Warp roles (384 threads): 0 gathers K tiles, 2 V tiles through the block table
 //   by 3-D TMA boxes (head_dim half, one head, rows of a block), 1 and 3 issue the
 //   MMAs of S and of P V, 4-7 and 8-11 are two softmax warpgroups on alternate
-//   tiles.  Warp 2 also brings the queries, and splits them, so that no launch has
-//   to come before this one.  K and V have rings of 96 KB each.  Block entries are
-//   loaded 32 segments ahead, a lane each, and a unit's queries with its first
-//   ones; the scales follow by cp.async, whose arrival the tile's mask barrier
-//   counts.
+//   tiles, the one that has a unit's last tile writes its output.  Warp 2 also
+//   brings the queries, and splits them, so that no launch has to come before this
+//   one.  K and V have rings of 96 KB each.  Block entries are loaded 32 segments
+//   ahead, a lane each, and a unit's queries with its first ones; the scales follow
+//   by cp.async, whose arrival the tile's mask barrier counts.
 // * V rows that no query row of the group sees, and segments that were not loaded,
 //   are zeroed before P V; a row that only some see is, too, if it is not finite,
-//   and those that see it become NaN.
+//   and those that see it become NaN.  That lies behind the store of P, when the
+//   V tile has landed anyway.
 // * Every wait is bounded (~2 s), after which the CTA records 1 << 24 in
 //   err_count, frees its tensor memory and exits.
+//
+// FIGURES
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -558,14 +571,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + wg * 4 * kN;
         uint32_t gphase = 0;
         // Bounded barrier of the warpgroup's four warps.
-        auto group_sync = [&]() -> bool {
+        auto group_arrive = [&] {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_group(wg));
+        };
+        auto group_wait = [&]() -> bool {
             bool r = false;
             for (int i = 0; i < 64 && !r; ++i) r = __all_sync(0xffffffffu, mbar_test(bar_group(wg), gphase));
             if (!r) r = mbar_wait_warp(bar_group(wg), gphase, abort_flag);
             gphase ^= 1u;
             return r;
+        };
+        auto group_sync = [&]() -> bool {
+            group_arrive();
+            return group_wait();
         };
         auto load_o = [&](float (&v)[NQ]) {
             if constexpr (kF8) tmem_ld_sum2<NQ>(o_col, v);
@@ -654,8 +673,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
-                // Does a reference have to be set or moved?  The warpgroup's warps agree on it.
-                bool move = (have & every) != every;
+                // The weights as they go to P V (E4M3: NQ / 4 words of first parts, then the second ones), and into the sums.
+                uint32_t pw[NQ / 2];
+                auto weigh = [&] {
+                    if constexpr (kF8) {
+#pragma unroll
+                        for (int n = 0; n < NQ; n += 4) {
+                            float w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                w[i] = fast_exp2(sv[n + i]);
+                                lsum[n + i] = fmaf(w[i], rv, lsum[n + i]);
+                            }
+                            uint32_t h0, h1, l0, l1;
+                            split2(w[0], w[1], h0, l0);
+                            split2(w[2], w[3], h1, l1);
+                            pw[n / 4] = __byte_perm(h0, h1, 0x5410);
+                            pw[NQ / 4 + n / 4] = __byte_perm(l0, l1, 0x5410);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NQ; n += 2) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(fast_exp2(sv[n]), fast_exp2(sv[n + 1]));
+                            pw[n / 2] = *reinterpret_cast<const uint32_t *>(&b2);
+                            lsum[n] += __uint_as_float(pw[n / 2] << 16);
+                            lsum[n + 1] += __uint_as_float(pw[n / 2] & 0xffff0000u);
+                        }
+                    }
+                };
+                // Does a reference have to be set or moved?  The warpgroup's warps agree on it; a warp that sees no need
+                // works out its weights while the others arrive.
+                bool move = (have & every) != every, weighed = false;
                 if (!move) {
                     float top = fmaxf(sv[0], sv[1]);
 #pragma unroll
@@ -663,7 +711,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool up = __any_sync(0xffffffffu, top > kPMax);
                     uint32_t *flags = reinterpret_cast<uint32_t *>(smem + C::kOffFlag) + (wg * 2 + (int)par) * 4;
                     if (lane == 0) flags[wq] = up;
-                    if (!group_sync()) {
+                    group_arrive();
+                    if (!up) {
+                        weigh();
+                        weighed = true;
+                    }
+                    if (!group_wait()) {
                         ok = false;
                         break;
                     }
@@ -671,6 +724,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     move = (f.x | f.y | f.z | f.w) != 0u;
                 }
                 if (move) {
+                    if (weighed) {
+                        // out of the sums again: a sum is off by its own rounding, and the same weights follow
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+                            lsum[n] -= kF8 ? fast_exp2(sv[n]) * rv : __bfloat162float(__float2bfloat16_rn(fast_exp2(sv[n])));
+                    }
                     // (the last reading of these maxima lies behind a barrier below)
                     const float wmax = warp_reduce_rows<true, NQ>(sv, lane);
                     if (red_writer) rm[red_row * 4 + wq] = wmax;
@@ -714,6 +773,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         tmem_st_wait();
                     }
+                    weigh();
                 }
                 // P, once the last P V has read its buffer
                 if (j >= 2 && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) {
@@ -721,38 +781,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 }
                 if constexpr (kF8) {
-                    uint32_t hi[NQ / 4], lo[NQ / 4];
-#pragma unroll
-                    for (int n = 0; n < NQ; n += 4) {
-                        float w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            w[i] = fast_exp2(sv[n + i]);
-                            lsum[n + i] = fmaf(w[i], rv, lsum[n + i]);
-                        }
-                        uint32_t h0, h1, l0, l1;
-                        split2(w[0], w[1], h0, l0);
-                        split2(w[2], w[3], h1, l1);
-                        hi[n / 4] = __byte_perm(h0, h1, 0x5410);
-                        lo[n / 4] = __byte_perm(l0, l1, 0x5410);
-                    }
-                    put_words(p_hi, hi);
-                    put_words(p_lo, lo);
+                    put_words(p_hi, reinterpret_cast<const uint32_t(&)[NQ / 4]>(pw[0]));
+                    put_words(p_lo, reinterpret_cast<const uint32_t(&)[NQ / 4]>(pw[NQ / 4]));
+                } else if constexpr (NQ == 16) {
+                    put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(pw[0]));
+                    put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(pw[4]));
                 } else {
-                    uint32_t w[NQ / 2];
-#pragma unroll
-                    for (int n = 0; n < NQ; n += 2) {
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(fast_exp2(sv[n]), fast_exp2(sv[n + 1]));
-                        w[n / 2] = *reinterpret_cast<const uint32_t *>(&b2);
-                        lsum[n] += __uint_as_float(w[n / 2] << 16);
-                        lsum[n + 1] += __uint_as_float(w[n / 2] & 0xffff0000u);
-                    }
-                    if constexpr (NQ == 16) {
-                        put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(w[0]));
-                        put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(w[4]));
-                    } else {
-                        put_words(p_hi, w);
-                    }
+                    put_words(p_hi, pw);
                 }
                 if (!tile_all) {
                     // V rows that must not reach P V, once the tile is there.  (Behind the wait for the warpgroup's last
