@@ -93,8 +93,9 @@ struct TcCfg {
     static constexpr int kOffQ = 2 * kStages * kSlot;
     static constexpr int kPBytes = kTcTile * 32;                      // a position's weights: 16 bf16, or 16 + 16 E4M3 parts
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
-    static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][16][4 warps] floats
-    static constexpr int kOffFlag = kOffMax + 2 * 4 * kN * 4;         // [warpgroup][2][4 warps] words
+    static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][2][16][4 warps] floats
+    static constexpr int kOffRows = kOffMax + 4 * 4 * kN * 4;         // [softmax warp][3][16] floats
+    static constexpr int kOffFlag = kOffRows + 8 * 3 * kN * 4;        // [warpgroup][2][4 warps] words
     static constexpr int kOffSum = kOffFlag + 2 * 2 * 4 * 4;          // [warpgroup][2][16][4] floats
     static constexpr int kOffXm = kOffSum + 4 * kN * 4 * 4;           // [set][16] (max, sum)
     static constexpr int kOffQs = kOffXm + kSets * kN * 8;            // [set][16] scores' factors
@@ -107,10 +108,12 @@ struct TcCfg {
     static constexpr int kOffSums = kOffAbort + 4;                    // a word a warp: prefix sum's scratch
     static constexpr int kOffPre = (kOffSums + kTcThreads / 32 * 4 + 15) / 16 * 16;
     static constexpr int kOffLens = kOffPre + (kMaxReqs + 4) * 4;
-    static constexpr int kOffRow = kOffLens + kMaxReqs * 4;           // [16] where a group's rows stand in their request
+    static constexpr int kOffRow = (kOffLens + kMaxReqs * 4 + 15) / 16 * 16;   // [16] where a group's rows stand in their request
     static constexpr int kSmem = kOffRow + kN * 4 + 1024;             // slack for 1024 alignment
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA exceeds the sm_103a limit");
-    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
+    static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0 && kOffScale % 16 == 0 && kOffRow % 16 == 0 &&
+                      kOffQs % 16 == 0,
+                  "alignment");
     static_assert(kStages + kSTiles < kRing, "a ring word is rewritten behind its readers");
 };
 
@@ -568,7 +571,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool red_writer = reduced_writer<NQ>(lane);
         const int flip = (row >> 2) & 1;
         uint8_t *p_hi = smem + C::kOffP + wg * C::kPBytes + row * 32 + 16 * flip, *p_lo = p_hi + 16 - 32 * flip;
-        float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + wg * 4 * kN;
+        float *rm = reinterpret_cast<float *>(smem + C::kOffMax) + wg * 2 * 4 * kN;
+        // What belongs to a query row and not to a position is worked out by one lane a row (lanes past NQ repeat others)
+        // and handed to the warp through shared memory: three arrays of 16, a warp's own.  Every use of one ends with a
+        // __syncwarp further on, before the next.
+        float *warp_rows = reinterpret_cast<float *>(smem + C::kOffRows) + (warp - kWarpS) * 3 * kN;
+        const int my_row = lane & (NQ - 1);
+        auto hand_out = [&](int k, float mine) {
+            if (lane < NQ) warp_rows[k * kN + lane] = mine;
+        };
+        auto take = [&](int k, float (&v)[NQ]) {   // behind a __syncwarp
+#pragma unroll
+            for (int n = 0; n < NQ; n += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(warp_rows + k * kN + n);
+                v[n] = f.x, v[n + 1] = f.y, v[n + 2] = f.z, v[n + 3] = f.w;
+            }
+        };
+        uint32_t moves = 0;
         uint32_t gphase = 0;
         // Bounded barrier of the warpgroup's four warps.
         auto group_arrive = [&] {
@@ -624,7 +643,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // least six behind this unit's last, and its S tile's last reader this warpgroup, past this unit.
                 if (!mbar_wait_warp(bar_qscale(us & (kQSets - 1)), (uint32_t)(us / kQSets) & 1u, abort_flag)) break;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? qs[(us & (kQSets - 1)) * kN + n] : 0.f;
+                for (int n = 0; n < NQ; n += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qs + (us & (kQSets - 1)) * kN + n);
+                    cs[n] = f.x, cs[n + 1] = f.y, cs[n + 2] = f.z, cs[n + 3] = f.w;
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? cs[n] : 0.f;
             }
             for (int jt = 0; jt < x.nt; ++jt, ++j, vring.advance(kStages)) {
                 if ((j & 1) != wg) continue;
@@ -730,40 +754,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int n = 0; n < NQ; ++n)
                             lsum[n] -= kF8 ? fast_exp2(sv[n]) * rv : __bfloat162float(__float2bfloat16_rn(fast_exp2(sv[n])));
                     }
-                    // (the last reading of these maxima lies behind a barrier below)
+                    // (two sets of maxima in turn: one is written again behind the next move's barrier, which all
+                    // passed after reading it)
+                    float *tops = rm + (moves++ & 1u) * (4 * kN);
                     const float wmax = warp_reduce_rows<true, NQ>(sv, lane);
-                    if (red_writer) rm[red_row * 4 + wq] = wmax;
+                    if (red_writer) tops[red_row * 4 + wq] = wmax;
                     if (!group_sync()) {
                         ok = false;
                         break;
                     }
-                    float top[NQ];
+                    const float4 t4 = *reinterpret_cast<const float4 *>(tops + my_row * 4);
+                    const float top = fmaxf(max3(t4.x, t4.y, t4.z), t4.w);
+                    const bool had = (have >> my_row) & 1u;
+                    const bool to = had ? top > kPMax : top > -INFINITY;
+                    const float down = to ? top - kPExp<kF8> : 0.f;
+                    hand_out(0, down);
+                    hand_out(1, had ? fast_exp2(-down) : 1.f);
+                    const bool scale = have != 0u;   // there is something in the sums and in O
+                    have |= __ballot_sync(0xffffffffu, to) & ((1u << NQ) - 1u);
+                    __syncwarp();
+                    float by[NQ];
+                    take(0, by);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        const float4 t4 = *reinterpret_cast<const float4 *>(rm + n * 4);
-                        top[n] = fmaxf(max3(t4.x, t4.y, t4.z), t4.w);
+                        ref[n] += by[n];
+                        sv[n] -= by[n];
                     }
-                    const bool first = jt < 2;   // nothing in O yet
-                    // the last P V into O, and the readers of the maxima
-                    if ((!first && !mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) || !group_sync()) {
-                        ok = false;
-                        break;
-                    }
-                    float corr[NQ];
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const bool had = (have >> n) & 1u;
-                        const bool to = had ? top[n] > kPMax : top[n] > -INFINITY;
-                        const float by = to ? top[n] - kPExp<kF8> : 0.f;
-                        corr[n] = had ? fast_exp2(-by) : 1.f;
-                        ref[n] += by;
-                        sv[n] -= by;
-                        lsum[n] *= corr[n];
-                        have |= to ? 1u << n : 0u;
-                    }
-                    if (!first) {
+                    if (scale) {
+                        if (!mbar_wait_warp(bar_ofull(wg), par ^ 1u, abort_flag)) {   // the last P V into O
+                            ok = false;
+                            break;
+                        }
                         tc_fence_after();
-                        float o[NQ];
+                        float corr[NQ], o[NQ];
+                        take(1, corr);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) lsum[n] *= corr[n];
 #pragma unroll
                         for (int h = 0; h < (kF8 ? 2 : 1); ++h) {
                             tmem_ld_cols<NQ>(o_col + 16u * h, o);
@@ -842,19 +868,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++mu;
             const float wsum = warp_reduce_rows<false, NQ>(lsum, lane);
             if (red_writer) sums[red_row * 4 + wq] = wsum;
+            if (lane == 0) {
+#pragma unroll
+                for (int n = 0; n < NQ; n += 4)
+                    *reinterpret_cast<float4 *>(warp_rows + n) = make_float4(ref[n], ref[n + 1], ref[n + 2], ref[n + 3]);
+            }
             // the warpgroup's last tile here is j - 1 or j - 2
             const int last = (j - 1 - wg) >> 1;
-            if (!group_sync() || !mbar_wait_warp(bar_ofull(wg), (uint32_t)last & 1u, abort_flag)) break;
-            tc_fence_after();
-            float o[NQ];
-            load_o(o);
-            auto total = [&](int n) {
-                const float4 t4 = *reinterpret_cast<const float4 *>(sums + n * 4);
-                return (t4.x + t4.y) + (t4.z + t4.w);
-            };
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-                if (!((have >> n) & 1u)) ref[n] = -INFINITY;   // no key, or none whose score is a number
+            if (!group_sync()) break;
+            const float4 s4 = *reinterpret_cast<const float4 *>(sums + my_row * 4);
+            float my_sum = (s4.x + s4.y) + (s4.z + s4.w);
+            float my_ref = (have >> my_row) & 1u ? warp_rows[my_row] : -INFINITY;   // no key, or none whose score is a number
             // The warpgroup of the unit's last tile finishes it; the other hands its part over through tensor memory and
             // goes on.  A set is written again four exchanges on, behind a P V that follows one of the other's tiles of
             // the exchange after this one, which it begins when it has read this.
@@ -864,49 +888,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float2 *xm = reinterpret_cast<float2 *>(smem + C::kOffXm) + set * kN;
             const uint32_t x_par = (uint32_t)(xs >> 2) & 1u;
             if (both) ++xs;
+            if (!mbar_wait_warp(bar_ofull(wg), (uint32_t)last & 1u, abort_flag)) break;
+            tc_fence_after();
+            float o[NQ];
+            load_o(o);
             if (!finish) {
                 tmem_st_cols<NQ>(x_col, o);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    if (row == n) xm[n] = make_float2(ref[n], total(n));
+                if (row < NQ) xm[row] = make_float2(my_ref, my_sum);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_x(set));
                 continue;
             }
-            float l[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) l[n] = total(n);
+            float f0 = 1.f, f1 = 0.f;
+            float o1[NQ];
             if (both) {
                 if (!mbar_wait_warp(bar_x(set), x_par, abort_flag)) break;
                 tc_fence_after();
-                float o1[NQ];
                 tmem_ld_cols<NQ>(x_col, o1);
+                const float2 ml = xm[my_row];
+                const float mn = fmaxf(my_ref, ml.x);
+                f0 = mn == -INFINITY ? 1.f : fast_exp2(my_ref - mn);
+                f1 = mn == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+                my_sum = my_sum * f0 + ml.y * f1;
+                my_ref = mn;
+            } else {
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const float2 ml = xm[n];
-                    const float mn = fmaxf(ref[n], ml.x);
-                    const float f0 = mn == -INFINITY ? 1.f : fast_exp2(ref[n] - mn);
-                    const float f1 = mn == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
-                    o[n] = o[n] * f0 + o1[n] * f1;
-                    l[n] = l[n] * f0 + ml.y * f1;
-                    ref[n] = mn;
-                }
+                for (int n = 0; n < NQ; ++n) o1[n] = 0.f;
             }
+            if (x.whole) {
+                const float inv = inverse(my_sum);
+                f0 *= inv;
+                f1 *= inv;
+            }
+            hand_out(1, f0);
+            hand_out(2, f1);
+            __syncwarp();
+            float by[NQ];
+            take(1, by);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) o[n] *= by[n];
+            take(2, by);
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) o[n] = fmaf(o1[n], by[n], o[n]);
             if (x.whole) {
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + x.r * req_elems + row;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    if (n < rows) out[row_at[n]] = __float2bfloat16_rn(l[n] == 0.f ? 0.f : __fdividef(o[n], l[n]));
+                for (int n = 0; n < NQ; n += 4) {
+                    const int4 to = *reinterpret_cast<const int4 *>(row_at + n);
+                    if (n < rows) out[to.x] = __float2bfloat16_rn(o[n]);
+                    if (n + 1 < rows) out[to.y] = __float2bfloat16_rn(o[n + 1]);
+                    if (n + 2 < rows) out[to.z] = __float2bfloat16_rn(o[n + 2]);
+                    if (n + 3 < rows) out[to.w] = __float2bfloat16_rn(o[n + 3]);
+                }
             } else {
                 const int64_t at = ((int64_t)hp * (2 * a.P) + x.slot) * a.NR;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    if (n >= rows) break;
-                    a.ws_o[(at + n) * kD + row] = o[n];
-                    if (row == n) *reinterpret_cast<float2 *>(a.ws_ml + (at + n) * 2) = make_float2(ref[n], l[n]);
-                }
+                for (int n = 0; n < NQ; ++n)
+                    if (n < rows) a.ws_o[(at + n) * kD + row] = o[n];
+                if (row < rows) *reinterpret_cast<float2 *>(a.ws_ml + (at + row) * 2) = make_float2(my_ref, my_sum);
             }
         }
     }
