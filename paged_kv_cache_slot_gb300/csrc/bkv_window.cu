@@ -211,6 +211,12 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         // bits of the steps in the ring, the next one to work on first
         uint32_t fifo[kStages];
         int32_t ent = fetch(0), ent_next = fetch(1);
+        Eight<T> raw[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            raw[n].zero();
+            if (n < rows && ne > 0) raw[n].load(static_cast<const T *>(a.q) + out_row(x.r, n) + e0, ne, vec);
+        }
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
             if (i % kBatch == 0) {
@@ -225,26 +231,14 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         float m[NR], l[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            Eight<T> raw;
-            raw.zero();
-            if (n < rows && ne > 0) raw.load(static_cast<const T *>(a.q) + out_row(x.r, n) + e0, ne, vec);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = raw.two(i);
+                const float2 f = raw[n].two(i);
                 qv[n][i] = make_float2(f.x * a.scale_log2, f.y * a.scale_log2);
                 o[n][i] = make_float2(0.f, 0.f);
             }
             m[n] = -INFINITY;
             l[n] = 0.f;
-        }
-        // Bad entries among the blocks that the unit begins, counted once a KV head: every block that the span
-        // reads begins once in it, at its first position there.
-        if (a.err && grp == 0) {
-            for (int v = x.f * kCcTile + (int)threadIdx.x; v < v_end; v += kCcThreads) {
-                const int32_t p = s.pos(v), lb = block_of(p);
-                if (p != lb * a.bs && !(s.gap > 0 && v == s.sb && (s.sb == 0 || lb != block_of(s.sb - 1)))) continue;
-                if (lb >= a.bt_cols || __ldg(table + lb) >= a.total_blocks) atomicAdd(a.err, 1);
-            }
         }
         const uint32_t full = (1u << rows) - 1u;
         // which of the rows see position p, as bits
@@ -384,6 +378,15 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                             if ((see[u] >> n) & 1u) o[n][c] = fma2(make_float2(sc[u][n], sc[u][n]), f, o[n][c]);
                     }
                 }
+            }
+        }
+        // Bad entries among the blocks that the unit begins, counted once a KV head: every block that the span
+        // reads begins once in it, at its first position there.
+        if (a.err && grp == 0) {
+            for (int v = x.f * kCcTile + (int)threadIdx.x; v < v_end; v += kCcThreads) {
+                const int32_t p = s.pos(v), lb = block_of(p);
+                if (p != lb * a.bs && !(s.gap > 0 && v == s.sb && (s.sb == 0 || lb != block_of(s.sb - 1)))) continue;
+                if (lb >= a.bt_cols || __ldg(table + lb) >= a.total_blocks) atomicAdd(a.err, 1);
             }
         }
         // join the warp's sets of lanes, then the warps
