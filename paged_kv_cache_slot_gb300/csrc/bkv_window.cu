@@ -35,9 +35,13 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 //
 // A CTA of four warps walks its column's units for one (KV head, row group).
 // LP lanes hold a position's row, eight elements each, so a warp takes 32 / LP
-// positions at a time and U of those a step.  Each set of LP lanes keeps its own
-// running maximum, sum and output for the NR query rows, and the sets are joined
-// when the unit ends.
+// positions at a time and U of those a step.  A set of LP lanes sums its U NR scores
+// across by halves: at each round a lane hands the other one the half that it does
+// not keep, and ends with one or two scores of one query row, whose maximum, weights
+// and sum are its own to keep; the weights go back through shared memory.  (Every
+// lane with every score took log2 LP shuffles a score and all exponentials LP times:
+// 196 us in place of 172 in the first case below.)  The sets are joined when the
+// unit ends.
 //
 // Rows come by cp.async through a ring of kStages steps in shared memory, each
 // lane copying exactly what it reads itself, so that the only wait is its own:
@@ -46,10 +50,11 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 // block entries loaded that much ahead, and handed to the lanes that copy them by
 // shuffles.  Multiply-adds go two an instruction.
 //
-// 64 requests of 6000, 32 / 8 heads of 64, bf16: 196 us, 4.0 TB/s (rows in registers
+// 64 requests of 6000, 32 / 8 heads of 64, bf16: 172 us, 4.6 TB/s (rows in registers
 // one step at a time 505, places worked out a step at a time 275); fp32 heads of 128:
-// 777 us, 4.1 TB/s.  Bound there by instructions at 12 warps an SM: a score's sum
-// over LP lanes is log2 LP shuffles a row and position.  Small calls are bound by
+// 793 us, 4.0 TB/s; E4M3, heads of 256: 1051 us, 1.5 TB/s.  Bound there by
+// instructions' latency at 12 warps an SM: the rate is one of elements, some 2.3e12 a
+// second for 4 query rows, whatever their bytes.  Small calls are bound by
 // the chain of dependent loads and, more, by the unrolled code's first pass (13
 // requests of up to 5000 in a window of 777, 15 / 5 heads of 64, fp32: 16.5 us, its
 // warps wait 3.0 cycles an instruction for instructions).
@@ -108,11 +113,18 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int32_t pre[kMaxReqs + 1], lens[kMaxReqs], sums[kCcThreads / 32];
     __shared__ float sm[4][NR], sl[4][NR];
+    // A step has N scores a set of lanes.  Their sums over the lanes end with kOwn of them a lane, of one query row, which
+    // keeps that row's maximum and sum with the row's other lanes; the weights go back to all lanes through shared memory
+    // (two buffers in turn, so that one is written behind a __syncwarp that all passed after reading it).
+    constexpr int N = U * NR, kOwn = N > LP ? N / LP : 1, kRowLanes = LP / NR;
+    __shared__ __align__(16) float weights[4][2][PW][N];
     float(*so)[NR][DP] = reinterpret_cast<float(*)[NR][DP]>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * (kStages * S::kStep) + lane * kPiece;   // this lane's part of the warp's ring
     const uint32_t ring_s = shared_at(ring);
     const int sub = lane / LP, e0 = (lane % LP) * 8;   // this lane's position of PW, and elements
+    const int own = (lane % LP) * N / LP, own_n = own / U, own_u = own % U;   // score n U + u: row n, position u
+    const int row_lane = lane & -LP;                   // row n's first lane: row_lane + n kRowLanes
     const int ne = min(max(a.D - e0, 0), 8);
     const int HP = a.H_kv * a.groups;
     const int q = (int)blockIdx.x / HP, hp = (int)blockIdx.x - q * HP;
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         float2 qv[NR][4], o[NR][4];
-        float m[NR], l[NR];
+        float own_m = -INFINITY, own_l = 0.f;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
@@ -243,8 +255,6 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 qv[n][i] = make_float2(f.x * a.scale_log2, f.y * a.scale_log2);
                 o[n][i] = make_float2(0.f, 0.f);
             }
-            m[n] = -INFINITY;
-            l[n] = 0.f;
         }
         const uint32_t full = (1u << rows) - 1u;
         // which of the rows see position p, as bits
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 }
                 return e;
             };
-            float sc[U][NR], vs[U];
+            float v[N];
             uint32_t see[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -317,49 +327,72 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
 #pragma unroll
                     for (int n = 0; n < NR; ++n) acc[n] = fma2(qv[n][c], f, acc[n]);
                 }
-                float ks = 1.f;
-                vs[u] = 1.f;
-                if constexpr (kF8) {
-                    const float *sp = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32) + u * 64 + lane;
-                    ks = sp[0];
-                    vs[u] = fminf(fmaxf(sp[32], kScaleMin), kScaleMax);
-                }
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float d = acc[n].x + acc[n].y;
+                for (int n = 0; n < NR; ++n) v[n * U + u] = acc[n].x + acc[n].y;
+            }
+            // sums over the LP lanes: a lane hands over the half of its scores that the other one keeps
+            {
+                int have = N;
 #pragma unroll
-                    for (int w = LP / 2; w > 0; w >>= 1) d += __shfl_xor_sync(0xffffffffu, d, w);
-                    sc[u][n] = (see[u] >> n) & 1u ? (kF8 ? d * ks : d) : -INFINITY;
+                for (int w = LP / 2; w > 0; w >>= 1) {
+                    if (have > 1) {
+                        have /= 2;
+                        const bool upper = lane & w;
+#pragma unroll
+                        for (int k = 0; k < N / 2; ++k) {
+                            if (k >= have) break;
+                            const float keep = upper ? v[k + have] : v[k], give = upper ? v[k] : v[k + have];
+                            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+                        }
+                    } else {
+                        v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+                    }
                 }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                if constexpr (kF8) v[k] *= reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + lane];
+                if (!every) {
+                    uint32_t bits = see[0];
+#pragma unroll
+                    for (int u = 1; u < U; ++u) bits = own_u + k == u ? see[u] : bits;
+                    if (!((bits >> own_n) & 1u)) v[k] = -INFINITY;
+                }
+                top = fmaxf(top, v[k]);
             }
             // a new maximum anywhere in the warp: all rescale (seldom, behind the first steps)
-            float mn[NR];
-            bool up = false;
+            if (__any_sync(0xffffffffu, top > own_m)) {
+                top = fmaxf(top, own_m);
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                mn[n] = m[n];
-#pragma unroll
-                for (int u = 0; u < U; ++u) mn[n] = fmaxf(mn[n], sc[u][n]);
-                up |= mn[n] != m[n];
-            }
-            if (__any_sync(0xffffffffu, up)) {
+                for (int w = 1; w < kRowLanes; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float corr = top == -INFINITY ? 1.f : two_to(own_m - top);
+                own_m = top;
+                own_l *= corr;
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
-                    const float corr = mn[n] == -INFINITY ? 1.f : two_to(m[n] - mn[n]);
-                    m[n] = mn[n];
-                    l[n] *= corr;
+                    const float by = __shfl_sync(0xffffffffu, corr, row_lane + n * kRowLanes);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[n][c].x *= corr, o[n][c].y *= corr;
+                    for (int c = 0; c < 4; ++c) o[n][c].x *= by, o[n][c].y *= by;
                 }
             }
+            float *wb = weights[warp][i & 1][sub];
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    sc[u][n] = sc[u][n] == -INFINITY ? 0.f : two_to(sc[u][n] - m[n]);
-                    l[n] += sc[u][n];
-                    if constexpr (kF8) sc[u][n] *= vs[u];
+            for (int k = 0; k < kOwn; ++k) {
+                float w = v[k] == -INFINITY ? 0.f : two_to(v[k] - own_m);
+                own_l += w;
+                if constexpr (kF8) {
+                    const float vs = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + 32 + lane];
+                    w *= fminf(fmaxf(vs, kScaleMin), kScaleMax);
                 }
+                wb[own + k] = w;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(wb + k);
+                v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+            }
             // a value that some rows do not see reaches only those that do, whatever it is
             if (every) {
 #pragma unroll
@@ -369,7 +402,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                     for (int c = 0; c < 4; ++c) {
                         const float2 f = val.two(c);
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) o[n][c] = fma2(make_float2(sc[u][n], sc[u][n]), f, o[n][c]);
+                        for (int n = 0; n < NR; ++n) o[n][c] = fma2(make_float2(v[n * U + u], v[n * U + u]), f, o[n][c]);
                     }
                 }
             } else {
@@ -381,7 +414,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                         const float2 f = val.two(c);
 #pragma unroll
                         for (int n = 0; n < NR; ++n)
-                            if ((see[u] >> n) & 1u) o[n][c] = fma2(make_float2(sc[u][n], sc[u][n]), f, o[n][c]);
+                            if ((see[u] >> n) & 1u) o[n][c] = fma2(make_float2(v[n * U + u], v[n * U + u]), f, o[n][c]);
                     }
                 }
             }
@@ -404,6 +437,15 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         };
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();   // every warp is through with its ring
+        // (above 16 lanes a score stands in two)
+#pragma unroll
+        for (int w = LP > N ? LP / N : 1; w < kRowLanes; w <<= 1) own_l += __shfl_xor_sync(0xffffffffu, own_l, w);
+        float m[NR], l[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            m[n] = __shfl_sync(0xffffffffu, own_m, row_lane + n * kRowLanes);
+            l[n] = __shfl_sync(0xffffffffu, own_l, row_lane + n * kRowLanes);
+        }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
