@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         auto issue = [&](int i) -> uint32_t {
             const uint32_t slot = (uint32_t)(i % kStages) * S::kStep;
             const int from = (i % kBatch) * kMine;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+            constexpr int kRow = kPieces * 32 * kPiece;
+            auto one = [&](int u, bool whole) {
                 const int64_t at = __shfl_sync(0xffffffffu, place, from + u * PW + sub);
                 const int n = at >= 0 && ne > 0 ? kPiece : 0;
                 const int64_t mine = n > 0 ? at + e0 : 0;
@@ -201,8 +201,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const KV *src = static_cast<const KV *>(kv ? a.v : a.k) + mine;
-                    constexpr int kRow = kPieces * 32 * kPiece;
-                    if (vec) {
+                    if (whole) {
 #pragma unroll
                         for (int c = 0; c < kPieces; ++c)
                             copy_async<kPiece>(ring_s + slot + (u * 2 + kv) * kRow + c * (32 * kPiece),
@@ -222,6 +221,13 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                         copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((u * 2 + kv) * 32 + lane) * 4,
                                       (kv ? a.vs : a.ks) + (at >= 0 ? sc : 0), at >= 0 ? 4 : 0);
                 }
+            };
+            if (vec) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) one(u, true);
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) one(u, false);
             }
             constexpr uint32_t kBits = (1u << kMine) - 1u;
             return ((there_bits >> from) & kBits) | ((all_bits >> from) & kBits) << 16;
@@ -235,14 +241,16 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             raw[n].zero();
             if (n < rows && ne > 0) raw[n].load(static_cast<const T *>(a.q) + out_row(x.r, n) + e0, ne, vec);
         }
-#pragma unroll
+#pragma unroll 1   // (code that runs once comes as slowly as it is long)
         for (int i = 0; i < kStages - 1; ++i) {
             if (i % kBatch == 0) {
                 locate(i / kBatch, ent);
                 ent = ent_next;
                 ent_next = fetch(i / kBatch + 2);
             }
-            fifo[i] = issue(i);
+#pragma unroll
+            for (int k = 0; k < kStages - 2; ++k) fifo[k] = fifo[k + 1];
+            fifo[kStages - 2] = issue(i);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         float2 qv[NR][4], o[NR][4];
