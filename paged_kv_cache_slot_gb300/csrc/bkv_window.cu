@@ -122,10 +122,33 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * (kStages * S::kStep) + lane * kPiece;   // this lane's part of the warp's ring
     const uint32_t ring_s = shared_at(ring);
-    const int sub = lane / LP, e0 = (lane % LP) * 8;   // this lane's position of PW, and elements
+    // This lane's position of PW, and its elements: four from e0 on and four from e1 on, side by side but for fp32 rows,
+    // of which they are two pieces that LP lanes copy as one run of the row each.
+    constexpr bool kApart = sizeof(KV) == 4;
+    const int sub = lane / LP, e0 = (lane % LP) * (kApart ? 4 : 8), e1 = e0 + (kApart ? 4 * LP : 4);
     const int own = (lane % LP) * N / LP, own_n = own / U, own_u = own % U;   // score n U + u: row n, position u
     const int row_lane = lane & -LP;                   // row n's first lane: row_lane + n kRowLanes
-    const int ne = min(max(a.D - e0, 0), 8);
+    const int ne = min(max(a.D - e0, 0), kApart ? 4 : 8), ne1 = min(max(a.D - e1, 0), 4);   // (ne counts both if side by side)
+    auto load_row = [&](auto &x, const auto *row, bool whole) {
+        if constexpr (kApart) {
+            x.zero();
+            if (whole) {
+                const uint4 lo = ne > 0 ? __ldg(reinterpret_cast<const uint4 *>(row + e0)) : make_uint4(0, 0, 0, 0);
+                const uint4 hi = ne1 > 0 ? __ldg(reinterpret_cast<const uint4 *>(row + e1)) : make_uint4(0, 0, 0, 0);
+                x.w[0] = lo.x, x.w[1] = lo.y, x.w[2] = lo.z, x.w[3] = lo.w;
+                x.w[4] = hi.x, x.w[5] = hi.y, x.w[6] = hi.z, x.w[7] = hi.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i < ne) x.w[i] = __float_as_uint(row[e0 + i]);
+                    if (i < ne1) x.w[4 + i] = __float_as_uint(row[e1 + i]);
+                }
+            }
+        } else {
+            x.zero();
+            if (ne > 0) x.load(row + e0, ne, whole);
+        }
+    };
     const int HP = a.H_kv * a.groups;
     const int q = (int)blockIdx.x / HP, hp = (int)blockIdx.x - q * HP;
     const int g = hp / a.groups, grp = hp - g * a.groups;
@@ -194,28 +217,27 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             constexpr int kRow = kPieces * 32 * kPiece;
             auto one = [&](int u, bool whole) {
                 const int64_t at = __shfl_sync(0xffffffffu, place, from + u * PW + sub);
-                const int n = at >= 0 && ne > 0 ? kPiece : 0;
-                const int64_t mine = n > 0 ? at + e0 : 0;
                 int64_t sc = 0;
                 if constexpr (kF8) sc = __shfl_sync(0xffffffffu, scale_at, from + u * PW + sub);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const KV *src = static_cast<const KV *>(kv ? a.v : a.k) + mine;
+                    const KV *src = static_cast<const KV *>(kv ? a.v : a.k);
+                    const uint32_t to = slot + (u * 2 + kv) * kRow;
                     if (whole) {
 #pragma unroll
-                        for (int c = 0; c < kPieces; ++c)
-                            copy_async<kPiece>(ring_s + slot + (u * 2 + kv) * kRow + c * (32 * kPiece),
-                                               reinterpret_cast<const uint8_t *>(src) + c * kPiece, n);
+                        for (int c = 0; c < kPieces; ++c) {
+                            const int n = at >= 0 && (c ? ne1 : ne) > 0 ? kPiece : 0;
+                            copy_async<kPiece>(ring_s + to + c * (32 * kPiece), src + (n > 0 ? at + (c ? e1 : e0) : 0), n);
+                        }
                     } else {
                         Eight<KV> e;
                         e.zero();
-                        if (n > 0) e.load(src, ne, false);
+                        if (at >= 0) load_row(e, src + at, false);
 #pragma unroll
                         for (int c = 0; c < kPieces; ++c)
 #pragma unroll
                             for (int w = 0; w < kPiece / 4; ++w)
-                                reinterpret_cast<uint32_t *>(ring + slot + (u * 2 + kv) * kRow + c * (32 * kPiece))[w] =
-                                    e.w[c * (kPiece / 4) + w];
+                                reinterpret_cast<uint32_t *>(ring + to + c * (32 * kPiece))[w] = e.w[c * (kPiece / 4) + w];
                     }
                     if constexpr (kF8)   // (behind the rows, a word a lane)
                         copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((u * 2 + kv) * 32 + lane) * 4,
@@ -239,7 +261,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             raw[n].zero();
-            if (n < rows && ne > 0) raw[n].load(static_cast<const T *>(a.q) + out_row(x.r, n) + e0, ne, vec);
+            if (n < rows) load_row(raw[n], static_cast<const T *>(a.q) + out_row(x.r, n), vec);
         }
 #pragma unroll 1   // (code that runs once comes as slowly as it is long)
         for (int i = 0; i < kStages - 1; ++i) {
@@ -316,15 +338,18 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 return e;
             };
             float v[N];
-            uint32_t see[U];
+            uint32_t see = 0u;   // bit u NR + n: row n sees position u
+            if (!every) {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    const int k = u * PW + sub;
+                    uint32_t bits = 0u;
+                    if ((here >> k) & 1u) bits = (here >> (16 + k)) & 1u ? full : seen(s.pos(v_first + i * kStepPos + k));
+                    see |= bits << (u * NR);
+                }
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                see[u] = full;
-                if (!every) {
-                    const int k = u * PW + sub;
-                    if (!((here >> k) & 1u)) see[u] = 0u;
-                    else if (!((here >> (16 + k)) & 1u)) see[u] = seen(s.pos(v_first + i * kStepPos + k));
-                }
                 const Eight<KV> k = held(u, 0);
                 float2 acc[NR];
 #pragma unroll
@@ -361,12 +386,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
                 if constexpr (kF8) v[k] *= reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + lane];
-                if (!every) {
-                    uint32_t bits = see[0];
-#pragma unroll
-                    for (int u = 1; u < U; ++u) bits = own_u + k == u ? see[u] : bits;
-                    if (!((bits >> own_n) & 1u)) v[k] = -INFINITY;
-                }
+                if (!every && !((see >> ((own_u + k) * NR + own_n)) & 1u)) v[k] = -INFINITY;
                 top = fmaxf(top, v[k]);
             }
             // a new maximum anywhere in the warp: all rescale (seldom, behind the first steps)
@@ -393,38 +413,32 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                     const float vs = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + 32 + lane];
                     w *= fminf(fmaxf(vs, kScaleMin), kScaleMax);
                 }
-                wb[own + k] = w;
+                wb[(own_u + k) * NR + own_n] = w;
             }
             __syncwarp();
-#pragma unroll
-            for (int k = 0; k < N; k += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(wb + k);
-                v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
-            }
             // a value that some rows do not see reaches only those that do, whatever it is
+            auto values = [&](int u, uint32_t bits) {
+                const Eight<KV> val = held(u, 1);
+                float w[NR];
+#pragma unroll
+                for (int n = 0; n < NR; n += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(wb + u * NR + n);
+                    w[n] = f.x, w[n + 1] = f.y, w[n + 2] = f.z, w[n + 3] = f.w;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 f = val.two(c);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        if ((bits >> n) & 1u) o[n][c] = fma2(make_float2(w[n], w[n]), f, o[n][c]);
+                }
+            };
             if (every) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const Eight<KV> val = held(u, 1);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 f = val.two(c);
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) o[n][c] = fma2(make_float2(v[n * U + u], v[n * U + u]), f, o[n][c]);
-                    }
-                }
+                for (int u = 0; u < U; ++u) values(u, ~0u);
             } else {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const Eight<KV> val = held(u, 1);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 f = val.two(c);
-#pragma unroll
-                        for (int n = 0; n < NR; ++n)
-                            if ((see[u] >> n) & 1u) o[n][c] = fma2(make_float2(v[n * U + u], v[n * U + u]), f, o[n][c]);
-                    }
-                }
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) values(u, see >> (u * NR));
             }
         }
         // Bad entries among the blocks that the unit begins, counted once a KV head: every block that the span
@@ -470,7 +484,8 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             }
             if (lane < LP) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) *reinterpret_cast<float2 *>(&so[warp][n][e0 + 2 * c]) = o[n][c];
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<float2 *>(&so[warp][n][c < 2 ? e0 + 2 * c : e1 + 2 * (c - 2)]) = o[n][c];
             }
             if (lane == 0) {
                 sm[warp][n] = m[n];
