@@ -72,7 +72,7 @@ struct CcShape {
     static constexpr int U = NR <= 4 ? 4 : 2;
     static constexpr int kStages = sizeof(KV) * U == 16 ? 2 : 4;         // steps in a warp's ring
     static constexpr int kChunk = 8 * (int)sizeof(KV);                   // a lane's piece of a row
-    static constexpr int kStep = U * 2 * kChunk * 32 + (sizeof(KV) == 1 ? U * 2 * 4 * 32 : 0);   // rows, and scales
+    static constexpr int kStep = U * 2 * kChunk * 32 + (sizeof(KV) == 1 ? 2 * 2 * 4 * 32 : 0);   // rows, and scales of two scores a lane
     static constexpr int kRing = 4 * kStages * kStep;
 };
 template <typename KV, int NR, int LP>
@@ -196,12 +196,13 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
         // where batch `b` stands: the row's first element of this head (-1: nothing there) and, E4M3, its scales; and,
         // as bits by lane, which positions are there, and are seen by every row
         int64_t place = -1;
-        int64_t scale_at = 0;
+        int64_t scale_at = -1;
         uint32_t there_bits = 0u, all_bits = 0u;
         auto locate = [&](int b, int32_t ent) {
             const bool there = ent > 0 && ent < a.total_blocks;
             const int32_t p = s.pos(span_at(b));
             place = -1;
+            scale_at = -1;
             if (there) {
                 place = (((int64_t)ent * a.bs + (p - block_of(p) * a.bs)) * a.H_kv + g) * a.D;
                 scale_at = (int64_t)ent * a.H_kv + g;
@@ -217,8 +218,6 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             constexpr int kRow = kPieces * 32 * kPiece;
             auto one = [&](int u, bool whole) {
                 const int64_t at = __shfl_sync(0xffffffffu, place, from + u * PW + sub);
-                int64_t sc = 0;
-                if constexpr (kF8) sc = __shfl_sync(0xffffffffu, scale_at, from + u * PW + sub);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const KV *src = static_cast<const KV *>(kv ? a.v : a.k);
@@ -239,9 +238,6 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                             for (int w = 0; w < kPiece / 4; ++w)
                                 reinterpret_cast<uint32_t *>(ring + to + c * (32 * kPiece))[w] = e.w[c * (kPiece / 4) + w];
                     }
-                    if constexpr (kF8)   // (behind the rows, a word a lane)
-                        copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((u * 2 + kv) * 32 + lane) * 4,
-                                      (kv ? a.vs : a.ks) + (at >= 0 ? sc : 0), at >= 0 ? 4 : 0);
                 }
             };
             if (vec) {
@@ -250,6 +246,16 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
             } else {
 #pragma unroll 1
                 for (int u = 0; u < U; ++u) one(u, false);
+            }
+            if constexpr (kF8) {   // behind the rows, the scales of this lane's own scores
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    const int64_t sc = __shfl_sync(0xffffffffu, scale_at, from + (own_u + k) * PW + sub);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv)
+                        copy_async<4>(ring_s + slot - lane * kPiece + U * 2 * S::kChunk * 32 + ((k * 2 + kv) * 32 + lane) * 4,
+                                      (kv ? a.vs : a.ks) + (sc >= 0 ? sc : 0), sc >= 0 ? 4 : 0);
+                }
             }
             constexpr uint32_t kBits = (1u << kMine) - 1u;
             return ((there_bits >> from) & kBits) | ((all_bits >> from) & kBits) << 16;
@@ -382,10 +388,11 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                     }
                 }
             }
+            const float *scales = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32) + lane;   // E4M3
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
-                if constexpr (kF8) v[k] *= reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + lane];
+                if constexpr (kF8) v[k] *= scales[k * 64];
                 if (!every && !((see >> ((own_u + k) * NR + own_n)) & 1u)) v[k] = -INFINITY;
                 top = fmaxf(top, v[k]);
             }
@@ -410,8 +417,7 @@ __global__ void __launch_bounds__(kCcThreads, kCcPerSm<NR>) window_cc_kernel(con
                 float w = v[k] == -INFINITY ? 0.f : two_to(v[k] - own_m);
                 own_l += w;
                 if constexpr (kF8) {
-                    const float vs = reinterpret_cast<const float *>(slot - lane * kPiece + U * 2 * S::kChunk * 32)[(own_u + k) * 64 + 32 + lane];
-                    w *= fminf(fmaxf(vs, kScaleMin), kScaleMax);
+                    w *= fminf(fmaxf(scales[k * 64 + 32], kScaleMin), kScaleMax);
                 }
                 wb[(own_u + k) * NR + own_n] = w;
             }
