@@ -40,24 +40,25 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 // not keep, and ends with one or two scores of one query row, whose maximum, weights
 // and sum are its own to keep; the weights go back through shared memory.  (Every
 // lane with every score took log2 LP shuffles a score and all exponentials LP times:
-// 196 us in place of 172 in the first case below.)  The sets are joined when the
+// the first case below 196 us in place of 172 then.)  The sets are joined when the
 // unit ends.
 //
 // Rows come by cp.async through a ring of kStages steps in shared memory, each
 // lane copying exactly what it reads itself, so that the only wait is its own:
 // 12 KB a warp are in flight however many registers the rows' arithmetic takes.
+// An fp32 row is two runs of 16 bytes a lane (eight elements side by side asked for
+// every sector twice: 809 us in place of 480 in the second case), and E4M3 scales
+// are copied for a lane's own scores alone (for all U: the third 940 in place of 538).
 // Where the rows stand is worked out for 32 positions at a time, a lane each, their
 // block entries loaded that much ahead, and handed to the lanes that copy them by
-// shuffles.  Multiply-adds go two an instruction.
+// shuffles.  Multiply-adds go two an instruction.  What seldom runs is kept short, in
+// loops that are not unrolled: the code of a step has to stay near (172 -> 140 us).
 //
-// 64 requests of 6000, 32 / 8 heads of 64, bf16: 172 us, 4.6 TB/s (rows in registers
-// one step at a time 505, places worked out a step at a time 275); fp32 heads of 128:
-// 793 us, 4.0 TB/s; E4M3, heads of 256: 1051 us, 1.5 TB/s.  Bound there by
-// instructions' latency at 12 warps an SM: the rate is one of elements, some 2.3e12 a
-// second for 4 query rows, whatever their bytes.  Small calls are bound by
-// the chain of dependent loads and, more, by the unrolled code's first pass (13
-// requests of up to 5000 in a window of 777, 15 / 5 heads of 64, fp32: 16.5 us, its
-// warps wait 3.0 cycles an instruction for instructions).
+// 64 requests of 6000, 32 / 8 heads: bf16 heads of 64 140 us, 5.6 TB/s; fp32 heads of
+// 128 480 us, 6.5 TB/s, near HBM's rate; E4M3 heads of 256 538 us, 2.9 TB/s: there, and
+// with more query rows, bound by instructions at 12 warps an SM.  Small calls are bound
+// by the chain of dependent loads and the code's first pass (13 requests of 33 to 5000
+// in a window of 777, 15 / 5 heads of 64, fp32: 11.4 us).
 // ---------------------------------------------------------------------------
 constexpr int kCcThreads = 128;
 constexpr int kCcTile = 64;
