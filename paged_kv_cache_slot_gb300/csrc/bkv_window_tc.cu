@@ -55,17 +55,17 @@
 // Bound by HBM where requests are long, and by what stands still at a request's
 // start and end where they are short.  Device times (of 6.79 TB/s measured):
 // * bf16, 256 requests of 9 to 16384, 4 tokens, window of 2048 and 4 first tokens,
-//   32 / 8 heads, blocks of 16: 156 us, 5.7 TB/s; 32 of 8192: 6.6 TB/s with one
+//   32 / 8 heads, blocks of 16: 153 us, 5.9 TB/s; 32 of 8192: 6.6 TB/s with one
 //   token, 6.4 with four.
-// * E4M3, 8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 106 us, 5.6 TB/s;
+// * E4M3, 8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 107 us, 5.5 TB/s;
 //   32 of 512 to 4096, one token, 32 / 8 heads: 25.6 us, of which some 9 are the
 //   chain lengths -> table -> first tile and the last unit's end with the merge.
-// * One-tile requests, 16 rows: 2.8 us of a CTA each (bf16), 5.1 (E4M3: the query
+// * One-tile requests, 16 rows: 3.0 us of a CTA each (bf16), 5.1 (E4M3: the query
 //   split is one warp's).
 // What a row needs once a unit (references, factors, sums) is one lane's a row, not
 // every thread's: the unrolled code of 16 rows ran once a unit, at the rate that
-// instructions come in, and took as long as four tiles (the first case 189 us, the
-// second 126).  Warps ask for instructions and wait (1.1 cycles an instruction
+// instructions come in, and took as long as four tiles (the first case 189 us in
+// place of 156 then, the second 126).  Warps ask for instructions and wait (1.1 cycles an instruction
 // issued) more than for anything but memory and each other still.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -845,13 +845,15 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                     }
                     if (!all) {
                         uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
-                        constexpr int kParts = kF8 ? 1 : 2;
+                        // (code that seldom runs is kept short: sink windows of bf16 156 -> 153 us; over E4M3 caches the
+                        // counters of 16 rows would spill: 107 -> 114)
+                        constexpr int kParts = kF8 ? 1 : 2, kScan = kF8 ? 8 : 4, kClear = kF8 ? 8 : 1;
                         bool clear = !any;
                         if (any) {
                             // seen by some rows and not by others: not finite?
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < kParts; ++h)
-#pragma unroll
+#pragma unroll kScan
                                 for (int c = 0; c < 8; ++c) {
                                     const uint4 w = vr[h * (kHalfBytes / 16) + ((c + lane) & 7)];
                                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -868,9 +870,9 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                             }
                         }
                         if (clear) {
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < kParts; ++h)
-#pragma unroll
+#pragma unroll kClear
                                 for (int c = 0; c < 8; ++c) vr[h * (kHalfBytes / 16) + ((c + lane) & 7)] = make_uint4(0, 0, 0, 0);
                         }
                     }
