@@ -16,10 +16,10 @@
 //   P^T, so that a decode step's few query rows fill the N side and a position is
 //   a thread's.  With a position a thread, the scales of its block are two
 //   registers: k's joins the score's factor, and v's the exponent: with s'_j =
-//   s_j + log2 vs_j the weights that enter P V are p'_j = 2^(s'_j - m'), m' their
-//   running maximum, and the row sum is sum_j p'_j / vs_j.  The value tile stays
-//   the codes that TMA brought, and the weights are rounded relative to what
-//   matters most to the output, whatever the blocks' scales.
+//   s_j + log2 vs_j the weights that enter P V are p'_j = 2^(s'_j - ref), ref near
+//   their running maximum (below), and the row sum is sum_j p'_j / vs_j.  The value
+//   tile stays the codes that TMA brought, and the weights are rounded relative to
+//   what matters most to the output, whatever the blocks' scales.
 // * E4M3 caches: both products in kind::f8f6f4 on the codes.  A query row is
 //   divided by a power of two and split into two E4M3 parts (exact for elements
 //   down to 2^-10 of the row's largest, within 2^-17 of it below), P into two
@@ -65,8 +65,8 @@
 // What a row needs once a unit (references, factors, sums) is one lane's a row, not
 // every thread's: the unrolled code of 16 rows ran once a unit, at the rate that
 // instructions come in, and took as long as four tiles (the first case 189 us in
-// place of 156 then, the second 126).  Warps ask for instructions and wait (1.1 cycles an instruction
-// issued) more than for anything but memory and each other still.
+// place of 156 then, the second 126 in place of 106).  Warps still wait 1.1 cycles an
+// instruction issued for instructions.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
