@@ -866,6 +866,14 @@ int bkv_paged_decode_sink(const void *q, const void *k_cache, const void *v_cach
  *   e4m3(c) * v_scales[b][h] (sliding_window 0: full attention).  Any positive
  *   scales are read, not powers of two alone; one of V outside [2^-40, 2^40] is
  *   taken as the nearer end.
+ *   bf16 q with head_dim 128 and blocks of 8 to 64 or of a multiple of 128 runs the
+ *   tensor-core kernel on E4M3 parts: a query row's elements within 2^-17 of its
+ *   largest, a weight of P . V within 2^-8 of itself down to 2^-22 of the row's largest
+ *   weight (times its block's scale of V) and within 2^-31 of that below, so that a
+ *   row of n keys loses n 2^-31 of it at most (max_context_len above 2^22: 2^-25, 2^-34,
+ *   n 2^-34); a query row with an element that is not finite is NaN where it sees a
+ *   key.  Anything else runs the CUDA-core kernel on the exact values, with fp32
+ *   weights.  (bkv_paged_decode_sink's tensor-core kernel rounds weights to bf16.)
  *   k_scales, v_scales fp32 [total_blocks][num_kv_heads]; dtype: the type of q and
  *   out.  Other arguments, masks, errors and workspace as bkv_paged_decode_sink.
  */

@@ -18,33 +18,44 @@
 //   registers: k's joins the score's factor, and v's the exponent: with s'_j =
 //   s_j + log2 vs_j the weights that enter P V are p'_j = 2^(s'_j - ref), ref near
 //   their running maximum (below), and the row sum is sum_j p'_j / vs_j.  The value
-//   tile stays the codes that TMA brought, and the weights are rounded relative to
-//   what matters most to the output, whatever the blocks' scales.
+//   tile stays the codes that TMA brought.
 // * E4M3 caches: both products in kind::f8f6f4 on the codes.  A query row is
 //   divided by a power of two and split into two E4M3 parts (exact for elements
-//   down to 2^-10 of the row's largest, within 2^-17 of it below), P into two
-//   (within 2^-10 of the largest weight); the parts are columns [0, 16) and [16,
-//   32) of one MMA, summed as they are read.  Row sums take fp32 weights.
-//   bf16 caches: weights are rounded to bf16 (2^-8 of each), and the row sums take
+//   down to 2^-10 of the row's largest, within 2^-17 of it below), which are columns
+//   [0, 16) and [16, 32) of one MMA, summed as they are read.
+// * E4M3 weights have four parts, columns of one MMA whose sums are worth 1, 2^-5,
+//   2^-14 and 2^-19.  A weight p' (256 at most) from 2^-6 on is hi + lo / 32, lo the
+//   code of 32 times what hi leaves (8 at most: no code overflows); a smaller one is
+//   that of 2^14 p', in the other two columns.  Both codes are normal numbers, or lo's
+//   step is 2^-14, so that a weight keeps 2^-8 of itself down to 2^-20 and is within
+//   2^-29 below: 2^-22 and 2^-31 of the row's largest, or, as a fresh reference is
+//   2^5 in place of 2^2 where lengths may pass 2^22, 2^-25 and 2^-34.  What a row of n
+//   keys loses by that is n 2^-31 (n 2^-34) of its largest weight at most, 2^-8 whatever
+//   the length.  (Rounding errors of small weights have one sign where their keys' scores
+//   are alike.  Two parts of one fixed step, 2^-9, lost all weights below 2^-15 of the
+//   first maximum from the product and not from the sums: 30 to 50% of an output where
+//   one key has 0.9 of the weight and 8192 share the rest.)  Row sums take fp32 weights.
+// * bf16 caches: weights are rounded to bf16 (2^-8 of each), and the row sums take
 //   the rounded ones.
 // * O stays in tensor memory over a unit, one of each softmax warpgroup (even and
 //   odd tiles), joined at the unit's end.  The reference that weights are taken
 //   from, ref, is not the running maximum: it moves when a weight passes 2^8 (and
 //   O is rescaled then), which a unit's first tiles do and few others.  A tile's
 //   warps agree on it by a vote over a barrier, and work out their weights while
-//   the others arrive.  (E4M3 weights of a fresh reference are at most 2^5, so that
-//   what grows later stays below 448, and 2^-14 of the largest is still a code.)
-// * P is MN-major: a position's 16 weights are one 32-byte span, one or two stores
-//   a thread, with no transposition and no bank conflicts.
+//   the others arrive.
+// * P is MN-major: a position's 16 weights (or four parts of 8) are one 32-byte span,
+//   four parts of 16 two, with no transposition and no bank conflicts.
 // * Four S tiles let the S issuer run two tiles ahead of each warpgroup.
 // * Warp roles (384 threads): 0 gathers K tiles, 2 V tiles through the block table
 //   by 3-D TMA boxes (head_dim half, one head, rows of a block), 1 and 3 issue the
 //   MMAs of S and of P V, 4-7 and 8-11 are two softmax warpgroups on alternate
 //   tiles, the one that has a unit's last tile writes its output.  Warp 2 also
 //   brings the queries, and splits them, so that no launch has to come before this
-//   one.  K and V have rings of 96 KB each.  Block entries are loaded 32 segments
-//   ahead, a lane each, and a unit's queries with its first ones; the scales follow
-//   by cp.async, whose arrival the tile's mask barrier counts.
+//   one.  K and V have rings of 96 KB each, or 64 (16 rows over E4M3 caches: five
+//   stages in place of four were 3 us slower in the second case below).  Block
+//   entries are loaded 32 segments ahead, a lane each, and a unit's queries with its
+//   first ones; the scales follow by cp.async, whose arrival the tile's mask barrier
+//   counts.
 // * V rows that no query row of the group sees, and segments that were not loaded,
 //   are zeroed before P V; a row that only some see is, too, if it is not finite,
 //   and those that see it become NaN.  That lies behind the store of P, when the
@@ -57,10 +68,10 @@
 // * bf16, 256 requests of 9 to 16384, 4 tokens, window of 2048 and 4 first tokens,
 //   32 / 8 heads, blocks of 16: 153 us, 5.9 TB/s; 32 of 8192: 6.6 TB/s with one
 //   token, 6.4 with four.
-// * E4M3, 8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 107 us, 5.5 TB/s;
+// * E4M3, 8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 99 us, 6.0 TB/s;
 //   32 of 512 to 4096, one token, 32 / 8 heads: 25.6 us, of which some 9 are the
 //   chain lengths -> table -> first tile and the last unit's end with the merge.
-// * One-tile requests, 16 rows: 3.0 us of a CTA each (bf16), 5.1 (E4M3: the query
+// * One-tile requests, 16 rows: 3.0 us of a CTA each (bf16), 5.2 (E4M3: the query
 //   split is one warp's).
 // What a row needs once a unit (references, factors, sums) is one lane's a row, not
 // every thread's: the unrolled code of 16 rows ran once a unit, at the rate that
@@ -88,24 +99,35 @@ constexpr int kHalfBytes = kTcTile * 128;            // a bf16 tile's half of he
 constexpr int kRing = 16;                            // tiles whose segment words and scales are kept
 constexpr int kSTiles = 4;                           // S tiles in tensor memory, two a warpgroup
 constexpr int kSets = 4, kQSets = 8;                 // exchanges, and units whose query scales are kept
-constexpr int kTmemCols = 256;
-constexpr uint32_t kColO = 32 * kSTiles, kColX = kColO + 64;   // S tiles, O of both warpgroups, exchanges (16 columns each)
-static_assert(kColX + 16 * kSets <= kTmemCols, "tensor memory");
+constexpr uint32_t kColO = 32 * kSTiles;             // tensor memory: S tiles, O of both warpgroups, exchanges
 constexpr int kTimeoutErr = 1 << 24;
-// The softmax's reference is a power 2^kPExp below the maximum it was taken from and moves when a weight passes
-// 2^kPMax, so that O is seldom rescaled: weights are at most 256 < 448, E4M3's largest value.
-constexpr float kPMax = 8.f;
-template <bool kF8>
-constexpr float kPExp = kF8 ? 5.f : 0.f;
+// The softmax's reference moves when a weight passes 2^kPMax, so that O is seldom rescaled: weights are at most 256 <
+// 448, E4M3's largest value.  Over E4M3 caches a fresh reference puts the largest weight at 2^kFresh, so that small ones
+// have codes, and at 2^kFreshLong where a request may be longer than kLong: what the codes lose of its weights stays
+// below 2^-8.  (8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 99 us with 2^2, 101 with 2^3, 106 with 2^5, whose
+// references move more often.)
+constexpr float kPMax = 8.f, kFresh = 2.f, kFreshLong = 5.f;
+constexpr int32_t kLong = 1 << 22;
 
-template <bool kF8>
+// E4M3 weights: below kSmall a weight enters P V times kLift, in columns of its own, and a second part times 32.
+constexpr float kSmall = 0.015625f, kLift = 16384.f;               // 2^-6, 2^14
+constexpr float kLowered = 6.103515625e-05f, kSecond = 0.03125f;   // 2^-14, 2^-5: what the columns' sums are worth
+
+template <int NQ, bool kF8>
 struct TcCfg {
-    static constexpr int kStages = kF8 ? 6 : 3;
+    // columns between two parts of the weights (NQ of them are used), and of O, which has four parts
+    static constexpr int kPart = NQ == 16 ? 16 : 8;
+    static constexpr int kOCols = kF8 ? 4 * kPart : 32;
+    static constexpr uint32_t kColX = kColO + 2 * kOCols;             // 16 columns each
+    static constexpr int kTmemCols = kColX + 16 * kSets <= 256 ? 256 : 512;
+    static constexpr int kStages = !kF8 ? 3 : NQ == 16 ? 4 : 6;
     static constexpr int kSlot = kF8 ? kTcTile * 128 : 2 * kHalfBytes;
     static constexpr int kQBytes = 2 * kN * 128;                      // two halves (bf16) or parts (E4M3) of 16 rows
     static constexpr int kOffV = kStages * kSlot;
     static constexpr int kOffQ = 2 * kStages * kSlot;
-    static constexpr int kPBytes = kTcTile * 32;                      // a position's weights: 16 bf16, or 16 + 16 E4M3 parts
+    // a position's weights: a span of 32 bytes (16 bf16, or four E4M3 parts of 8), or two (four parts of 16)
+    static constexpr int kPSpans = kF8 && NQ == 16 ? 2 : 1;
+    static constexpr int kPBytes = kPSpans * kTcTile * 32;
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
     static constexpr int kOffMax = kOffP + 2 * kPBytes;               // [warpgroup][2][16][4 warps] floats
     static constexpr int kOffRows = kOffMax + 4 * 4 * kN * 4;         // [softmax warp][3][16] floats
@@ -129,6 +151,7 @@ struct TcCfg {
                       kOffQs % 16 == 0,
                   "alignment");
     static_assert(kStages + kSTiles < kRing, "a ring word is rewritten behind its readers");
+    static_assert(kColX + 16 * kSets <= kTmemCols, "tensor memory");
 };
 
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *v) {
@@ -177,16 +200,18 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 }
 
 // Two numbers of at most 256 as E4M3 codes hi, hi' and the remainders' lo, lo', in half precision: x to 11 bits, hi to 4
-// of them, lo to 4 of the rest.
+// of them, lo to 4 of the rest.  kTimes32: the second parts are those of 32 times the remainder, which is 8 at most.
+template <bool kTimes32>
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x0, x1);
     const __nv_fp8x2_storage_t a = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
-    const __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
+    __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
+    if constexpr (kTimes32) r = __hmul2(r, __half2half2(__ushort_as_half(0x5000)));   // (exact)
     hi = a;
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The first NQ weights of a position, as one span of 32 bytes; chunk c of 16 bytes stands at c ^ (position / 4 & 1).
+// Weights of a position; chunk c of a span's two of 16 bytes stands at c ^ (position / 4 & 1).
 template <int W>
 __device__ __forceinline__ void put_words(uint8_t *at, const uint32_t (&w)[W]) {
     if constexpr (W == 1) *reinterpret_cast<uint32_t *>(at) = w[0];
@@ -223,7 +248,7 @@ constexpr int kRegThreads = NQ <= 8 ? 512 : kTcThreads;
 template <int NQ, bool kF8>
 __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Args a) {
-    using C = TcCfg<kF8>;
+    using C = TcCfg<NQ, kF8>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols)
+                     "r"(C::kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -372,19 +397,21 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t h0, h1, l0, l1;
-                        split2(__uint_as_float(w[2 * k] << 16) * down, __uint_as_float(w[2 * k] & 0xffff0000u) * down, h0, l0);
-                        split2(__uint_as_float(w[2 * k + 1] << 16) * down, __uint_as_float(w[2 * k + 1] & 0xffff0000u) * down,
-                               h1, l1);
+                        split2<false>(__uint_as_float(w[2 * k] << 16) * down, __uint_as_float(w[2 * k] & 0xffff0000u) * down, h0, l0);
+                        split2<false>(__uint_as_float(w[2 * k + 1] << 16) * down,
+                                      __uint_as_float(w[2 * k + 1] & 0xffff0000u) * down, h1, l1);
                         hi[k] = __byte_perm(h0, h1, 0x5410);
                         lo[k] = __byte_perm(l0, l1, 0x5410);
                     }
                     uint8_t *at = dst + n * 128 + (((col >> 1) ^ (n & 7)) << 4) + (col & 1) * 8;
                     *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(at + kN * 128) = make_uint2(lo[0], lo[1]);
-                    // a row that is not finite makes its scores NaN
+                    // a row that is not finite makes its scores NaN (rows past the group's: 0)
                     if (col == 0)
-                        qs[(us & (kQSets - 1)) * kN + n] = t < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
-                                                                          : __uint_as_float(0x7fffffffu);
+                        qs[(us & (kQSets - 1)) * kN + n] =
+                            n >= rows ? 0.f
+                                      : t < 0x7f800000u ? a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
+                                                        : __uint_as_float(0x7fffffffu);
                 }
             } else {
                 // 64 elements a half; 16-byte chunk c of row n at c ^ (n & 7)
@@ -551,8 +578,9 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                 }
             }
         } else if (lane == 0) {
-            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, 2 * kN, 1, 1) : idesc_bf16(128, kN, 1, 1);
-            const uint32_t v_lo = desc_lo(sm_v, kF8 ? 16 : kHalfBytes), p_lo = desc_lo(sm_p, 16);
+            constexpr uint32_t kIdesc = kF8 ? idesc_f16(128, C::kOCols, 1, 1) : idesc_bf16(128, kN, 1, 1);
+            const uint32_t v_lo = desc_lo(sm_v, kF8 ? 16 : kHalfBytes);
+            const uint32_t p_lo = desc_lo(sm_p, C::kPSpans == 2 ? kTcTile * 32 : 16);
             int j = 0;
             Ring ring;
             bool ok = true;
@@ -565,11 +593,11 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem + kColO + 32u * (uint32_t)b, v = v_lo + ring.slot * (C::kSlot >> 4);
+                    const uint32_t d = tmem + kColO + (uint32_t)(C::kOCols * b), v = v_lo + ring.slot * (C::kSlot >> 4);
                     const uint32_t p = p_lo + b * (C::kPBytes >> 4);
                     const uint32_t more = jt >= 2;   // a warpgroup's first tile of a unit begins its O
                     // V^T and P^T MN-major: a row's 128 codes (64 bf16) are one 128-byte span, a position's weights one
-                    // of 32 bytes
+                    // or two of 32 bytes
 #pragma unroll
                     for (int kk = 0; kk < (kF8 ? kTcTile / 32 : kTcTile / 16); ++kk)
                         mma_words<kF8, kDesc128, kDesc32>(d, v + kk * (kF8 ? 256 : 128), p + kk * (kF8 ? 64 : 32), kIdesc,
@@ -585,7 +613,7 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
         const int wg = (warp - kWarpS) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                  // TMEM lane: position in the tile, and head_dim row
         const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-        const uint32_t o_col = tmem + lane_base + kColO + 32u * (uint32_t)wg;
+        const uint32_t o_col = tmem + lane_base + kColO + (uint32_t)(C::kOCols * wg);
         const int red_row = reduced_row<NQ>(lane);
         const bool red_writer = reduced_writer<NQ>(lane);
         const int flip = (row >> 2) & 1;
@@ -625,10 +653,20 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
             return group_wait();
         };
         auto load_o = [&](float (&v)[NQ]) {
-            if constexpr (kF8) tmem_ld_sum2<NQ>(o_col, v);
-            else tmem_ld_cols<NQ>(o_col, v);
+            tmem_ld_cols<NQ>(o_col, v);
+            if constexpr (kF8) {   // the parts, each worth its power of two
+                float part[NQ];
+#pragma unroll 1
+                for (int k = 1; k < 4; ++k) {
+                    tmem_ld_cols<NQ>(o_col + (uint32_t)(C::kPart * k), part);
+                    const float worth = (k & 1 ? kSecond : 1.f) * (k & 2 ? kLowered : 1.f);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) v[n] = fmaf(part[n], worth, v[n]);
+                }
+            }
         };
         const int tok_lo = i0 / a.G, tok_hi = (i0 + rows - 1) / a.G, head0 = i0 % a.G;
+        const float fresh = !kF8 ? 0.f : a.max_ctx > kLong ? kFreshLong : kFresh;
         int j = 0, xs = 0, mu = 0;   // tile, exchange and own unit number
         Ring vring;
         bool ok = true;
@@ -648,26 +686,19 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
             const int32_t first_hi = a.window > 0 ? t_hi - a.window + 1 : INT32_MIN;
             // A row's weights are 2^(s - ref): ref is set at the first tile in which the row sees a key (bit n of
             // `have`) and moved when a weight passes 2^kPMax.
-            float lsum[NQ], ref[NQ], cs[NQ];
+            float lsum[NQ], ref[NQ];
             uint32_t have = 0u;
             const uint32_t every = (1u << rows) - 1u;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 lsum[n] = 0.f;
                 ref[n] = 0.f;
-                cs[n] = a.scale_log2;
             }
+            const float *cs = qs + (us & (kQSets - 1)) * kN;   // E4M3: the scores' factors, read in every tile
             if constexpr (kF8) {
                 // A set is rewritten eight units on, behind the S MMAs of the sixth unit after this one: its last tile is at
                 // least six behind this unit's last, and its S tile's last reader this warpgroup, past this unit.
                 if (!mbar_wait_warp(bar_qscale(us & (kQSets - 1)), (uint32_t)(us / kQSets) & 1u, abort_flag)) break;
-#pragma unroll
-                for (int n = 0; n < NQ; n += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(qs + (us & (kQSets - 1)) * kN + n);
-                    cs[n] = f.x, cs[n + 1] = f.y, cs[n + 2] = f.z, cs[n + 3] = f.w;
-                }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) cs[n] = n < rows ? cs[n] : 0.f;
             }
             for (int jt = 0; jt < x.nt; ++jt, ++j, vring.advance(kStages)) {
                 if ((j & 1) != wg) continue;
@@ -700,8 +731,19 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                 const bool in = loaded && v < s.len, sink = p < a.sinks;
                 const bool any = in && p <= last_hi && (p >= first_lo || sink);
                 const bool all = in && p <= last_lo && (p >= first_hi || sink);
+                if constexpr (kF8) {
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) sv[n] = kF8 ? fmaf(sv[n], cs[n] * ks, lv - ref[n]) : fmaf(sv[n], cs[n], -ref[n]);
+                    for (int n = 0; n < NQ; n += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(cs + n);
+                        sv[n] = fmaf(sv[n], f.x * ks, lv - ref[n]);
+                        sv[n + 1] = fmaf(sv[n + 1], f.y * ks, lv - ref[n + 1]);
+                        sv[n + 2] = fmaf(sv[n + 2], f.z * ks, lv - ref[n + 2]);
+                        sv[n + 3] = fmaf(sv[n + 3], f.w * ks, lv - ref[n + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) sv[n] = fmaf(sv[n], a.scale_log2, -ref[n]);
+                }
                 const bool tile_all = __all_sync(0xffffffffu, all);
                 if (!tile_all && !all) {
                     // rows that see a position, one by one: row n's token is at position t
@@ -716,23 +758,29 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                         }
                     }
                 }
-                // The weights as they go to P V (E4M3: NQ / 4 words of first parts, then the second ones), and into the sums.
-                uint32_t pw[NQ / 2];
+                // The weights as they go to P V (E4M3: NQ / 4 words of each part), and into the sums.
+                uint32_t pw[kF8 ? NQ : NQ / 2];
                 auto weigh = [&] {
                     if constexpr (kF8) {
 #pragma unroll
                         for (int n = 0; n < NQ; n += 4) {
                             float w[4];
+                            uint32_t low = 0u;   // a byte of ones for each small weight
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 w[i] = fast_exp2(sv[n + i]);
                                 lsum[n + i] = fmaf(w[i], rv, lsum[n + i]);
+                                const bool small = w[i] < kSmall;
+                                if (small) w[i] *= kLift, low |= 0xffu << (8 * i);
                             }
                             uint32_t h0, h1, l0, l1;
-                            split2(w[0], w[1], h0, l0);
-                            split2(w[2], w[3], h1, l1);
-                            pw[n / 4] = __byte_perm(h0, h1, 0x5410);
-                            pw[NQ / 4 + n / 4] = __byte_perm(l0, l1, 0x5410);
+                            split2<true>(w[0], w[1], h0, l0);
+                            split2<true>(w[2], w[3], h1, l1);
+                            const uint32_t hi = __byte_perm(h0, h1, 0x5410), lo = __byte_perm(l0, l1, 0x5410);
+                            pw[n / 4] = hi & ~low;
+                            pw[NQ / 4 + n / 4] = lo & ~low;
+                            pw[NQ / 2 + n / 4] = hi & low;
+                            pw[3 * NQ / 4 + n / 4] = lo & low;
                         }
                     } else {
 #pragma unroll
@@ -786,7 +834,7 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                     const float top = fmaxf(max3(t4.x, t4.y, t4.z), t4.w);
                     const bool had = (have >> my_row) & 1u;
                     const bool to = had ? top > kPMax : top > -INFINITY;
-                    const float down = to ? top - kPExp<kF8> : 0.f;
+                    const float down = to ? top - fresh : 0.f;
                     hand_out(0, down);
                     hand_out(1, had ? fast_exp2(-down) : 1.f);
                     const bool scale = have != 0u;   // there is something in the sums and in O
@@ -809,12 +857,12 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                         take(1, corr);
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) lsum[n] *= corr[n];
-#pragma unroll
-                        for (int h = 0; h < (kF8 ? 2 : 1); ++h) {
-                            tmem_ld_cols<NQ>(o_col + 16u * h, o);
+#pragma unroll 1
+                        for (int k = 0; k < (kF8 ? 4 : 1); ++k) {
+                            tmem_ld_cols<NQ>(o_col + (uint32_t)(C::kPart * k), o);
 #pragma unroll
                             for (int n = 0; n < NQ; ++n) o[n] *= corr[n];
-                            tmem_st_cols<NQ>(o_col + 16u * h, o);
+                            tmem_st_cols<NQ>(o_col + (uint32_t)(C::kPart * k), o);
                         }
                         tmem_st_wait();
                     }
@@ -825,9 +873,18 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                     ok = false;
                     break;
                 }
-                if constexpr (kF8) {
-                    put_words(p_hi, reinterpret_cast<const uint32_t(&)[NQ / 4]>(pw[0]));
-                    put_words(p_lo, reinterpret_cast<const uint32_t(&)[NQ / 4]>(pw[NQ / 4]));
+                if constexpr (kF8 && NQ == 16) {
+                    put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(pw[0]));
+                    put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(pw[4]));
+                    put_words(p_hi + kTcTile * 32, reinterpret_cast<const uint32_t(&)[4]>(pw[8]));
+                    put_words(p_lo + kTcTile * 32, reinterpret_cast<const uint32_t(&)[4]>(pw[12]));
+                } else if constexpr (kF8 && NQ == 8) {
+                    put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(pw[0]));
+                    put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(pw[4]));
+                } else if constexpr (kF8) {
+                    const uint32_t w0[4] = {pw[0], 0u, pw[1], 0u}, w1[4] = {pw[2], 0u, pw[3], 0u};
+                    put_words(p_hi, w0);
+                    put_words(p_lo, w1);
                 } else if constexpr (NQ == 16) {
                     put_words(p_hi, reinterpret_cast<const uint32_t(&)[4]>(pw[0]));
                     put_words(p_lo, reinterpret_cast<const uint32_t(&)[4]>(pw[4]));
@@ -905,7 +962,7 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
             // the exchange after this one, which it begins when it has read this.
             const bool finish = ((j - 1) & 1) == wg;
             const int set = xs & (kSets - 1);
-            const uint32_t x_col = tmem + lane_base + kColX + 16u * (uint32_t)set;
+            const uint32_t x_col = tmem + lane_base + C::kColX + 16u * (uint32_t)set;
             float2 *xm = reinterpret_cast<float2 *>(smem + C::kOffXm) + set * kN;
             const uint32_t x_par = (uint32_t)(xs >> 2) & 1u;
             if (both) ++xs;
@@ -979,7 +1036,7 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
     if (*abort_flag && threadIdx.x == 0 && a.err) atomicAdd(a.err, kTimeoutErr);
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
     }
 }
 
@@ -1005,7 +1062,7 @@ bool prepare_tc(const Args &a, TcLaunch *t) {
 template <int NQ, bool kF8>
 static int launch(const Args &a, const TcLaunch &t, cudaStream_t st) {
     auto kern = window_tc_kernel<NQ, kF8>;
-    constexpr int smem = TcCfg<kF8>::kSmem;
+    constexpr int smem = TcCfg<NQ, kF8>::kSmem;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
