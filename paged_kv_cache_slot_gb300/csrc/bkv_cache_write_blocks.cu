@@ -72,8 +72,8 @@ __device__ __forceinline__ int32_t number_of(const Args &a, int r, int32_t start
 }
 
 // A touched block's rows: `cnt` tokens from `tok` on go to rows `first` on of the
-// block whose table entry is `entry` (INT32_MAX: past the table's columns); cnt
-// 0: nothing.
+// block whose table entry is `entry`; first -1: the block lies past the table's
+// columns; cnt 0: nothing.
 struct Part {
     int32_t tok, first, cnt, entry;
 };
@@ -117,9 +117,10 @@ __device__ __forceinline__ Part part_of(const Args &a, int32_t u, bool count) {
     const int64_t b0 = (int64_t)lb * a.bs;
     const int32_t p0 = (int32_t)max((int64_t)start, b0), p1 = (int32_t)min((int64_t)L, b0 + a.bs);
     if (b0 >= L) return p;
-    p.entry = lb < a.bt_cols ? __ldg(a.bt + (int64_t)lo * a.bt_stride + lb) : INT32_MAX;
+    const bool past = lb >= a.bt_cols;
+    p.entry = past ? 0 : __ldg(a.bt + (int64_t)lo * a.bt_stride + lb);
     p.tok = t0 + (p0 - start);
-    p.first = (int32_t)(p0 - b0);
+    p.first = past ? -1 : (int32_t)(p0 - b0);
     p.cnt = p1 - p0;
     return p;
 }
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreadsOf<W>, 512 / kThreadsOf<W>) write_bloc
         load(xv, 1, now, hp);
         // a real block, and its scales so far
         const bool real = now.entry > 0 && now.entry < a.total_blocks;
-        if (now.entry >= a.total_blocks && hp == 0 && gl == 0 && a.err) atomicAdd(a.err, 1);
+        if ((now.first < 0 || now.entry >= a.total_blocks) && hp == 0 && gl == 0 && a.err) atomicAdd(a.err, 1);
         float old_k = 0.f, old_v = 0.f;
         if (real && now.first > 0) {
             old_k = a.ks[(int64_t)now.entry * a.hkv + hp];
