@@ -113,10 +113,12 @@ __device__ __forceinline__ Part part_of(const Args &a, int32_t u, bool count) {
         if (count && j == 0 && lane == 0 && a.err) atomicAdd(a.err, 1);
         return p;
     }
-    const int32_t start = L - (t1 - t0), lb = a.block_of(start) + j;
-    const int64_t b0 = (int64_t)lb * a.bs;
-    const int32_t p0 = (int32_t)max((int64_t)start, b0), p1 = (int32_t)min((int64_t)L, b0 + a.bs);
+    const int32_t start = L - (t1 - t0);
+    // (64 bits: the numbers behind the last request's blocks are its own as well, however many they are)
+    const int64_t b0 = ((int64_t)a.block_of(start) + j) * a.bs;
     if (b0 >= L) return p;
+    const int32_t lb = a.block_of(start) + j;
+    const int32_t p0 = max(start, (int32_t)b0), p1 = (int32_t)min((int64_t)L, b0 + a.bs);
     const bool past = lb >= a.bt_cols;
     p.entry = past ? 0 : __ldg(a.bt + (int64_t)lo * a.bt_stride + lb);
     p.tok = t0 + (p0 - start);

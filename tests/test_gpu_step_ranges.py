@@ -34,3 +34,19 @@ def test_a_cache_of_2_to_the_31_blocks():
     assert int(err) == 1
     assert float(ks[-1]) == float(ks[7]) and int(k[-1]) == int(k[7]) != 0
     assert int((k.view(-1) != 0).sum()) == 2
+
+
+def test_lengths_near_2_to_the_31():
+    """A request that ends at position 2^31 - 2, with rows of the step behind its last token: its one block is past the
+    table's columns, and the rows behind belong to nobody."""
+    k, v = (torch.zeros((5, 1, 1, 8), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.ones((5, 1), device=DEV) for _ in range(2))
+    x = torch.ones((6, 1, 8), device=DEV)
+    for lens, qsl in (([2 ** 31 - 1], [0, 1]), ([1, 2 ** 31 - 1], [0, 1, 2]), ([2 ** 31 - 1, 1], [0, 1, 2])):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        k.zero_(), v.zero_()
+        table = torch.full((len(lens), 3), 2, dtype=torch.int32, device=DEV)
+        bkv.bkv_cache_write_fp8_blocks(x, x, _i32(*qsl), _i32(*lens), table, k, v, ks, vs, err_count=err)
+        assert int(err) == 1
+        assert bool((k[[0, 1, 3, 4]] == 0).all()) and bool((v[[0, 1, 3, 4]] == 0).all())
+        assert bool((k[2] != 0).all()) == (len(lens) == 2)
