@@ -754,8 +754,8 @@ int bkv_verify_draft_tree(const float *target_probs, int64_t target_req_stride, 
  *   blocks, once (those tokens get slot -1); every block that the free list lacks
  *   (-1); a step of more than max_num_tokens tokens, once (those past it are not
  *   listed).
- *   INVALID_ARG: block_size <= 0, negative sizes, num_reqs above 2^30, bt_stride <
- *   bt_cols, null pointers, context_lens the same array as an input.
+ *   INVALID_ARG: block_size <= 0, negative sizes, num_reqs or bt_cols above 2^30,
+ *   bt_stride < bt_cols, null pointers, context_lens the same array as an input.
  */
 int bkv_build_step(const int32_t *cached_lens, const int32_t *new_lens, int32_t num_reqs, const int32_t *free_blocks,
                    int32_t num_free, int32_t block_size, int32_t *block_table, int64_t bt_stride, int32_t bt_cols,

@@ -209,7 +209,7 @@ extern "C" int bkv_build_step(const int32_t *cached_lens, const int32_t *new_len
     using namespace bkv;
     if (num_reqs < 0 || num_free < 0 || block_size <= 0 || bt_cols < 0 || bt_stride < bt_cols || max_num_tokens < 0)
         return BKV_ERR_INVALID_ARG;
-    if (num_reqs > 1 << 30) return BKV_ERR_INVALID_ARG;   // (walks by 32 rows stay within int32)
+    if (num_reqs > 1 << 30 || bt_cols > 1 << 30) return BKV_ERR_INVALID_ARG;   // (walks over them stay within int32)
     if (!query_start_loc || !blocks_used) return BKV_ERR_INVALID_ARG;
     if (num_reqs > 0 && (!cached_lens || !new_lens || !context_lens || (bt_cols > 0 && !block_table)))
         return BKV_ERR_INVALID_ARG;
