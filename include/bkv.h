@@ -349,7 +349,10 @@ int bkv_slot_mapping_cache_write_fp8(const int32_t *block_table, int32_t num_req
  *   E4M3 tensor cores with each query row split into two E4M3 parts (exact
  *   for elements down to 2^-10 of the row's largest, within 2^-17 of it
  *   below), P . v on E4M3 tensor cores with the value codes as stored and
- *   the weights as two E4M3 parts (within 2^-10 of p 2^8); anything else
+ *   the weights as two E4M3 parts (within 2^-10 of p 2^8: weights below
+ *   2^-18 of a row's largest are lost, so that a row of one heavy key and
+ *   thousands of light ones loses their part, where
+ *   bkv_paged_decode_fp8_blocks does not); anything else
  *   runs the CUDA-core kernel on the exact code values.  The workspace
  *   (bkv_paged_decode_workspace_size) includes the split queries.
  *   Errors: as bkv_paged_decode_swa, plus INVALID_ARG for a scale that is

@@ -45,7 +45,9 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 //
 // Rows come by cp.async through a ring of kStages steps in shared memory, each
 // lane copying exactly what it reads itself, so that the only wait is its own:
-// 12 KB a warp are in flight however many registers the rows' arithmetic takes.
+// what is in flight does not hang on the registers that the rows' arithmetic takes
+// (12 KB a warp for bf16 rows and up to 4 query rows, 8 for fp32 ones; with 8 query
+// rows 6 and 12; E4M3 7.5 and 4.5).
 // An fp32 row is two runs of 16 bytes a lane (eight elements side by side asked for
 // every sector twice: 809 us in place of 480 in the second case), and E4M3 scales
 // are copied for a lane's own scores alone (for all U: the third 940 in place of 538).

@@ -69,8 +69,9 @@
 //   32 / 8 heads, blocks of 16: 153 us, 5.9 TB/s; 32 of 8192: 6.6 TB/s with one
 //   token, 6.4 with four.
 // * E4M3, 8 requests of 4000 to 131071, 2 tokens, 64 / 8 heads: 99 us, 6.0 TB/s;
-//   32 of 512 to 4096, one token, 32 / 8 heads: 25.6 us, of which some 9 are the
-//   chain lengths -> table -> first tile and the last unit's end with the merge.
+//   32 of 512 to 4096, one token, 32 / 8 heads: 28.6 us (26 where L2 holds them in
+//   part), of which some 9 are the chain lengths -> table -> first tile and the last
+//   unit's end with the merge.
 // * One-tile requests, 16 rows: 3.0 us of a CTA each (bf16), 5.2 (E4M3: the query
 //   split is one warp's).
 // What a row needs once a unit (references, factors, sums) is one lane's a row, not
@@ -241,7 +242,8 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 }
 
 // Few rows' registers are held to what 512 threads could have: the merge's CTAs then wait beside this kernel's from its
-// start on, and begin as it ends (one request of 700, E4M3: 9.5 -> 8.5 us; 16 rows would spill).
+// start on, and begin as it ends (one request of 700, E4M3: 9.5 -> 8.5 us; 16 rows take all 168 that 384 threads can have,
+// and spill 8 bytes over E4M3 caches).
 template <int NQ>
 constexpr int kRegThreads = NQ <= 8 ? 512 : kTcThreads;
 
@@ -902,8 +904,8 @@ __global__ void __launch_bounds__(kRegThreads<NQ>, 1)
                     }
                     if (!all) {
                         uint4 *vr = reinterpret_cast<uint4 *>(smem + C::kOffV + vslot * C::kSlot + row * 128);
-                        // (code that seldom runs is kept short: sink windows of bf16 156 -> 153 us; over E4M3 caches the
-                        // counters of 16 rows would spill: 107 -> 114)
+                        // (code that seldom runs is kept short: sink windows of bf16 156 -> 153 us; over E4M3 caches, where
+                        // 16 rows leave no registers for its counters, it was 107 -> 114)
                         constexpr int kParts = kF8 ? 1 : 2, kScan = kF8 ? 8 : 4, kClear = kF8 ? 8 : 1;
                         bool clear = !any;
                         if (any) {
